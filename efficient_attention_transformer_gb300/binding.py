@@ -6,6 +6,7 @@ of the computation runs in the library's CUDA kernels.  Loading fails loudly
 when the library has not been built.
 """
 
+import contextlib
 import ctypes
 import os
 
@@ -50,6 +51,11 @@ EXPORTED = (
     "flash_gau_forward_host_workspace_bytes",
     "flash_gau_forward_host",
     "flash_gau_selftest_bounded_wait",
+    "flash_gau_residual_norm",
+    "flash_gau_residual_norm_backward_workspace_bytes",
+    "flash_gau_residual_norm_backward",
+    "flash_gau_adamw_step",
+    "flash_gau_adamw_moments",
 )
 
 # Capacity of the static scratch behind flash_gau_forward_noalloc.
@@ -92,6 +98,53 @@ class Block(ctypes.Structure):
         ("rope_base", ctypes.c_float),
         ("pos_offset", ctypes.c_int),
         ("residual", ctypes.c_int),
+    ]
+
+
+class Residual(ctypes.Structure):
+    """flash_gau_residual: norms, scale and gate of the residual stream."""
+    _fields_ = [
+        ("post", ctypes.c_int),
+        ("norm", ctypes.c_int),
+        ("post_g", ctypes.c_void_p),
+        ("post_b", ctypes.c_void_p),
+        ("norm_g", ctypes.c_void_p),
+        ("norm_b", ctypes.c_void_p),
+        ("scale", ctypes.c_void_p),
+        ("gate", ctypes.c_void_p),
+        ("eps", ctypes.c_float),
+    ]
+
+
+class ResidualGrads(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in
+                ("dh", "dy", "dgate", "dscale", "dpost_g", "dpost_b", "dnorm_g", "dnorm_b")]
+
+
+class AdamWTensor(ctypes.Structure):
+    _fields_ = [
+        ("p", ctypes.c_void_p),
+        ("copy", ctypes.c_void_p),
+        ("g", ctypes.c_void_p),
+        ("m", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("m_scale", ctypes.c_void_p),
+        ("v_scale", ctypes.c_void_p),
+        ("n", ctypes.c_longlong),
+        ("g_dtype", ctypes.c_int),
+        ("weight_decay", ctypes.c_float),
+    ]
+
+
+class AdamWHyper(ctypes.Structure):
+    _fields_ = [
+        ("lr", ctypes.c_double),
+        ("beta1", ctypes.c_double),
+        ("beta2", ctypes.c_double),
+        ("eps", ctypes.c_double),
+        ("step", ctypes.c_longlong),
+        ("state_bits", ctypes.c_int),
+        ("grad_scale", ctypes.c_void_p),
     ]
 
 
@@ -162,6 +215,20 @@ def lib():
         L.flash_gau_decode_state_bytes.restype = sz
         L.flash_gau_decode_step.argtypes = [p, ctypes.POINTER(Weights), i, i, i, p, sz, p, p]
         L.flash_gau_decode_step.restype = i
+        ll = ctypes.c_longlong
+        L.flash_gau_residual_norm.argtypes = [p, p, ctypes.POINTER(Residual), ll, i, i, p, p, p]
+        L.flash_gau_residual_norm.restype = i
+        L.flash_gau_residual_norm_backward_workspace_bytes.argtypes = [ll, i]
+        L.flash_gau_residual_norm_backward_workspace_bytes.restype = sz
+        L.flash_gau_residual_norm_backward.argtypes = [p, p, p, p, ctypes.POINTER(Residual), ll, i,
+                                                       i, ctypes.POINTER(ResidualGrads), p, sz, p]
+        L.flash_gau_residual_norm_backward.restype = i
+        L.flash_gau_adamw_step.argtypes = [ctypes.POINTER(AdamWTensor), i,
+                                           ctypes.POINTER(AdamWHyper), p]
+        L.flash_gau_adamw_step.restype = i
+        L.flash_gau_adamw_moments.argtypes = [ctypes.POINTER(AdamWTensor), i, ctypes.POINTER(p),
+                                              ctypes.POINTER(p), p]
+        L.flash_gau_adamw_moments.restype = i
         _lib = L
     return _lib
 
@@ -486,3 +553,224 @@ class Decoder:
             self.weights.dtype, _dev_ptr(self.state, "state"), self.state.numel(),
             _dev_ptr(out, "out", x.dtype), stream.cuda_stream))
         return out
+
+
+def _scope(device, stream):
+    """Context of one call on `device`: the device is current, and where a
+    stream is given it is too, so that what the call allocates belongs to it."""
+    if stream is not None:
+        return torch.cuda.stream(stream)
+    if torch.cuda.current_device() != device.index:
+        return torch.cuda.device(device)
+    return contextlib.nullcontext()
+
+
+def _rows(t, name, like):
+    """Pointer of a tensor of rows that has to be as `like` is, or None."""
+    if t is None:
+        return None
+    if t.shape != like.shape or t.device != like.device:
+        raise ValueError("%s must have the shape and device of the stream" % name)
+    return _dev_ptr(t, name, like.dtype)
+
+
+def _param(t, name, n, device):
+    if t is None:
+        return None
+    if t.numel() != n or t.device != device:
+        raise ValueError("%s must hold %d values on %s" % (name, n, device))
+    return _dev_ptr(t, name, torch.float32)
+
+
+def _residual(like, post_norm, post_g, post_b, gate, scale, norm, norm_g, norm_b, eps):
+    d, dev = like.shape[-1], like.device
+    return Residual(int(post_norm), int(norm),
+                    _param(post_g, "post_g", d if post_norm == NORM_LAYER else 1, dev),
+                    _param(post_b, "post_b", d, dev),
+                    _param(norm_g, "norm_g", d if norm == NORM_LAYER else 1, dev),
+                    _param(norm_b, "norm_b", d, dev), _param(scale, "scale", d, dev),
+                    _rows(gate, "gate", like), float(eps))
+
+
+def residual_norm(h, y=None, post_norm=NORM_NONE, post_g=None, post_b=None, gate=None, scale=None,
+                  norm=NORM_LAYER, norm_g=None, norm_b=None, eps=1e-5, out_r=None, out_n=None,
+                  stream=None):
+    """(r, n) with r = h + scale * gate * post(y) and n = norm(r), through
+    flash_gau_residual_norm.  h, y, gate: [..., d] in one io type; scale and
+    the norms' parameters fp32 ([d], a ScaleNorm's g [1]).  Without y only the
+    norm is taken and r is h; with norm NORM_NONE n is None."""
+    dt = dtype_code(h.dtype)
+    o = _residual(h, post_norm, post_g, post_b, gate, scale, norm, norm_g, norm_b, eps)
+    hp = _dev_ptr(h, "h", h.dtype)
+    d = h.shape[-1]
+    with _scope(h.device, stream):
+        if out_r is None and y is not None:
+            out_r = torch.empty_like(h)
+        if out_n is None and norm != NORM_NONE:
+            out_n = torch.empty_like(h)
+        sp = torch.cuda.current_stream(h.device).cuda_stream
+        _check(lib().flash_gau_residual_norm(
+            hp, _rows(y, "y", h), ctypes.byref(o), h.numel() // max(d, 1), d, dt,
+            _rows(out_r, "out_r", h), _rows(out_n, "out_n", h), sp))
+    return (h if out_r is None else out_r), out_n
+
+
+def residual_norm_backward(dr, dn, r, y, post_norm=NORM_NONE, post_g=None, post_b=None, gate=None,
+                           scale=None, norm=NORM_LAYER, norm_g=None, norm_b=None, eps=1e-5,
+                           out=None, workspace=None, stream=None):
+    """Gradients of sum(dr * r) + sum(dn * n) through
+    flash_gau_residual_norm_backward: a dict with dh, dy, dgate (io type) and
+    dscale, dpost_g, dpost_b, dnorm_g, dnorm_b (fp32), None for what the
+    options leave out.  dr may be None (nothing else reads the stream); y is
+    the forward's y, None when the forward had none.  `out`: tensors to write
+    to, by the same names (dh may be dr itself, for instance)."""
+    like = dr if dr is not None else dn
+    if like is None:
+        raise ValueError("one of dr and dn must be given")
+    dt = dtype_code(like.dtype)
+    _dev_ptr(like, "dr" if dr is not None else "dn")
+    o = _residual(like, post_norm, post_g, post_b, gate, scale, norm, norm_g, norm_b, eps)
+    d = like.shape[-1]
+    M = like.numel() // max(d, 1)
+    f32, dev = torch.float32, like.device
+    out = dict(out or {})
+    with _scope(dev, stream):
+        for name, there in (("dh", True), ("dy", y is not None), ("dgate", gate is not None)):
+            if out.get(name) is None:
+                out[name] = torch.empty_like(like) if there else None
+        for name, there, n in (("dscale", scale is not None, d),
+                               ("dpost_g", post_norm, d if post_norm == NORM_LAYER else 1),
+                               ("dpost_b", post_norm == NORM_LAYER, d),
+                               ("dnorm_g", norm, d if norm == NORM_LAYER else 1),
+                               ("dnorm_b", norm == NORM_LAYER, d)):
+            if out.get(name) is None:
+                out[name] = torch.empty(n, dtype=f32, device=dev) if there else None
+            elif not there or out[name].numel() != n:
+                raise ValueError("%s must hold the gradient of its parameter" % name)
+        g = ResidualGrads(*(_rows(out[k], k, like) for k in ("dh", "dy", "dgate")),
+                          *(None if out[k] is None else _dev_ptr(out[k], k, f32)
+                            for k in ("dscale", "dpost_g", "dpost_b", "dnorm_g", "dnorm_b")))
+        n = lib().flash_gau_residual_norm_backward_workspace_bytes(M, d)
+        if n == 0:
+            raise FlashGauError(ENOTSUP if M > 0 and d > 0 else EINVAL,
+                                "invalid or unsupported problem")
+        if workspace is None:
+            workspace = torch.empty(n, dtype=torch.uint8, device=dev)
+        sp = torch.cuda.current_stream(dev).cuda_stream
+        _check(lib().flash_gau_residual_norm_backward(
+            _rows(dr, "dr", like), _rows(dn, "dn", like), _rows(r, "r", like),
+            _rows(y, "y", like), ctypes.byref(o), M, d, dt, ctypes.byref(g),
+            _dev_ptr(workspace, "workspace"), workspace.numel() * workspace.element_size(), sp))
+    return out
+
+
+class AdamW:
+    """AdamW over a list of fp32 parameter tensors, one launch per step
+    through flash_gau_adamw_step.
+
+    params: contiguous fp32 CUDA tensors of one device, updated in place.
+    copies: for each a bf16 tensor of its shape that receives the updated
+    values (the weights that a bf16 layer reads), or None; None: no copies.
+    weight_decay: one value, or one for each tensor.  state_bits: 32 (fp32
+    moments) or 8 (codes with a scale for each 256 elements).  m, v, m_scale,
+    v_scale: lists of existing moments (a checkpoint's) in place of zeros;
+    they are updated in place."""
+
+    def __init__(self, params, copies=None, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.0,
+                 state_bits=32, m=None, v=None, m_scale=None, v_scale=None):
+        if state_bits not in (8, 32):
+            raise ValueError("state_bits must be 8 or 32")
+        self.params, k = list(params), len(params)
+        self.copies = [None] * k if copies is None else list(copies)
+        decay = list(weight_decay) if isinstance(weight_decay, (list, tuple)) else [weight_decay] * k
+        f32 = torch.float32
+        md, vd = (f32, f32) if state_bits == 32 else (torch.int8, torch.uint8)
+
+        def made(given, dtype, count=None):
+            if given is not None:
+                return list(given)
+            return [torch.zeros(p.shape if count is None else count(p.numel()), dtype=dtype,
+                                device=p.device) for p in self.params]
+
+        blocks = (lambda n: -(-n // 256))
+        self.m, self.v = made(m, md), made(v, vd)
+        eight = state_bits == 8
+        self.m_scale = made(m_scale, f32, blocks) if eight else [None] * k
+        self.v_scale = made(v_scale, f32, blocks) if eight else [None] * k
+        lists = (self.copies, decay, self.m, self.v, self.m_scale, self.v_scale)
+        if any(len(x) != k for x in lists):
+            raise ValueError("every list must have one entry for each parameter")
+        self.device = self.params[0].device if k else None
+        self._array = (AdamWTensor * max(k, 1))()
+        spans = []
+        for i, p in enumerate(self.params):
+            e, n = self._array[i], p.numel()
+            parts = [("p", p, f32, n), ("m", self.m[i], md, n), ("v", self.v[i], vd, n)]
+            if self.copies[i] is not None:
+                parts.append(("copy", self.copies[i], torch.bfloat16, n))
+            if eight:
+                parts += [("m_scale", self.m_scale[i], f32, blocks(n)),
+                          ("v_scale", self.v_scale[i], f32, blocks(n))]
+            for name, t, dtype, size in parts:
+                ptr = _dev_ptr(t, name, dtype)
+                if t.numel() != size or t.device != self.device:
+                    raise ValueError("%s of tensor %d must hold %d values on %s"
+                                     % (name, i, size, self.device))
+                setattr(e, name, ptr)
+                if size:
+                    spans.append((ptr, ptr + size * t.element_size()))
+            e.n, e.weight_decay = n, float(decay[i])
+        spans.sort()
+        if any(a[1] > b[0] for a, b in zip(spans, spans[1:])):
+            raise ValueError("the tensors' parameters, copies and moments must not overlap")
+        self.hyper = AdamWHyper(0.0, float(betas[0]), float(betas[1]), float(eps), 0, state_bits,
+                                None)
+        self.state_bits, self.steps = state_bits, 0
+
+    def step(self, grads, lr, step=None, grad_scale=None, stream=None):
+        """One update with `grads`, a list of fp32 or bf16 tensors like the
+        parameters.  step: its number from 1 (None: one more than the last
+        one's).  grad_scale: a device fp32 scalar on the gradients, or None."""
+        if len(grads) != len(self.params):
+            raise ValueError("one gradient is needed for each parameter")
+        if not grads:
+            return
+        array, h = self._array, self.hyper
+        for i, g in enumerate(grads):
+            p, dtype = self.params[i], g.dtype
+            if g.shape != p.shape or g.device != self.device:
+                raise ValueError("gradient %d must be like its parameter" % i)
+            array[i].g, array[i].g_dtype = _dev_ptr(g, "gradient", dtype), dtype_code(dtype)
+        h.lr, h.step = float(lr), self.steps + 1 if step is None else int(step)
+        h.grad_scale = _param(grad_scale, "grad_scale", 1, self.device)
+        with _scope(self.device, stream):
+            sp = torch.cuda.current_stream(self.device).cuda_stream
+            _check(lib().flash_gau_adamw_step(array, len(grads), ctypes.byref(h), sp))
+        self.steps = h.step
+
+    def moments(self, out_m=None, out_v=None, stream=None):
+        """The moments' values (m, v), two lists of fp32 tensors like the
+        parameters: the tensors themselves with 32-bit moments (unless out
+        lists are given), decoded through flash_gau_adamw_moments with 8-bit
+        ones."""
+        if self.state_bits == 32:
+            for src, out in ((self.m, out_m), (self.v, out_v)):
+                for a, b in zip(src, out or []):
+                    b.copy_(a)
+            return out_m or self.m, out_v or self.v
+        if not self.params:
+            return [], []
+        k = len(self.params)
+        with _scope(self.device, stream):
+            out_m = out_m or [torch.empty_like(p) for p in self.params]
+            out_v = out_v or [torch.empty_like(p) for p in self.params]
+            ptrs = []
+            for name, out in (("out_m", out_m), ("out_v", out_v)):
+                if len(out) != k or any(o.numel() != p.numel() or o.device != self.device
+                                        for o, p in zip(out, self.params)):
+                    raise ValueError("%s must hold a tensor like each parameter" % name)
+                ptrs.append((ctypes.c_void_p * k)(*(_dev_ptr(o, name, torch.float32)
+                                                    for o in out)))
+            sp = torch.cuda.current_stream(self.device).cuda_stream
+            _check(lib().flash_gau_adamw_moments(self._array, k, ptrs[0], ptrs[1], sp))
+        return out_m, out_v

@@ -289,6 +289,8 @@ int check_block(const flash_gau_block *blk, int s) {
 
 }  // namespace
 
+int flashgau::current_sms(int *num_sms) { return device_info(num_sms); }
+
 int flashgau::check_forward(const void *X, const flash_gau_weights *w, int B, int T, int C,
                             int causal, int dtype, const void *out, const void *workspace,
                             size_t workspace_bytes, flash_gau_workspace_layout *L,
@@ -608,6 +610,6 @@ const char *flash_gau_strerror(int status) {
   }
 }
 
-int flash_gau_version(void) { return 107; }
+int flash_gau_version(void) { return 108; }
 
 }  // extern "C"

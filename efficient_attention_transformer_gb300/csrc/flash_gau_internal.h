@@ -283,6 +283,36 @@ struct BackwardProblem {
 cudaError_t backward_f32(const BackwardProblem &q);
 cudaError_t backward_bf16(const BackwardProblem &q);
 
+// SM count of the current device (FLASH_GAU_EDEVICE unless it is an sm_103).
+int current_sms(int *num_sms);
+
+// AdamW step (adamw.cu); the tensors are checked by the caller.
+struct AdamwProblem {
+  const flash_gau_adamw_tensor *tensors;
+  int n_tensors, state_bits;
+  double lr, beta1, beta2, eps;
+  long long step;
+  const float *grad_scale;
+  cudaStream_t stream;
+};
+cudaError_t adamw_step(const AdamwProblem &q);
+cudaError_t adamw_moments(const AdamwProblem &q, float *const *m_out, float *const *v_out);
+
+// Residual stream and norms (residual_norm.cu).
+struct ResidualProblem {
+  flash_gau_residual o;
+  const void *y;
+  long long M;
+  int d, dtype, num_sms;
+  cudaStream_t stream;
+};
+constexpr int kResidualMaxD = 4096;
+constexpr int kResidualMaxBlocks = 608;  // of the gradient kernel, four a SM
+int residual_norm_blocks(long long M, int d);  // parts of the column sums
+cudaError_t residual_norm(const ResidualProblem &q, const void *h, void *r, void *n);
+cudaError_t residual_norm_grad(const ResidualProblem &q, const void *dr, const void *dn,
+                               const void *r, const flash_gau_residual_grads &g, void *workspace);
+
 using StageFn = cudaError_t (*)(const Problem &);
 
 // Launches `kernel` on the problem's stream with programmatic stream

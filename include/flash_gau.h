@@ -361,6 +361,117 @@ int flash_gau_decode_step(const void *x, const flash_gau_weights *w, int B, int 
 int flash_gau_rope_toeplitz_bias(const float *a, const float *b, int m, int C,
                                  float rope_base, float *relpos, void *stream);
 
+/* ---- residual stream and block norms ------------------------------------ */
+/* What stands between two blocks of a stack, in one pass over the rows:
+ *   r = h + scale * gate * post(y)      the residual stream after a block
+ *   n = norm(r)                         the next block's normalised input
+ * h is the stream before the block and y the block's output; post and norm
+ * are FLASH_GAU_NORM_* of the flash_block wrapper, with the same formulas.
+ * n is taken from r before its rounding to the io type.  Row statistics are
+ * fp32.  All rows have d columns; any 1 <= d <= 4096 (larger:
+ * FLASH_GAU_ENOTSUP), rows and arrays need only their element's alignment
+ * (16-byte aligned arrays and d a multiple of 16 bytes run fastest).       */
+typedef struct flash_gau_residual {
+  int post;             /* norm of the block's output, FLASH_GAU_NORM_*      */
+  int norm;             /* norm of the stream, FLASH_GAU_NORM_*              */
+  const float *post_g;  /* device fp32: LayerNorm scale [d], ScaleNorm g [1] */
+  const float *post_b;  /* device fp32: LayerNorm shift [d], or NULL (zero)  */
+  const float *norm_g;  /* as post_g                                         */
+  const float *norm_b;  /* as post_b                                         */
+  const float *scale;   /* device fp32 [d]: residual scale, or NULL (ones)   */
+  const void *gate;     /* device [M, d], io type, or NULL (ones)            */
+  float eps;            /* of both norms; > 0                                */
+} flash_gau_residual;
+
+/* h, y: device [M, d], io type; y may be NULL (then r = h; post, gate and
+ * scale must be unset).  r, n: device [M, d], io type; r may be NULL (the
+ * stream is not wanted); n is NULL exactly when o->norm is NONE.  An output
+ * may be the same array as an input of its type, otherwise arrays must not
+ * overlap.  One kernel, no workspace.  Returns FLASH_GAU_OK,
+ * FLASH_GAU_EINVAL, FLASH_GAU_ENOTSUP, FLASH_GAU_EDEVICE or
+ * FLASH_GAU_ECUDA.                                                         */
+int flash_gau_residual_norm(const void *h, const void *y, const flash_gau_residual *o,
+                            long long M, int d, int dtype, void *r, void *n, void *stream);
+
+/* Gradients of sum(dr * r) + sum(dn * n) by the formulas' derivatives at the
+ * stored r.  Written, not added.  dh and dy in the io type; parameters' in
+ * fp32, summed over the rows in a fixed order (a call repeats bit for bit). */
+typedef struct flash_gau_residual_grads {
+  void *dh;             /* device [M, d]                                     */
+  void *dy;             /* device [M, d], or NULL: the forward had no y      */
+  void *dgate;          /* device [M, d], or NULL: not wanted                */
+  float *dscale;        /* device [d], or NULL: not wanted (so the others)   */
+  float *dpost_g;       /* device [d], ScaleNorm [1]                         */
+  float *dpost_b;       /* device [d], LayerNorm only                        */
+  float *dnorm_g;       /* device [d], ScaleNorm [1]                         */
+  float *dnorm_b;       /* device [d], LayerNorm only                        */
+} flash_gau_residual_grads;
+
+/* Workspace bytes of the backward, or 0 when M or d is invalid.            */
+size_t flash_gau_residual_norm_backward_workspace_bytes(long long M, int d);
+
+/* dr: device [M, d], the gradient that reaches r from elsewhere, or NULL
+ * (zero); dn: device [M, d], n's gradient (NULL exactly when o->norm is
+ * NONE); r: the forward's r (needed with a norm); y: the forward's y (needed
+ * with post, gate or scale).  g (a host pointer): a gradient of something
+ * that the options leave out must be NULL.  dh, dy and dgate may each be
+ * the same array as an input, otherwise arrays must not overlap.
+ * workspace: device, 256-byte aligned.                                     */
+int flash_gau_residual_norm_backward(const void *dr, const void *dn, const void *r,
+                                     const void *y, const flash_gau_residual *o,
+                                     long long M, int d, int dtype,
+                                     const flash_gau_residual_grads *g, void *workspace,
+                                     size_t workspace_bytes, void *stream);
+
+/* ---- AdamW ---------------------------------------------------------------- */
+/* One step of Adam with decoupled weight decay over a list of tensors, in
+ * place, for the gradients of flash_gau_backward, flash_gau_xent and
+ * flash_gau_residual_norm_backward:
+ *   g' = grad_scale g
+ *   m  = beta1 m + (1 - beta1) g'       v = beta2 v + (1 - beta2) g' g'
+ *   p  = (1 - lr weight_decay) p
+ *        - lr / (1 - beta1^step) m / (sqrt(v / (1 - beta2^step)) + eps)
+ * Parameters are fp32; bf16 weights are kept as `copy`, which receives the
+ * updated p rounded to nearest.  Moments are fp32 or 8-bit codes: each 256
+ * consecutive elements share an fp32 scale, m = m_scale c |c| with a signed
+ * code c, v = (v_scale c c)^2 with an unsigned one; a zeroed state starts
+ * from zero moments either way.                                            */
+typedef struct flash_gau_adamw_tensor {
+  float *p;             /* device [n], updated                               */
+  void *copy;           /* device [n] bf16: the updated p, or NULL           */
+  const void *g;        /* device [n] gradient, of g_dtype                   */
+  void *m;              /* device [n] fp32, or int8 codes                    */
+  void *v;              /* device [n] fp32, or uint8 codes                   */
+  float *m_scale;       /* device [(n + 255) / 256], 8-bit moments only      */
+  float *v_scale;       /* as m_scale                                        */
+  long long n;          /* elements; an empty tensor is skipped              */
+  int g_dtype;          /* FLASH_GAU_FP32 or FLASH_GAU_BF16                  */
+  float weight_decay;   /* >= 0, of this tensor                              */
+} flash_gau_adamw_tensor;
+
+typedef struct flash_gau_adamw_hyper {
+  double lr;            /* >= 0                                              */
+  double beta1, beta2;  /* in [0, 1)                                         */
+  double eps;           /* > 0                                               */
+  long long step;       /* number of this step, from 1                       */
+  int state_bits;       /* 32 or 8: how every tensor's moments are held      */
+  const float *grad_scale;  /* device fp32 scalar, or NULL (one)             */
+} flash_gau_adamw_hyper;
+
+/* tensors and h are host pointers, read during the call (a call captured in
+ * a CUDA graph replays with the values it was captured with; grad_scale is
+ * read at each replay).  No tensor's arrays may overlap another's, or one
+ * another.  One launch per 384 tensors, no workspace.  Returns
+ * FLASH_GAU_OK, FLASH_GAU_EINVAL, FLASH_GAU_EDEVICE or FLASH_GAU_ECUDA.     */
+int flash_gau_adamw_step(const flash_gau_adamw_tensor *tensors, int n_tensors,
+                         const flash_gau_adamw_hyper *h, void *stream);
+
+/* The values of 8-bit moments (m, v and the scales of each tensor are read)
+ * as fp32: m_out[k], v_out[k] device [n] of tensor k; the two lists are host
+ * arrays, read during the call.                                            */
+int flash_gau_adamw_moments(const flash_gau_adamw_tensor *tensors, int n_tensors,
+                            float *const *m_out, float *const *v_out, void *stream);
+
 /* ---- allocation-free variant ------------------------------------------- */
 /* No counterpart on the pages: this entry point exists for deployment, not
  * for the method.

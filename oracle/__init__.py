@@ -22,3 +22,7 @@ from .flash_gau import (  # noqa: F401
 )
 from .backward import swish_grad, flash_gau_backward  # noqa: F401,E402
 from .decode import DecodeState  # noqa: F401,E402
+from .training import (  # noqa: F401,E402
+    norm_rows, residual_norm, residual_norm_grad, xent, adamw, adamw_codes, decode_moments,
+    encode_moments,
+)

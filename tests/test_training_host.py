@@ -1,0 +1,266 @@
+"""Host-side checks of the training operators: the oracle against automatic
+differentiation and differences, and the refusals of the C ABI and the
+binding, all of which come before anything touches a device."""
+
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from efficient_attention_transformer_gb300 import binding as bd
+from efficient_attention_transformer_gb300 import build as buildmod
+
+EPS = 1e-5
+KINDS = ["none", "layer", "scale"]
+
+
+@pytest.fixture(scope="module")
+def L():
+    buildmod.build()
+    return bd.lib()
+
+
+# ---- the oracle --------------------------------------------------------------
+def _case(post, norm, gate, scale, seed, M=5, d=7):
+    rng = np.random.default_rng(seed)
+    par = lambda kind: ((None, None) if kind == "none" else  # noqa: E731
+                        (rng.normal(1, 0.2, d), rng.normal(0, 0.2, d)) if kind == "layer" else
+                        (rng.normal(2, 0.2, 1), None))
+    pg, pb = par(post)
+    ng, nb = par(norm)
+    return dict(post=post, post_g=pg, post_b=pb, norm=norm, norm_g=ng, norm_b=nb,
+                gate=rng.normal(size=(M, d)) if gate else None,
+                scale=rng.normal(size=d) if scale else None, eps=EPS), rng
+
+
+@pytest.mark.parametrize("post", KINDS)
+@pytest.mark.parametrize("norm", KINDS)
+@pytest.mark.parametrize("gate,scale", [(True, True), (False, False)])
+def test_oracle_residual_norm_against_autograd_and_differences(post, norm, gate, scale):
+    o, rng = _case(post, norm, gate, scale, 3)
+    M, d = 5, 7
+    h, y, dr, dn = (rng.normal(size=(M, d)) for _ in range(4))
+    r, n = oracle.residual_norm(h, y, **o)
+    T = lambda a: None if a is None else torch.tensor(a, requires_grad=True)  # noqa: E731
+    th, ty = T(h), T(y)
+    tp = {k: T(o[k]) for k in ("post_g", "post_b", "norm_g", "norm_b", "gate", "scale")}
+
+    def tnorm(x, kind, g, b):
+        if kind == "none":
+            return x
+        if kind == "layer":
+            return torch.nn.functional.layer_norm(x, (d,), g, b, EPS)
+        return torch.nn.functional.normalize(x, dim=1, eps=EPS) * g
+
+    add = tnorm(ty, post, tp["post_g"], tp["post_b"])
+    add = add if tp["gate"] is None else add * tp["gate"]
+    add = add if tp["scale"] is None else add * tp["scale"]
+    tr = th + add
+    tn = tnorm(tr, norm, tp["norm_g"], tp["norm_b"])
+    np.testing.assert_allclose(r, tr.detach().numpy(), rtol=1e-12, atol=1e-12)
+    np.testing.assert_allclose(n, tn.detach().numpy(), rtol=1e-12, atol=1e-12)
+    ((tr * torch.tensor(dr)).sum() + (tn * torch.tensor(dn)).sum()).backward()
+    g = oracle.residual_norm_grad(dr, dn if norm != "none" else None, r, y, **o)
+    if norm == "none":  # n is r: its gradient comes in dr
+        g = oracle.residual_norm_grad(dr + dn, None, r, y, **o)
+    want = {"dh": th, "dy": ty, "dgate": tp["gate"], "dscale": tp["scale"],
+            "dpost_g": tp["post_g"], "dpost_b": tp["post_b"], "dnorm_g": tp["norm_g"],
+            "dnorm_b": tp["norm_b"]}
+    for k, t in want.items():
+        if t is None:
+            assert g[k] is None
+        else:
+            np.testing.assert_allclose(g[k], t.grad.numpy(), rtol=1e-9, atol=1e-10, err_msg=k)
+
+    def f(h_):
+        r_, n_ = oracle.residual_norm(h_, y, **o)
+        return (dr * r_).sum() + (dn * n_).sum()
+
+    step = rng.normal(size=h.shape)
+    diff = (f(h + 1e-6 * step) - f(h - 1e-6 * step)) / 2e-6
+    assert abs(diff - (g["dh"] * step).sum()) <= 1e-6 * (1 + abs(diff))
+
+
+def test_oracle_scale_norm_of_short_rows():
+    """Below eps the ScaleNorm divides by eps: linear, no projection."""
+    x = np.array([[1e-6, -2e-6], [0.0, 0.0]])
+    g = oracle.residual_norm_grad(None, np.ones((2, 2)), x, None, "none", None, None, None, None,
+                                  "scale", np.array([3.0]), None, EPS)
+    np.testing.assert_allclose(g["dh"], np.full((2, 2), 3.0 / EPS), rtol=1e-12)
+
+
+def test_oracle_adamw_against_torch():
+    rng = np.random.default_rng(5)
+    p = torch.tensor(rng.normal(size=50), requires_grad=True)
+    opt = torch.optim.AdamW([p], lr=1e-2, betas=(0.8, 0.95), eps=1e-6, weight_decay=0.1)
+    q, m, v = p.detach().numpy().copy(), np.zeros(50), np.zeros(50)
+    for t in range(1, 5):
+        g = rng.normal(size=50)
+        p.grad = torch.tensor(g)
+        opt.step()
+        q, m, v = oracle.adamw(q, g, m, v, 1e-2, 0.8, 0.95, 1e-6, 0.1, t)
+        np.testing.assert_allclose(q, p.detach().numpy(), rtol=1e-12)
+
+
+def test_oracle_codes():
+    """Codes meet a block's largest value, keep zeros and nonzero seconds, and
+    are off by at most half a step: with |x| = s c^2, half a step of c is
+    s (c + 1/4) of x, and fp32 rounding adds less than 1e-4 of a step."""
+    rng = np.random.default_rng(6)
+    x = (rng.normal(size=600) * np.exp(rng.normal(size=600) * 3)).astype(np.float32)
+    x[7] = 0.0
+    for top, a in ((127, x), (255, np.abs(x))):
+        c, s = oracle.encode_moments(a, top)
+        full = np.repeat(s, 256)[:600].astype(np.float64)
+        got = full * c.astype(np.float64) * np.abs(c.astype(np.float64))
+        # the fourth of a step: (c + 1/2)^2 - c^2 = c + 1/4; a value that is
+        # raised to code 1 is off by less than one
+        bound = full * (np.abs(c.astype(np.float64)) + 0.2501 + 1e-4)
+        raised = (c == 1) & (top == 255)
+        assert np.all(np.abs(got - a) <= np.where(raised, full * 1.2502, bound))
+        assert c[7] == 0 and np.all(c[a != 0] != 0) if top == 255 else c[7] == 0
+        for k in range(3):
+            b = slice(256 * k, min(256 * k + 256, 600))
+            assert np.abs(c[b].astype(int)).max() == top
+    c, s = oracle.encode_moments(np.full(256, 2.0 ** -61, np.float32), 255)
+    assert not c.any() and s[0] == 0
+
+
+# ---- refusals of the C ABI -----------------------------------------------------
+A, B, C, D, E_, F_ = (1 << 32, 2 << 32, 3 << 32, 4 << 32, 5 << 32, 6 << 32)  # fake arrays
+
+
+def _residual(**kw):
+    o = dict(post=bd.NORM_NONE, norm=bd.NORM_LAYER, post_g=None, post_b=None, norm_g=64,
+             norm_b=None, scale=None, gate=None, eps=EPS)
+    o.update(kw)
+    return bd.Residual(*(o[k] for k, _ in bd.Residual._fields_))
+
+
+@pytest.mark.parametrize("opts,args,code", [
+    (dict(), dict(h=None), bd.EINVAL),
+    (dict(), dict(M=0), bd.EINVAL),
+    (dict(), dict(d=0), bd.EINVAL),
+    (dict(), dict(d=4097), bd.ENOTSUP),
+    (dict(), dict(dtype=2), bd.EINVAL),
+    (dict(norm=3), dict(), bd.EINVAL),
+    (dict(post=-1), dict(), bd.EINVAL),
+    (dict(norm_g=None), dict(), bd.EINVAL),
+    (dict(eps=0.0), dict(), bd.EINVAL),
+    (dict(eps=float("nan")), dict(), bd.EINVAL),
+    (dict(), dict(n=None), bd.EINVAL),                   # a norm and no place for it
+    (dict(norm=bd.NORM_NONE), dict(), bd.EINVAL),        # a place and no norm
+    (dict(norm=bd.NORM_NONE), dict(n=None, r=None), bd.EINVAL),
+    (dict(scale=64), dict(y=None), bd.EINVAL),           # a scale of nothing
+    (dict(post=bd.NORM_SCALE, post_g=64), dict(y=None), bd.EINVAL),
+    (dict(), dict(r=A + 4), bd.EINVAL),                  # overlaps h
+    (dict(), dict(n=C), bd.EINVAL),                      # n is r
+    (dict(), dict(h=A + 1), bd.EINVAL),                  # odd address
+    (dict(scale=C + 8), dict(), bd.EINVAL),              # the scale inside r
+])
+def test_residual_norm_refuses(L, opts, args, code):
+    a = dict(h=A, y=B, M=10, d=64, dtype=bd.BF16, r=C, n=D)
+    a.update(args)
+    o = _residual(**opts)
+    assert L.flash_gau_residual_norm(a["h"], a["y"], ctypes.byref(o), a["M"], a["d"], a["dtype"],
+                                     a["r"], a["n"], None) == code
+    assert L.flash_gau_residual_norm(a["h"], a["y"], None, a["M"], a["d"], a["dtype"], a["r"],
+                                     a["n"], None) == bd.EINVAL
+
+
+@pytest.mark.parametrize("opts,args,code", [
+    (dict(), dict(dh=None), bd.EINVAL),
+    (dict(), dict(dn=None), bd.EINVAL),
+    (dict(), dict(r=None), bd.EINVAL),
+    (dict(norm=bd.NORM_NONE), dict(dn=None, dr=None), bd.EINVAL),
+    (dict(norm=bd.NORM_NONE), dict(), bd.EINVAL),               # dn without a norm
+    (dict(scale=64), dict(y=None), bd.EINVAL),
+    (dict(scale=64), dict(dy=None), bd.EINVAL),
+    (dict(), dict(dgate=F_), bd.EINVAL),                        # no gate
+    (dict(), dict(dscale=F_), bd.EINVAL),
+    (dict(), dict(dpost_g=F_), bd.EINVAL),
+    (dict(norm=bd.NORM_SCALE), dict(dnorm_b=F_), bd.EINVAL),
+    (dict(), dict(dh=A + 2), bd.EINVAL),                        # overlaps dr
+    (dict(), dict(dy=E_), bd.EINVAL),                           # dy is dh
+    (dict(), dict(dnorm_g=64), bd.EINVAL),                      # the parameter itself
+    (dict(), dict(dnorm_g=C), bd.EINVAL),                       # inside r
+    (dict(), dict(ws=1 << 40 | 8), bd.EWORKSPACE),
+    (dict(), dict(wsb=100), bd.EWORKSPACE),
+    (dict(), dict(ws=E_), bd.EINVAL),                           # the workspace is dh
+    (dict(), dict(d=5000), bd.ENOTSUP),
+])
+def test_residual_norm_backward_refuses(L, opts, args, code):
+    a = dict(dr=A, dn=B, r=C, y=D, M=10, d=64, dtype=bd.BF16, dh=E_, dy=7 << 32, ws=1 << 40,
+             wsb=1 << 30, dgate=None, dscale=None, dpost_g=None, dpost_b=None, dnorm_g=None,
+             dnorm_b=None)
+    a.update(args)
+    o = _residual(**opts)
+    g = bd.ResidualGrads(*(a[k] for k, _ in bd.ResidualGrads._fields_))
+    assert L.flash_gau_residual_norm_backward(
+        a["dr"], a["dn"], a["r"], a["y"], ctypes.byref(o), a["M"], a["d"], a["dtype"],
+        ctypes.byref(g), a["ws"], a["wsb"], None) == code
+
+
+def test_residual_norm_backward_workspace(L):
+    f = L.flash_gau_residual_norm_backward_workspace_bytes
+    assert f(0, 64) == 0 and f(4, 0) == 0 and f(4, 4097) == 0
+    assert f(1, 1) >= 20 and f(1 << 30, 4096) <= 608 * 5 * 4096 * 4
+
+
+def _tensor(**kw):
+    t = dict(p=A, copy=None, g=B, m=C, v=D, m_scale=None, v_scale=None, n=1000, g_dtype=bd.FP32,
+             weight_decay=0.0)
+    t.update(kw)
+    return bd.AdamWTensor(*(t[k] for k, _ in bd.AdamWTensor._fields_))
+
+
+def _hyper(**kw):
+    h = dict(lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8, step=1, state_bits=32, grad_scale=None)
+    h.update(kw)
+    return bd.AdamWHyper(*(h[k] for k, _ in bd.AdamWHyper._fields_))
+
+
+@pytest.mark.parametrize("tensor,hyper", [
+    (dict(p=None), {}), (dict(g=None), {}), (dict(m=None), {}), (dict(n=-1), {}),
+    (dict(g_dtype=5), {}), (dict(weight_decay=-0.1), {}), (dict(weight_decay=float("nan")), {}),
+    (dict(p=A + 2), {}), (dict(g=B + 1), {}), (dict(v=C + 100), {}), (dict(copy=A + 16), {}),
+    (dict(g=A), {}),                                            # the gradient is the parameter
+    ({}, dict(lr=-1.0)), ({}, dict(lr=float("inf"))), ({}, dict(beta1=1.0)),
+    ({}, dict(beta2=-0.5)), ({}, dict(beta1=float("nan"))), ({}, dict(eps=0.0)),
+    ({}, dict(step=0)), ({}, dict(state_bits=16)), ({}, dict(grad_scale=3)),
+    ({}, dict(state_bits=8)),                                   # no scales
+    (dict(m_scale=E_, v_scale=E_ + 8), dict(state_bits=8)),     # scales overlap
+])
+def test_adamw_refuses(L, tensor, hyper):
+    t, h = _tensor(**tensor), _hyper(**hyper)
+    assert L.flash_gau_adamw_step(ctypes.byref(t), 1, ctypes.byref(h), None) == bd.EINVAL
+    assert L.flash_gau_adamw_step(ctypes.byref(t), 1, None, None) == bd.EINVAL
+    assert L.flash_gau_adamw_step(None, 1, ctypes.byref(_hyper()), None) == bd.EINVAL
+    assert L.flash_gau_adamw_step(None, -1, ctypes.byref(_hyper()), None) == bd.EINVAL
+
+
+def test_adamw_moments_refuses(L):
+    P = ctypes.c_void_p
+    t = _tensor(m_scale=E_, v_scale=F_)
+    for m, v in ((None, 8), (8, None), (9, 8)):
+        assert L.flash_gau_adamw_moments(ctypes.byref(t), 1, (P * 1)(m), (P * 1)(v),
+                                         None) == bd.EINVAL
+    assert L.flash_gau_adamw_moments(ctypes.byref(_tensor()), 1, (P * 1)(8), (P * 1)(8),
+                                     None) == bd.EINVAL
+    assert L.flash_gau_adamw_moments(ctypes.byref(t), 1, None, (P * 1)(8), None) == bd.EINVAL
+
+
+def test_binding_refuses_host_tensors(L):
+    x = torch.zeros(4, 8)
+    with pytest.raises(ValueError):
+        bd.residual_norm(x, x, norm=bd.NORM_NONE)
+    with pytest.raises(ValueError):
+        bd.residual_norm_backward(x, None, x, x, norm=bd.NORM_NONE)
+    with pytest.raises(ValueError):
+        bd.AdamW([x])
+    with pytest.raises(TypeError):
+        bd.residual_norm(x.half(), None)
+    with pytest.raises(ValueError):
+        bd.AdamW([x], state_bits=4)
