@@ -9,8 +9,8 @@ input generator used by the tests and the benchmark.
 from .binding import (  # noqa: F401
     FP32, BF16, GauWeights, FlashGauError, forward, workspace_layout,
     workspace_status, num_stages, stage_names, lib, strerror, EXPORTED,
-    residual_norm, residual_norm_backward, AdamW,
-    NORM_NONE, NORM_LAYER, NORM_SCALE,
+    xent, xent_workspace_bytes, residual_norm, residual_norm_backward, AdamW,
+    NORM_NONE, NORM_LAYER, NORM_SCALE, MEAN, SUM,
 )
 
 __version__ = "0.1.0"

@@ -25,6 +25,9 @@ ECUDA = -4
 EDEVICE = -5
 ETIMEOUT = -6
 
+MEAN = 0
+SUM = 1
+
 NORM_NONE = 0
 NORM_LAYER = 1
 NORM_SCALE = 2
@@ -51,6 +54,8 @@ EXPORTED = (
     "flash_gau_forward_host_workspace_bytes",
     "flash_gau_forward_host",
     "flash_gau_selftest_bounded_wait",
+    "flash_gau_xent_workspace_bytes",
+    "flash_gau_xent",
     "flash_gau_residual_norm",
     "flash_gau_residual_norm_backward_workspace_bytes",
     "flash_gau_residual_norm_backward",
@@ -119,6 +124,10 @@ class Residual(ctypes.Structure):
 class ResidualGrads(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in
                 ("dh", "dy", "dgate", "dscale", "dpost_g", "dpost_b", "dnorm_g", "dnorm_b")]
+
+
+class XentOut(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("total", "loss", "lse", "dX", "dW")]
 
 
 class AdamWTensor(ctypes.Structure):
@@ -216,6 +225,11 @@ def lib():
         L.flash_gau_decode_step.argtypes = [p, ctypes.POINTER(Weights), i, i, i, p, sz, p, p]
         L.flash_gau_decode_step.restype = i
         ll = ctypes.c_longlong
+        L.flash_gau_xent_workspace_bytes.argtypes = [ll, i, i, i, i]
+        L.flash_gau_xent_workspace_bytes.restype = sz
+        L.flash_gau_xent.argtypes = [p, p, p, ll, i, i, i, i, ctypes.c_float,
+                                     ctypes.POINTER(XentOut), p, sz, p]
+        L.flash_gau_xent.restype = i
         L.flash_gau_residual_norm.argtypes = [p, p, ctypes.POINTER(Residual), ll, i, i, p, p, p]
         L.flash_gau_residual_norm.restype = i
         L.flash_gau_residual_norm_backward_workspace_bytes.argtypes = [ll, i]
@@ -660,6 +674,55 @@ def residual_norm_backward(dr, dn, r, y, post_norm=NORM_NONE, post_g=None, post_
         _check(lib().flash_gau_residual_norm_backward(
             _rows(dr, "dr", like), _rows(dn, "dn", like), _rows(r, "r", like),
             _rows(y, "y", like), ctypes.byref(o), M, d, dt, ctypes.byref(g),
+            _dev_ptr(workspace, "workspace"), workspace.numel() * workspace.element_size(), sp))
+    return out
+
+
+def xent_workspace_bytes(N, d, V, dtype, grad=True):
+    """Workspace bytes of xent for N tokens and V words (dtype FP32 or BF16)."""
+    n = lib().flash_gau_xent_workspace_bytes(N, d, V, dtype, int(bool(grad)))
+    if n == 0:
+        raise FlashGauError(EINVAL, "invalid or unsupported problem")
+    return n
+
+
+def xent(X, W, labels, reduction=MEAN, scale=1.0, grad=True, out=None, workspace=None,
+         stream=None):
+    """Cross entropy of softmax(X W^T) at the labels, through flash_gau_xent:
+    a dict with total ([1]), loss and lse (like labels, fp32), and with grad
+    dX and dW, the gradients of total in the io type.  X: [..., d], W: [V, d],
+    labels: int32, X's leading shape; a label outside [0, V) leaves its token
+    out.  total is scale times the MEAN over the labelled tokens or the SUM.
+    `out`: tensors to write to, by the same names."""
+    dt = dtype_code(X.dtype)
+    xp, wp = _dev_ptr(X, "X"), _dev_ptr(W, "W", X.dtype)
+    lp = _dev_ptr(labels, "labels", torch.int32)
+    if W.dim() != 2 or X.shape[-1:] != W.shape[1:] or labels.shape != X.shape[:-1]:
+        raise ValueError("X must be [..., d], W [V, d] and labels X's leading shape")
+    V, d = W.shape
+    N, dev = labels.numel(), X.device
+    if W.device != dev or labels.device != dev:
+        raise ValueError("X, W and labels must be on one device")
+    f32 = torch.float32
+    out = dict(out or {})
+    with _scope(dev, stream):
+        for name, shape, dtype in (("total", (1,), f32), ("loss", labels.shape, f32),
+                                   ("lse", labels.shape, f32), ("dX", X.shape, X.dtype),
+                                   ("dW", W.shape, X.dtype)):
+            if name[0] == "d" and not grad:
+                out[name] = None
+            elif out.get(name) is None:
+                out[name] = torch.empty(shape, dtype=dtype, device=dev)
+            elif out[name].shape != shape or out[name].device != dev:
+                raise ValueError("%s must be %s on %s" % (name, tuple(shape), dev))
+        o = XentOut(*(_dev_ptr(out[k], k, f32) for k in ("total", "loss", "lse")),
+                    *(_dev_ptr(out[k], k, X.dtype) if grad else None for k in ("dX", "dW")))
+        if workspace is None:
+            workspace = torch.empty(xent_workspace_bytes(N, d, V, dt, grad), dtype=torch.uint8,
+                                    device=dev)
+        sp = torch.cuda.current_stream(dev).cuda_stream
+        _check(lib().flash_gau_xent(
+            xp, wp, lp, N, d, V, dt, int(reduction), float(scale), ctypes.byref(o),
             _dev_ptr(workspace, "workspace"), workspace.numel() * workspace.element_size(), sp))
     return out
 

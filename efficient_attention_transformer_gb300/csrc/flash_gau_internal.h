@@ -313,6 +313,41 @@ cudaError_t residual_norm(const ResidualProblem &q, const void *h, void *r, void
 cudaError_t residual_norm_grad(const ResidualProblem &q, const void *dr, const void *dn,
                                const void *r, const flash_gau_residual_grads &g, void *workspace);
 
+// Cross entropy over a vocabulary (xent.cu bf16, xent_f32.cu fp32).
+struct XentLayout {
+  int *status;       // FLASH_GAU_ETIMEOUT on a timed-out wait
+  float *factor;     // the gradients' factor: scale, or scale / number of labels
+  long long piece;   // tokens of a piece
+  long long ldE;     // columns between rows of E
+  float *ref;        // [piece] bf16: the label's logit, in units of ln 2
+  float *row_scale;  // [piece] bf16: factor / normaliser
+  float2 *part;      // [V / 128][piece] bf16: (reference, sum) of 128 words
+  void *E;           // [piece, ldE] bf16: exp(l - reference); fp32: the logits, then P
+  void *Xs;          // [piece, d] bf16: scaled rows of X
+  float *dx_part;    // [splits][piece][d] parts of dX
+  float *dw_sum;     // [V, d] bf16, several pieces: the sum of their dW
+};
+struct XentProblem {
+  const void *X, *W;
+  const int *labels;
+  long long N;
+  int d, V, mean;
+  float scale;
+  float *loss, *lse, *total;
+  void *dX, *dW;
+  XentLayout L;
+  int num_sms;
+  cudaStream_t stream;
+};
+// splits of dX's sum over the words, planned for a whole GB300 (the workspace
+// is sized without a device)
+constexpr int kXentPlanSms = 152;
+int xent_dx_splits(int rows, int d, int V);
+int xent_f32_dx_splits(int rows, int d, int V);
+cudaError_t xent_bf16(const XentProblem &q);
+cudaError_t xent_f32(const XentProblem &q);
+cudaError_t xent_total(const XentProblem &q);
+
 using StageFn = cudaError_t (*)(const Problem &);
 
 // Launches `kernel` on the problem's stream with programmatic stream

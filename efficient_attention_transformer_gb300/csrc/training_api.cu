@@ -1,6 +1,6 @@
 // C ABI of the operators around the layer in a training step: argument
 // checks, then the launches on the caller's stream (kernels in
-// residual_norm.cu and adamw.cu).
+// residual_norm.cu, adamw.cu, xent.cu and xent_f32.cu).
 #include <math.h>
 
 #include "flash_gau_internal.h"
@@ -69,6 +69,67 @@ ResidualProblem residual_problem(const flash_gau_residual *o, const void *y, lon
   q.num_sms = 0;
   q.stream = static_cast<cudaStream_t>(stream);
   return q;
+}
+
+// ---- cross entropy ---------------------------------------------------------
+constexpr size_t kPieceBytes = (size_t)2 << 30;  // of a piece's [tokens, V]
+
+int check_xent(long long N, int d, int V, int dtype) {
+  if (N <= 0 || d <= 0 || V <= 0 || !io_type(dtype)) return FLASH_GAU_EINVAL;
+  if (N > (1LL << 30) || V > (1 << 22) || d > 65536) return FLASH_GAU_ENOTSUP;
+  if (dtype == FLASH_GAU_BF16 && d % 8 != 0) return FLASH_GAU_ENOTSUP;
+  return FLASH_GAU_OK;
+}
+
+size_t xent_layout(long long N, int d, int V, int dtype, bool grad, char *base, XentLayout *L) {
+  const bool bf16 = dtype == FLASH_GAU_BF16;
+  const size_t io = bf16 ? 2 : 4;
+  XentLayout l = {};
+  l.ldE = ((long long)V + 63) / 64 * 64;
+  // whole tiles of tokens, pieces of about the same size
+  long long most = (long long)(kPieceBytes / (l.ldE * io)) / 256 * 256;
+  if (most < 256) most = 256;
+  if (!bf16 && most > 65535LL * 128) most = 65535LL * 128;  // grid rows of the products
+  if (bf16 && !grad) {
+    // only the sums of 128 words are held: at most 256 MiB of them
+    most = (long long)(kPieceBytes / 8 / (((size_t)V + 127) / 128 * sizeof(float2))) / 256 * 256;
+    if (most < 256) most = 256;
+  }
+  const long long about = (N + most - 1) / most;
+  const long long even = ((N + about - 1) / about + 255) / 256 * 256;
+  l.piece = N < even ? N : even;
+  const long long pieces = (N + l.piece - 1) / l.piece;
+  size_t off = 0;
+  auto take = [&](size_t bytes) -> char * {
+    char *p = base ? base + off : nullptr;
+    off = (off + bytes + kAlign - 1) / kAlign * kAlign;
+    return p;
+  };
+  const size_t n = (size_t)l.piece;
+  l.status = reinterpret_cast<int *>(take(sizeof(int)));
+  l.factor = reinterpret_cast<float *>(take(sizeof(float)));
+  if (bf16) {
+    l.ref = reinterpret_cast<float *>(take(n * 4));
+    l.part = reinterpret_cast<float2 *>(take(((size_t)V + 127) / 128 * n * sizeof(float2)));
+  }
+  if (bf16 && grad) {
+    l.row_scale = reinterpret_cast<float *>(take(n * 4));
+    l.Xs = take(n * d * 2);
+    if (pieces > 1) l.dw_sum = reinterpret_cast<float *>(take((size_t)V * d * 4));
+  }
+  if (grad) {
+    // the last piece may be shorter and split further
+    size_t parts = 0;
+    for (long long rows : {l.piece, N - (pieces - 1) * l.piece}) {
+      const int s = bf16 ? xent_dx_splits((int)rows, d, V) : xent_f32_dx_splits((int)rows, d, V);
+      const size_t b = s > 1 ? (size_t)s * ((rows + 31) / 32 * 32) * d * 4 : 0;
+      parts = b > parts ? b : parts;
+    }
+    l.dx_part = reinterpret_cast<float *>(take(parts));
+  }
+  if (grad || !bf16) l.E = take(n * l.ldE * io);
+  if (L) *L = l;
+  return off;
 }
 
 // ---- AdamW -----------------------------------------------------------------
@@ -168,6 +229,53 @@ int flash_gau_residual_norm_backward(const void *dr, const void *dn, const void 
   ResidualProblem q = residual_problem(o, y, M, d, dtype, stream);
   if ((st = current_sms(&q.num_sms)) != FLASH_GAU_OK) return st;
   return status_of(residual_norm_grad(q, dr, dn, r, *g, workspace));
+}
+
+size_t flash_gau_xent_workspace_bytes(long long N, int d, int V, int dtype, int grad) {
+  if (check_xent(N, d, V, dtype) != FLASH_GAU_OK) return 0;
+  return xent_layout(N, d, V, dtype, grad != 0, nullptr, nullptr);
+}
+
+int flash_gau_xent(const void *X, const void *W, const int *labels, long long N, int d, int V,
+                   int dtype, int reduction, float scale, const flash_gau_xent_out *out,
+                   void *workspace, size_t workspace_bytes, void *stream) {
+  if (!X || !W || !labels || !out || !out->total || !out->loss || !workspace)
+    return FLASH_GAU_EINVAL;
+  if ((reduction != FLASH_GAU_MEAN && reduction != FLASH_GAU_SUM) || !isfinite(scale))
+    return FLASH_GAU_EINVAL;
+  int st = check_xent(N, d, V, dtype);
+  if (st != FLASH_GAU_OK) return st;
+  const bool bf16 = dtype == FLASH_GAU_BF16, grad = out->dX || out->dW;
+  const size_t align = bf16 ? 16 : 4, io = bf16 ? 2 : 4;
+  for (const void *p : {X, W, (const void *)out->dX, (const void *)out->dW})
+    if (!aligned(p, align)) return FLASH_GAU_EINVAL;
+  for (const void *p : {(const void *)labels, (const void *)out->total, (const void *)out->loss,
+                        (const void *)out->lse})
+    if (!aligned(p, 4)) return FLASH_GAU_EINVAL;
+  XentProblem q;
+  const size_t bytes = xent_layout(N, d, V, dtype, grad, static_cast<char *>(workspace), &q.L);
+  if (!aligned(workspace, kAlign) || workspace_bytes < bytes) return FLASH_GAU_EWORKSPACE;
+  const size_t n = (size_t)N;
+  const Span outs[6] = {{out->total, 4}, {out->loss, n * 4}, {out->lse, n * 4},
+                        {out->dX, n * d * io}, {out->dW, (size_t)V * d * io}, {workspace, bytes}};
+  const Span in[3] = {{X, n * d * io}, {W, (size_t)V * d * io}, {labels, n * 4}};
+  if (!separate(outs, in, false)) return FLASH_GAU_EINVAL;
+  if ((st = current_sms(&q.num_sms)) != FLASH_GAU_OK) return st;
+  q.X = X;
+  q.W = W;
+  q.labels = labels;
+  q.N = N;
+  q.d = d;
+  q.V = V;
+  q.mean = reduction == FLASH_GAU_MEAN;
+  q.scale = scale;
+  q.loss = out->loss;
+  q.lse = out->lse;
+  q.total = out->total;
+  q.dX = out->dX;
+  q.dW = out->dW;
+  q.stream = static_cast<cudaStream_t>(stream);
+  return status_of(bf16 ? xent_bf16(q) : xent_f32(q));
 }
 
 int flash_gau_adamw_step(const flash_gau_adamw_tensor *tensors, int n_tensors,

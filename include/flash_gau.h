@@ -361,6 +361,49 @@ int flash_gau_decode_step(const void *x, const flash_gau_weights *w, int B, int 
 int flash_gau_rope_toeplitz_bias(const float *a, const float *b, int m, int C,
                                  float rope_base, float *relpos, void *stream);
 
+/* ---- cross entropy over a vocabulary -------------------------------------- */
+/* The loss of a language model's head and its gradients, without the logits
+ * in memory:
+ *   l_i = x_i W^T        lse_i = log sum_v exp(l_iv)
+ *   loss_i = lse_i - l_i[y_i]
+ *   total = scale * mean or sum of the loss_i
+ *   dX = d total / dX    dW = d total / dW
+ * X is [N, d] (the last block's output), W [V, d] (one row a word).  A token
+ * whose label y_i is outside [0, V) is left out: its loss, lse and row of dX
+ * are zero, it adds nothing to dW, the mean is over the others (of none: 0),
+ * and what its row of X holds, NaN included, has no effect.  The tokens are
+ * taken in pieces of at most 2 GiB of [tokens, V] in the workspace.  bf16:
+ * the products run on the tensor cores with fp32 accumulation and sums; the
+ * exponentials enter the gradients' products rounded to bf16.  fp32: all in
+ * fp32 on the CUDA cores.                                                   */
+#define FLASH_GAU_MEAN 0
+#define FLASH_GAU_SUM 1
+
+typedef struct flash_gau_xent_out {
+  float *total;         /* device [1]                                        */
+  float *loss;          /* device [N]                                        */
+  float *lse;           /* device [N], or NULL                               */
+  void *dX;             /* device [N, d], io type, or NULL: not wanted       */
+  void *dW;             /* device [V, d], io type, or NULL: not wanted       */
+} flash_gau_xent_out;
+
+/* Supported: N up to 2^30, V up to 2^22, d up to 65536; BF16: d a multiple
+ * of 8.
+ * Workspace bytes for a call with (grad nonzero) or without gradients, or 0
+ * when the arguments are invalid or unsupported.                            */
+size_t flash_gau_xent_workspace_bytes(long long N, int d, int V, int dtype, int grad);
+
+/* X, W: device, io type, 16-byte aligned for bf16 (as dX and dW); labels:
+ * device int32 [N]; reduction: FLASH_GAU_MEAN or _SUM; out: host pointer,
+ * read during the call.  Outputs must not overlap the inputs, the workspace
+ * or one another.  workspace: device, 256-byte aligned; its first word is
+ * the status word of flash_gau_workspace_status.  Results repeat bit for
+ * bit.  Returns FLASH_GAU_OK, FLASH_GAU_EINVAL, FLASH_GAU_ENOTSUP,
+ * FLASH_GAU_EWORKSPACE, FLASH_GAU_EDEVICE or FLASH_GAU_ECUDA.               */
+int flash_gau_xent(const void *X, const void *W, const int *labels, long long N, int d, int V,
+                   int dtype, int reduction, float scale, const flash_gau_xent_out *out,
+                   void *workspace, size_t workspace_bytes, void *stream);
+
 /* ---- residual stream and block norms ------------------------------------ */
 /* What stands between two blocks of a stack, in one pass over the rows:
  *   r = h + scale * gate * post(y)      the residual stream after a block

@@ -96,7 +96,13 @@ def xent(X, W, labels, reduction="mean", scale=1.0):
     logits = X @ W.T
     top = logits.max(axis=1)
     lse = top + np.log(np.exp(logits - top[:, None]).sum(axis=1))
-    loss = np.where(live, lse - logits[at, y], 0.0)
+    # lse - l_y as the logarithm of 1 + the others' share, which keeps the
+    # digits of a small loss
+    d = logits - logits[at, y][:, None]
+    d[at, y] = -np.inf
+    m = np.maximum(d.max(axis=1), 0.0)
+    r = np.exp(d - m[:, None]).sum(axis=1)
+    loss = np.where(live, np.where(m > 0, m + np.log(np.exp(-m) + r), np.log1p(r)), 0.0)
     n = max(int(live.sum()), 1) if reduction == "mean" else 1
     P = np.exp(logits - lse[:, None])
     # p - 1 at the label as minus the others' sum

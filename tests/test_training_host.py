@@ -264,3 +264,66 @@ def test_binding_refuses_host_tensors(L):
         bd.residual_norm(x.half(), None)
     with pytest.raises(ValueError):
         bd.AdamW([x], state_bits=4)
+
+
+# ---- cross entropy ------------------------------------------------------------
+@pytest.mark.parametrize("reduction", ["mean", "sum"])
+def test_oracle_xent_against_autograd(reduction):
+    rng = np.random.default_rng(8)
+    X, W = rng.normal(size=(9, 6)), rng.normal(size=(11, 6))
+    labels = np.array([0, 10, 3, -1, 5, 11, 7, 7, -100])
+    X[3] = np.nan
+    x, w = torch.tensor(np.nan_to_num(X), requires_grad=True), torch.tensor(W, requires_grad=True)
+    keep = (labels >= 0) & (labels < 11)
+    t = torch.tensor(np.where(keep, labels, -100))
+    loss = torch.nn.functional.cross_entropy(x @ w.t(), t, reduction=reduction) * 0.5
+    loss.backward()
+    got = oracle.xent(X, W, labels, reduction, 0.5)
+    assert abs(got["total"] - float(loss.detach())) < 1e-12
+    np.testing.assert_allclose(got["dX"], x.grad.numpy(), rtol=1e-10, atol=1e-13)
+    np.testing.assert_allclose(got["dW"], w.grad.numpy(), rtol=1e-10, atol=1e-13)
+    assert not got["dX"][~keep].any() and not got["loss"][~keep].any()
+    none = oracle.xent(X, W, np.full(9, -1), reduction)
+    assert none["total"] == 0 and not none["dW"].any()
+
+
+@pytest.mark.parametrize("args,out,code", [
+    (dict(X=None), {}, bd.EINVAL), (dict(W=None), {}, bd.EINVAL), (dict(labels=None), {}, bd.EINVAL),
+    (dict(N=0), {}, bd.EINVAL), (dict(d=0), {}, bd.EINVAL), (dict(V=-1), {}, bd.EINVAL),
+    (dict(dtype=9), {}, bd.EINVAL), (dict(reduction=2), {}, bd.EINVAL),
+    (dict(scale=float("inf")), {}, bd.EINVAL),
+    (dict(d=60), {}, bd.ENOTSUP), (dict(V=(1 << 22) + 1), {}, bd.ENOTSUP),
+    (dict(d=65544), {}, bd.ENOTSUP),
+    (dict(X=A + 8), {}, bd.EINVAL), (dict(labels=C + 2), {}, bd.EINVAL),
+    ({}, dict(total=None), bd.EINVAL), ({}, dict(loss=None), bd.EINVAL),
+    ({}, dict(dX=A), bd.EINVAL), ({}, dict(dW=B + 160), bd.EINVAL), ({}, dict(dW=9 << 32 | 2), bd.EINVAL),
+    ({}, dict(lse=F_), bd.EINVAL),                       # the losses
+    (dict(ws=1 << 44 | 64), {}, bd.EWORKSPACE), (dict(wsb=1000), {}, bd.EWORKSPACE),
+    (dict(ws=A), {}, bd.EINVAL),
+])
+def test_xent_refuses(L, args, out, code):
+    a = dict(X=A, W=B, labels=C, N=40, d=64, V=500, dtype=bd.BF16, reduction=bd.MEAN, scale=1.0,
+             ws=1 << 44, wsb=1 << 30)
+    a.update(args)
+    o = dict(total=D, loss=F_, lse=None, dX=7 << 32, dW=8 << 32)
+    o.update(out)
+    x = bd.XentOut(*(o[k] for k, _ in bd.XentOut._fields_))
+    assert L.flash_gau_xent(a["X"], a["W"], a["labels"], a["N"], a["d"], a["V"], a["dtype"],
+                            a["reduction"], a["scale"], ctypes.byref(x), a["ws"], a["wsb"],
+                            None) == code
+
+
+def test_xent_workspace(L):
+    f = L.flash_gau_xent_workspace_bytes
+    assert f(0, 64, 10, bd.BF16, 1) == 0 and f(4, 64, 10, 7, 1) == 0 and f(4, 4, 10, bd.BF16, 1) == 0
+    assert f(4, 4, 10, bd.FP32, 1) > 0
+    # a piece's [tokens, V] never passes 2 GiB however many tokens there are
+    for N in (1, 1000, 16384, 1 << 20, 1 << 30):
+        n = f(N, 768, 50257, bd.BF16, 1)
+        assert 0 < n < (3 << 30)
+        assert 0 < f(N, 768, 50257, bd.BF16, 0) < (300 << 20)
+
+
+def test_xent_binding_refuses_host_tensors(L):
+    with pytest.raises(ValueError):
+        bd.xent(torch.zeros(4, 8), torch.zeros(5, 8), torch.zeros(4, dtype=torch.int32))
