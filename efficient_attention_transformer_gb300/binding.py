@@ -689,7 +689,7 @@ def xent_workspace_bytes(N, d, V, dtype, grad=True):
 def xent(X, W, labels, reduction=MEAN, scale=1.0, grad=True, out=None, workspace=None,
          stream=None):
     """Cross entropy of softmax(X W^T) at the labels, through flash_gau_xent:
-    a dict with total ([1]), loss and lse (like labels, fp32), and with grad
+    a dict with total (a scalar), loss and lse (like labels, fp32), and with grad
     dX and dW, the gradients of total in the io type.  X: [..., d], W: [V, d],
     labels: int32, X's leading shape; a label outside [0, V) leaves its token
     out.  total is scale times the MEAN over the labelled tokens or the SUM.
@@ -706,7 +706,7 @@ def xent(X, W, labels, reduction=MEAN, scale=1.0, grad=True, out=None, workspace
     f32 = torch.float32
     out = dict(out or {})
     with _scope(dev, stream):
-        for name, shape, dtype in (("total", (1,), f32), ("loss", labels.shape, f32),
+        for name, shape, dtype in (("total", (), f32), ("loss", labels.shape, f32),
                                    ("lse", labels.shape, f32), ("dX", X.shape, X.dtype),
                                    ("dW", W.shape, X.dtype)):
             if name[0] == "d" and not grad:

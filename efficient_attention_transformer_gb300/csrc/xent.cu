@@ -20,7 +20,9 @@
 //   E_y := -Zx (p_y - 1 = -Zx / Z without cancellation),
 //   dX_i = (g / Z_i) sum_v E_iv W_v         (scaled in the epilogue)
 //   dW_v = sum_i E_iv (g / Z_i) x_i         (x scaled and rounded once)
-// Roundings to bf16: E, the scaled x, and the results.
+// Roundings to bf16: E, the scaled x, and the results.  The label's term
+// outweighs the others, so the row's factor takes its E's rounding out again
+// (and puts that half step on the other words' terms).
 //
 // All three products run on the 2-SM tcgen05 tiles of the layer's projection
 // (256 x 256 of a CTA pair, 64-deep k-blocks by TMA into a 6-stage ring, two
@@ -579,8 +581,13 @@ __global__ void __launch_bounds__(256) xent_rows_kernel(const RowArgs a) {
       a.loss[row] = loss;
       if (a.lse) a.lse[row] = label >= 0 ? fmaf(ref, kLn2, loss) : 0.f;
       if (a.E) {
+        if (label >= 0) {
+          const __nv_bfloat16 own = __float2bfloat16_rn(-sum);
+          a.E[(size_t)row * a.ldE + label] = own;
+          // its rounding goes into the row's factor
+          if (sum > 0.f && sum < INFINITY) scale *= sum / -__bfloat162float(own);
+        }
         a.scale[row] = scale;
-        if (label >= 0) a.E[(size_t)row * a.ldE + label] = __float2bfloat16_rn(-sum);
       }
     }
     row_ref[lane] = top;
