@@ -306,9 +306,10 @@ struct ResidualProblem {
   int d, dtype, num_sms;
   cudaStream_t stream;
 };
-constexpr int kResidualMaxD = 4096;
+constexpr int kResidualMaxD = 8192;
 constexpr int kResidualMaxBlocks = 608;  // of the gradient kernel, four a SM
-int residual_norm_blocks(long long M, int d);  // parts of the column sums
+constexpr int kGradSmemMax = 227 * 1024 - 1024;  // its largest tile, less its static part
+size_t residual_norm_part_bytes(long long M, int d);  // parts of the column sums
 cudaError_t residual_norm(const ResidualProblem &q, const void *h, void *r, void *n);
 cudaError_t residual_norm_grad(const ResidualProblem &q, const void *dr, const void *dn,
                                const void *r, const flash_gau_residual_grads &g, void *workspace);

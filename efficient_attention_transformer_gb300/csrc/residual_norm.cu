@@ -6,24 +6,30 @@
 //   LayerNorm  (x - mean) / sqrt(var + eps) * g + b     (biased variance)
 //   ScaleNorm  g x / max(|x|, eps)                      (g a single scalar)
 //
-// Backward, with u the normalised row without its parameters and
-// w = g * (gradient of the norm's output):
-//   LayerNorm  dx = (w - mean(w) - u mean(w u)) / sqrt(var + eps)
-//   ScaleNorm  dx = (w - u sum(w u)) / max(|x|, eps), the second term only
-//              where |x| > eps
+// Backward, with u the normalised row without its parameters, i = 1 / spread
+// and w = g * (gradient of the norm's output):
+//   LayerNorm  dx = i (w - mean(w) - u mean(w u))
+//   ScaleNorm  dx = i (w - u sum(w u)), the second term only where |x| > eps
 //   dh = dr + dx_norm(dn; r)      dgate = dh * post(y) * scale
 //   dy = dx_post(dh * scale * gate; y)
 // and the column sums over the rows for the parameters.
 //
-// Both directions only move rows (at d = 768, bf16: 4 rows in and out
-// forward, 6 to 8 backward), so each value is read once and stays in
-// registers.  A thread block is one row wide (8 columns a thread) and takes
-// R rows at a time, so that the barriers of the row sums are shared by R rows
-// and R rows' loads are in flight; a thread keeps its columns for the whole
-// launch, so the parameters, and backward the column sums of their
-// gradients, stay in registers too.  Statistics are fp32: within a warp the
-// mean first and the squares around it second, warps joined by their counts
-// (no difference of large squares).
+// Both directions only move rows (at d = 768, bf16: 5 rows in and out
+// forward with a gate, 8 backward), so the aim is to read each value once
+// from memory with many rows in flight.
+//
+// Forward, one warp a row in registers: 256 columns a step of the warp (16
+// bytes a lane), no block-wide step at all.  Rows wider than 2048 columns, or
+// not on 16-byte boundaries, take a plain form that reads the row again from
+// L1 for each of its sums.
+//
+// Backward, a tile of rows (about 44 KB, four blocks an SM) is brought into
+// shared memory by asynchronous copies.  First one warp a row takes the row's sums;
+// means come first and squares around them second (no difference of large
+// squares), and the sums that dx needs ride along, three passes over shared
+// memory in all.  Then the threads turn by 90 degrees: each keeps four
+// columns for the whole launch, forms the outputs of the tile's rows from
+// the rows' sums, and adds up the parameters' gradients in registers.
 #include <cuda_bf16.h>
 
 #include "flash_gau_internal.h"
@@ -32,8 +38,6 @@
 namespace flashgau {
 namespace {
 
-constexpr int kCols = 8;        // columns of a thread
-constexpr int kMaxWarps = 16;   // of a block: d <= 4096
 constexpr unsigned kAll = 0xffffffffu;
 
 struct Args {
@@ -43,114 +47,20 @@ struct Args {
   void *r, *n;               // forward outputs
   void *dh, *dy, *dgate;     // backward outputs
   const float *norm_g, *norm_b, *post_g, *post_b, *scale;
-  float *part;               // backward: [blocks][kSums][d] column sums
+  float *part;               // backward: [parts][kSums][d] column sums
+  float *scalar_part;        // backward: [2][blocks][kMaxWarps], ScaleNorm's g
   long long M;
   int d, norm, post;
   float eps;
+  int rows, subsets;         // backward: rows of a tile, threads that share a column
 };
 
 // the column sums, in the workspace's order
 enum { kNormG = 0, kNormB = 1, kPostG = 2, kPostB = 3, kScale = 4, kSums = 5 };
+constexpr int kMaxWarps = 16;
 
-// Column q of thread t.  VEC elements are consecutive: 8 (bf16) or 4 (fp32)
-// for 16-byte accesses, or 1, any d and alignment.
-template <int VEC>
-__device__ __forceinline__ int column(int t, int threads, int q) {
-  if (VEC == 8) return t * 8 + q;
-  if (VEC == 4) return (q / 4) * threads * 4 + t * 4 + q % 4;
-  return q * threads + t;
-}
-
-// Eight values of one row as loaded (bf16 packed).
-template <typename T>
-struct Raw;
-template <>
-struct Raw<float> {
-  float x[8];
-  __device__ float get(int q) const { return x[q]; }
-  __device__ void set(int q, float v) { x[q] = v; }
-};
-template <>
-struct Raw<__nv_bfloat16> {
-  uint32_t w[4];
-  __device__ float get(int q) const {
-    return __uint_as_float((q & 1) ? (w[q / 2] & 0xffff0000u) : (w[q / 2] << 16));
-  }
-  __device__ void set2(int q2, float a, float b) {
-    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-    w[q2] = *reinterpret_cast<const uint32_t *>(&v);
-  }
-};
-
-template <typename T, int VEC>
-__device__ __forceinline__ void load_row(const void *base, long long row, int d, int t, int threads,
-                                         Raw<T> &out) {
-  const T *p = static_cast<const T *>(base) + row * d;
-  if constexpr (VEC == 8) {
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (t * 8 < d) v = *reinterpret_cast<const uint4 *>(p + t * 8);
-    out.w[0] = v.x; out.w[1] = v.y; out.w[2] = v.z; out.w[3] = v.w;
-  } else if constexpr (VEC == 4) {
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int c = column<4>(t, threads, 4 * k);
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (c < d) v = *reinterpret_cast<const float4 *>(p + c);
-      out.x[4 * k] = v.x; out.x[4 * k + 1] = v.y; out.x[4 * k + 2] = v.z; out.x[4 * k + 3] = v.w;
-    }
-  } else {
-    float x[8];
-#pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      const int c = column<1>(t, threads, q);
-      x[q] = c < d ? (float)p[c] : 0.f;
-    }
-    if constexpr (sizeof(T) == 4) {
-#pragma unroll
-      for (int q = 0; q < 8; ++q) out.set(q, x[q]);
-    } else {
-#pragma unroll
-      for (int q = 0; q < 4; ++q) out.set2(q, x[2 * q], x[2 * q + 1]);
-    }
-  }
-}
-
-template <typename T, int VEC>
-__device__ __forceinline__ void store_row(void *base, long long row, int d, int t, int threads,
-                                          const float (&x)[8]) {
-  T *p = static_cast<T *>(base) + row * d;
-  if constexpr (VEC == 8) {
-    Raw<__nv_bfloat16> o;
-#pragma unroll
-    for (int q = 0; q < 4; ++q) o.set2(q, x[2 * q], x[2 * q + 1]);
-    if (t * 8 < d) *reinterpret_cast<uint4 *>(p + t * 8) = make_uint4(o.w[0], o.w[1], o.w[2], o.w[3]);
-  } else if constexpr (VEC == 4) {
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int c = column<4>(t, threads, 4 * k);
-      if (c < d)
-        *reinterpret_cast<float4 *>(p + c) =
-            make_float4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
-    }
-  } else {
-#pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      const int c = column<1>(t, threads, q);
-      if (c < d) p[c] = (T)x[q];
-    }
-  }
-}
-
-// a parameter's values in this thread's columns (`fill` where there is none)
-template <int VEC>
-__device__ __forceinline__ void load_param(const float *p, int d, int t, int threads, float fill,
-                                           float (&x)[8]) {
-#pragma unroll
-  for (int q = 0; q < 8; ++q) {
-    const int c = column<VEC>(t, threads, q);
-    x[q] = p ? (c < d ? __ldg(p + c) : 0.f) : fill;
-  }
-}
+__device__ __forceinline__ float to_f(float x) { return x; }
+__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
 
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
@@ -158,439 +68,687 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-// Sums and statistics over a row, R rows at a time, for a block of one or
-// more warps.  Buffers alternate, so one barrier a reduction is enough: a
-// warp writes a buffer again only after the barrier that follows every
-// warp's reading of it.
-template <int R>
-struct Rows {
-  float2 (*buf)[kMaxWarps][2 * R];  // [2]
-  const float *count;               // columns of each warp
-  int warps, warp, lane, d;
-  int flip;
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ float2 unpack_bf16(uint32_t w) {
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
 
-  // every warp's 2 R pairs; `use` reads them in order
-  template <typename Use>
-  __device__ void exchange(const float2 (&x)[2 * R], Use use) {
-    if (warps == 1) {
-#pragma unroll
-      for (int k = 0; k < 2 * R; ++k) use(0, k, x[k]);
-      return;
-    }
-    if (lane == 0) {
-#pragma unroll
-      for (int k = 0; k < 2 * R; ++k) buf[flip][warp][k] = x[k];
-    }
-    __syncthreads();
-    for (int w = 0; w < warps; ++w)
-#pragma unroll
-      for (int k = 0; k < 2 * R; ++k) use(w, k, buf[flip][w][k]);
-    flip ^= 1;
+// 1 / spread of a row from its sum of squares around the mean (LayerNorm) or
+// around zero (ScaleNorm)
+__device__ __forceinline__ float inv_spread(float m2, int kind, int d, float eps) {
+  return kind == FLASH_GAU_NORM_LAYER ? 1.0f / sqrtf(m2 / (float)d + eps)
+                                      : 1.0f / fmaxf(sqrtf(m2), eps);
+}
+
+// ---------------------------------------------------------------- forward --
+// Eight columns of a row a lane: chunk k covers columns 256 k .. 256 k + 255,
+// as 8 consecutive bf16 or two runs of 4 fp32.
+template <typename T>
+struct Eight;
+template <>
+struct Eight<__nv_bfloat16> {
+  uint4 w;
+  static __device__ int column(int k, int lane, int q) { return 256 * k + 8 * lane + q; }
+  __device__ void load(const __nv_bfloat16 *row, int k, int lane, int d) {
+    const int c = column(k, lane, 0);
+    w = c < d ? *reinterpret_cast<const uint4 *>(row + c) : make_uint4(0, 0, 0, 0);
+  }
+  __device__ float get(int q) const {
+    const uint32_t v = q < 2 ? w.x : q < 4 ? w.y : q < 6 ? w.z : w.w;
+    const float2 f = unpack_bf16(v);
+    return (q & 1) ? f.y : f.x;
+  }
+  static __device__ void store(__nv_bfloat16 *row, int k, int lane, int d, const float (&x)[8]) {
+    const int c = column(k, lane, 0);
+    if (c < d)
+      *reinterpret_cast<uint4 *>(row + c) =
+          make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]),
+                     pack_bf16(x[6], x[7]));
+  }
+};
+template <>
+struct Eight<float> {
+  float4 a, b;
+  static __device__ int column(int k, int lane, int q) {
+    return 256 * k + 4 * lane + (q & 3) + (q < 4 ? 0 : 128);
+  }
+  __device__ void load(const float *row, int k, int lane, int d) {
+    const int c0 = column(k, lane, 0), c1 = column(k, lane, 4);
+    const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+    a = c0 < d ? *reinterpret_cast<const float4 *>(row + c0) : zero;
+    b = c1 < d ? *reinterpret_cast<const float4 *>(row + c1) : zero;
+  }
+  __device__ float get(int q) const {
+    const float4 &v = q < 4 ? a : b;
+    return (q & 3) == 0 ? v.x : (q & 3) == 1 ? v.y : (q & 3) == 2 ? v.z : v.w;
+  }
+  static __device__ void store(float *row, int k, int lane, int d, const float (&x)[8]) {
+    const int c0 = column(k, lane, 0), c1 = column(k, lane, 4);
+    if (c0 < d) *reinterpret_cast<float4 *>(row + c0) = make_float4(x[0], x[1], x[2], x[3]);
+    if (c1 < d) *reinterpret_cast<float4 *>(row + c1) = make_float4(x[4], x[5], x[6], x[7]);
   }
 };
 
-// (mean, 1 / spread) of a row from its warps' (mean, squares around it): the
-// LayerNorm's 1 / sqrt(var + eps), or the ScaleNorm's 1 / max(|x|, eps)
-struct Stat {
-  float mean, inv;
-  bool long_;  // ScaleNorm: |x| > eps
-};
+// a parameter's values in a lane's columns of chunk k; columns behind the row
+// read as zero, so that their results are never stored anyway
+template <typename T>
+__device__ __forceinline__ void load_param(const float *p, int k, int lane, int d, float (&x)[8]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int c = Eight<T>::column(k, lane, 4 * h);
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (c < d) {  // 4-byte alignment is all that is asked of parameters
+      v.x = __ldg(p + c);
+      v.y = __ldg(p + c + 1);
+      v.z = __ldg(p + c + 2);
+      v.w = __ldg(p + c + 3);
+    }
+    x[4 * h] = v.x; x[4 * h + 1] = v.y; x[4 * h + 2] = v.z; x[4 * h + 3] = v.w;
+  }
+}
 
-// this warp's (mean, sum of squares around it) of one row
-template <int VEC>
-__device__ __forceinline__ float2 warp_stat(const float (&x)[8], int kind, float count, int d,
-                                            int t, int threads) {
+// (mean, 1 / spread) of a row of NC chunks in registers
+template <typename T, int NC, typename Get>
+__device__ __forceinline__ float2 row_stat(Get get, int kind, int lane, int d, float eps) {
   float mean = 0.f;
   if (kind == FLASH_GAU_NORM_LAYER) {
     float s = 0.f;
 #pragma unroll
-    for (int q = 0; q < 8; ++q) s += x[q];  // zeros behind the row
-    mean = warp_sum(s) / count;
-  }
-  float s2 = 0.f;
+    for (int k = 0; k < NC; ++k)
 #pragma unroll
-  for (int q = 0; q < 8; ++q) {
-    const float c = column<VEC>(t, threads, q) < d ? x[q] - mean : 0.f;
-    s2 = fmaf(c, c, s2);
+      for (int q = 0; q < 8; ++q) s += get(k, q);  // zeros behind the row
+    mean = warp_sum(s) / (float)d;
   }
-  return make_float2(mean, warp_sum(s2));
+  float m2 = 0.f;
+#pragma unroll
+  for (int k = 0; k < NC; ++k)
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      const float c = Eight<T>::column(k, lane, q) < d ? get(k, q) - mean : 0.f;
+      m2 = fmaf(c, c, m2);
+    }
+  return make_float2(mean, inv_spread(warp_sum(m2), kind, d, eps));
 }
 
-// Joins the warps' statistics: pairs 0 .. R - 1 are of norm ka, the others of
-// norm kb.
-template <int R>
-__device__ __forceinline__ void join(Rows<R> &rows, const float2 (&x)[2 * R], int ka, int kb,
-                                     float eps, Stat (&out)[2 * R]) {
-  float m2[2 * R], means[2 * R];
+template <typename T, int NC>
+__global__ void __launch_bounds__(128) residual_norm_kernel(const Args a) {
+  ptx::griddep_wait();
+  const int lane = threadIdx.x & 31, d = a.d;
+  const long long row = blockIdx.x * (long long)(blockDim.x >> 5) + (threadIdx.x >> 5);
+  if (row >= a.M) return;
+  Eight<T> h[NC], y[NC], gt[NC];
 #pragma unroll
-  for (int k = 0; k < 2 * R; ++k) m2[k] = means[k] = 0.f;
-  // joined one warp at a time: the running mean and the squares around it
-  float seen = 0.f, ratio = 1.f, weight = 0.f;
-  rows.exchange(x, [&](int w, int k, float2 v) {
-    if (k == 0) {
-      const float c = rows.count[w];
-      ratio = c / (seen + c);
-      weight = seen * ratio;
-      seen += c;
+  for (int k = 0; k < NC; ++k) {
+    h[k].load(static_cast<const T *>(a.h) + row * d, k, lane, d);
+    if (a.y) y[k].load(static_cast<const T *>(a.y) + row * d, k, lane, d);
+    if (a.gate) gt[k].load(static_cast<const T *>(a.gate) + row * d, k, lane, d);
+  }
+  float r[NC][8];
+  if (a.y) {
+    const bool layer = a.post == FLASH_GAU_NORM_LAYER;
+    float2 st = make_float2(0.f, 1.f);
+    if (a.post)
+      st = row_stat<T, NC>([&](int k, int q) { return y[k].get(q); }, a.post, lane, d, a.eps);
+    if (a.post == FLASH_GAU_NORM_SCALE) st.y *= __ldg(a.post_g);
+#pragma unroll
+    for (int k = 0; k < NC; ++k) {
+      float g[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) r[k][q] = (y[k].get(q) - st.x) * st.y;
+      if (layer) {
+        load_param<T>(a.post_g, k, lane, d, g);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) r[k][q] *= g[q];
+        if (a.post_b) {
+          load_param<T>(a.post_b, k, lane, d, g);
+#pragma unroll
+          for (int q = 0; q < 8; ++q) r[k][q] += g[q];
+        }
+      }
+      if (a.gate) {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) r[k][q] *= gt[k].get(q);
+      }
+      if (a.scale) {
+        load_param<T>(a.scale, k, lane, d, g);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) r[k][q] *= g[q];
+      }
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        r[k][q] = Eight<T>::column(k, lane, q) < d ? r[k][q] + h[k].get(q) : 0.f;
     }
-    const float delta = v.x - means[k];
-    means[k] = fmaf(delta, ratio, means[k]);
-    m2[k] += fmaf(delta * delta, weight, v.y);
-  });
+  } else {
 #pragma unroll
-  for (int k = 0; k < 2 * R; ++k) {
-    const int kind = k < R ? ka : kb;
-    out[k].mean = means[k];
+    for (int k = 0; k < NC; ++k)
+#pragma unroll
+      for (int q = 0; q < 8; ++q) r[k][q] = h[k].get(q);
+  }
+  if (a.r) {
+#pragma unroll
+    for (int k = 0; k < NC; ++k) Eight<T>::store(static_cast<T *>(a.r) + row * d, k, lane, d, r[k]);
+  }
+  if (!a.norm) return;
+  float2 st = row_stat<T, NC>([&](int k, int q) { return r[k][q]; }, a.norm, lane, d, a.eps);
+  const bool layer = a.norm == FLASH_GAU_NORM_LAYER;
+  if (!layer) st.y *= __ldg(a.norm_g);
+#pragma unroll
+  for (int k = 0; k < NC; ++k) {
+    float g[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) r[k][q] = (r[k][q] - st.x) * st.y;
+    if (layer) {
+      load_param<T>(a.norm_g, k, lane, d, g);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) r[k][q] *= g[q];
+      if (a.norm_b) {
+        load_param<T>(a.norm_b, k, lane, d, g);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) r[k][q] += g[q];
+      }
+    }
+    Eight<T>::store(static_cast<T *>(a.n) + row * d, k, lane, d, r[k]);
+  }
+}
+
+// Any width and alignment: one warp a row, element by element, the row read
+// again for each sum.  Outputs are written last, each after the same
+// element's inputs, so they may be the inputs' arrays.
+template <typename T>
+__global__ void __launch_bounds__(128) residual_norm_any_kernel(const Args a) {
+  ptx::griddep_wait();
+  const int lane = threadIdx.x & 31, d = a.d;
+  const long long row = blockIdx.x * (long long)(blockDim.x >> 5) + (threadIdx.x >> 5);
+  if (row >= a.M) return;
+  const T *h = static_cast<const T *>(a.h) + row * d;
+  const T *y = a.y ? static_cast<const T *>(a.y) + row * d : nullptr;
+  const T *gate = a.gate ? static_cast<const T *>(a.gate) + row * d : nullptr;
+  auto stat = [&](auto get, int kind) {
+    float mean = 0.f, m2 = 0.f;
     if (kind == FLASH_GAU_NORM_LAYER) {
-      out[k].inv = 1.0f / sqrtf(m2[k] / (float)rows.d + eps);
-      out[k].long_ = true;
-    } else {
-      const float len = sqrtf(m2[k]);
-      out[k].inv = 1.0f / fmaxf(len, eps);
-      out[k].long_ = len > eps;
+      float s = 0.f;
+      for (int c = lane; c < d; c += 32) s += get(c);
+      mean = warp_sum(s) / (float)d;
     }
+    for (int c = lane; c < d; c += 32) {
+      const float v = get(c) - mean;
+      m2 = fmaf(v, v, m2);
+    }
+    return make_float2(mean, inv_spread(warp_sum(m2), kind, d, a.eps));
+  };
+  auto affine = [&](float u, int kind, const float *g, const float *b, int c) {
+    if (kind == FLASH_GAU_NORM_LAYER) return fmaf(u, g[c], b ? b[c] : 0.f);
+    return kind == FLASH_GAU_NORM_SCALE ? u * g[0] : u;
+  };
+  float2 sy = make_float2(0.f, 1.f);
+  if (y && a.post) sy = stat([&](int c) { return to_f(y[c]); }, a.post);
+  auto r = [&](int c) {
+    if (!y) return to_f(h[c]);
+    float v = affine((to_f(y[c]) - sy.x) * sy.y, a.post, a.post_g, a.post_b, c);
+    if (gate) v *= to_f(gate[c]);
+    if (a.scale) v *= a.scale[c];
+    return to_f(h[c]) + v;
+  };
+  float2 sr = make_float2(0.f, 1.f);
+  if (a.norm) sr = stat(r, a.norm);
+  for (int c = lane; c < d; c += 32) {
+    const float v = r(c);
+    const float n = affine((v - sr.x) * sr.y, a.norm, a.norm_g, a.norm_b, c);
+    if (a.r) static_cast<T *>(a.r)[row * d + c] = (T)v;
+    if (a.norm) static_cast<T *>(a.n)[row * d + c] = (T)n;
   }
 }
 
-template <int R>
-__device__ __forceinline__ Rows<R> make_rows(float2 (*buf)[kMaxWarps][2 * R], float *count, int d,
-                                             int own) {
-  Rows<R> rows;
-  rows.buf = buf;
-  rows.count = count;
-  rows.warps = blockDim.x >> 5;
-  rows.warp = threadIdx.x >> 5;
-  rows.lane = threadIdx.x & 31;
-  rows.d = d;
-  rows.flip = 0;
-  const float c = warp_sum((float)own);
-  if (rows.lane == 0) count[rows.warp] = c;
-  __syncthreads();
-  return rows;
+// --------------------------------------------------------------- backward --
+// Four columns of a row: consecutive ones from c on (VEC; 8 bytes of bf16,
+// 16 of fp32), or c, c + stride, c + 2 stride, c + 3 stride, zeros behind d.
+template <bool VEC>
+__device__ __forceinline__ void load4(const float *row, int c, int stride, int d, float (&x)[4]) {
+  if (VEC) {
+    const float4 v = *reinterpret_cast<const float4 *>(row + c);
+    x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+  } else {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) x[q] = c + q * stride < d ? row[c + q * stride] : 0.f;
+  }
 }
-
-template <int VEC>
-__device__ __forceinline__ int own_columns(int d, int t, int threads) {
-  int n = 0;
+template <bool VEC>
+__device__ __forceinline__ void load4(const __nv_bfloat16 *row, int c, int stride, int d,
+                                      float (&x)[4]) {
+  if (VEC) {
+    const uint2 v = *reinterpret_cast<const uint2 *>(row + c);
+    const float2 a = unpack_bf16(v.x), b = unpack_bf16(v.y);
+    x[0] = a.x; x[1] = a.y; x[2] = b.x; x[3] = b.y;
+  } else {
 #pragma unroll
-  for (int q = 0; q < 8; ++q) n += column<VEC>(t, threads, q) < d;
-  return n;
+    for (int q = 0; q < 4; ++q)
+      x[q] = c + q * stride < d ? __bfloat162float(row[c + q * stride]) : 0.f;
+  }
 }
-
-template <typename T, int VEC, int R, int MAXT>
-__global__ void __launch_bounds__(MAXT) residual_norm_kernel(const Args a) {
-  __shared__ float2 buf[2][kMaxWarps][2 * R];
-  __shared__ float count[kMaxWarps];
-  const int t = threadIdx.x, threads = blockDim.x, d = a.d;
-  Rows<R> rows = make_rows<R>(buf, count, d, own_columns<VEC>(d, t, threads));
-  ptx::griddep_wait();
-  const bool post_layer = a.post == FLASH_GAU_NORM_LAYER, layer = a.norm == FLASH_GAU_NORM_LAYER;
-  float pg[8], pb[8], sc[8], ng[8], nb[8];
-  load_param<VEC>(post_layer ? a.post_g : nullptr, d, t, threads, a.post ? (post_layer ? 1.f : a.post_g[0]) : 1.f, pg);
-  load_param<VEC>(post_layer ? a.post_b : nullptr, d, t, threads, 0.f, pb);
-  load_param<VEC>(a.scale, d, t, threads, 1.f, sc);
-  load_param<VEC>(layer ? a.norm_g : nullptr, d, t, threads, a.norm ? (layer ? 1.f : a.norm_g[0]) : 1.f, ng);
-  load_param<VEC>(layer ? a.norm_b : nullptr, d, t, threads, 0.f, nb);
-  const float wc = count[rows.warp];
-  for (long long row0 = (long long)blockIdx.x * R; row0 < a.M; row0 += (long long)gridDim.x * R) {
-    Raw<T> h[R], y[R], gt[R];
+template <bool VEC>
+__device__ __forceinline__ void store4(float *row, int c, int stride, int d, const float (&x)[4]) {
+  if (VEC) {
+    *reinterpret_cast<float4 *>(row + c) = make_float4(x[0], x[1], x[2], x[3]);
+  } else {
 #pragma unroll
-    for (int k = 0; k < R; ++k) {
-      const long long row = min(row0 + k, a.M - 1);
-      load_row<T, VEC>(a.h, row, d, t, threads, h[k]);
-      if (a.y) load_row<T, VEC>(a.y, row, d, t, threads, y[k]);
-      if (a.gate) load_row<T, VEC>(a.gate, row, d, t, threads, gt[k]);
-    }
-    float r[R][8];
-    if (a.y) {
-      Stat st[2 * R];
-      if (a.post) {
-        float2 w[2 * R];
+    for (int q = 0; q < 4; ++q)
+      if (c + q * stride < d) row[c + q * stride] = x[q];
+  }
+}
+template <bool VEC>
+__device__ __forceinline__ void store4(__nv_bfloat16 *row, int c, int stride, int d,
+                                       const float (&x)[4]) {
+  if (VEC) {
+    *reinterpret_cast<uint2 *>(row + c) = make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
+  } else {
 #pragma unroll
-        for (int k = 0; k < R; ++k) {
-          float x[8];
-#pragma unroll
-          for (int q = 0; q < 8; ++q) x[q] = y[k].get(q);
-          w[k] = warp_stat<VEC>(x, a.post, wc, d, t, threads);
-          w[R + k] = make_float2(0.f, 0.f);
-        }
-        join<R>(rows, w, a.post, a.post, a.eps, st);
-      }
-#pragma unroll
-      for (int k = 0; k < R; ++k)
-#pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          float v = y[k].get(q);
-          if (a.post) v = fmaf((v - st[k].mean) * st[k].inv, pg[q], pb[q]);
-          if (a.gate) v *= gt[k].get(q);
-          r[k][q] = fmaf(v, sc[q], h[k].get(q));
-        }
-      if (a.r) {
-#pragma unroll
-        for (int k = 0; k < R; ++k)
-          if (row0 + k < a.M) store_row<T, VEC>(a.r, row0 + k, d, t, threads, r[k]);
-      }
-    } else {
-#pragma unroll
-      for (int k = 0; k < R; ++k)
-#pragma unroll
-        for (int q = 0; q < 8; ++q) r[k][q] = h[k].get(q);
-    }
-    if (a.norm) {
-      float2 w[2 * R];
-      Stat st[2 * R];
-#pragma unroll
-      for (int k = 0; k < R; ++k) {
-        w[k] = warp_stat<VEC>(r[k], a.norm, wc, d, t, threads);
-        w[R + k] = make_float2(0.f, 0.f);
-      }
-      join<R>(rows, w, a.norm, a.norm, a.eps, st);
-#pragma unroll
-      for (int k = 0; k < R; ++k) {
-        float o[8];
-#pragma unroll
-        for (int q = 0; q < 8; ++q) o[q] = fmaf((r[k][q] - st[k].mean) * st[k].inv, ng[q], nb[q]);
-        if (row0 + k < a.M) store_row<T, VEC>(a.n, row0 + k, d, t, threads, o);
-      }
-    }
+    for (int q = 0; q < 4; ++q)
+      if (c + q * stride < d) row[c + q * stride] = __float2bfloat16_rn(x[q]);
   }
 }
 
-// The input gradient of a norm from its row sums: x the row, w = g * (its
-// output's gradient), s = (sum of w, sum of w u).
-__device__ __forceinline__ float norm_grad(float u, float w, float2 s, const Stat &st, int kind,
-                                           float inv_d) {
-  if (kind == FLASH_GAU_NORM_LAYER) return st.inv * (w - s.x * inv_d - u * (s.y * inv_d));
-  return st.inv * (w - (st.long_ ? u * s.y : 0.f));
+// 16 bytes from global into shared memory without passing through registers
+__device__ __forceinline__ void cp_async16(void *dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ptx::smem_u32(dst)), "l"(src)
+               : "memory");
+}
+// this thread's copies have landed
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
 }
 
-template <typename T, int VEC, int R, int MAXT>
+// A row's sums as the second half needs them: u = (x - mean) i, and
+// dx = i (w - a - u b).
+struct RowSums {
+  float mean_r, inv_r, a_r, b_r, mean_y, inv_y, a_y, b_y;
+};
+
+template <typename T, bool VEC, int NG, int MAXT>
 __global__ void __launch_bounds__(MAXT) residual_norm_grad_kernel(const Args a) {
-  __shared__ float2 buf[2][kMaxWarps][2 * R];
-  __shared__ float count[kMaxWarps];
-  const int t = threadIdx.x, threads = blockDim.x, d = a.d;
-  Rows<R> rows = make_rows<R>(buf, count, d, own_columns<VEC>(d, t, threads));
+  extern __shared__ __align__(16) uint8_t smem[];
+  const int t = threadIdx.x, threads = blockDim.x, lane = t & 31, warp = t >> 5, d = a.d;
+  const int warps = threads >> 5;
+  const bool norm_layer = a.norm == FLASH_GAU_NORM_LAYER, post_layer = a.post == FLASH_GAU_NORM_LAYER;
+  // the tile's arrays, then w's and dy's column factors, then the rows' sums
+  const size_t array = (size_t)a.rows * d * sizeof(T), pitch = (array + 15) / 16 * 16;
+  const T *src[5] = {static_cast<const T *>(a.norm ? a.h : nullptr), static_cast<const T *>(a.dn),
+                     static_cast<const T *>(a.dr), static_cast<const T *>(a.y),
+                     static_cast<const T *>(a.gate)};
+  T *tile[5];
+  uint8_t *at = smem;
+#pragma unroll
+  for (int k = 0; k < 5; ++k) {
+    tile[k] = reinterpret_cast<T *>(at);
+    if (src[k]) at += pitch;
+  }
+  T *const tx = tile[0], *const tdn = tile[1], *const tdr = tile[2], *const ty = tile[3],
+           *const tg = tile[4];
+  const int dp = (d + 3) / 4 * 4;
+  float *ng = reinterpret_cast<float *>(at), *kp = ng + dp;
+  RowSums *sums = reinterpret_cast<RowSums *>(kp + dp);
   ptx::griddep_wait();
-  const bool post_layer = a.post == FLASH_GAU_NORM_LAYER, layer = a.norm == FLASH_GAU_NORM_LAYER;
-  float pg[8], pb[8], sc[8], ng[8];
-  load_param<VEC>(post_layer ? a.post_g : nullptr, d, t, threads, a.post ? (post_layer ? 1.f : a.post_g[0]) : 1.f, pg);
-  load_param<VEC>(post_layer ? a.post_b : nullptr, d, t, threads, 0.f, pb);
-  load_param<VEC>(a.scale, d, t, threads, 1.f, sc);
-  load_param<VEC>(layer ? a.norm_g : nullptr, d, t, threads, a.norm ? (layer ? 1.f : a.norm_g[0]) : 1.f, ng);
-  float acc[kSums][8] = {};
-  const float wc = count[rows.warp], inv_d = 1.0f / (float)d;
-  const bool need_y = a.y && (a.post || a.gate || a.scale);
-  for (long long row0 = (long long)blockIdx.x * R; row0 < a.M; row0 += (long long)gridDim.x * R) {
-    Raw<T> x[R], y[R], gt[R], dn[R], dr[R];
+  for (int c = t; c < d; c += threads) {
+    ng[c] = a.norm ? a.norm_g[norm_layer ? c : 0] : 1.f;
+    kp[c] = (a.post ? a.post_g[post_layer ? c : 0] : 1.f) * (a.scale ? a.scale[c] : 1.f);
+  }
+  __syncthreads();
+  // this thread's columns: group g of four, and which share of a tile's rows
+  const int per = (d + 3) / 4;
+  const int lanes = NG == 1 ? per : threads;  // threads that have columns of their own
+  const int sub = t / lanes, own = t % lanes;
+  const bool active = sub < a.subsets;
+  const int stride = lanes;  // element-wise: between a group's columns
+  auto column = [&](int g) { return VEC ? 4 * (own + g * threads) : own + 4 * g * threads; };
+  float pg[NG][4], pb[NG][4], sc[NG][4], gn[NG][4], acc[kSums][NG][4];
 #pragma unroll
-    for (int k = 0; k < R; ++k) {
-      const long long row = min(row0 + k, a.M - 1);
-      if (a.norm) {
-        load_row<T, VEC>(a.h, row, d, t, threads, x[k]);
-        load_row<T, VEC>(a.dn, row, d, t, threads, dn[k]);
-      }
-      if (need_y) load_row<T, VEC>(a.y, row, d, t, threads, y[k]);
-      if (a.gate) load_row<T, VEC>(a.gate, row, d, t, threads, gt[k]);
-      if (a.dr) load_row<T, VEC>(a.dr, row, d, t, threads, dr[k]);
+  for (int g = 0; g < NG; ++g)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int c = VEC ? column(g) + q : column(g) + q * stride;
+      const bool in = active && c < d;
+      gn[g][q] = in ? ng[c] : 0.f;
+      sc[g][q] = in ? (a.scale ? a.scale[c] : 1.f) : 0.f;
+      pg[g][q] = in ? (a.post ? a.post_g[post_layer ? c : 0] : 1.f) : 0.f;
+      pb[g][q] = in && post_layer && a.post_b ? a.post_b[c] : 0.f;
+#pragma unroll
+      for (int s = 0; s < kSums; ++s) acc[s][g][q] = 0.f;
     }
-    Stat st[2 * R];  // of r, then of y
-    if (a.norm || a.post) {
-      float2 w[2 * R];
+  const float inv_d = 1.0f / (float)d;
+  for (long long row0 = (long long)blockIdx.x * a.rows; row0 < a.M;
+       row0 += (long long)gridDim.x * a.rows) {
+    const int rows = (int)(a.M - row0 < a.rows ? a.M - row0 : a.rows);
+    const int n = rows * d;
 #pragma unroll
-      for (int k = 0; k < R; ++k) {
-        float v[8];
-        w[k] = w[R + k] = make_float2(0.f, 0.f);
+    for (int k = 0; k < 5; ++k) {
+      if (!src[k]) continue;
+      const T *from = src[k] + row0 * d;
+      if (VEC) {
+        constexpr int W = 16 / sizeof(T);
+        for (int i = t * W; i < n; i += threads * W) cp_async16(tile[k] + i, from + i);
+      } else {
+        for (int i = t; i < n; i += threads) tile[k][i] = from[i];
+      }
+    }
+    if (VEC) cp_async_wait();
+    __syncthreads();
+    // ---- one warp a row: its sums
+    for (int k = warp; k < rows; k += warps) {
+      const T *x = tx + (size_t)k * d, *dn = tdn + (size_t)k * d, *dr = tdr + (size_t)k * d;
+      const T *y = ty + (size_t)k * d, *gt = tg + (size_t)k * d;
+      const int c0 = VEC ? 4 * lane : lane;
+      auto in = [&](int c, int q) { return VEC || c + 32 * q < d; };
+      RowSums s = {0.f, 1.f, 0.f, 0.f, 0.f, 1.f, 0.f, 0.f};
+      if (norm_layer || post_layer) {
+        float sr = 0.f, sy = 0.f;
+        for (int c = c0; c < d; c += 128) {
+          float v[4];
+          if (norm_layer) {
+            load4<VEC>(x, c, 32, d, v);
+            sr += (v[0] + v[1]) + (v[2] + v[3]);
+          }
+          if (post_layer) {
+            load4<VEC>(y, c, 32, d, v);
+            sy += (v[0] + v[1]) + (v[2] + v[3]);
+          }
+        }
+        if (norm_layer) s.mean_r = warp_sum(sr) * inv_d;
+        if (post_layer) s.mean_y = warp_sum(sy) * inv_d;
+      }
+      if (a.norm || a.post) {
+        float m2r = 0.f, m2y = 0.f, sw = 0.f, swx = 0.f;
+        for (int c = c0; c < d; c += 128) {
+          float v[4], g[4], w[4];
+          if (a.norm) {
+            load4<VEC>(x, c, 32, d, v);
+            load4<VEC>(dn, c, 32, d, g);
+            load4<VEC>(ng, c, 32, d, w);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const float e = in(c, q) ? v[q] - s.mean_r : 0.f;
+              m2r = fmaf(e, e, m2r);
+              w[q] *= g[q];
+              sw += w[q];
+              swx = fmaf(w[q], e, swx);
+            }
+          }
+          if (a.post) {
+            load4<VEC>(y, c, 32, d, v);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const float e = in(c, q) ? v[q] - s.mean_y : 0.f;
+              m2y = fmaf(e, e, m2y);
+            }
+          }
+        }
         if (a.norm) {
-#pragma unroll
-          for (int q = 0; q < 8; ++q) v[q] = x[k].get(q);
-          w[k] = warp_stat<VEC>(v, a.norm, wc, d, t, threads);
+          m2r = warp_sum(m2r);
+          s.inv_r = inv_spread(m2r, a.norm, d, a.eps);
+          swx = warp_sum(swx) * s.inv_r;
+          if (norm_layer) {
+            s.a_r = warp_sum(sw) * inv_d;
+            s.b_r = swx * inv_d;
+          } else {
+            s.b_r = sqrtf(m2r) > a.eps ? swx : 0.f;
+          }
         }
         if (a.post) {
+          m2y = warp_sum(m2y);
+          s.inv_y = inv_spread(m2y, a.post, d, a.eps);
+          float sg = 0.f, sgy = 0.f;
+          for (int c = c0; c < d; c += 128) {
+            float dh[4] = {0.f, 0.f, 0.f, 0.f}, v[4], g[4], w[4];
+            if (a.dr) load4<VEC>(dr, c, 32, d, dh);
+            if (a.norm) {
+              load4<VEC>(x, c, 32, d, v);
+              load4<VEC>(dn, c, 32, d, g);
+              load4<VEC>(ng, c, 32, d, w);
 #pragma unroll
-          for (int q = 0; q < 8; ++q) v[q] = y[k].get(q);
-          w[R + k] = warp_stat<VEC>(v, a.post, wc, d, t, threads);
-        }
-      }
-      join<R>(rows, w, a.norm, a.post, a.eps, st);
-    }
-    float dh[R][8];
-    if (a.norm) {
-      float2 w[2 * R], s[2 * R];
+              for (int q = 0; q < 4; ++q)
+                dh[q] += s.inv_r * (w[q] * g[q] - s.a_r - (v[q] - s.mean_r) * s.inv_r * s.b_r);
+            }
+            load4<VEC>(kp, c, 32, d, w);  // zero behind the row
+            load4<VEC>(y, c, 32, d, v);
+            if (a.gate) {
+              load4<VEC>(gt, c, 32, d, g);
 #pragma unroll
-      for (int k = 0; k < R; ++k) {
-        float s1 = 0.f, s2 = 0.f;
+              for (int q = 0; q < 4; ++q) w[q] *= g[q];
+            }
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          const float u = (x[k].get(q) - st[k].mean) * st[k].inv, g = dn[k].get(q) * ng[q];
-          s1 += g;
-          s2 = fmaf(g, u, s2);
-        }
-        w[k] = make_float2(layer ? warp_sum(s1) : 0.f, warp_sum(s2));
-        w[R + k] = make_float2(0.f, 0.f);
-        s[k] = make_float2(0.f, 0.f);
-      }
-      rows.exchange(w, [&](int, int k, float2 v) {
-        if (k < R) {
-          s[k].x += v.x;
-          s[k].y += v.y;
-        }
-      });
-#pragma unroll
-      for (int k = 0; k < R; ++k) {
-        const bool live = row0 + k < a.M;
-#pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          const float u = (x[k].get(q) - st[k].mean) * st[k].inv, g = dn[k].get(q);
-          dh[k][q] = norm_grad(u, g * ng[q], s[k], st[k], a.norm, inv_d);
-          if (a.dr) dh[k][q] += dr[k].get(q);
-          if (live && column<VEC>(t, threads, q) < d) {
-            acc[kNormG][q] = fmaf(g, u, acc[kNormG][q]);
-            acc[kNormB][q] += g;
+            for (int q = 0; q < 4; ++q) {
+              const float e = dh[q] * w[q];
+              sg += e;
+              sgy = fmaf(e, v[q] - s.mean_y, sgy);
+            }
+          }
+          sgy = warp_sum(sgy) * s.inv_y;
+          if (post_layer) {
+            s.a_y = warp_sum(sg) * inv_d;
+            s.b_y = sgy * inv_d;
+          } else {
+            s.b_y = sqrtf(m2y) > a.eps ? sgy : 0.f;
           }
         }
       }
-    } else {
-#pragma unroll
-      for (int k = 0; k < R; ++k)
-#pragma unroll
-        for (int q = 0; q < 8; ++q) dh[k][q] = a.dr ? dr[k].get(q) : 0.f;
+      if (lane == 0) sums[k] = s;
     }
+    __syncthreads();
+    // ---- four columns a thread and group: outputs and column sums
+    if (active) {
+      for (int k = sub; k < rows; k += a.subsets) {
+        const RowSums s = sums[k];
+        const long long out = (row0 + k) * d;
 #pragma unroll
-    for (int k = 0; k < R; ++k)
-      if (row0 + k < a.M) store_row<T, VEC>(a.dh, row0 + k, d, t, threads, dh[k]);
-    if (!a.dy) continue;
-    // dh becomes the gradient of post(y)
-    float2 w[2 * R], s[2 * R];
+        for (int g = 0; g < NG; ++g) {
+          const int c = column(g);
+          if (c >= d) continue;
+          float dh[4] = {0.f, 0.f, 0.f, 0.f}, v[4], e[4];
+          if (a.dr) load4<VEC>(tdr + (size_t)k * d, c, stride, d, dh);
+          if (a.norm) {
+            load4<VEC>(tx + (size_t)k * d, c, stride, d, v);
+            load4<VEC>(tdn + (size_t)k * d, c, stride, d, e);
 #pragma unroll
-    for (int k = 0; k < R; ++k) {
-      const bool live = row0 + k < a.M;
-      float s1 = 0.f, s2 = 0.f, dg[8];
+            for (int q = 0; q < 4; ++q) {
+              const float u = (v[q] - s.mean_r) * s.inv_r;
+              dh[q] += s.inv_r * (e[q] * gn[g][q] - s.a_r - u * s.b_r);
+              acc[kNormG][g][q] = fmaf(e[q], u, acc[kNormG][g][q]);
+              acc[kNormB][g][q] += e[q];
+            }
+          }
+          store4<VEC>(static_cast<T *>(a.dh) + out, c, stride, d, dh);
+          if (!a.dy) continue;
+          float gv[4] = {1.f, 1.f, 1.f, 1.f};
+          if (a.y) load4<VEC>(ty + (size_t)k * d, c, stride, d, v);
+          else v[0] = v[1] = v[2] = v[3] = 0.f;
+          if (a.gate) load4<VEC>(tg + (size_t)k * d, c, stride, d, gv);
 #pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        const bool in = live && column<VEC>(t, threads, q) < d;
-        float u = need_y ? y[k].get(q) : 0.f, p = u;
-        if (a.post) {
-          u = (u - st[R + k].mean) * st[R + k].inv;
-          p = fmaf(u, pg[q], pb[q]);
-        }
-        const float gv = a.gate ? gt[k].get(q) : 1.f;
-        dg[q] = dh[k][q] * p * sc[q];
-        if (in) acc[kScale][q] = fmaf(dh[k][q] * p, gv, acc[kScale][q]);
-        const float dp = dh[k][q] * gv * sc[q];
-        if (in) {
-          acc[kPostG][q] = fmaf(dp, u, acc[kPostG][q]);
-          acc[kPostB][q] += dp;
-        }
-        const float g = dp * pg[q];
-        dh[k][q] = g;
-        if (column<VEC>(t, threads, q) < d) {
-          s1 += g;
-          s2 = fmaf(g, u, s2);
+          for (int q = 0; q < 4; ++q) {
+            const float u = (v[q] - s.mean_y) * s.inv_y;
+            const float p = dh[q] * fmaf(u, pg[g][q], pb[g][q]);
+            acc[kScale][g][q] = fmaf(p, gv[q], acc[kScale][g][q]);
+            const float dp = dh[q] * gv[q] * sc[g][q];
+            acc[kPostG][g][q] = fmaf(dp, u, acc[kPostG][g][q]);
+            acc[kPostB][g][q] += dp;
+            v[q] = s.inv_y * (dp * pg[g][q] - s.a_y - u * s.b_y);
+            e[q] = p * sc[g][q];
+          }
+          if (a.dgate) store4<VEC>(static_cast<T *>(a.dgate) + out, c, stride, d, e);
+          store4<VEC>(static_cast<T *>(a.dy) + out, c, stride, d, v);
         }
       }
-      if (a.gate && live && a.dgate) store_row<T, VEC>(a.dgate, row0 + k, d, t, threads, dg);
-      w[R + k] = make_float2(0.f, 0.f);
-      s[k] = make_float2(0.f, 0.f);
-      if (a.post) w[k] = make_float2(post_layer ? warp_sum(s1) : 0.f, warp_sum(s2));
     }
-    if (a.post) {
-      rows.exchange(w, [&](int, int k, float2 v) {
-        if (k < R) {
-          s[k].x += v.x;
-          s[k].y += v.y;
-        }
-      });
-#pragma unroll
-      for (int k = 0; k < R; ++k)
-#pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          const float u = (y[k].get(q) - st[R + k].mean) * st[R + k].inv;
-          dh[k][q] = norm_grad(u, dh[k][q], s[k], st[R + k], a.post, inv_d);
-        }
-    }
-#pragma unroll
-    for (int k = 0; k < R; ++k)
-      if (row0 + k < a.M) store_row<T, VEC>(a.dy, row0 + k, d, t, threads, dh[k]);
+    __syncthreads();
   }
-  // this block's column sums
-  float *part = a.part + (long long)blockIdx.x * kSums * d;
+  // this thread's column sums, and the warps' sums for a ScaleNorm's g
+  if (active) {
+    float *part = a.part + ((long long)blockIdx.x * a.subsets + sub) * kSums * d;
 #pragma unroll
-  for (int s = 0; s < kSums; ++s)
+    for (int s = 0; s < kSums; ++s)
 #pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      const int c = column<VEC>(t, threads, q);
-      if (c < d) part[s * (long long)d + c] = acc[s][q];
-    }
+      for (int g = 0; g < NG; ++g)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int c = VEC ? column(g) + q : column(g) + q * stride;
+          if (c < d) part[s * (long long)d + c] = acc[s][g][q];
+        }
+  }
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    float v = 0.f;
+#pragma unroll
+    for (int g = 0; g < NG; ++g)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) v += acc[s ? kPostG : kNormG][g][q];
+    v = warp_sum(v);
+    if (lane == 0) a.scalar_part[((long long)s * gridDim.x + blockIdx.x) * kMaxWarps + warp] = v;
+  }
 }
 
 struct SumArgs {
-  const float *part;
+  const float *part, *scalar_part;
   float *out[kSums];    // null: not wanted
-  int scalar[kSums];    // the gradient of a single scalar: also summed over the columns
-  int blocks, d;
+  int scalar[kSums];    // a ScaleNorm's g: one value
+  int parts, blocks, warps, d;
 };
 
-// Sums the blocks' parts in a fixed order: a thread block takes 32 columns of
-// one kind (blockIdx.y), 8 threads a column; a scalar's gradient one thread
-// block for all its columns.
-__global__ void __launch_bounds__(256) sum_parts_kernel(const SumArgs a) {
+// Sums the parts in a fixed order: a thread block takes 32 columns of one
+// kind (blockIdx.y), 32 threads a column.
+__global__ void __launch_bounds__(1024) sum_parts_kernel(const SumArgs a) {
   ptx::griddep_wait();
   const int s = blockIdx.y;
   if (!a.out[s] || (a.scalar[s] && blockIdx.x)) return;
-  __shared__ float buf[8][32];
+  __shared__ float buf[32][33];
   const int lane = threadIdx.x & 31, sub = threadIdx.x >> 5;
-  float total = 0.f;
-  for (int c0 = blockIdx.x * 32; c0 < a.d; c0 += a.scalar[s] ? 32 : a.d) {
-    const int c = c0 + lane;
-    float v = 0.f;
-    if (c < a.d)
-      for (int b = sub; b < a.blocks; b += 8) v += a.part[((long long)b * kSums + s) * a.d + c];
-    total += v;
-  }
-  buf[sub][lane] = total;
-  __syncthreads();
-  if (sub) return;
+  const int c = blockIdx.x * 32 + lane;
   float v = 0.f;
-#pragma unroll
-  for (int k = 0; k < 8; ++k) v += buf[k][lane];
   if (a.scalar[s]) {
-    v = warp_sum(v);
-    if (lane == 0) a.out[s][0] = v;
-  } else if (blockIdx.x * 32 + lane < a.d) {
-    a.out[s][blockIdx.x * 32 + lane] = v;
+    const float *p = a.scalar_part + (s == kPostG ? (long long)a.blocks * kMaxWarps : 0);
+    if (lane < a.warps)
+      for (int b = sub; b < a.blocks; b += 32) v += p[(long long)b * kMaxWarps + lane];
+  } else if (c < a.d) {
+    const float *p = a.part + (long long)s * a.d + c;
+    const long long step = (long long)kSums * a.d;
+#pragma unroll 4
+    for (int b = sub; b < a.parts; b += 32) v += p[b * step];
+  }
+  buf[lane][sub] = v;
+  __syncthreads();
+  // warp w joins column w
+  v = warp_sum(buf[sub][lane]);
+  if (a.scalar[s]) {
+    __syncthreads();
+    if (lane == 0) buf[0][sub] = v;
+    __syncthreads();
+    if (sub == 0) {
+      v = warp_sum(buf[0][lane]);
+      if (lane == 0) a.out[s][0] = v;
+    }
+  } else if (lane == 0 && blockIdx.x * 32 + sub < a.d) {
+    a.out[s][blockIdx.x * 32 + sub] = v;
   }
 }
 
 bool aligned16(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
-constexpr int kRows = 2;  // rows a block takes at a time
-
-int threads_of(int d) { return (d + 32 * kCols - 1) / (32 * kCols) * 32; }
-
-template <typename T, int VEC, int R, int MAXT>
-cudaError_t launch(const Args &a, bool grad, int blocks, cudaStream_t stream) {
-  const dim3 grid(blocks), block(threads_of(a.d));
-  return grad ? launch_pdl(residual_norm_grad_kernel<T, VEC, R, MAXT>, grid, block, 0, stream, a)
-              : launch_pdl(residual_norm_kernel<T, VEC, R, MAXT>, grid, block, 0, stream, a);
-}
-
-template <typename T, int VEC>
-cudaError_t dispatch(const Args &a, bool grad, int blocks, cudaStream_t stream) {
-  if (threads_of(a.d) <= 128) return launch<T, VEC, kRows, 128>(a, grad, blocks, stream);
-  return launch<T, VEC, 1, 32 * kMaxWarps>(a, grad, blocks, stream);
-}
-
-cudaError_t run(const Args &a, bool grad, int dtype, int blocks, cudaStream_t stream) {
-  const bool bf16 = dtype == FLASH_GAU_BF16;
-  bool vec = a.d % (bf16 ? 8 : 4) == 0;
+// the accesses of 16 bytes that rows allow
+bool vectors(const Args &a, int io) {
+  bool vec = (long long)a.d * io % 16 == 0;
   for (const void *p : {a.h, a.y, a.gate, a.dr, a.dn, (const void *)a.r, (const void *)a.n,
                         (const void *)a.dh, (const void *)a.dy, (const void *)a.dgate})
     vec = vec && aligned16(p);
-  if (bf16)
-    return vec ? dispatch<__nv_bfloat16, 8>(a, grad, blocks, stream)
-               : dispatch<__nv_bfloat16, 1>(a, grad, blocks, stream);
-  return vec ? dispatch<float, 4>(a, grad, blocks, stream)
-             : dispatch<float, 1>(a, grad, blocks, stream);
+  return vec;
+}
+
+template <typename T>
+cudaError_t forward(const Args &a, cudaStream_t stream) {
+  // a warp a row: few rows go to as many SMs as there are
+  const int warps = a.M <= kResidualMaxBlocks ? 1 : 4;
+  const dim3 grid((unsigned)((a.M + warps - 1) / warps)), block(32 * warps);
+  const int chunks = (a.d + 255) / 256;
+  if (!vectors(a, sizeof(T)) || chunks > 8)
+    return launch_pdl(residual_norm_any_kernel<T>, grid, block, 0, stream, a);
+  switch (chunks) {
+    case 1: return launch_pdl(residual_norm_kernel<T, 1>, grid, block, 0, stream, a);
+    case 2: return launch_pdl(residual_norm_kernel<T, 2>, grid, block, 0, stream, a);
+    case 3: return launch_pdl(residual_norm_kernel<T, 3>, grid, block, 0, stream, a);
+    case 4: return launch_pdl(residual_norm_kernel<T, 4>, grid, block, 0, stream, a);
+    case 5:
+    case 6: return launch_pdl(residual_norm_kernel<T, 6>, grid, block, 0, stream, a);
+    default: return launch_pdl(residual_norm_kernel<T, 8>, grid, block, 0, stream, a);
+  }
+}
+
+// The backward's shape: four columns a thread (a group), up to 256 threads
+// with up to four groups each, 512 above 4096 columns; narrow rows share a
+// block of 128 threads among `subsets` rows.
+struct Shape {
+  int groups, threads, subsets;
+};
+Shape shape_of(int d) {
+  const int per = (d + 3) / 4;
+  Shape s;
+  s.groups = per <= 256 ? 1 : per <= 512 ? 2 : 4;
+  const int t = ((per + s.groups - 1) / s.groups + 31) / 32 * 32;
+  s.threads = t < 128 ? 128 : t;
+  s.subsets = s.groups == 1 ? s.threads / per : 1;
+  return s;
+}
+
+template <typename T, bool VEC, int NG, int MAXT>
+cudaError_t launch_grad(const Args &a, const Shape &s, int blocks, size_t smem, cudaStream_t stream) {
+  auto kernel = residual_norm_grad_kernel<T, VEC, NG, MAXT>;
+  static size_t allowed[64];  // per device: the largest set so far
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (smem > 48 * 1024 && allowed[dev] == 0) {
+    // the most that any call asks for
+    err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kGradSmemMax);
+    if (err != cudaSuccess) return err;
+    allowed[dev] = kGradSmemMax;
+  }
+  return launch_pdl(kernel, dim3(blocks), dim3(s.threads), smem, stream, a);
+}
+
+template <typename T, bool VEC>
+cudaError_t backward(Args &a, int num_sms, int *blocks_out, cudaStream_t stream) {
+  const Shape s = shape_of(a.d);
+  int arrays = 0;
+  for (const void *p : {a.norm ? a.h : nullptr, a.dn, a.dr, a.y, a.gate}) arrays += p != nullptr;
+  const size_t row = (size_t)arrays * a.d * sizeof(T);
+  // rows of a tile: one for each warp while four blocks fit an SM, more of
+  // narrow rows, and of wide ones half as many as warps where that fits at all
+  const int warps = s.threads / 32;
+  long long rows = (44 * 1024) / (long long)(row ? row : 1);
+  if (rows > 4 * warps) rows = 4 * warps;
+  if (rows > warps) rows = rows / warps * warps;
+  const long long few = (warps + 1) / 2;
+  if (rows < few) rows = few * (long long)row <= 160 * 1024 ? few : (160 * 1024) / (long long)row;
+  if (rows < 1) rows = 1;
+  // few rows in all: spread them over the SMs
+  const long long even = (a.M + num_sms - 1) / num_sms;
+  if (rows > even) rows = even;
+  a.rows = (int)rows;
+  a.subsets = s.subsets;
+  const size_t pitch = ((size_t)rows * a.d * sizeof(T) + 15) / 16 * 16;
+  const size_t smem = pitch * arrays + (size_t)((a.d + 3) / 4 * 4) * 8 + rows * sizeof(RowSums);
+  const long long tiles = (a.M + rows - 1) / rows;
+  long long per_sm = (long long)(224 * 1024 / (smem + 1024));
+  if (per_sm > 2048 / s.threads) per_sm = 2048 / s.threads;
+  if (per_sm < 1) per_sm = 1;
+  if (per_sm > 4) per_sm = 4;
+  long long blocks = per_sm * num_sms;
+  if (blocks > kResidualMaxBlocks) blocks = kResidualMaxBlocks;
+  if (blocks > tiles) blocks = tiles;
+  *blocks_out = (int)blocks;
+  a.scalar_part = a.part + (long long)blocks * s.subsets * kSums * a.d;
+  if (s.groups == 1) return launch_grad<T, VEC, 1, 256>(a, s, (int)blocks, smem, stream);
+  if (s.groups == 2) return launch_grad<T, VEC, 2, 256>(a, s, (int)blocks, smem, stream);
+  if (s.threads <= 256) return launch_grad<T, VEC, 4, 256>(a, s, (int)blocks, smem, stream);
+  return launch_grad<T, VEC, 4, 512>(a, s, (int)blocks, smem, stream);
 }
 
 Args args_of(const ResidualProblem &q) {
@@ -612,10 +770,9 @@ Args args_of(const ResidualProblem &q) {
 
 }  // namespace
 
-int residual_norm_blocks(long long M, int d) {
-  const int rows = threads_of(d) <= 128 ? kRows : 1;
-  const long long n = (M + rows - 1) / rows;
-  return (int)(n < kResidualMaxBlocks ? n : kResidualMaxBlocks);
+size_t residual_norm_part_bytes(long long M, int d) {
+  const size_t blocks = (size_t)(M < kResidualMaxBlocks ? M : kResidualMaxBlocks);
+  return (blocks * shape_of(d).subsets * kSums * d + 2 * blocks * kMaxWarps) * sizeof(float);
 }
 
 cudaError_t residual_norm(const ResidualProblem &q, const void *h, void *r, void *n) {
@@ -623,10 +780,8 @@ cudaError_t residual_norm(const ResidualProblem &q, const void *h, void *r, void
   a.h = h;
   a.r = r;
   a.n = n;
-  const int rows = threads_of(q.d) <= 128 ? kRows : 1;
-  const long long blocks = (q.M + rows - 1) / rows;
-  const int most = q.num_sms * (2048 / threads_of(q.d) < 8 ? 2048 / threads_of(q.d) : 8);
-  return run(a, false, q.dtype, (int)(blocks < most ? blocks : most), q.stream);
+  return q.dtype == FLASH_GAU_BF16 ? forward<__nv_bfloat16>(a, q.stream)
+                                   : forward<float>(a, q.stream);
 }
 
 cudaError_t residual_norm_grad(const ResidualProblem &q, const void *dr, const void *dn,
@@ -639,12 +794,22 @@ cudaError_t residual_norm_grad(const ResidualProblem &q, const void *dr, const v
   a.dy = g.dy;
   a.dgate = g.dgate;
   a.part = static_cast<float *>(workspace);
-  const int blocks = residual_norm_blocks(q.M, q.d);
-  cudaError_t err = run(a, true, q.dtype, blocks, q.stream);
+  if (!a.post && !a.gate && !a.scale) a.y = nullptr;  // nothing needs its values
+  int blocks = 0;
+  cudaError_t err;
+  if (q.dtype == FLASH_GAU_BF16)
+    err = vectors(a, 2) ? backward<__nv_bfloat16, true>(a, q.num_sms, &blocks, q.stream)
+                        : backward<__nv_bfloat16, false>(a, q.num_sms, &blocks, q.stream);
+  else
+    err = vectors(a, 4) ? backward<float, true>(a, q.num_sms, &blocks, q.stream)
+                        : backward<float, false>(a, q.num_sms, &blocks, q.stream);
   if (err != cudaSuccess) return err;
   SumArgs s = {};
   s.part = a.part;
+  s.scalar_part = a.scalar_part;
+  s.parts = blocks * a.subsets;
   s.blocks = blocks;
+  s.warps = shape_of(q.d).threads / 32;
   s.d = q.d;
   s.out[kNormG] = a.norm ? g.dnorm_g : nullptr;
   s.out[kNormB] = a.norm == FLASH_GAU_NORM_LAYER ? g.dnorm_b : nullptr;
@@ -656,7 +821,7 @@ cudaError_t residual_norm_grad(const ResidualProblem &q, const void *dr, const v
   bool any = false;
   for (const float *p : s.out) any = any || p;
   if (!any) return cudaSuccess;
-  return launch_pdl(sum_parts_kernel, dim3((q.d + 31) / 32, kSums), dim3(256), 0, q.stream, s);
+  return launch_pdl(sum_parts_kernel, dim3((q.d + 31) / 32, kSums), dim3(1024), 0, q.stream, s);
 }
 
 }  // namespace flashgau

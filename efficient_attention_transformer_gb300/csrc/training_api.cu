@@ -54,7 +54,7 @@ int check_residual(const flash_gau_residual *o, long long M, int d, int dtype) {
   int st = check_norm(o->post, o->post_g, o->post_b);
   if (st == FLASH_GAU_OK) st = check_norm(o->norm, o->norm_g, o->norm_b);
   if (st != FLASH_GAU_OK) return st;
-  if (d > kResidualMaxD || M > (1LL << 40)) return FLASH_GAU_ENOTSUP;
+  if (d > kResidualMaxD || M > (1LL << 32)) return FLASH_GAU_ENOTSUP;
   return FLASH_GAU_OK;
 }
 
@@ -181,8 +181,8 @@ int flash_gau_residual_norm(const void *h, const void *y, const flash_gau_residu
 }
 
 size_t flash_gau_residual_norm_backward_workspace_bytes(long long M, int d) {
-  if (M <= 0 || d <= 0 || d > kResidualMaxD || M > (1LL << 40)) return 0;
-  const size_t n = (size_t)residual_norm_blocks(M, d) * 5 * d * sizeof(float);
+  if (M <= 0 || d <= 0 || d > kResidualMaxD || M > (1LL << 32)) return 0;
+  const size_t n = residual_norm_part_bytes(M, d);
   return (n + kAlign - 1) / kAlign * kAlign;
 }
 

@@ -411,8 +411,8 @@ int flash_gau_xent(const void *X, const void *W, const int *labels, long long N,
  * h is the stream before the block and y the block's output; post and norm
  * are FLASH_GAU_NORM_* of the flash_block wrapper, with the same formulas.
  * n is taken from r before its rounding to the io type.  Row statistics are
- * fp32.  All rows have d columns; any 1 <= d <= 4096 (larger:
- * FLASH_GAU_ENOTSUP), rows and arrays need only their element's alignment
+ * fp32.  All rows have d columns; any 1 <= d <= 8192 and
+ * 1 <= M <= 2^32 (more: FLASH_GAU_ENOTSUP), rows and arrays need only their element's alignment
  * (16-byte aligned arrays and d a multiple of 16 bytes run fastest).       */
 typedef struct flash_gau_residual {
   int post;             /* norm of the block's output, FLASH_GAU_NORM_*      */

@@ -3,13 +3,15 @@ the same io-typed inputs.
 
 Bounds, element by element, with u = 2^-24 and the io rounding of half a step
 (2^-8 of the value for bf16, u for fp32).  A row sum of the kernel is at most
-8 additions in a thread, 5 shuffles and 16 warps behind one another: its
-error is under 40 u of the sum of magnitudes, and so is that of what is
-formed from a few of them.  With s = 1 / spread of a row, a normalised value
-u_j is off by at most 40 u (|u_j| + s (|x_j| + mean|x|)) =: e_j.  What a
-gradient is formed of enters with the same 40 u of its terms' magnitudes and
-with e_j where it reads u_j.  Column sums add rows one after another in a
-block (at most rows / 608 + 2 of them), then an eighth of the blocks' parts."""
+d / 32 additions in a lane (fewer in a tree) and 5 shuffles behind one
+another: its error is under (d / 32 + 32) u =: k u of the sum of magnitudes,
+and so is that of what is formed from a few of them.  With s = 1 / spread of
+a row, a normalised value u_j is off by at most
+k u (|u_j| + s (|x_j| + mean|x|)) =: e_j.  What a gradient is formed of enters
+with the same k u of its terms' magnitudes and with e_j where it reads u_j.
+Column sums add rows one after another in a thread (rows / 608 of them, and a
+tile of up to 64), then a 32nd of the threads' parts behind one another: 608
+blocks of 128 / (d / 4) threads a column, one where d is wider."""
 
 import itertools
 
@@ -76,7 +78,7 @@ def unit_error(x, kind, eps):
     u, s, _ = oracle.norm_rows(x, kind, 1.0, None, eps)
     if kind == "none":
         return np.zeros_like(u), u, s
-    return 40 * U * (np.abs(u) + s * (np.abs(x) + np.abs(x).mean(1, keepdims=True))), u, s
+    return (x.shape[1] / 32 + 32) * U * (np.abs(u) + s * (np.abs(x) + np.abs(x).mean(1, keepdims=True))), u, s
 
 
 def within(name, got, want, bound):
@@ -127,8 +129,8 @@ def grad_error(x, kind, g, dout, edout, eps):
     au = np.abs(u)
     base = w + au * mean(w * au) + (mean(w) if kind == "layer" else 0.0)
     err = ew + mean(ew) * (kind == "layer") + au * mean(ew * au + w * e) + e * mean(w * au)
-    # the sums', the products' and s's own roundings: 80 u of the terms
-    return s * (80 * U * base + err), edout * au + np.abs(dout) * (e + 4 * U * au)
+    # the sums', the products' and s's own roundings: 2 k u of the terms
+    return s * (2 * (x.shape[1] / 32 + 32) * U * base + err), edout * au + np.abs(dout) * (e + 4 * U * au)
 
 
 def check_backward(p):
@@ -138,7 +140,7 @@ def check_backward(p):
     dr, r, y = f64(p.dr), f64(p.h), f64(p.y)
     dn = f64(p.dn) if p.norm != "none" else None
     want = oracle.residual_norm_grad(dr, dn, r, y, **q)
-    adds = p.M / 608 + 2 + 608 / 8 + 8
+    adds = min(p.M, p.M / 608 + 64 + 608 / 32 * max(1, 128 // -(-p.d // 4))) + 40
     col = lambda terms, err: err.sum(0) + adds * U * np.abs(terms).sum(0)  # noqa: E731
     edh = 4 * U * np.abs(dr)
     if p.norm != "none":
@@ -181,7 +183,8 @@ def check_backward(p):
 
 
 SIZES = [(1, 768), (2, 1), (3, 5), (7, 31), (64, 64), (5, 257), (130, 768), (33, 1001), (9, 1032),
-         (3, 2048), (2, 4096), (2, 4095), (1300, 40)]
+         (3, 2048), (2, 4096), (2, 4095), (1300, 40), (700, 3), (40, 2056), (17, 8192), (9, 8191),
+         (5, 6000), (400, 1536)]
 
 
 @pytest.mark.parametrize("dtype", ["fp32", "bf16"])
@@ -315,7 +318,7 @@ def test_refusals():
     with pytest.raises(bd.FlashGauError):
         bd.residual_norm(p.h, p.y, out_r=p.h, out_n=p.h, norm_g=p.kw["norm_g"])
     with pytest.raises(bd.FlashGauError):
-        wide = torch.zeros(1, 4104, dtype=torch.bfloat16, device="cuda")
+        wide = torch.zeros(1, 8200, dtype=torch.bfloat16, device="cuda")
         bd.residual_norm(wide, None, norm=bd.NORM_SCALE, norm_g=torch.ones(1, device="cuda"))
     with pytest.raises(bd.FlashGauError):
         empty = torch.zeros(0, 16, dtype=torch.bfloat16, device="cuda")

@@ -143,7 +143,7 @@ def _residual(**kw):
     (dict(), dict(h=None), bd.EINVAL),
     (dict(), dict(M=0), bd.EINVAL),
     (dict(), dict(d=0), bd.EINVAL),
-    (dict(), dict(d=4097), bd.ENOTSUP),
+    (dict(), dict(d=8193), bd.ENOTSUP),
     (dict(), dict(dtype=2), bd.EINVAL),
     (dict(norm=3), dict(), bd.EINVAL),
     (dict(post=-1), dict(), bd.EINVAL),
@@ -189,7 +189,7 @@ def test_residual_norm_refuses(L, opts, args, code):
     (dict(), dict(ws=1 << 40 | 8), bd.EWORKSPACE),
     (dict(), dict(wsb=100), bd.EWORKSPACE),
     (dict(), dict(ws=E_), bd.EINVAL),                           # the workspace is dh
-    (dict(), dict(d=5000), bd.ENOTSUP),
+    (dict(), dict(d=9000), bd.ENOTSUP),
 ])
 def test_residual_norm_backward_refuses(L, opts, args, code):
     a = dict(dr=A, dn=B, r=C, y=D, M=10, d=64, dtype=bd.BF16, dh=E_, dy=7 << 32, ws=1 << 40,
@@ -205,8 +205,8 @@ def test_residual_norm_backward_refuses(L, opts, args, code):
 
 def test_residual_norm_backward_workspace(L):
     f = L.flash_gau_residual_norm_backward_workspace_bytes
-    assert f(0, 64) == 0 and f(4, 0) == 0 and f(4, 4097) == 0
-    assert f(1, 1) >= 20 and f(1 << 30, 4096) <= 608 * 5 * 4096 * 4
+    assert f(0, 64) == 0 and f(4, 0) == 0 and f(4, 8193) == 0
+    assert f(1, 1) >= 20 and f(1 << 30, 4096) <= 608 * (5 * 4096 + 32) * 4
 
 
 def _tensor(**kw):
