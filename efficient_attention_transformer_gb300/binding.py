@@ -6,7 +6,6 @@ of the computation runs in the library's CUDA kernels.  Loading fails loudly
 when the library has not been built.
 """
 
-import contextlib
 import ctypes
 import os
 
@@ -569,41 +568,52 @@ class Decoder:
         return out
 
 
+def _elsewhere(device, stream):
+    """Whether a call on `device` needs _scope: a stream of its own, or another
+    device than the current one."""
+    return stream is not None or device.index != torch.cuda.current_device()
+
+
 def _scope(device, stream):
     """Context of one call on `device`: the device is current, and where a
     stream is given it is too, so that what the call allocates belongs to it."""
-    if stream is not None:
-        return torch.cuda.stream(stream)
-    if torch.cuda.current_device() != device.index:
-        return torch.cuda.device(device)
-    return contextlib.nullcontext()
+    return torch.cuda.stream(stream) if stream is not None else torch.cuda.device(device)
 
 
-def _rows(t, name, like):
-    """Pointer of a tensor of rows that has to be as `like` is, or None."""
+def _stream(device):
+    """The current stream of the device, as the library takes it."""
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+def _like(t, name, shape, dtype, index):
+    """Pointer of a tensor of this shape and type on device `index`, or None."""
     if t is None:
         return None
-    if t.shape != like.shape or t.device != like.device:
-        raise ValueError("%s must have the shape and device of the stream" % name)
-    return _dev_ptr(t, name, like.dtype)
+    if t.shape != shape or t.dtype != dtype or t.get_device() != index:
+        raise ValueError("%s must be %s %s on device %d" % (name, tuple(shape), dtype, index))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    return t.data_ptr()
 
 
-def _param(t, name, n, device):
+def _param(t, name, n, index):
+    """Pointer of n fp32 values on device `index`, or None."""
     if t is None:
         return None
-    if t.numel() != n or t.device != device:
-        raise ValueError("%s must hold %d values on %s" % (name, n, device))
+    if t.numel() != n or t.get_device() != index:
+        raise ValueError("%s must hold %d values on device %d" % (name, n, index))
     return _dev_ptr(t, name, torch.float32)
 
 
-def _residual(like, post_norm, post_g, post_b, gate, scale, norm, norm_g, norm_b, eps):
-    d, dev = like.shape[-1], like.device
-    return Residual(int(post_norm), int(norm),
-                    _param(post_g, "post_g", d if post_norm == NORM_LAYER else 1, dev),
-                    _param(post_b, "post_b", d, dev),
-                    _param(norm_g, "norm_g", d if norm == NORM_LAYER else 1, dev),
-                    _param(norm_b, "norm_b", d, dev), _param(scale, "scale", d, dev),
-                    _rows(gate, "gate", like), float(eps))
+def _residual(shape, dtype, index, post_norm, post_g, post_b, gate, scale, norm, norm_g, norm_b,
+              eps):
+    d = shape[-1]
+    return Residual(post_norm, norm,
+                    _param(post_g, "post_g", d if post_norm == NORM_LAYER else 1, index),
+                    _param(post_b, "post_b", d, index),
+                    _param(norm_g, "norm_g", d if norm == NORM_LAYER else 1, index),
+                    _param(norm_b, "norm_b", d, index), _param(scale, "scale", d, index),
+                    _like(gate, "gate", shape, dtype, index), eps)
 
 
 def residual_norm(h, y=None, post_norm=NORM_NONE, post_g=None, post_b=None, gate=None, scale=None,
@@ -613,20 +623,28 @@ def residual_norm(h, y=None, post_norm=NORM_NONE, post_g=None, post_b=None, gate
     flash_gau_residual_norm.  h, y, gate: [..., d] in one io type; scale and
     the norms' parameters fp32 ([d], a ScaleNorm's g [1]).  Without y only the
     norm is taken and r is h; with norm NORM_NONE n is None."""
-    dt = dtype_code(h.dtype)
-    o = _residual(h, post_norm, post_g, post_b, gate, scale, norm, norm_g, norm_b, eps)
-    hp = _dev_ptr(h, "h", h.dtype)
-    d = h.shape[-1]
-    with _scope(h.device, stream):
-        if out_r is None and y is not None:
-            out_r = torch.empty_like(h)
-        if out_n is None and norm != NORM_NONE:
-            out_n = torch.empty_like(h)
-        sp = torch.cuda.current_stream(h.device).cuda_stream
-        _check(lib().flash_gau_residual_norm(
-            hp, _rows(y, "y", h), ctypes.byref(o), h.numel() // max(d, 1), d, dt,
-            _rows(out_r, "out_r", h), _rows(out_n, "out_n", h), sp))
+    shape, dtype = h.shape, h.dtype
+    dt, hp, dev = dtype_code(dtype), _dev_ptr(h, "h"), h.device
+    if _elsewhere(dev, stream):
+        with _scope(dev, stream):
+            return residual_norm(h, y, post_norm, post_g, post_b, gate, scale, norm, norm_g,
+                                 norm_b, eps, out_r, out_n)
+    at = dev.index
+    o = _residual(shape, dtype, at, post_norm, post_g, post_b, gate, scale, norm, norm_g, norm_b,
+                  eps)
+    if out_r is None and y is not None:
+        out_r = torch.empty_like(h)
+    if out_n is None and norm != NORM_NONE:
+        out_n = torch.empty_like(h)
+    d = shape[-1]
+    _check(lib().flash_gau_residual_norm(
+        hp, _like(y, "y", shape, dtype, at), o, h.numel() // max(d, 1), d, dt,
+        _like(out_r, "out_r", shape, dtype, at), _like(out_n, "out_n", shape, dtype, at),
+        _stream(dev)))
     return (h if out_r is None else out_r), out_n
+
+
+_GRADS = ("dh", "dy", "dgate", "dscale", "dpost_g", "dpost_b", "dnorm_g", "dnorm_b")
 
 
 def residual_norm_backward(dr, dn, r, y, post_norm=NORM_NONE, post_g=None, post_b=None, gate=None,
@@ -641,40 +659,45 @@ def residual_norm_backward(dr, dn, r, y, post_norm=NORM_NONE, post_g=None, post_
     like = dr if dr is not None else dn
     if like is None:
         raise ValueError("one of dr and dn must be given")
-    dt = dtype_code(like.dtype)
+    shape, dtype, dev = like.shape, like.dtype, like.device
+    dt = dtype_code(dtype)
     _dev_ptr(like, "dr" if dr is not None else "dn")
-    o = _residual(like, post_norm, post_g, post_b, gate, scale, norm, norm_g, norm_b, eps)
-    d = like.shape[-1]
+    if _elsewhere(dev, stream):
+        with _scope(dev, stream):
+            return residual_norm_backward(dr, dn, r, y, post_norm, post_g, post_b, gate, scale,
+                                          norm, norm_g, norm_b, eps, out, workspace)
+    at, f32, d = dev.index, torch.float32, shape[-1]
+    o = _residual(shape, dtype, at, post_norm, post_g, post_b, gate, scale, norm, norm_g, norm_b,
+                  eps)
     M = like.numel() // max(d, 1)
-    f32, dev = torch.float32, like.device
-    out = dict(out or {})
-    with _scope(dev, stream):
-        for name, there in (("dh", True), ("dy", y is not None), ("dgate", gate is not None)):
-            if out.get(name) is None:
-                out[name] = torch.empty_like(like) if there else None
-        for name, there, n in (("dscale", scale is not None, d),
-                               ("dpost_g", post_norm, d if post_norm == NORM_LAYER else 1),
-                               ("dpost_b", post_norm == NORM_LAYER, d),
-                               ("dnorm_g", norm, d if norm == NORM_LAYER else 1),
-                               ("dnorm_b", norm == NORM_LAYER, d)):
-            if out.get(name) is None:
-                out[name] = torch.empty(n, dtype=f32, device=dev) if there else None
-            elif not there or out[name].numel() != n:
-                raise ValueError("%s must hold the gradient of its parameter" % name)
-        g = ResidualGrads(*(_rows(out[k], k, like) for k in ("dh", "dy", "dgate")),
-                          *(None if out[k] is None else _dev_ptr(out[k], k, f32)
-                            for k in ("dscale", "dpost_g", "dpost_b", "dnorm_g", "dnorm_b")))
-        n = lib().flash_gau_residual_norm_backward_workspace_bytes(M, d)
-        if n == 0:
-            raise FlashGauError(ENOTSUP if M > 0 and d > 0 else EINVAL,
-                                "invalid or unsupported problem")
-        if workspace is None:
-            workspace = torch.empty(n, dtype=torch.uint8, device=dev)
-        sp = torch.cuda.current_stream(dev).cuda_stream
-        _check(lib().flash_gau_residual_norm_backward(
-            _rows(dr, "dr", like), _rows(dn, "dn", like), _rows(r, "r", like),
-            _rows(y, "y", like), ctypes.byref(o), M, d, dt, ctypes.byref(g),
-            _dev_ptr(workspace, "workspace"), workspace.numel() * workspace.element_size(), sp))
+    nw = lib().flash_gau_residual_norm_backward_workspace_bytes(M, d)
+    if nw == 0:
+        raise FlashGauError(ENOTSUP if M > 0 and d > 0 else EINVAL, "invalid or unsupported problem")
+    given, out = out or {}, dict.fromkeys(_GRADS)
+    out.update(given)
+    # what is not given: the rows one by one, the parameters' gradients and the
+    # workspace as parts of one array
+    for name, there in (("dh", True), ("dy", y is not None), ("dgate", gate is not None)):
+        if there and out[name] is None:
+            out[name] = torch.empty_like(like)
+    sizes = (d if scale is not None else 0,
+             (0, d, 1)[post_norm] if 0 <= post_norm < 3 else 0, d if post_norm == NORM_LAYER else 0,
+             (0, d, 1)[norm] if 0 <= norm < 3 else 0, d if norm == NORM_LAYER else 0)
+    made = [(name, n) for name, n in zip(_GRADS[3:], sizes) if n and out[name] is None]
+    if made:
+        parts = torch.empty(sum([n for _, n in made]), dtype=f32, device=dev)
+        for (name, _), part in zip(made, parts.split_with_sizes([n for _, n in made])):
+            out[name] = part
+    if workspace is None:
+        workspace = torch.empty(nw, dtype=torch.uint8, device=dev)
+    else:
+        nw = workspace.numel() * workspace.element_size()
+    g = ResidualGrads(*[_like(out[k], k, shape, dtype, at) for k in _GRADS[:3]],
+                      *[_param(out[k], k, n, at) for k, n in zip(_GRADS[3:], sizes)])
+    _check(lib().flash_gau_residual_norm_backward(
+        _like(dr, "dr", shape, dtype, at), _like(dn, "dn", shape, dtype, at),
+        _like(r, "r", shape, dtype, at), _like(y, "y", shape, dtype, at), o, M, d, dt, g,
+        _dev_ptr(workspace, "workspace"), nw, _stream(dev)))
     return out
 
 
@@ -703,27 +726,28 @@ def xent(X, W, labels, reduction=MEAN, scale=1.0, grad=True, out=None, workspace
     N, dev = labels.numel(), X.device
     if W.device != dev or labels.device != dev:
         raise ValueError("X, W and labels must be on one device")
+    if _elsewhere(dev, stream):
+        with _scope(dev, stream):
+            return xent(X, W, labels, reduction, scale, grad, out, workspace)
     f32 = torch.float32
-    out = dict(out or {})
-    with _scope(dev, stream):
-        for name, shape, dtype in (("total", (), f32), ("loss", labels.shape, f32),
-                                   ("lse", labels.shape, f32), ("dX", X.shape, X.dtype),
-                                   ("dW", W.shape, X.dtype)):
-            if name[0] == "d" and not grad:
-                out[name] = None
-            elif out.get(name) is None:
-                out[name] = torch.empty(shape, dtype=dtype, device=dev)
-            elif out[name].shape != shape or out[name].device != dev:
-                raise ValueError("%s must be %s on %s" % (name, tuple(shape), dev))
-        o = XentOut(*(_dev_ptr(out[k], k, f32) for k in ("total", "loss", "lse")),
-                    *(_dev_ptr(out[k], k, X.dtype) if grad else None for k in ("dX", "dW")))
-        if workspace is None:
-            workspace = torch.empty(xent_workspace_bytes(N, d, V, dt, grad), dtype=torch.uint8,
-                                    device=dev)
-        sp = torch.cuda.current_stream(dev).cuda_stream
-        _check(lib().flash_gau_xent(
-            xp, wp, lp, N, d, V, dt, int(reduction), float(scale), ctypes.byref(o),
-            _dev_ptr(workspace, "workspace"), workspace.numel() * workspace.element_size(), sp))
+    out, ptrs = dict(out or ()), []
+    for name, like, dtype in (("total", None, f32), ("loss", labels, f32), ("lse", labels, f32),
+                              ("dX", X, X.dtype), ("dW", W, X.dtype)):
+        t, shape = out.get(name), () if like is None else like.shape
+        if name[0] == "d" and not grad:
+            t = out[name] = None
+        elif t is None:
+            t = out[name] = torch.empty(shape, dtype=dtype, device=dev)
+        elif t.shape != shape or t.device != dev:
+            raise ValueError("%s must be %s on %s" % (name, tuple(shape), dev))
+        ptrs.append(None if t is None else _dev_ptr(t, name, dtype))
+    if workspace is None:
+        workspace = torch.empty(xent_workspace_bytes(N, d, V, dt, grad), dtype=torch.uint8,
+                                device=dev)
+    _check(lib().flash_gau_xent(
+        xp, wp, lp, N, d, V, dt, reduction, scale, XentOut(*ptrs),
+        _dev_ptr(workspace, "workspace"), workspace.numel() * workspace.element_size(),
+        _stream(dev)))
     return out
 
 
@@ -798,17 +822,17 @@ class AdamW:
             raise ValueError("one gradient is needed for each parameter")
         if not grads:
             return
-        array, h = self._array, self.hyper
-        for i, g in enumerate(grads):
-            p, dtype = self.params[i], g.dtype
-            if g.shape != p.shape or g.device != self.device:
-                raise ValueError("gradient %d must be like its parameter" % i)
-            array[i].g, array[i].g_dtype = _dev_ptr(g, "gradient", dtype), dtype_code(dtype)
-        h.lr, h.step = float(lr), self.steps + 1 if step is None else int(step)
-        h.grad_scale = _param(grad_scale, "grad_scale", 1, self.device)
-        with _scope(self.device, stream):
-            sp = torch.cuda.current_stream(self.device).cuda_stream
-            _check(lib().flash_gau_adamw_step(array, len(grads), ctypes.byref(h), sp))
+        if _elsewhere(self.device, stream):
+            with _scope(self.device, stream):
+                return self.step(grads, lr, step, grad_scale)
+        h, dev = self.hyper, self.device
+        for e, p, g in zip(self._array, self.params, grads):
+            if g.shape != p.shape or g.device != dev:
+                raise ValueError("each gradient must be like its parameter")
+            e.g, e.g_dtype = _dev_ptr(g, "gradient"), dtype_code(g.dtype)
+        h.lr, h.step = lr, self.steps + 1 if step is None else step
+        h.grad_scale = _param(grad_scale, "grad_scale", 1, dev.index)
+        _check(lib().flash_gau_adamw_step(self._array, len(grads), h, _stream(dev)))
         self.steps = h.step
 
     def moments(self, out_m=None, out_v=None, stream=None):
@@ -823,17 +847,16 @@ class AdamW:
             return out_m or self.m, out_v or self.v
         if not self.params:
             return [], []
-        k = len(self.params)
-        with _scope(self.device, stream):
-            out_m = out_m or [torch.empty_like(p) for p in self.params]
-            out_v = out_v or [torch.empty_like(p) for p in self.params]
-            ptrs = []
-            for name, out in (("out_m", out_m), ("out_v", out_v)):
-                if len(out) != k or any(o.numel() != p.numel() or o.device != self.device
-                                        for o, p in zip(out, self.params)):
-                    raise ValueError("%s must hold a tensor like each parameter" % name)
-                ptrs.append((ctypes.c_void_p * k)(*(_dev_ptr(o, name, torch.float32)
-                                                    for o in out)))
-            sp = torch.cuda.current_stream(self.device).cuda_stream
-            _check(lib().flash_gau_adamw_moments(self._array, k, ptrs[0], ptrs[1], sp))
+        if _elsewhere(self.device, stream):
+            with _scope(self.device, stream):
+                return self.moments(out_m, out_v)
+        k, dev, ptrs = len(self.params), self.device, []
+        out_m = out_m or [torch.empty_like(p) for p in self.params]
+        out_v = out_v or [torch.empty_like(p) for p in self.params]
+        for name, out in (("out_m", out_m), ("out_v", out_v)):
+            if len(out) != k or any(o.numel() != p.numel() or o.device != dev
+                                    for o, p in zip(out, self.params)):
+                raise ValueError("%s must hold a tensor like each parameter" % name)
+            ptrs.append((ctypes.c_void_p * k)(*(_dev_ptr(o, name, torch.float32) for o in out)))
+        _check(lib().flash_gau_adamw_moments(self._array, k, *ptrs, _stream(dev)))
         return out_m, out_v

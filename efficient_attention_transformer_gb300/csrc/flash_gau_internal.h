@@ -307,7 +307,7 @@ struct ResidualProblem {
   cudaStream_t stream;
 };
 constexpr int kResidualMaxD = 8192;
-constexpr int kResidualMaxBlocks = 608;  // of the gradient kernel, four a SM
+constexpr int kResidualMaxBlocks = 608;  // of the gradient kernels, four a SM
 constexpr int kGradSmemMax = 227 * 1024 - 1024;  // its largest tile, less its static part
 size_t residual_norm_part_bytes(long long M, int d);  // parts of the column sums
 cudaError_t residual_norm(const ResidualProblem &q, const void *h, void *r, void *n);

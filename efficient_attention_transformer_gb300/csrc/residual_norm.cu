@@ -32,6 +32,9 @@
 // the rows' sums, and adds up the parameters' gradients in registers.
 #include <cuda_bf16.h>
 
+#include <atomic>
+#include <type_traits>
+
 #include "flash_gau_internal.h"
 #include "sm103_ptx.cuh"
 
@@ -53,6 +56,7 @@ struct Args {
   int d, norm, post;
   float eps;
   int rows, subsets;         // backward: rows of a tile, threads that share a column
+  int flat;                  // backward: tiles start on 16-byte boundaries
 };
 
 // the column sums, in the workspace's order
@@ -77,11 +81,15 @@ __device__ __forceinline__ float2 unpack_bf16(uint32_t w) {
 }
 
 // 1 / spread of a row from its sum of squares around the mean (LayerNorm) or
-// around zero (ScaleNorm)
-__device__ __forceinline__ float inv_spread(float m2, int kind, int d, float eps) {
-  return kind == FLASH_GAU_NORM_LAYER ? 1.0f / sqrtf(m2 / (float)d + eps)
-                                      : 1.0f / fmaxf(sqrtf(m2), eps);
+// around zero (ScaleNorm).  The hardware's reciprocal square root (off by at
+// most 2 units in the last place): exact division and root cost a row more
+// instructions than its sums do.
+__device__ __forceinline__ float inv_spread(float m2, int kind, float inv_d, float eps) {
+  return kind == FLASH_GAU_NORM_LAYER ? rsqrtf(fmaf(m2, inv_d, eps))
+                                      : fminf(rsqrtf(m2), 1.0f / eps);
 }
+// ScaleNorm: whether |x| > eps, where the gradient has its second term
+__device__ __forceinline__ bool longer(float m2, float eps) { return m2 > eps * eps; }
 
 // ---------------------------------------------------------------- forward --
 // Eight columns of a row a lane: chunk k covers columns 256 k .. 256 k + 255,
@@ -140,12 +148,7 @@ __device__ __forceinline__ void load_param(const float *p, int k, int lane, int 
   for (int h = 0; h < 2; ++h) {
     const int c = Eight<T>::column(k, lane, 4 * h);
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (c < d) {  // 4-byte alignment is all that is asked of parameters
-      v.x = __ldg(p + c);
-      v.y = __ldg(p + c + 1);
-      v.z = __ldg(p + c + 2);
-      v.w = __ldg(p + c + 3);
-    }
+    if (c < d) v = __ldg(reinterpret_cast<const float4 *>(p + c));
     x[4 * h] = v.x; x[4 * h + 1] = v.y; x[4 * h + 2] = v.z; x[4 * h + 3] = v.w;
   }
 }
@@ -170,7 +173,7 @@ __device__ __forceinline__ float2 row_stat(Get get, int kind, int lane, int d, f
       const float c = Eight<T>::column(k, lane, q) < d ? get(k, q) - mean : 0.f;
       m2 = fmaf(c, c, m2);
     }
-  return make_float2(mean, inv_spread(warp_sum(m2), kind, d, eps));
+  return make_float2(mean, inv_spread(warp_sum(m2), kind, 1.0f / (float)d, eps));
 }
 
 template <typename T, int NC>
@@ -277,7 +280,7 @@ __global__ void __launch_bounds__(128) residual_norm_any_kernel(const Args a) {
       const float v = get(c) - mean;
       m2 = fmaf(v, v, m2);
     }
-    return make_float2(mean, inv_spread(warp_sum(m2), kind, d, a.eps));
+    return make_float2(mean, inv_spread(warp_sum(m2), kind, 1.0f / (float)d, a.eps));
   };
   auto affine = [&](float u, int kind, const float *g, const float *b, int c) {
     if (kind == FLASH_GAU_NORM_LAYER) return fmaf(u, g[c], b ? b[c] : 0.f);
@@ -303,51 +306,104 @@ __global__ void __launch_bounds__(128) residual_norm_any_kernel(const Args a) {
 }
 
 // --------------------------------------------------------------- backward --
+// Two fp32 values that one instruction works on (fma.rn.f32x2 and the like):
+// the backward is bound by instruction issue more than by memory, and half of
+// what it issues is such arithmetic.
+using f2 = unsigned long long;
+__device__ __forceinline__ f2 pair(float a, float b) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ f2 both(float a) { return pair(a, a); }
+__device__ __forceinline__ float2 split(f2 v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ float sum(f2 v) {
+  const float2 r = split(v);
+  return r.x + r.y;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+  f2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+  f2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+  f2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
 // Four columns of a row: consecutive ones from c on (VEC; 8 bytes of bf16,
 // 16 of fp32), or c, c + stride, c + 2 stride, c + 3 stride, zeros behind d.
+struct F4 {
+  f2 a, b;
+};
 template <bool VEC>
-__device__ __forceinline__ void load4(const float *row, int c, int stride, int d, float (&x)[4]) {
+__device__ __forceinline__ F4 load4(const float *row, int c, int stride, int d) {
   if (VEC) {
-    const float4 v = *reinterpret_cast<const float4 *>(row + c);
-    x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
-  } else {
-#pragma unroll
-    for (int q = 0; q < 4; ++q) x[q] = c + q * stride < d ? row[c + q * stride] : 0.f;
+    const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(row + c);
+    return {v.x, v.y};
   }
+  float x[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) x[q] = c + q * stride < d ? row[c + q * stride] : 0.f;
+  return {pair(x[0], x[1]), pair(x[2], x[3])};
 }
 template <bool VEC>
-__device__ __forceinline__ void load4(const __nv_bfloat16 *row, int c, int stride, int d,
-                                      float (&x)[4]) {
+__device__ __forceinline__ F4 load4(const __nv_bfloat16 *row, int c, int stride, int d) {
   if (VEC) {
     const uint2 v = *reinterpret_cast<const uint2 *>(row + c);
     const float2 a = unpack_bf16(v.x), b = unpack_bf16(v.y);
-    x[0] = a.x; x[1] = a.y; x[2] = b.x; x[3] = b.y;
-  } else {
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-      x[q] = c + q * stride < d ? __bfloat162float(row[c + q * stride]) : 0.f;
+    return {pair(a.x, a.y), pair(b.x, b.y)};
   }
+  float x[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    x[q] = c + q * stride < d ? __bfloat162float(row[c + q * stride]) : 0.f;
+  return {pair(x[0], x[1]), pair(x[2], x[3])};
 }
 template <bool VEC>
-__device__ __forceinline__ void store4(float *row, int c, int stride, int d, const float (&x)[4]) {
+__device__ __forceinline__ void store4(float *row, int c, int stride, int d, const F4 &x) {
   if (VEC) {
-    *reinterpret_cast<float4 *>(row + c) = make_float4(x[0], x[1], x[2], x[3]);
-  } else {
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-      if (c + q * stride < d) row[c + q * stride] = x[q];
+    *reinterpret_cast<ulonglong2 *>(row + c) = make_ulonglong2(x.a, x.b);
+    return;
   }
+  const float2 a = split(x.a), b = split(x.b);
+  const float v[4] = {a.x, a.y, b.x, b.y};
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    if (c + q * stride < d) row[c + q * stride] = v[q];
 }
 template <bool VEC>
-__device__ __forceinline__ void store4(__nv_bfloat16 *row, int c, int stride, int d,
-                                       const float (&x)[4]) {
+__device__ __forceinline__ void store4(__nv_bfloat16 *row, int c, int stride, int d, const F4 &x) {
+  const float2 a = split(x.a), b = split(x.b);
   if (VEC) {
-    *reinterpret_cast<uint2 *>(row + c) = make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
-  } else {
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-      if (c + q * stride < d) row[c + q * stride] = __float2bfloat16_rn(x[q]);
+    *reinterpret_cast<uint2 *>(row + c) = make_uint2(pack_bf16(a.x, a.y), pack_bf16(b.x, b.y));
+    return;
   }
+  const float v[4] = {a.x, a.y, b.x, b.y};
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    if (c + q * stride < d) row[c + q * stride] = __float2bfloat16_rn(v[q]);
+}
+// x + m, but zero behind d (element-wise columns; others are inside)
+template <bool VEC>
+__device__ __forceinline__ F4 shift4(const F4 &x, f2 m, int c, int stride, int d) {
+  F4 r = {add2(x.a, m), add2(x.b, m)};
+  if (!VEC) {
+    const float2 a = split(r.a), b = split(r.b);
+    r.a = pair(c < d ? a.x : 0.f, c + stride < d ? a.y : 0.f);
+    r.b = pair(c + 2 * stride < d ? b.x : 0.f, c + 3 * stride < d ? b.y : 0.f);
+  }
+  return r;
 }
 
 // 16 bytes from global into shared memory without passing through registers
@@ -360,63 +416,148 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
 }
 
-// A row's sums as the second half needs them: u = (x - mean) i, and
-// dx = i (w - a - u b).
-struct RowSums {
-  float mean_r, inv_r, a_r, b_r, mean_y, inv_y, a_y, b_y;
+// A row's sums as the second half needs them: u = x i + m (m = -mean i), and
+// dx = i (w + a + u b).
+struct __align__(16) RowSums {
+  float inv_r, m_r, a_r, b_r, inv_y, m_y, a_y, b_y;
 };
 
-template <typename T, bool VEC, int NG, int MAXT>
-__global__ void __launch_bounds__(MAXT) residual_norm_grad_kernel(const Args a) {
+// The tile in shared memory: rows of r, dn, dr, y and gate where there are
+// such, and the column factors of w (ng) and of dy (kp = scale post_g).
+template <typename T>
+struct TileRows {
+  const T *x, *dn, *dr, *y, *gate;
+  const float *ng, *kp;
+};
+
+// The sums of row k of a tile, by one warp, columns c = 4 lane + 128 j (VEC,
+// conflict-free) or lane + 128 j + 32 q; the row is read again for each sum.
+template <typename T, bool VEC>
+__device__ __forceinline__ RowSums row_sums(const Args &a, const TileRows<T> &t, int k, int lane) {
+  const int d = a.d, c0 = VEC ? 4 * lane : lane;
+  const float inv_d = 1.0f / (float)d;
+  const bool norm_layer = a.norm == FLASH_GAU_NORM_LAYER, post_layer = a.post == FLASH_GAU_NORM_LAYER;
+  const size_t at = (size_t)k * d;
+  const T *x = t.x + at, *dn = t.dn + at, *dr = t.dr + at, *y = t.y + at, *gt = t.gate + at;
+  RowSums s = {1.f, 0.f, 0.f, 0.f, 1.f, 0.f, 0.f, 0.f};
+  float mean_r = 0.f, mean_y = 0.f;
+  if (norm_layer) {
+    f2 v = 0;
+    for (int c = c0; c < d; c += 128) {
+      const F4 e = load4<VEC>(x, c, 32, d);
+      v = add2(v, add2(e.a, e.b));
+    }
+    mean_r = warp_sum(sum(v)) * inv_d;
+  }
+  if (post_layer) {
+    f2 v = 0;
+    for (int c = c0; c < d; c += 128) {
+      const F4 e = load4<VEC>(y, c, 32, d);
+      v = add2(v, add2(e.a, e.b));
+    }
+    mean_y = warp_sum(sum(v)) * inv_d;
+  }
+  float ub = 0.f;
+  if (a.norm) {
+    f2 m2 = 0, sw = 0, swx = 0;
+    const f2 shift = both(-mean_r);
+    for (int c = c0; c < d; c += 128) {
+      const F4 e = shift4<VEC>(load4<VEC>(x, c, 32, d), shift, c, 32, d);
+      const F4 g = load4<VEC>(dn, c, 32, d), w = load4<VEC>(t.ng, c, 32, d);
+      const f2 wa = mul2(w.a, g.a), wb = mul2(w.b, g.b);
+      m2 = fma2(e.a, e.a, fma2(e.b, e.b, m2));
+      sw = add2(sw, add2(wa, wb));
+      swx = fma2(wa, e.a, fma2(wb, e.b, swx));
+    }
+    const float q = warp_sum(sum(m2));
+    s.inv_r = inv_spread(q, a.norm, inv_d, a.eps);
+    s.m_r = -mean_r * s.inv_r;
+    const float swu = warp_sum(sum(swx)) * s.inv_r;
+    if (norm_layer) {
+      s.a_r = -warp_sum(sum(sw)) * inv_d;
+      s.b_r = -swu * inv_d;
+    } else {
+      s.b_r = longer(q, a.eps) ? -swu : 0.f;
+    }
+    ub = s.inv_r * s.b_r;
+  }
+  if (!a.post) return s;
+  f2 m2 = 0, sg = 0, sgy = 0;
+  const f2 inv_r = both(s.inv_r), a_r = both(s.a_r), ubb = both(ub), shift_y = both(-mean_y),
+           shift_r = both(-mean_r);
+  for (int c = c0; c < d; c += 128) {
+    F4 dh = {0, 0};
+    if (a.dr) dh = load4<VEC>(dr, c, 32, d);
+    if (a.norm) {
+      const F4 e = shift4<VEC>(load4<VEC>(x, c, 32, d), shift_r, c, 32, d);
+      const F4 g = load4<VEC>(dn, c, 32, d), w = load4<VEC>(t.ng, c, 32, d);
+      dh.a = fma2(inv_r, fma2(e.a, ubb, fma2(w.a, g.a, a_r)), dh.a);
+      dh.b = fma2(inv_r, fma2(e.b, ubb, fma2(w.b, g.b, a_r)), dh.b);
+    }
+    F4 w = load4<VEC>(t.kp, c, 32, d);  // zero behind the row
+    if (a.gate) {
+      const F4 g = load4<VEC>(gt, c, 32, d);
+      w.a = mul2(w.a, g.a);
+      w.b = mul2(w.b, g.b);
+    }
+    const F4 e = shift4<VEC>(load4<VEC>(y, c, 32, d), shift_y, c, 32, d);
+    const f2 fa = mul2(dh.a, w.a), fb = mul2(dh.b, w.b);
+    m2 = fma2(e.a, e.a, fma2(e.b, e.b, m2));
+    sg = add2(sg, add2(fa, fb));
+    sgy = fma2(fa, e.a, fma2(fb, e.b, sgy));
+  }
+  const float q = warp_sum(sum(m2));
+  s.inv_y = inv_spread(q, a.post, inv_d, a.eps);
+  s.m_y = -mean_y * s.inv_y;
+  const float sgu = warp_sum(sum(sgy)) * s.inv_y;
+  if (post_layer) {
+    s.a_y = -warp_sum(sum(sg)) * inv_d;
+    s.b_y = -sgu * inv_d;
+  } else {
+    s.b_y = longer(q, a.eps) ? -sgu : 0.f;
+  }
+  return s;
+}
+
+template <typename T, bool VEC, int NG, int MAXT, int BLOCKS>
+__global__ void __launch_bounds__(MAXT, BLOCKS) residual_norm_grad_kernel(const Args a) {
   extern __shared__ __align__(16) uint8_t smem[];
   const int t = threadIdx.x, threads = blockDim.x, lane = t & 31, warp = t >> 5, d = a.d;
   const int warps = threads >> 5;
   const bool norm_layer = a.norm == FLASH_GAU_NORM_LAYER, post_layer = a.post == FLASH_GAU_NORM_LAYER;
-  // the tile's arrays, then w's and dy's column factors, then the rows' sums
-  const size_t array = (size_t)a.rows * d * sizeof(T), pitch = (array + 15) / 16 * 16;
+  // the rows' sums, w's and dy's column factors, then the tile's arrays
+  RowSums *sums = reinterpret_cast<RowSums *>(smem);
+  const int dp = (d + 3) / 4 * 4;
+  float *ng = reinterpret_cast<float *>(sums + a.rows), *kp = ng + dp;
+  const size_t pitch = ((size_t)a.rows * d * sizeof(T) + 15) / 16 * 16;
   const T *src[5] = {static_cast<const T *>(a.norm ? a.h : nullptr), static_cast<const T *>(a.dn),
                      static_cast<const T *>(a.dr), static_cast<const T *>(a.y),
                      static_cast<const T *>(a.gate)};
   T *tile[5];
-  uint8_t *at = smem;
+  uint8_t *at = reinterpret_cast<uint8_t *>(kp + dp);
 #pragma unroll
   for (int k = 0; k < 5; ++k) {
     tile[k] = reinterpret_cast<T *>(at);
     if (src[k]) at += pitch;
   }
-  T *const tx = tile[0], *const tdn = tile[1], *const tdr = tile[2], *const ty = tile[3],
-           *const tg = tile[4];
-  const int dp = (d + 3) / 4 * 4;
-  float *ng = reinterpret_cast<float *>(at), *kp = ng + dp;
-  RowSums *sums = reinterpret_cast<RowSums *>(kp + dp);
+  const TileRows<T> rows_in = {tile[0], tile[1], tile[2], tile[3], tile[4], ng, kp};
   ptx::griddep_wait();
   for (int c = t; c < d; c += threads) {
     ng[c] = a.norm ? a.norm_g[norm_layer ? c : 0] : 1.f;
     kp[c] = (a.post ? a.post_g[post_layer ? c : 0] : 1.f) * (a.scale ? a.scale[c] : 1.f);
   }
   __syncthreads();
-  // this thread's columns: group g of four, and which share of a tile's rows
+  // this thread's columns: groups of four, and which share of a tile's rows
   const int per = (d + 3) / 4;
-  const int lanes = NG == 1 ? per : threads;  // threads that have columns of their own
-  const int sub = t / lanes, own = t % lanes;
+  const int stride = NG == 1 ? per : threads;  // threads that have columns of their own
+  const int sub = t / stride, own = t % stride;
   const bool active = sub < a.subsets;
-  const int stride = lanes;  // element-wise: between a group's columns
   auto column = [&](int g) { return VEC ? 4 * (own + g * threads) : own + 4 * g * threads; };
-  float pg[NG][4], pb[NG][4], sc[NG][4], gn[NG][4], acc[kSums][NG][4];
+  F4 acc[kSums][NG];
 #pragma unroll
-  for (int g = 0; g < NG; ++g)
+  for (int s = 0; s < kSums; ++s)
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int c = VEC ? column(g) + q : column(g) + q * stride;
-      const bool in = active && c < d;
-      gn[g][q] = in ? ng[c] : 0.f;
-      sc[g][q] = in ? (a.scale ? a.scale[c] : 1.f) : 0.f;
-      pg[g][q] = in ? (a.post ? a.post_g[post_layer ? c : 0] : 1.f) : 0.f;
-      pb[g][q] = in && post_layer && a.post_b ? a.post_b[c] : 0.f;
-#pragma unroll
-      for (int s = 0; s < kSums; ++s) acc[s][g][q] = 0.f;
-    }
-  const float inv_d = 1.0f / (float)d;
+    for (int g = 0; g < NG; ++g) acc[s][g] = {0, 0};
   for (long long row0 = (long long)blockIdx.x * a.rows; row0 < a.M;
        row0 += (long long)gridDim.x * a.rows) {
     const int rows = (int)(a.M - row0 < a.rows ? a.M - row0 : a.rows);
@@ -425,157 +566,90 @@ __global__ void __launch_bounds__(MAXT) residual_norm_grad_kernel(const Args a) 
     for (int k = 0; k < 5; ++k) {
       if (!src[k]) continue;
       const T *from = src[k] + row0 * d;
-      if (VEC) {
-        constexpr int W = 16 / sizeof(T);
-        for (int i = t * W; i < n; i += threads * W) cp_async16(tile[k] + i, from + i);
-      } else {
-        for (int i = t; i < n; i += threads) tile[k][i] = from[i];
-      }
+      // a tile's rows are one run of memory, on a 16-byte boundary (a.flat)
+      // or not; its last elements may not fill 16 bytes
+      constexpr int W = 16 / sizeof(T);
+      const int whole = a.flat ? n / W * W : 0;
+      for (int i = t * W; i < whole; i += threads * W) cp_async16(tile[k] + i, from + i);
+      for (int i = whole + t; i < n; i += threads) tile[k][i] = from[i];
     }
-    if (VEC) cp_async_wait();
+    cp_async_wait();
     __syncthreads();
     // ---- one warp a row: its sums
     for (int k = warp; k < rows; k += warps) {
-      const T *x = tx + (size_t)k * d, *dn = tdn + (size_t)k * d, *dr = tdr + (size_t)k * d;
-      const T *y = ty + (size_t)k * d, *gt = tg + (size_t)k * d;
-      const int c0 = VEC ? 4 * lane : lane;
-      auto in = [&](int c, int q) { return VEC || c + 32 * q < d; };
-      RowSums s = {0.f, 1.f, 0.f, 0.f, 0.f, 1.f, 0.f, 0.f};
-      if (norm_layer || post_layer) {
-        float sr = 0.f, sy = 0.f;
-        for (int c = c0; c < d; c += 128) {
-          float v[4];
-          if (norm_layer) {
-            load4<VEC>(x, c, 32, d, v);
-            sr += (v[0] + v[1]) + (v[2] + v[3]);
-          }
-          if (post_layer) {
-            load4<VEC>(y, c, 32, d, v);
-            sy += (v[0] + v[1]) + (v[2] + v[3]);
-          }
-        }
-        if (norm_layer) s.mean_r = warp_sum(sr) * inv_d;
-        if (post_layer) s.mean_y = warp_sum(sy) * inv_d;
-      }
-      if (a.norm || a.post) {
-        float m2r = 0.f, m2y = 0.f, sw = 0.f, swx = 0.f;
-        for (int c = c0; c < d; c += 128) {
-          float v[4], g[4], w[4];
-          if (a.norm) {
-            load4<VEC>(x, c, 32, d, v);
-            load4<VEC>(dn, c, 32, d, g);
-            load4<VEC>(ng, c, 32, d, w);
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const float e = in(c, q) ? v[q] - s.mean_r : 0.f;
-              m2r = fmaf(e, e, m2r);
-              w[q] *= g[q];
-              sw += w[q];
-              swx = fmaf(w[q], e, swx);
-            }
-          }
-          if (a.post) {
-            load4<VEC>(y, c, 32, d, v);
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const float e = in(c, q) ? v[q] - s.mean_y : 0.f;
-              m2y = fmaf(e, e, m2y);
-            }
-          }
-        }
-        if (a.norm) {
-          m2r = warp_sum(m2r);
-          s.inv_r = inv_spread(m2r, a.norm, d, a.eps);
-          swx = warp_sum(swx) * s.inv_r;
-          if (norm_layer) {
-            s.a_r = warp_sum(sw) * inv_d;
-            s.b_r = swx * inv_d;
-          } else {
-            s.b_r = sqrtf(m2r) > a.eps ? swx : 0.f;
-          }
-        }
-        if (a.post) {
-          m2y = warp_sum(m2y);
-          s.inv_y = inv_spread(m2y, a.post, d, a.eps);
-          float sg = 0.f, sgy = 0.f;
-          for (int c = c0; c < d; c += 128) {
-            float dh[4] = {0.f, 0.f, 0.f, 0.f}, v[4], g[4], w[4];
-            if (a.dr) load4<VEC>(dr, c, 32, d, dh);
-            if (a.norm) {
-              load4<VEC>(x, c, 32, d, v);
-              load4<VEC>(dn, c, 32, d, g);
-              load4<VEC>(ng, c, 32, d, w);
-#pragma unroll
-              for (int q = 0; q < 4; ++q)
-                dh[q] += s.inv_r * (w[q] * g[q] - s.a_r - (v[q] - s.mean_r) * s.inv_r * s.b_r);
-            }
-            load4<VEC>(kp, c, 32, d, w);  // zero behind the row
-            load4<VEC>(y, c, 32, d, v);
-            if (a.gate) {
-              load4<VEC>(gt, c, 32, d, g);
-#pragma unroll
-              for (int q = 0; q < 4; ++q) w[q] *= g[q];
-            }
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const float e = dh[q] * w[q];
-              sg += e;
-              sgy = fmaf(e, v[q] - s.mean_y, sgy);
-            }
-          }
-          sgy = warp_sum(sgy) * s.inv_y;
-          if (post_layer) {
-            s.a_y = warp_sum(sg) * inv_d;
-            s.b_y = sgy * inv_d;
-          } else {
-            s.b_y = sqrtf(m2y) > a.eps ? sgy : 0.f;
-          }
-        }
-      }
+      const RowSums s = row_sums<T, VEC>(a, rows_in, k, lane);
       if (lane == 0) sums[k] = s;
     }
     __syncthreads();
     // ---- four columns a thread and group: outputs and column sums
     if (active) {
-      for (int k = sub; k < rows; k += a.subsets) {
-        const RowSums s = sums[k];
-        const long long out = (row0 + k) * d;
 #pragma unroll
-        for (int g = 0; g < NG; ++g) {
-          const int c = column(g);
-          if (c >= d) continue;
-          float dh[4] = {0.f, 0.f, 0.f, 0.f}, v[4], e[4];
-          if (a.dr) load4<VEC>(tdr + (size_t)k * d, c, stride, d, dh);
+      for (int g = 0; g < NG; ++g) {
+        const int c = column(g);
+        if (c >= d) continue;
+        // the columns' parameters, read again for each tile: registers are
+        // better spent on more blocks
+        const F4 gn = load4<VEC>(ng, c, stride, d);
+        float x[3][4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int cq = VEC ? c + q : c + q * stride;
+          const bool in = cq < d;
+          x[0][q] = in ? (a.post ? __ldg(a.post_g + (post_layer ? cq : 0)) : 1.f) : 0.f;
+          x[1][q] = in && post_layer && a.post_b ? __ldg(a.post_b + cq) : 0.f;
+          x[2][q] = in ? (a.scale ? __ldg(a.scale + cq) : 1.f) : 0.f;
+        }
+        const F4 pg = {pair(x[0][0], x[0][1]), pair(x[0][2], x[0][3])};
+        const F4 pb = {pair(x[1][0], x[1][1]), pair(x[1][2], x[1][3])};
+        const F4 sc = {pair(x[2][0], x[2][1]), pair(x[2][2], x[2][3])};
+        for (int k = sub; k < rows; k += a.subsets) {
+          const RowSums s = sums[k];
+          const int in = k * d;
+          const long long out = (row0 + k) * d;
+          F4 dh = {0, 0};
+          if (a.dr) dh = load4<VEC>(rows_in.dr + in, c, stride, d);
           if (a.norm) {
-            load4<VEC>(tx + (size_t)k * d, c, stride, d, v);
-            load4<VEC>(tdn + (size_t)k * d, c, stride, d, e);
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const float u = (v[q] - s.mean_r) * s.inv_r;
-              dh[q] += s.inv_r * (e[q] * gn[g][q] - s.a_r - u * s.b_r);
-              acc[kNormG][g][q] = fmaf(e[q], u, acc[kNormG][g][q]);
-              acc[kNormB][g][q] += e[q];
-            }
+            const F4 x = load4<VEC>(rows_in.x + in, c, stride, d);
+            const F4 e = load4<VEC>(rows_in.dn + in, c, stride, d);
+            const f2 i = both(s.inv_r), m = both(s.m_r), ar = both(s.a_r), br = both(s.b_r);
+            const f2 ua = fma2(x.a, i, m), ub = fma2(x.b, i, m);
+            dh.a = fma2(i, fma2(ua, br, fma2(e.a, gn.a, ar)), dh.a);
+            dh.b = fma2(i, fma2(ub, br, fma2(e.b, gn.b, ar)), dh.b);
+            acc[kNormG][g].a = fma2(e.a, ua, acc[kNormG][g].a);
+            acc[kNormG][g].b = fma2(e.b, ub, acc[kNormG][g].b);
+            acc[kNormB][g].a = add2(e.a, acc[kNormB][g].a);
+            acc[kNormB][g].b = add2(e.b, acc[kNormB][g].b);
           }
           store4<VEC>(static_cast<T *>(a.dh) + out, c, stride, d, dh);
           if (!a.dy) continue;
-          float gv[4] = {1.f, 1.f, 1.f, 1.f};
-          if (a.y) load4<VEC>(ty + (size_t)k * d, c, stride, d, v);
-          else v[0] = v[1] = v[2] = v[3] = 0.f;
-          if (a.gate) load4<VEC>(tg + (size_t)k * d, c, stride, d, gv);
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const float u = (v[q] - s.mean_y) * s.inv_y;
-            const float p = dh[q] * fmaf(u, pg[g][q], pb[g][q]);
-            acc[kScale][g][q] = fmaf(p, gv[q], acc[kScale][g][q]);
-            const float dp = dh[q] * gv[q] * sc[g][q];
-            acc[kPostG][g][q] = fmaf(dp, u, acc[kPostG][g][q]);
-            acc[kPostB][g][q] += dp;
-            v[q] = s.inv_y * (dp * pg[g][q] - s.a_y - u * s.b_y);
-            e[q] = p * sc[g][q];
+          F4 y = {0, 0};
+          if (a.y) y = load4<VEC>(rows_in.y + in, c, stride, d);
+          const f2 i = both(s.inv_y), m = both(s.m_y), ay = both(s.a_y), by = both(s.b_y);
+          const f2 ua = fma2(y.a, i, m), ub = fma2(y.b, i, m);
+          // p = dh post(y); dp = dh scale gate
+          const f2 pa = mul2(dh.a, fma2(ua, pg.a, pb.a));
+          const f2 pb2 = mul2(dh.b, fma2(ub, pg.b, pb.b));
+          f2 dpa = mul2(dh.a, sc.a), dpb = mul2(dh.b, sc.b);
+          if (a.gate) {
+            const F4 gv = load4<VEC>(rows_in.gate + in, c, stride, d);
+            if (a.dgate)
+              store4<VEC>(static_cast<T *>(a.dgate) + out, c, stride, d,
+                          F4{mul2(pa, sc.a), mul2(pb2, sc.b)});
+            acc[kScale][g].a = fma2(pa, gv.a, acc[kScale][g].a);
+            acc[kScale][g].b = fma2(pb2, gv.b, acc[kScale][g].b);
+            dpa = mul2(dpa, gv.a);
+            dpb = mul2(dpb, gv.b);
+          } else {
+            acc[kScale][g].a = add2(pa, acc[kScale][g].a);
+            acc[kScale][g].b = add2(pb2, acc[kScale][g].b);
           }
-          if (a.dgate) store4<VEC>(static_cast<T *>(a.dgate) + out, c, stride, d, e);
-          store4<VEC>(static_cast<T *>(a.dy) + out, c, stride, d, v);
+          acc[kPostG][g].a = fma2(dpa, ua, acc[kPostG][g].a);
+          acc[kPostG][g].b = fma2(dpb, ub, acc[kPostG][g].b);
+          acc[kPostB][g].a = add2(dpa, acc[kPostB][g].a);
+          acc[kPostB][g].b = add2(dpb, acc[kPostB][g].b);
+          store4<VEC>(static_cast<T *>(a.dy) + out, c, stride, d,
+                      F4{mul2(i, fma2(ua, by, fma2(dpa, pg.a, ay))),
+                         mul2(i, fma2(ub, by, fma2(dpb, pg.b, ay)))});
         }
       }
     }
@@ -587,22 +661,292 @@ __global__ void __launch_bounds__(MAXT) residual_norm_grad_kernel(const Args a) 
 #pragma unroll
     for (int s = 0; s < kSums; ++s)
 #pragma unroll
-      for (int g = 0; g < NG; ++g)
+      for (int g = 0; g < NG; ++g) {
+        const float2 v = split(acc[s][g].a), w = split(acc[s][g].b);
+        const float x[4] = {v.x, v.y, w.x, w.y};
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           const int c = VEC ? column(g) + q : column(g) + q * stride;
-          if (c < d) part[s * (long long)d + c] = acc[s][g][q];
+          if (c < d) part[s * (long long)d + c] = x[q];
         }
+      }
   }
 #pragma unroll
   for (int s = 0; s < 2; ++s) {
-    float v = 0.f;
+    f2 v = 0;
 #pragma unroll
-    for (int g = 0; g < NG; ++g)
+    for (int g = 0; g < NG; ++g) {
+      const F4 &x = acc[s ? kPostG : kNormG][g];
+      v = add2(v, add2(x.a, x.b));
+    }
+    const float w = warp_sum(sum(v));
+    if (lane == 0) a.scalar_part[((long long)s * gridDim.x + blockIdx.x) * kMaxWarps + warp] = w;
+  }
+}
+
+// ---- rows of up to 2048 columns, on 16-byte boundaries
+// WPR warps a row from its loads to its outputs, each a run of 128 NJ
+// columns: the row's values stay in registers, the column sums of a lane's
+// columns too, for the whole launch, and the next rows are on their way into
+// the warp's own part of shared memory meanwhile.  Row sums pass between a row's
+// warps through shared memory, one named barrier of theirs each.
+//
+// What a row costs in instructions beside its columns' arithmetic decides the
+// time, so nothing in the loops over columns asks about the call's options:
+// an array that is not there is a row of zeros (the gate: ones) written to
+// shared memory once, columns behind d are zeros there, a missing norm is
+// one whose row scalars change nothing, and the two norms differ in their
+// row scalars alone.  Only what would hold registers is a template argument,
+// the column sums: NORM_COL, of a LayerNorm's parameters; PS, behind the
+// addition (0 none, 1 the scale's, 2 the scale's and a LayerNorm's).  A
+// ScaleNorm's g takes one sum a lane.
+constexpr int kRowWarps = 4;
+// rows of a warp in shared memory: the one it works on and those on their
+// way, about as many bytes of either type
+template <typename T>
+__host__ __device__ constexpr int row_slots() { return sizeof(T) == 2 ? 3 : 2; }
+template <bool B>
+using Is = std::integral_constant<bool, B>;
+
+template <typename T, int WPR, int NJ, bool NORM_COL, int PS>
+__global__ void __launch_bounds__(32 * kRowWarps, NJ * (NORM_COL * 2 + PS + (PS == 2)) <= 9 ? 4 : 3)
+residual_norm_grad_rows_kernel(const Args a) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ float4 shared_sums[2][kRowWarps];
+  constexpr int kWidth = 128 * NJ;       // columns of a warp
+  constexpr int kRow = kWidth * WPR;     // and of a row, d and what is behind it
+  constexpr int kSlot = 5 * kWidth;      // r, dn, dr, y, gate
+  constexpr int kSlots = row_slots<T>();
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5, d = a.d;
+  const int first = kWidth * (warp % WPR), c0 = first + 4 * lane;
+  const bool norm_layer = a.norm == FLASH_GAU_NORM_LAYER, post_layer = a.post == FLASH_GAU_NORM_LAYER;
+  const float inv_d = 1.0f / (float)d, inv_eps = 1.0f / a.eps;
+  // the columns' parameters, then the slots of rows of each warp
+  float *ng = reinterpret_cast<float *>(smem), *sc = ng + kRow, *pg = sc + kRow, *pb = pg + kRow;
+  T *const ring = reinterpret_cast<T *>(pb + (PS == 2 ? kRow : 0)) + warp * kSlots * kSlot;
+  const T *src[5] = {static_cast<const T *>(a.norm ? a.h : nullptr), static_cast<const T *>(a.dn),
+                     static_cast<const T *>(a.dr), static_cast<const T *>(a.y),
+                     static_cast<const T *>(a.gate)};
+  constexpr int kRowsAtOnce = kRowWarps / WPR;
+  const long long step = (long long)gridDim.x * kRowsAtOnce;
+  const long long row_first = (long long)blockIdx.x * kRowsAtOnce + warp / WPR;
+  constexpr int W = 16 / sizeof(T);
+  auto fetch = [&](long long row, int s) {
+    if (row < a.M) {
+      const long long off = row * d + first + lane * W;
+      T *to = ring + s * kSlot + lane * W;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) v += acc[s ? kPostG : kNormG][g][q];
-    v = warp_sum(v);
-    if (lane == 0) a.scalar_part[((long long)s * gridDim.x + blockIdx.x) * kMaxWarps + warp] = v;
+      for (int k = 0; k < 5; ++k) {
+        if (!src[k]) continue;
+#pragma unroll
+        for (int j = 0; j < (kWidth + 32 * W - 1) / (32 * W); ++j) {
+          const int c = (lane + 32 * j) * W;
+          if (c < kWidth && first + c < d)
+            cp_async16(to + k * kWidth + 32 * j * W, src[k] + off + 32 * j * W);
+        }
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  for (int i = lane; i < kSlots * kSlot; i += 32)
+    ring[i] = T(!a.gate && i % kSlot >= 4 * kWidth ? 1.f : 0.f);
+  __syncwarp();
+  ptx::griddep_wait();
+#pragma unroll
+  for (int k = 0; k < kSlots - 1; ++k) fetch(row_first + k * step, k);
+  for (int c = t; c < kRow; c += 32 * kRowWarps) {
+    const bool in = c < d;
+    ng[c] = in && a.norm ? a.norm_g[norm_layer ? c : 0] : 0.f;
+    sc[c] = !in ? 0.f : a.scale ? a.scale[c] : 1.f;
+    pg[c] = !in ? 0.f : a.post ? a.post_g[post_layer ? c : 0] : 1.f;
+    if (PS == 2) pb[c] = in && a.post_b ? a.post_b[c] : 0.f;
+  }
+  __syncthreads();
+  F4 acc_ng[NORM_COL ? NJ : 1], acc_nb[NORM_COL ? NJ : 1], acc_sc[PS ? NJ : 1];
+  F4 acc_pg[PS == 2 ? NJ : 1], acc_pb[PS == 2 ? NJ : 1];
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) {
+    if (NORM_COL || j == 0) acc_ng[j] = acc_nb[j] = {0, 0};
+    if (PS || j == 0) acc_sc[j] = {0, 0};
+    if (PS == 2 || j == 0) acc_pg[j] = acc_pb[j] = {0, 0};
+  }
+  // sums of the row from its warps' sums, in the warps' order
+  int flip = 0;
+  auto row_sum = [&](float x, float y, auto with_z, float z) {
+    float4 r = make_float4(warp_sum(x), warp_sum(y), 0.f, 0.f);
+    if constexpr (decltype(with_z)::value) r.z = warp_sum(z);
+    if constexpr (WPR > 1) {
+      const int of = warp / WPR * WPR;
+      if (lane == 0) shared_sums[flip][warp] = r;
+      asm volatile("bar.sync %0, %1;" ::"r"(1 + warp / WPR), "r"(32 * WPR) : "memory");
+      r = shared_sums[flip][of];
+#pragma unroll
+      for (int w = 1; w < WPR; ++w) {
+        const float4 v = shared_sums[flip][of + w];
+        r.x += v.x;
+        r.y += v.y;
+        r.z += v.z;
+      }
+      flip ^= 1;  // written again only after the next barrier: everyone has read it
+    }
+    return r;
+  };
+  // added to a column of the row to take its mean off: zero behind the row
+  auto shift_of = [&](int j, f2 minus_mean) { return c0 + 128 * j < d ? minus_mean : f2(0); };
+  int s = 0;
+  for (long long row = row_first; row < a.M; row += step) {
+    fetch(row + (kSlots - 1) * step, s == 0 ? kSlots - 1 : s - 1);
+    asm volatile("cp.async.wait_group %0;" ::"n"(kSlots - 1) : "memory");
+    __syncwarp();
+    const T *in = ring + s * kSlot + 4 * lane;
+    const float *ngc = ng + c0, *scc = sc + c0, *pgc = pg + c0, *pbc = pb + c0;
+    const long long out = row * d + c0;
+    F4 x[NJ], y[NJ], dh[NJ];
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      x[j] = load4<true>(in + 128 * j, 0, 0, d);
+      y[j] = load4<true>(in + 3 * kWidth + 128 * j, 0, 0, d);
+    }
+    float mean_r = 0.f, mean_y = 0.f;
+    if (NORM_COL || PS == 2) {
+      f2 v = 0, vy = 0;
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) {
+        v = add2(v, add2(x[j].a, x[j].b));
+        vy = add2(vy, add2(y[j].a, y[j].b));
+      }
+      const float4 r = row_sum(sum(v), sum(vy), Is<false>(), 0.f);
+      mean_r = norm_layer ? r.x * inv_d : 0.f;
+      mean_y = post_layer ? r.y * inv_d : 0.f;
+      const f2 mr = both(-mean_r), my = both(-mean_y);
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) {
+        const f2 xs = shift_of(j, mr), ys = shift_of(j, my);
+        x[j] = {add2(x[j].a, xs), add2(x[j].b, xs)};
+        y[j] = {add2(y[j].a, ys), add2(y[j].b, ys)};
+      }
+    }
+    float inv_r, a_r = 0.f, b_r;
+    {
+      f2 m2 = 0, sw = 0, swx = 0;
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) {
+        const F4 g = load4<true>(in + kWidth + 128 * j, 0, 0, d), w = load4<true>(ngc + 128 * j, 0, 0, d);
+        dh[j] = {mul2(w.a, g.a), mul2(w.b, g.b)};
+        m2 = fma2(x[j].a, x[j].a, fma2(x[j].b, x[j].b, m2));
+        if (NORM_COL) sw = add2(sw, add2(dh[j].a, dh[j].b));
+        swx = fma2(dh[j].a, x[j].a, fma2(dh[j].b, x[j].b, swx));
+      }
+      const float4 q = row_sum(sum(m2), sum(swx), Is<NORM_COL>(), sum(sw));
+      if (NORM_COL) {
+        inv_r = rsqrtf(fmaf(q.x, inv_d, a.eps));
+        a_r = -q.z * inv_d;
+        b_r = -q.y * inv_r * inv_d;
+      } else {
+        inv_r = fminf(rsqrtf(q.x), inv_eps);
+        b_r = longer(q.x, a.eps) ? -q.y * inv_r : 0.f;
+      }
+    }
+    // dh = dr + i (w + a + u b), and the sums that dy needs
+    const f2 ir = both(inv_r), ar = both(a_r), br = both(b_r);
+    f2 m2 = 0, sg = 0, sgy = 0;
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      const F4 r = load4<true>(in + 2 * kWidth + 128 * j, 0, 0, d);
+      const F4 g = load4<true>(in + kWidth + 128 * j, 0, 0, d);
+      const f2 ua = mul2(x[j].a, ir), ub = mul2(x[j].b, ir);
+      F4 &n = acc_ng[NORM_COL ? j : 0], &nb = acc_nb[NORM_COL ? j : 0];
+      n = {fma2(g.a, ua, n.a), fma2(g.b, ub, n.b)};
+      if (NORM_COL) nb = {add2(nb.a, g.a), add2(nb.b, g.b)};
+      dh[j] = {fma2(ir, fma2(ua, br, add2(dh[j].a, ar)), r.a),
+               fma2(ir, fma2(ub, br, add2(dh[j].b, ar)), r.b)};
+      if (c0 + 128 * j < d) store4<true>(static_cast<T *>(a.dh) + out + 128 * j, 0, 0, d, dh[j]);
+      // dp = dh scale gate stays in x's place
+      const F4 w = load4<true>(scc + 128 * j, 0, 0, d), p = load4<true>(pgc + 128 * j, 0, 0, d);
+      const F4 gt = load4<true>(in + 4 * kWidth + 128 * j, 0, 0, d);
+      x[j] = {mul2(mul2(dh[j].a, w.a), gt.a), mul2(mul2(dh[j].b, w.b), gt.b)};
+      const f2 fa = mul2(x[j].a, p.a), fb = mul2(x[j].b, p.b);
+      m2 = fma2(y[j].a, y[j].a, fma2(y[j].b, y[j].b, m2));
+      if (PS == 2) sg = add2(sg, add2(fa, fb));
+      sgy = fma2(fa, y[j].a, fma2(fb, y[j].b, sgy));
+    }
+    if (a.dy) {
+      float inv_y = 1.f, a_y = 0.f, b_y = 0.f;
+      if (a.post) {
+        const float4 q = row_sum(sum(m2), sum(sgy), Is<PS == 2>(), sum(sg));
+        if (PS == 2) {
+          inv_y = rsqrtf(fmaf(q.x, inv_d, a.eps));
+          a_y = -q.z * inv_d;
+          b_y = -q.y * inv_y * inv_d;
+        } else {
+          inv_y = fminf(rsqrtf(q.x), inv_eps);
+          b_y = longer(q.x, a.eps) ? -q.y * inv_y : 0.f;
+        }
+      }
+      const f2 iy = both(inv_y), ay = both(a_y), by = both(b_y);
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) {
+        const F4 u = {mul2(y[j].a, iy), mul2(y[j].b, iy)};
+        const F4 g = load4<true>(pgc + 128 * j, 0, 0, d), w = load4<true>(scc + 128 * j, 0, 0, d);
+        const F4 gt = load4<true>(in + 4 * kWidth + 128 * j, 0, 0, d);
+        F4 p;  // dh post(y)
+        if (PS == 2) {
+          const F4 b = load4<true>(pbc + 128 * j, 0, 0, d);
+          p = {mul2(dh[j].a, fma2(u.a, g.a, b.a)), mul2(dh[j].b, fma2(u.b, g.b, b.b))};
+        } else {
+          p = {mul2(dh[j].a, mul2(u.a, g.a)), mul2(dh[j].b, mul2(u.b, g.b))};
+        }
+        F4 &as = acc_sc[PS ? j : 0], &ag = acc_pg[PS == 2 ? j : 0], &ab = acc_pb[PS == 2 ? j : 0];
+        if (PS) as = {fma2(p.a, gt.a, as.a), fma2(p.b, gt.b, as.b)};
+        ag = {fma2(x[j].a, u.a, ag.a), fma2(x[j].b, u.b, ag.b)};
+        if (PS == 2) ab = {add2(ab.a, x[j].a), add2(ab.b, x[j].b)};
+        const F4 dy = {mul2(iy, fma2(u.a, by, fma2(x[j].a, g.a, ay))),
+                       mul2(iy, fma2(u.b, by, fma2(x[j].b, g.b, ay)))};
+        if (c0 + 128 * j < d) {
+          store4<true>(static_cast<T *>(a.dy) + out + 128 * j, 0, 0, d, dy);
+          if (a.dgate)
+            store4<true>(static_cast<T *>(a.dgate) + out + 128 * j, 0, 0, d,
+                         F4{mul2(p.a, w.a), mul2(p.b, w.b)});
+        }
+      }
+    }
+    __syncwarp();  // the slot is read before it is filled again
+    s = s + 1 == kSlots ? 0 : s + 1;
+  }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  // the block's column sums, its rows' warps in order
+  float *buf = reinterpret_cast<float *>(smem);  // [rows at once][kRow], over the parameters and rows
+  float *part = a.part + (long long)blockIdx.x * kSums * d;
+  auto gather = [&](int which, const F4 *acc) {
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) store4<true>(buf + warp / WPR * kRow + c0 + 128 * j, 0, 0, d, acc[j]);
+    __syncthreads();
+    for (int c = t; c < d; c += 32 * kRowWarps) {
+      float v = buf[c];
+#pragma unroll
+      for (int w = 1; w < kRowsAtOnce; ++w) v += buf[w * kRow + c];
+      part[which * (long long)d + c] = v;
+    }
+  };
+  if constexpr (NORM_COL) {
+    gather(kNormG, acc_ng);
+    gather(kNormB, acc_nb);
+  }
+  if constexpr (PS > 0) gather(kScale, acc_sc);
+  if constexpr (PS == 2) {
+    gather(kPostG, acc_pg);
+    gather(kPostB, acc_pb);
+  }
+  // a ScaleNorm's g: one value a warp
+  float *scalar = a.scalar_part + (long long)blockIdx.x * kMaxWarps + warp;
+  if constexpr (!NORM_COL) {
+    const float v = warp_sum(sum(add2(acc_ng[0].a, acc_ng[0].b)));
+    if (lane == 0) scalar[0] = v;
+  }
+  if constexpr (PS != 2) {
+    const float v = warp_sum(sum(add2(acc_pg[0].a, acc_pg[0].b)));
+    if (lane == 0) scalar[(long long)gridDim.x * kMaxWarps] = v;
   }
 }
 
@@ -667,7 +1011,9 @@ cudaError_t forward(const Args &a, cudaStream_t stream) {
   const int warps = a.M <= kResidualMaxBlocks ? 1 : 4;
   const dim3 grid((unsigned)((a.M + warps - 1) / warps)), block(32 * warps);
   const int chunks = (a.d + 255) / 256;
-  if (!vectors(a, sizeof(T)) || chunks > 8)
+  const bool params = aligned16(a.norm_g) && aligned16(a.norm_b) && aligned16(a.post_g) &&
+                      aligned16(a.post_b) && aligned16(a.scale);
+  if (!vectors(a, sizeof(T)) || !params || chunks > 8)
     return launch_pdl(residual_norm_any_kernel<T>, grid, block, 0, stream, a);
   switch (chunks) {
     case 1: return launch_pdl(residual_norm_kernel<T, 1>, grid, block, 0, stream, a);
@@ -696,19 +1042,19 @@ Shape shape_of(int d) {
   return s;
 }
 
-template <typename T, bool VEC, int NG, int MAXT>
+template <typename T, bool VEC, int NG, int MAXT, int BLOCKS>
 cudaError_t launch_grad(const Args &a, const Shape &s, int blocks, size_t smem, cudaStream_t stream) {
-  auto kernel = residual_norm_grad_kernel<T, VEC, NG, MAXT>;
-  static size_t allowed[64];  // per device: the largest set so far
+  auto kernel = residual_norm_grad_kernel<T, VEC, NG, MAXT, BLOCKS>;
+  static std::atomic<int> allowed[64];  // per device
   int dev = 0;
   cudaError_t err = cudaGetDevice(&dev);
   if (err != cudaSuccess) return err;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  if (smem > 48 * 1024 && allowed[dev] == 0) {
+  if (!allowed[dev].load(std::memory_order_acquire)) {
     // the most that any call asks for
     err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kGradSmemMax);
     if (err != cudaSuccess) return err;
-    allowed[dev] = kGradSmemMax;
+    allowed[dev].store(1, std::memory_order_release);
   }
   return launch_pdl(kernel, dim3(blocks), dim3(s.threads), smem, stream, a);
 }
@@ -728,9 +1074,15 @@ cudaError_t backward(Args &a, int num_sms, int *blocks_out, cudaStream_t stream)
   const long long few = (warps + 1) / 2;
   if (rows < few) rows = few * (long long)row <= 160 * 1024 ? few : (160 * 1024) / (long long)row;
   if (rows < 1) rows = 1;
-  // few rows in all: spread them over the SMs
-  const long long even = (a.M + num_sms - 1) / num_sms;
+  // few rows in all: spread them over the blocks that fit the SMs
+  const long long even = (a.M + 4LL * num_sms - 1) / (4LL * num_sms);
   if (rows > even) rows = even;
+  // rows of odd widths: as many as keep the tiles on 16-byte boundaries
+  const long long unit = 16 / (int)sizeof(T);
+  if (!VEC && rows >= unit / 2 && (rows + unit - 1) / unit * unit * (long long)row <= 160 * 1024)
+    rows = (rows + unit - 1) / unit * unit;
+  a.flat = rows * a.d * (long long)sizeof(T) % 16 == 0;
+  for (const void *p : {a.h, a.y, a.gate, a.dr, a.dn}) a.flat = a.flat && aligned16(p);
   a.rows = (int)rows;
   a.subsets = s.subsets;
   const size_t pitch = ((size_t)rows * a.d * sizeof(T) + 15) / 16 * 16;
@@ -745,10 +1097,69 @@ cudaError_t backward(Args &a, int num_sms, int *blocks_out, cudaStream_t stream)
   if (blocks > tiles) blocks = tiles;
   *blocks_out = (int)blocks;
   a.scalar_part = a.part + (long long)blocks * s.subsets * kSums * a.d;
-  if (s.groups == 1) return launch_grad<T, VEC, 1, 256>(a, s, (int)blocks, smem, stream);
-  if (s.groups == 2) return launch_grad<T, VEC, 2, 256>(a, s, (int)blocks, smem, stream);
-  if (s.threads <= 256) return launch_grad<T, VEC, 4, 256>(a, s, (int)blocks, smem, stream);
-  return launch_grad<T, VEC, 4, 512>(a, s, (int)blocks, smem, stream);
+  const int n = (int)blocks;
+  if (s.groups == 1) return launch_grad<T, VEC, 1, 256, 2>(a, s, n, smem, stream);
+  if (s.groups == 2) return launch_grad<T, VEC, 2, 256, 1>(a, s, n, smem, stream);
+  if (s.threads <= 256) return launch_grad<T, VEC, 4, 256, 1>(a, s, n, smem, stream);
+  return launch_grad<T, VEC, 4, 512, 1>(a, s, n, smem, stream);
+}
+
+template <typename T, int WPR, int NJ, bool NORM_COL, int PS>
+cudaError_t launch_rows(Args &a, int num_sms, int *blocks_out, cudaStream_t stream) {
+  auto kernel = residual_norm_grad_rows_kernel<T, WPR, NJ, NORM_COL, PS>;
+  // as the kernel lays it out; the column sums' exchange is no larger
+  constexpr size_t row = 128 * NJ * WPR;
+  constexpr size_t smem =
+      (PS == 2 ? 4 : 3) * row * sizeof(float) + kRowWarps * row_slots<T>() * 5 * 128 * NJ * sizeof(T);
+  static_assert(kRowWarps / WPR * row * sizeof(float) <= smem, "exchange of the column sums");
+  static std::atomic<int> fit[64];  // per device: blocks that fit an SM
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  int per_sm = fit[dev].load(std::memory_order_acquire);
+  if (!per_sm) {
+    err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (err != cudaSuccess) return err;
+    err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, 32 * kRowWarps, smem);
+    if (err != cudaSuccess) return err;
+    if (per_sm < 1) per_sm = 1;
+    fit[dev].store(per_sm, std::memory_order_release);
+  }
+  long long blocks = (long long)num_sms * per_sm;
+  if (blocks > kResidualMaxBlocks) blocks = kResidualMaxBlocks;
+  const long long need = (a.M + kRowWarps / WPR - 1) / (kRowWarps / WPR);
+  if (blocks > need) blocks = need;
+  *blocks_out = (int)blocks;
+  a.subsets = 1;
+  a.scalar_part = a.part + (long long)blocks * kSums * a.d;
+  return launch_pdl(kernel, dim3((unsigned)blocks), dim3(32 * kRowWarps), smem, stream, a);
+}
+
+template <typename T, int WPR, int NJ>
+cudaError_t rows_by_sums(Args &a, int num_sms, int *blocks, cudaStream_t stream) {
+  const bool col = a.norm == FLASH_GAU_NORM_LAYER;
+  const int ps = a.post == FLASH_GAU_NORM_LAYER ? 2 : a.scale ? 1 : 0;
+  switch (ps + (col ? 3 : 0)) {
+    case 0: return launch_rows<T, WPR, NJ, false, 0>(a, num_sms, blocks, stream);
+    case 1: return launch_rows<T, WPR, NJ, false, 1>(a, num_sms, blocks, stream);
+    case 2: return launch_rows<T, WPR, NJ, false, 2>(a, num_sms, blocks, stream);
+    case 3: return launch_rows<T, WPR, NJ, true, 0>(a, num_sms, blocks, stream);
+    case 4: return launch_rows<T, WPR, NJ, true, 1>(a, num_sms, blocks, stream);
+    default: return launch_rows<T, WPR, NJ, true, 2>(a, num_sms, blocks, stream);
+  }
+}
+
+// rows on 16-byte boundaries of up to 2048 columns: up to 512 columns a warp,
+// fewer where that leaves registers for more warps
+template <typename T>
+cudaError_t backward_vec(Args &a, int num_sms, int *blocks, cudaStream_t stream) {
+  if (a.d <= 256) return rows_by_sums<T, 1, 2>(a, num_sms, blocks, stream);
+  if (a.d <= 512) return rows_by_sums<T, 2, 2>(a, num_sms, blocks, stream);
+  if (a.d <= 768) return rows_by_sums<T, 2, 3>(a, num_sms, blocks, stream);
+  if (a.d <= 1024) return rows_by_sums<T, 2, 4>(a, num_sms, blocks, stream);
+  if (a.d <= 2048) return rows_by_sums<T, 4, 4>(a, num_sms, blocks, stream);
+  return backward<T, true>(a, num_sms, blocks, stream);
 }
 
 Args args_of(const ResidualProblem &q) {
@@ -798,10 +1209,10 @@ cudaError_t residual_norm_grad(const ResidualProblem &q, const void *dr, const v
   int blocks = 0;
   cudaError_t err;
   if (q.dtype == FLASH_GAU_BF16)
-    err = vectors(a, 2) ? backward<__nv_bfloat16, true>(a, q.num_sms, &blocks, q.stream)
+    err = vectors(a, 2) ? backward_vec<__nv_bfloat16>(a, q.num_sms, &blocks, q.stream)
                         : backward<__nv_bfloat16, false>(a, q.num_sms, &blocks, q.stream);
   else
-    err = vectors(a, 4) ? backward<float, true>(a, q.num_sms, &blocks, q.stream)
+    err = vectors(a, 4) ? backward_vec<float>(a, q.num_sms, &blocks, q.stream)
                         : backward<float, false>(a, q.num_sms, &blocks, q.stream);
   if (err != cudaSuccess) return err;
   SumArgs s = {};
@@ -809,7 +1220,7 @@ cudaError_t residual_norm_grad(const ResidualProblem &q, const void *dr, const v
   s.scalar_part = a.scalar_part;
   s.parts = blocks * a.subsets;
   s.blocks = blocks;
-  s.warps = shape_of(q.d).threads / 32;
+  s.warps = a.rows ? shape_of(q.d).threads / 32 : kRowWarps;
   s.d = q.d;
   s.out[kNormG] = a.norm ? g.dnorm_g : nullptr;
   s.out[kNormB] = a.norm == FLASH_GAU_NORM_LAYER ? g.dnorm_b : nullptr;
