@@ -20,9 +20,9 @@
 // The work is memory traffic: 28 bytes a parameter with fp32 moments (p, m, v
 // in and out, g in), 16 with 8-bit ones, 2 more for a bf16 copy.  The list
 // goes into the kernel's parameters, so that a step is one launch (per 384
-// tensors), needs no workspace and can be captured; a block takes 2048
-// elements of one tensor, a warp 256 of them as two runs of 128, four
-// consecutive elements a lane (16-byte accesses).
+// tensors), needs no workspace and can be captured; a warp takes 256 elements
+// of one tensor at a time as two runs of 128, four consecutive elements a lane
+// (16-byte accesses).
 #include <cuda_bf16.h>
 #include <math.h>
 
@@ -32,9 +32,9 @@
 namespace flashgau {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kBlock = 256;                    // elements that share a scale
-constexpr int kChunk = kThreads / 32 * kBlock;  // elements of a thread block
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kBlock = 256;  // elements that share a scale; a warp's at a time
+constexpr int kRuns = 4;     // of them a warp takes from a long list
 
 struct Entry {
   float *p;
@@ -48,12 +48,18 @@ struct Entry {
   int g_bf16, vec;  // vec: every pointer aligned for four elements at a time
 };
 
+// The scalars of a step.
+struct Step {
+  float step_size, beta1, omb1, beta2, omb2, inv_c2, eps;
+  const float *grad_scale;
+};
+
 template <int CAP>
 struct List {
   Entry e[CAP];
   int count;
-  float step_size, beta1, omb1, beta2, omb2, inv_c2, eps;
-  const float *grad_scale;
+  int runs;  // blocks of 256 elements that a warp takes
+  Step step;
 };
 
 // the tensor of this thread block: the last entry whose first block is not
@@ -69,9 +75,11 @@ __device__ __forceinline__ int find(const List<CAP> &l, int b) {
   return lo;
 }
 
-// Four elements at i of an fp32 array, of which `n` are inside.
-__device__ __forceinline__ void load4(const float *a, long long i, int n, int vec, float (&x)[4]) {
-  if (vec && n == 4) {
+// Four elements at i of an array, of which `n` are inside (FULL: all, on a
+// boundary of four).
+template <bool FULL>
+__device__ __forceinline__ void load4(const float *a, long long i, int n, float (&x)[4]) {
+  if (FULL) {
     const float4 t = *reinterpret_cast<const float4 *>(a + i);
     x[0] = t.x; x[1] = t.y; x[2] = t.z; x[3] = t.w;
   } else {
@@ -79,9 +87,10 @@ __device__ __forceinline__ void load4(const float *a, long long i, int n, int ve
     for (int q = 0; q < 4; ++q) x[q] = q < n ? a[i + q] : 0.f;
   }
 }
-__device__ __forceinline__ void load4(const __nv_bfloat16 *a, long long i, int n, int vec,
+template <bool FULL>
+__device__ __forceinline__ void load4(const __nv_bfloat16 *a, long long i, int n,
                                       float (&x)[4]) {
-  if (vec && n == 4) {
+  if (FULL) {
     const uint2 t = *reinterpret_cast<const uint2 *>(a + i);
     const float2 u = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&t.x));
     const float2 w = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&t.y));
@@ -91,8 +100,9 @@ __device__ __forceinline__ void load4(const __nv_bfloat16 *a, long long i, int n
     for (int q = 0; q < 4; ++q) x[q] = q < n ? __bfloat162float(a[i + q]) : 0.f;
   }
 }
-__device__ __forceinline__ void store4(float *a, long long i, int n, int vec, const float (&x)[4]) {
-  if (vec && n == 4) {
+template <bool FULL>
+__device__ __forceinline__ void store4(float *a, long long i, int n, const float (&x)[4]) {
+  if (FULL) {
     *reinterpret_cast<float4 *>(a + i) = make_float4(x[0], x[1], x[2], x[3]);
   } else {
 #pragma unroll
@@ -100,9 +110,10 @@ __device__ __forceinline__ void store4(float *a, long long i, int n, int vec, co
       if (q < n) a[i + q] = x[q];
   }
 }
-__device__ __forceinline__ void store4(__nv_bfloat16 *a, long long i, int n, int vec,
+template <bool FULL>
+__device__ __forceinline__ void store4(__nv_bfloat16 *a, long long i, int n,
                                        const float (&x)[4]) {
-  if (vec && n == 4) {
+  if (FULL) {
     const __nv_bfloat162 u = __floats2bfloat162_rn(x[0], x[1]), w = __floats2bfloat162_rn(x[2], x[3]);
     uint2 t;
     t.x = *reinterpret_cast<const uint32_t *>(&u);
@@ -115,18 +126,20 @@ __device__ __forceinline__ void store4(__nv_bfloat16 *a, long long i, int n, int
   }
 }
 // Four codes as one word (byte q: element q).
-__device__ __forceinline__ uint32_t load_codes(const void *a, long long i, int n, int vec) {
+template <bool FULL>
+__device__ __forceinline__ uint32_t load_codes(const void *a, long long i, int n) {
   const uint8_t *c = static_cast<const uint8_t *>(a) + i;
-  if (vec && n == 4) return *reinterpret_cast<const uint32_t *>(c);
+  if (FULL) return *reinterpret_cast<const uint32_t *>(c);
   uint32_t w = 0;
 #pragma unroll
   for (int q = 0; q < 4; ++q)
     if (q < n) w |= (uint32_t)c[q] << (8 * q);
   return w;
 }
-__device__ __forceinline__ void store_codes(void *a, long long i, int n, int vec, uint32_t w) {
+template <bool FULL>
+__device__ __forceinline__ void store_codes(void *a, long long i, int n, uint32_t w) {
   uint8_t *c = static_cast<uint8_t *>(a) + i;
-  if (vec && n == 4) {
+  if (FULL) {
     *reinterpret_cast<uint32_t *>(c) = w;
   } else {
 #pragma unroll
@@ -135,13 +148,27 @@ __device__ __forceinline__ void store_codes(void *a, long long i, int n, int vec
   }
 }
 
+// Codes to and from fp32 without the conversion unit, which a step over 8-bit
+// moments would keep busier than memory: a byte becomes the low digits of
+// 2^23 (read) or is what adding 1.5 * 2^23 leaves in them (written, rounded to
+// nearest even, negative values as two's complement).
+__device__ __forceinline__ float byte_float(uint32_t w, int q, float bias) {
+  return __fadd_rn(__uint_as_float(__byte_perm(w, 0x4b000000u, 0x7650 | q)), -bias);
+}
+// four codes of first moments are read as w ^ 0x80808080
 __device__ __forceinline__ float decode_m(uint32_t w, int q, float scale) {
-  const int c = (int8_t)(w >> (8 * q));
-  return __fmul_rn((float)(c * abs(c)), scale);
+  const float c = byte_float(w, q, 8388608.0f + 128.0f);
+  return __fmul_rn(__fmul_rn(c, fabsf(c)), scale);
 }
 __device__ __forceinline__ float decode_root(uint32_t w, int q, float scale) {
-  const int c = (int)((w >> (8 * q)) & 255u);
-  return __fmul_rn((float)(c * c), scale);
+  const float c = byte_float(w, q, 8388608.0f);
+  return __fmul_rn(__fmul_rn(c, c), scale);
+}
+__device__ __forceinline__ uint32_t code_bits(float x) {
+  return __float_as_uint(__fadd_rn(x, 12582912.0f));
+}
+__device__ __forceinline__ uint32_t pack_codes(const uint32_t (&c)[4]) {
+  return __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
 }
 
 // A block's scale and its inverse from the largest magnitude (as bits: a
@@ -154,40 +181,69 @@ __device__ __forceinline__ void block_scale(uint32_t bits, float *scale, float *
   *inv = live ? __fmul_rn(__frcp_rn(big), (float)(TOP * TOP)) : 0.f;
 }
 
-template <int BITS, int CAP>
-__global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ List<CAP> l) {
-  ptx::griddep_wait();
-  const Entry &e = l.e[find(l, blockIdx.x)];
-  const int lane = threadIdx.x & 31;
-  const long long blk = (long long)(blockIdx.x - e.first) * (kChunk / kBlock) + (threadIdx.x >> 5);
+// The codes of eight elements, from correctly rounded roots or (EXACT not set)
+// from the hardware's approximate ones; then the return value says how far
+// from an integer the roots came at most.
+template <bool EXACT>
+__device__ __forceinline__ float encode(const float (&m)[2][4], const float (&root)[2][4], float mi,
+                                        float vi, float keep, uint32_t (&mw)[2], uint32_t (&vw)[2]) {
+  float off = 0.f;
+  auto rooted = [&](float x) {
+    if (EXACT) return __fsqrt_rn(x);
+    float y;
+    asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    const float whole = __fadd_rn(__fadd_rn(y, 12582912.0f), -12582912.0f);
+    off = fmaxf(off, fabsf(__fadd_rn(y, -whole)));
+    return y;
+  };
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    uint32_t mq[4], vq[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      // the block's largest value comes out a rounding above 127 or 255 at
+      // most, and rounds to it
+      mq[q] = code_bits(copysignf(rooted(__fmul_rn(fabsf(m[j][q]), mi)), m[j][q]));
+      vq[q] = code_bits(fmaxf(rooted(__fmul_rn(root[j][q], vi)), __saturatef(root[j][q] * keep)));
+    }
+    mw[j] = pack_codes(mq);
+    vw[j] = pack_codes(vq);
+  }
+  return off;
+}
+
+// One warp's 256 elements of a tensor, block `blk` of it.
+template <int BITS, bool FULL>
+__device__ __forceinline__ void update(const Entry &e, const Step &l, long long blk, int lane,
+                                       float gs) {
   const long long i0 = blk * kBlock + 4 * lane;
-  if (blk * kBlock >= e.n) return;
-  const float gs = l.grad_scale ? *l.grad_scale : 1.f;
   int n[2];
   float p[2][4], g[2][4], m[2][4], v[2][4];
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
     const long long i = i0 + 128 * j, left = e.n - i;
-    n[j] = left >= 4 ? 4 : (left > 0 ? (int)left : 0);
-    load4(e.p, i, n[j], e.vec, p[j]);
-    if (e.g_bf16) load4(static_cast<const __nv_bfloat16 *>(e.g), i, n[j], e.vec, g[j]);
-    else load4(static_cast<const float *>(e.g), i, n[j], e.vec, g[j]);
+    n[j] = FULL || left >= 4 ? 4 : (left > 0 ? (int)left : 0);
+    load4<FULL>(e.p, i, n[j], p[j]);
+    if (e.g_bf16) load4<FULL>(static_cast<const __nv_bfloat16 *>(e.g), i, n[j], g[j]);
+    else load4<FULL>(static_cast<const float *>(e.g), i, n[j], g[j]);
     if constexpr (BITS == 32) {
-      load4(static_cast<const float *>(e.m), i, n[j], e.vec, m[j]);
-      load4(static_cast<const float *>(e.v), i, n[j], e.vec, v[j]);
+      load4<FULL>(static_cast<const float *>(e.m), i, n[j], m[j]);
+      load4<FULL>(static_cast<const float *>(e.v), i, n[j], v[j]);
     }
   }
   if constexpr (BITS == 8) {
     const float ms = e.m_scale[blk], vs = e.v_scale[blk];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      const uint32_t mc = load_codes(e.m, i0 + 128 * j, n[j], e.vec);
-      const uint32_t vc = load_codes(e.v, i0 + 128 * j, n[j], e.vec);
+      const uint32_t mc = load_codes<FULL>(e.m, i0 + 128 * j, n[j]) ^ 0x80808080u;
+      const uint32_t vc = load_codes<FULL>(e.v, i0 + 128 * j, n[j]);
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         m[j][q] = decode_m(mc, q, ms);
         const float r = decode_root(vc, q, vs);
         v[j][q] = __fmul_rn(r, r);
+        // codes that were not read behind the end stand for zero
+        if (!FULL && q >= n[j]) m[j][q] = 0.f;
       }
     }
   }
@@ -197,11 +253,13 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
   for (int j = 0; j < 2; ++j)
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      const float gg = l.grad_scale ? __fmul_rn(g[j][q], gs) : g[j][q];
+      const float gg = __fmul_rn(g[j][q], gs);  // exact where gs is one
       m[j][q] = __fadd_rn(__fmul_rn(m[j][q], l.beta1), __fmul_rn(gg, l.omb1));
       v[j][q] = __fadd_rn(__fmul_rn(v[j][q], l.beta2), __fmul_rn(__fmul_rn(gg, l.omb2), gg));
       root[j][q] = __fsqrt_rn(v[j][q]);
-      p[j][q] = p[j][q] * e.decay - l.step_size * m[j][q] / fmaf(root[j][q], l.inv_c2, l.eps);
+      // a quotient of 2 units in the last place is far finer than p's own digits
+      p[j][q] = fmaf(p[j][q], e.decay,
+                     -__fdividef(l.step_size * m[j][q], fmaf(root[j][q], l.inv_c2, l.eps)));
       if (BITS == 8) {
         mmax = max(mmax, __float_as_uint(m[j][q]) & 0x7fffffffu);
         rmax = max(rmax, __float_as_uint(root[j][q]) & 0x7fffffffu);
@@ -210,11 +268,11 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
     const long long i = i0 + 128 * j;
-    store4(e.p, i, n[j], e.vec, p[j]);
-    if (e.copy) store4(e.copy, i, n[j], e.vec, p[j]);
+    store4<FULL>(e.p, i, n[j], p[j]);
+    if (e.copy) store4<FULL>(e.copy, i, n[j], p[j]);
     if constexpr (BITS == 32) {
-      store4(static_cast<float *>(e.m), i, n[j], e.vec, m[j]);
-      store4(static_cast<float *>(e.v), i, n[j], e.vec, v[j]);
+      store4<FULL>(static_cast<float *>(e.m), i, n[j], m[j]);
+      store4<FULL>(static_cast<float *>(e.v), i, n[j], v[j]);
     }
   }
   if constexpr (BITS == 8) {
@@ -228,38 +286,51 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
       e.m_scale[blk] = ms;
       e.v_scale[blk] = vs;
     }
+    // a nonzero sqrt(v) keeps a code of at least 1 (it is at least 2^-75)
+    const float keep = vs != 0.f ? 0x1p100f : 0.f;
+uint32_t mw[2], vw[2];
+    const float off = encode<false>(m, root, mi, vi, keep, mw, vw);
+    // A root off by 2^-23 of itself, 2^-15 at 255, rounds as the exact one
+    // does unless it comes this near to the middle between two codes.
+    if (off > 0.5f - 0x1p-14f) encode<true>(m, root, mi, vi, keep, mw, vw);
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      uint32_t mw = 0, vw = 0;
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        int c = min(__float2int_rn(__fsqrt_rn(__fmul_rn(fabsf(m[j][q]), mi))), 127);
-        if (m[j][q] < 0.f) c = -c;
-        mw |= (uint32_t)(c & 255) << (8 * q);
-        int r = min(__float2int_rn(__fsqrt_rn(__fmul_rn(root[j][q], vi))), 255);
-        if (r == 0 && root[j][q] > 0.f && vs != 0.f) r = 1;
-        vw |= (uint32_t)r << (8 * q);
-      }
-      store_codes(e.m, i0 + 128 * j, n[j], e.vec, mw);
-      store_codes(e.v, i0 + 128 * j, n[j], e.vec, vw);
+      store_codes<FULL>(e.m, i0 + 128 * j, n[j], mw[j]);
+      store_codes<FULL>(e.v, i0 + 128 * j, n[j], vw[j]);
     }
   }
 }
 
-// m and v of 8-bit moments as fp32: `p` holds m's values, `copy` v's.
-template <int CAP>
-__global__ void __launch_bounds__(kThreads) moments_kernel(const __grid_constant__ List<CAP> l) {
-  ptx::griddep_wait();
+// Calls f(entry, block, lane, full) for each of this warp's blocks.
+template <int CAP, typename F>
+__device__ __forceinline__ void each_block(const List<CAP> &l, F f) {
   const Entry &e = l.e[find(l, blockIdx.x)];
   const int lane = threadIdx.x & 31;
-  const long long blk = (long long)(blockIdx.x - e.first) * (kChunk / kBlock) + (threadIdx.x >> 5);
-  if (blk * kBlock >= e.n) return;
+  long long blk = ((long long)(blockIdx.x - e.first) * kWarps + (threadIdx.x >> 5)) * l.runs;
+  const long long end = min(blk + l.runs, (e.n + kBlock - 1) / kBlock);
+  for (; blk < end; ++blk) f(e, blk, lane, e.vec && blk * kBlock + kBlock <= e.n);
+}
+
+template <int BITS, int CAP>
+__global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ List<CAP> l) {
+  ptx::griddep_wait();
+  const float gs = l.step.grad_scale ? *l.step.grad_scale : 1.f;
+  each_block(l, [&](const Entry &e, long long blk, int lane, bool full) {
+    if (full) update<BITS, true>(e, l.step, blk, lane, gs);
+    else update<BITS, false>(e, l.step, blk, lane, gs);
+  });
+}
+
+// m and v of 8-bit moments as fp32: `p` holds m's values, `copy` v's.
+template <bool FULL>
+__device__ __forceinline__ void values(const Entry &e, long long blk, int lane) {
   const float ms = e.m_scale[blk], vs = e.v_scale[blk];
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
     const long long i = blk * kBlock + 4 * lane + 128 * j, left = e.n - i;
-    const int n = left >= 4 ? 4 : (left > 0 ? (int)left : 0);
-    const uint32_t mc = load_codes(e.m, i, n, e.vec), vc = load_codes(e.v, i, n, e.vec);
+    const int n = FULL || left >= 4 ? 4 : (left > 0 ? (int)left : 0);
+    const uint32_t mc = load_codes<FULL>(e.m, i, n) ^ 0x80808080u;
+    const uint32_t vc = load_codes<FULL>(e.v, i, n);
     float m[4], v[4];
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
@@ -267,24 +338,41 @@ __global__ void __launch_bounds__(kThreads) moments_kernel(const __grid_constant
       const float r = decode_root(vc, q, vs);
       v[q] = __fmul_rn(r, r);
     }
-    store4(e.p, i, n, e.vec, m);
-    store4(reinterpret_cast<float *>(e.copy), i, n, e.vec, v);
+    store4<FULL>(e.p, i, n, m);
+    store4<FULL>(reinterpret_cast<float *>(e.copy), i, n, v);
   }
+}
+
+template <int CAP>
+__global__ void __launch_bounds__(kThreads, 8) moments_kernel(const __grid_constant__ List<CAP> l) {
+  ptx::griddep_wait();
+  each_block(l, [&](const Entry &e, long long blk, int lane, bool full) {
+    if (full) values<true>(e, blk, lane);
+    else values<false>(e, blk, lane);
+  });
 }
 
 bool aligned(const void *p, unsigned bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
 
-template <int CAP, typename Kernel, typename Fill>
+template <int BITS, int CAP, typename Kernel, typename Fill>
 cudaError_t run(Kernel kernel, const AdamwProblem &q, Fill fill) {
   List<CAP> l;
-  l.step_size = (float)(q.lr / (1.0 - pow(q.beta1, (double)q.step)));
-  l.beta1 = (float)q.beta1;
-  l.omb1 = (float)(1.0 - q.beta1);
-  l.beta2 = (float)q.beta2;
-  l.omb2 = (float)(1.0 - q.beta2);
-  l.inv_c2 = (float)(1.0 / sqrt(1.0 - pow(q.beta2, (double)q.step)));
-  l.eps = (float)q.eps;
-  l.grad_scale = q.grad_scale;
+  l.step.step_size = (float)(q.lr / (1.0 - pow(q.beta1, (double)q.step)));
+  l.step.beta1 = (float)q.beta1;
+  l.step.omb1 = (float)(1.0 - q.beta1);
+  l.step.beta2 = (float)q.beta2;
+  l.step.omb2 = (float)(1.0 - q.beta2);
+  l.step.inv_c2 = (float)(1.0 / sqrt(1.0 - pow(q.beta2, (double)q.step)));
+  l.step.eps = (float)q.eps;
+  l.step.grad_scale = q.grad_scale;
+  // 8-bit moments are bound by instructions as much as by memory: of long
+  // lists a warp takes several blocks, so that finding its tensor counts for
+  // little (model of 82 M parameters: 0.36 -> 0.27 ms); with fp32 moments that
+  // costs registers and gains nothing (0.183 -> 0.188 ms for 44 M)
+  long long n = 0;
+  for (int k = 0; k < q.n_tensors; ++k) n += q.tensors[k].n;
+  l.runs = BITS == 8 && n >= (1LL << 22) ? kRuns : 1;
+  const long long chunk = (long long)kWarps * kBlock * l.runs;
   for (int k = 0; k < q.n_tensors;) {
     l.count = 0;
     long long blocks = 0;
@@ -292,7 +380,7 @@ cudaError_t run(Kernel kernel, const AdamwProblem &q, Fill fill) {
     for (; k < q.n_tensors && l.count < CAP; ++k) {
       const flash_gau_adamw_tensor &t = q.tensors[k];
       if (t.n == 0) continue;
-      const long long b = (t.n + kChunk - 1) / kChunk;
+      const long long b = (t.n + chunk - 1) / chunk;
       if (l.count && blocks + b > 0x7fffffffLL) break;
       Entry &e = l.e[l.count++];
       fill(k, e);
@@ -330,10 +418,10 @@ cudaError_t adamw_step(const AdamwProblem &q) {
             aligned(t.m, state) && aligned(t.v, state);
   };
   if (q.n_tensors <= kSmall)
-    return q.state_bits == 8 ? run<kSmall>(adamw_kernel<8, kSmall>, q, fill)
-                             : run<kSmall>(adamw_kernel<32, kSmall>, q, fill);
-  return q.state_bits == 8 ? run<kLarge>(adamw_kernel<8, kLarge>, q, fill)
-                           : run<kLarge>(adamw_kernel<32, kLarge>, q, fill);
+    return q.state_bits == 8 ? run<8, kSmall>(adamw_kernel<8, kSmall>, q, fill)
+                             : run<32, kSmall>(adamw_kernel<32, kSmall>, q, fill);
+  return q.state_bits == 8 ? run<8, kLarge>(adamw_kernel<8, kLarge>, q, fill)
+                           : run<32, kLarge>(adamw_kernel<32, kLarge>, q, fill);
 }
 
 cudaError_t adamw_moments(const AdamwProblem &q, float *const *m_out, float *const *v_out) {
@@ -348,8 +436,8 @@ cudaError_t adamw_moments(const AdamwProblem &q, float *const *m_out, float *con
     e.v_scale = t.v_scale;
     e.vec = aligned(e.p, 16) && aligned(e.copy, 16) && aligned(t.m, 4) && aligned(t.v, 4);
   };
-  return q.n_tensors <= kSmall ? run<kSmall>(moments_kernel<kSmall>, q, fill)
-                               : run<kLarge>(moments_kernel<kLarge>, q, fill);
+  return q.n_tensors <= kSmall ? run<32, kSmall>(moments_kernel<kSmall>, q, fill)
+                               : run<32, kLarge>(moments_kernel<kLarge>, q, fill);
 }
 
 }  // namespace flashgau

@@ -314,19 +314,29 @@ cudaError_t residual_norm(const ResidualProblem &q, const void *h, void *r, void
 cudaError_t residual_norm_grad(const ResidualProblem &q, const void *dr, const void *dn,
                                const void *r, const flash_gau_residual_grads &g, void *workspace);
 
-// Cross entropy over a vocabulary (xent.cu bf16, xent_f32.cu fp32).
+// Cross entropy over a vocabulary (xent.cu).  Rows are those of the tokens
+// with a label, one behind another; a piece is a range of them.
 struct XentLayout {
+  // one 256-byte slot
   int *status;       // FLASH_GAU_ETIMEOUT on a timed-out wait
-  float *factor;     // the gradients' factor: scale, or scale / number of labels
-  long long piece;   // tokens of a piece
-  long long ldE;     // columns between rows of E
-  float *ref;        // [piece] bf16: the label's logit, in units of ln 2
-  float *row_scale;  // [piece] bf16: factor / normaliser
-  float2 *part;      // [V / 128][piece] bf16: (reference, sum) of 128 words
-  void *E;           // [piece, ldE] bf16: exp(l - reference); fp32: the logits, then P
-  void *Xs;          // [piece, d] bf16: scaled rows of X
-  float *dx_part;    // [splits][piece][d] parts of dX
-  float *dw_sum;     // [V, d] bf16, several pieces: the sum of their dW
+  int *live;         // rows
+  int *done;         // blocks that have finished
+  float *factor;     // the gradients' factor: scale, or scale / rows
+  int *index;        // [N] the token a row belongs to
+  int *labels;       // [N, whole tiles] its label, -1 behind the last row
+  float *ref;        // [N] its label's logit, in units of ln 2
+  void *Xc;          // [piece][terms][term] bf16: rows of X, then scaled
+  int term;          // columns of a term: d, or for fp32 whole k-blocks
+  void *Ws;          // [V][3][term] bf16: W's terms (fp32)
+  long long piece;   // rows of a piece, whole tiles
+  float *row_scale;  // [piece] factor / normaliser
+  float2 *part;      // [V / 128][piece] (reference, sum) of 128 words
+  void *E;           // [piece][terms][ldE] bf16: exp(l - reference)
+  long long ldE;
+  float *dx_part;    // parts of dX, 256 rows each
+  int ld_part;
+  float *dw_sum;     // [V][ld_dw] dW of several pieces, or of rows that TMA
+  int ld_dw;         // cannot store; null: dW is written directly
 };
 struct XentProblem {
   const void *X, *W;
@@ -340,14 +350,15 @@ struct XentProblem {
   int num_sms;
   cudaStream_t stream;
 };
-// splits of dX's sum over the words, planned for a whole GB300 (the workspace
-// is sized without a device)
+// the plan of dX's sum, made for a whole GB300: the workspace is sized without
+// a device
 constexpr int kXentPlanSms = 152;
-int xent_dx_splits(int rows, int d, int V);
-int xent_f32_dx_splits(int rows, int d, int V);
-cudaError_t xent_bf16(const XentProblem &q);
-cudaError_t xent_f32(const XentProblem &q);
-cudaError_t xent_total(const XentProblem &q);
+constexpr int kXentFewBlocks = 4 * 152, kXentFewSmem = 64 * 1024;
+size_t xent_dx_part_rows(long long rows);
+// whether a call takes the form for a few tokens, whose workspace is the
+// slot, `ref` and `part` alone
+bool xent_few(long long N, int d, int dtype, bool grad);
+cudaError_t xent(const XentProblem &q, int dtype);
 
 using StageFn = cudaError_t (*)(const Problem &);
 

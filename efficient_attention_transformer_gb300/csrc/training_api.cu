@@ -1,6 +1,6 @@
 // C ABI of the operators around the layer in a training step: argument
 // checks, then the launches on the caller's stream (kernels in
-// residual_norm.cu, adamw.cu, xent.cu and xent_f32.cu).
+// residual_norm.cu, adamw.cu and xent.cu).
 #include <math.h>
 
 #include "flash_gau_internal.h"
@@ -83,51 +83,51 @@ int check_xent(long long N, int d, int V, int dtype) {
 
 size_t xent_layout(long long N, int d, int V, int dtype, bool grad, char *base, XentLayout *L) {
   const bool bf16 = dtype == FLASH_GAU_BF16;
-  const size_t io = bf16 ? 2 : 4;
+  const size_t terms = bf16 ? 1 : 3;
   XentLayout l = {};
-  l.ldE = ((long long)V + 63) / 64 * 64;
-  // whole tiles of tokens, pieces of about the same size
-  long long most = (long long)(kPieceBytes / (l.ldE * io)) / 256 * 256;
-  if (most < 256) most = 256;
-  if (!bf16 && most > 65535LL * 128) most = 65535LL * 128;  // grid rows of the products
-  if (bf16 && !grad) {
-    // only the sums of 128 words are held: at most 256 MiB of them
-    most = (long long)(kPieceBytes / 8 / (((size_t)V + 127) / 128 * sizeof(float2))) / 256 * 256;
-    if (most < 256) most = 256;
-  }
-  const long long about = (N + most - 1) / most;
-  const long long even = ((N + about - 1) / about + 255) / 256 * 256;
-  l.piece = N < even ? N : even;
-  const long long pieces = (N + l.piece - 1) / l.piece;
   size_t off = 0;
   auto take = [&](size_t bytes) -> char * {
     char *p = base ? base + off : nullptr;
     off = (off + bytes + kAlign - 1) / kAlign * kAlign;
     return p;
   };
-  const size_t n = (size_t)l.piece;
-  l.status = reinterpret_cast<int *>(take(sizeof(int)));
-  l.factor = reinterpret_cast<float *>(take(sizeof(float)));
-  if (bf16) {
-    l.ref = reinterpret_cast<float *>(take(n * 4));
-    l.part = reinterpret_cast<float2 *>(take(((size_t)V + 127) / 128 * n * sizeof(float2)));
+  l.status = reinterpret_cast<int *>(take(kAlign));
+  l.live = l.status + 16;
+  l.done = l.status + 17;
+  l.factor = reinterpret_cast<float *>(l.status + 18);
+  const size_t parts = ((size_t)V + 127) / 128;
+  if (xent_few(N, d, dtype, grad)) {
+    l.ref = reinterpret_cast<float *>(take(8 * sizeof(float)));
+    l.part = reinterpret_cast<float2 *>(take(kXentFewBlocks * 8 * sizeof(float2)));
+    if (L) *L = l;
+    return off;
   }
-  if (bf16 && grad) {
-    l.row_scale = reinterpret_cast<float *>(take(n * 4));
-    l.Xs = take(n * d * 2);
-    if (pieces > 1) l.dw_sum = reinterpret_cast<float *>(take((size_t)V * d * 4));
-  }
+  l.ldE = ((long long)V + 63) / 64 * 64;
+  l.term = bf16 ? d : (d + 63) / 64 * 64;
+  // whole tiles of rows, pieces of about the same size: [rows, V] of E, or
+  // without gradients an eighth of that of the sums of 128 words
+  const size_t row = grad ? terms * l.ldE * 2 : 8 * parts * sizeof(float2);
+  long long most = (long long)(kPieceBytes / row) / 256 * 256;
+  if (most < 256) most = 256;
+  const long long about = (N + most - 1) / most;
+  l.piece = ((N + about - 1) / about + 255) / 256 * 256;
+  const long long pieces = (N + l.piece - 1) / l.piece;
+  const size_t rows = ((size_t)N + 255) / 256 * 256, n = (size_t)l.piece;
+  l.index = reinterpret_cast<int *>(take(rows * 4));
+  l.labels = reinterpret_cast<int *>(take(rows * 4));
+  l.ref = reinterpret_cast<float *>(take(rows * 4));
+  l.Xc = take(n * terms * l.term * 2);
+  if (!bf16) l.Ws = take((size_t)V * terms * l.term * 2);
+  l.part = reinterpret_cast<float2 *>(take(parts * n * sizeof(float2)));
   if (grad) {
-    // the last piece may be shorter and split further
-    size_t parts = 0;
-    for (long long rows : {l.piece, N - (pieces - 1) * l.piece}) {
-      const int s = bf16 ? xent_dx_splits((int)rows, d, V) : xent_f32_dx_splits((int)rows, d, V);
-      const size_t b = s > 1 ? (size_t)s * ((rows + 31) / 32 * 32) * d * 4 : 0;
-      parts = b > parts ? b : parts;
-    }
-    l.dx_part = reinterpret_cast<float *>(take(parts));
+    l.row_scale = reinterpret_cast<float *>(take(n * 4));
+    l.E = take(n * terms * l.ldE * 2);
+    l.ld_part = (d + 63) / 64 * 64;
+    l.dx_part = reinterpret_cast<float *>(take(xent_dx_part_rows(l.piece) * l.ld_part * 4));
+    l.ld_dw = (d + 3) / 4 * 4;
+    if (pieces > 1 || (!bf16 && d % 4 != 0))
+      l.dw_sum = reinterpret_cast<float *>(take((size_t)V * l.ld_dw * 4));
   }
-  if (grad || !bf16) l.E = take(n * l.ldE * io);
   if (L) *L = l;
   return off;
 }
@@ -246,9 +246,9 @@ int flash_gau_xent(const void *X, const void *W, const int *labels, long long N,
   int st = check_xent(N, d, V, dtype);
   if (st != FLASH_GAU_OK) return st;
   const bool bf16 = dtype == FLASH_GAU_BF16, grad = out->dX || out->dW;
-  const size_t align = bf16 ? 16 : 4, io = bf16 ? 2 : 4;
+  const size_t io = bf16 ? 2 : 4;
   for (const void *p : {X, W, (const void *)out->dX, (const void *)out->dW})
-    if (!aligned(p, align)) return FLASH_GAU_EINVAL;
+    if (!aligned(p, 16)) return FLASH_GAU_EINVAL;
   for (const void *p : {(const void *)labels, (const void *)out->total, (const void *)out->loss,
                         (const void *)out->lse})
     if (!aligned(p, 4)) return FLASH_GAU_EINVAL;
@@ -275,7 +275,7 @@ int flash_gau_xent(const void *X, const void *W, const int *labels, long long N,
   q.dX = out->dX;
   q.dW = out->dW;
   q.stream = static_cast<cudaStream_t>(stream);
-  return status_of(bf16 ? xent_bf16(q) : xent_f32(q));
+  return status_of(xent(q, dtype));
 }
 
 int flash_gau_adamw_step(const flash_gau_adamw_tensor *tensors, int n_tensors,

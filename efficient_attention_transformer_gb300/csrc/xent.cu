@@ -1,34 +1,52 @@
 // Softmax cross entropy of the logits X W^T over a vocabulary, with the
-// gradients of X [N, d] and W [V, d], bf16 operands, fp32 accumulation:
+// gradients of X [N, d] and W [V, d]:
 //   l = x W^T     loss = log sum_v exp(l_v) - l_y
 //   dX_i = g (sum_v p_iv W_v - W_y)      dW_v = g sum_i (p_iv - [v = y_i]) x_i
-// The tokens are taken in pieces (xent_plan), so that no more than a piece's
-// [Nc, V] is held at any time, and the logits themselves are never stored.
+//
+// Tokens without a label cost nothing: xent_gather_kernel first copies the
+// others' rows behind one another (their number stays on the device, and the
+// kernels behind it take their tile counts from there).  The rows are then
+// taken in pieces, so that no more than a piece's [tokens, V] is held at any
+// time, and the logits themselves are never stored.
 //
 // The logits are formed once, 6 N d V operations in all: the product's
 // epilogue needs the row's normaliser for p = exp(l - lse), which is known
 // only after the last word, so it writes E = exp(l - ref) with a reference
 // that is known before the product, the label's logit t (a dot product a row,
-// xent_target_kernel).  E rounded to bf16 keeps its relative precision
-// whatever its size, and sum_v p_v >= p_y makes sum_v E >= 1: nothing that
-// counts is lost below.  Above, a (row, 128 words) whose largest l exceeds t
-// by 40 takes that largest l as its reference instead, writes it beside its
-// sum, and xent_rows_kernel rescales such rows' E to the row's largest
-// reference afterwards.  The rest is linear:
+// in the gather).  E rounded to bf16 keeps its relative precision whatever
+// its size, and sum_v p_v >= p_y makes sum_v E >= 1: nothing that counts is
+// lost below.  Above, a (row, 128 words) whose largest l exceeds t by 40
+// takes that largest l as its reference instead, writes it beside its sum,
+// and xent_rows_kernel rescales such rows' E to the row's largest reference
+// afterwards.  The rest is linear:
 //   Zx = sum_{v != y} E_v, Z = E_y + Zx, loss = log Z + ref - t
 //        (log1p(Zx) where the reference is t: exact for sure predictions),
 //   E_y := -Zx (p_y - 1 = -Zx / Z without cancellation),
-//   dX_i = (g / Z_i) sum_v E_iv W_v         (scaled in the epilogue)
+//   dX_i = (g / Z_i) sum_v E_iv W_v         (scaled when the parts are joined)
 //   dW_v = sum_i E_iv (g / Z_i) x_i         (x scaled and rounded once)
-// Roundings to bf16: E, the scaled x, and the results.  The label's term
-// outweighs the others, so the row's factor takes its E's rounding out again
-// (and puts that half step on the other words' terms).
+// Roundings with bf16 io: E, the scaled x, and the results, to bf16.  The
+// label's term outweighs the others, so the row's factor takes its E's
+// rounding out again (and puts that half step on the other words' terms).
 //
 // All three products run on the 2-SM tcgen05 tiles of the layer's projection
 // (256 x 256 of a CTA pair, 64-deep k-blocks by TMA into a 6-stage ring, two
 // TMEM accumulators, 8 epilogue warps a CTA).  Every extent may be ragged:
-// TMA fills what is behind an edge with zeros and clips stores.
+// what is behind an edge is zero (TMA's fill, or padding) and stores are
+// clipped.
+//
+// fp32 io runs on the same tiles.  An fp32 value is the sum of three bf16
+// ones, x = x1 + x2 + x3 (8 + 8 + 8 bits), kept side by side, and a product
+// of two such sums is taken as the six products that matter, x1 w1, x1 w2,
+// x2 w1, x2 w2, x1 w3, x3 w1: what is left out is below 2^-24 of a term, as
+// an fp32 product's rounding is.  The small products come first, so that the
+// accumulator's own rounding meets few large partial sums.  Six passes at the
+// bf16 rate are four times the fp32 units' (1931 / 6 against 80 TFLOP/s).
+//
+// A few tokens without gradients (xent_few_kernel) only read W: dot products
+// on the CUDA cores, one launch.
 #include <cuda_bf16.h>
+
+#include <atomic>
 
 #include "flash_gau_internal.h"
 #include "sm103_ptx.cuh"
@@ -54,24 +72,64 @@ constexpr uint16_t kPair = 0x3, kLeader = 0x1;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kRaise = 40.0f * kLog2e;  // how far above the label's logit E is kept to it
 
-// kLoss: the logits' product, sums only; kProbs: sums and E; kDX: E W with
-// scaled rows, or fp32 parts of a split sum; kDW: E^T X', stored in bf16, or
-// in fp32, or added to fp32
+// kLoss: the logits' product, sums only; kProbs: sums and E; kDX: E W as
+// fp32 parts; kDW: E^T X', stored in bf16, or in fp32, or added to fp32
 enum Epi { kLoss, kProbs, kDX, kDW };
 
+constexpr int kTerms = 3, kProducts = 6;  // of an fp32 value; of two
+
 struct Params {
-  int M, N, K;  // of the product; the logits' N is V
-  int row_pairs, n_tiles, splits, kb_split, total;
-  int rows_first;  // row pairs walk fastest (the logits), else columns
-  const float *ref;     // [M] the label's logit in units of ln 2
-  const int *labels;    // [M]
-  float2 *part;         // [N / 128, rounded up][M] (reference, sum without the label)
-  const float *scale;   // [M] kDX without splits: factors of the rows
-  int fp32;             // kDX / kDW: fp32 result
-  int add;              // kDW: add to the fp32 result
-  int part_rows;        // kDX with splits: rows between parts
+  // M rows of the result, N columns, K deep.  The side that tokens are on is
+  // what *live leaves of `rows` from `first` on.
+  int M, N, K;
+  const int *live;
+  long long first;
+  int rows;
+  int products;            // 1, or kProducts with operands' terms side by side
+  int a_term, b_term;      // columns from one term of an operand to the next
+  const float *ref;        // the label's logit in units of ln 2
+  const int *labels;
+  float2 *part;            // [N / 128, rounded up][rows] (reference, sum without the label)
+  int e_term;              // kProbs: columns between E's terms
+  int fp32;                // kDW: fp32 result
+  int add;                 // kDW: add to the fp32 result
   int *status;
 };
+
+// which terms of A and B a product takes, the small ones first
+__device__ __forceinline__ void terms_of(const Params &p, int product, int &a, int &b) {
+  if (p.products == 1) {
+    a = b = 0;
+    return;
+  }
+  constexpr uint32_t kA = 0x001102u, kB = 0x010120u;  // product k: hex digit k
+  a = (int)(kA >> (4 * product) & 15u);
+  b = (int)(kB >> (4 * product) & 15u);
+}
+
+// dX's sum over the words is long and its tiles are few, so it is dealt out
+// by k-blocks: `nt` pairs (one for each 256 columns) form a group, which takes
+// a run of `run` k-blocks of the row pairs' sums laid end to end.  A row pair
+// that two groups share has a part from each, at index row pair + group (each
+// step along the runs raises one or the other, so no two parts meet).
+struct DxPlan {
+  int row_pairs, nt, groups, run;
+  long long steps;  // k-blocks of a row pair
+};
+__host__ __device__ inline DxPlan dx_plan(long long rows, int d, int V, int products, int pairs) {
+  DxPlan q;
+  q.row_pairs = (int)((rows + 2 * BM - 1) / (2 * BM));
+  q.nt = (d + BN - 1) / BN;
+  q.steps = (long long)products * ((V + BK - 1) / BK);
+  q.groups = pairs / q.nt > 0 ? pairs / q.nt : 1;
+  const long long total = q.row_pairs * q.steps;
+  long long run = (total + q.groups - 1) / q.groups;
+  if (run < 8) run = 8;
+  q.run = (int)(run < 0x7fffffff ? run : 0x7fffffff);
+  q.groups = (int)((total + q.run - 1) / q.run);
+  return q;
+}
+constexpr int kPlanPairs = kXentPlanSms / 2;
 
 struct Smem {
   uint64_t full[STAGES], empty[STAGES];
@@ -97,30 +155,97 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-struct Tile {
-  int rp, n0, nsz, kb0, kb1, split;
+// A piece of work of one pair: the product of k-blocks k0 .. k1 for 256 rows
+// and nsz columns.
+struct Work {
+  int rp, n0, nsz;
+  long long k0, k1;
+  int part;  // kDX: where the result goes
+  bool add;  // it adds to what the work before has stored there
 };
-__device__ __forceinline__ Tile tile_of(const Params &p, int t) {
-  Tile x;
-  const int tiles = p.row_pairs * p.n_tiles;
-  x.split = t / tiles;
-  const int u = t - x.split * tiles;
-  int nt;
-  if (p.rows_first) {
-    x.rp = u % p.row_pairs;
-    nt = u / p.row_pairs;
-  } else {
-    nt = u % p.n_tiles;
-    x.rp = u / p.n_tiles;
+// The tensor cores cut off what an accumulator cannot hold at each step, so
+// a long sum comes out short, by 6e-8 of itself a k-block (fp32 io, 1400
+// k-blocks: 8e-5).  With fp32 io a sum of the gradients' products is
+// therefore taken in works of 32 k-blocks (2e-6), which add up in memory.
+constexpr int kFp32Blocks = 32;
+
+// The works of one pair, in order.  Every role of the kernel walks the same.
+template <int EPI>
+struct Walk {
+  const Params &p;
+  int M, row_pairs, n_tiles, step;
+  long long steps;    // k-blocks of a whole product
+  long long u;        // next tile (kDX: unit)
+  long long pos, end;  // what is left of the unit's run (kDX) or of the tile
+  int limit;           // k-blocks of a work
+  int part_before;
+  DxPlan dx;
+  __device__ Walk(const Params &params) : p(params) {
+    const long long left = *reinterpret_cast<const volatile int *>(p.live) - p.first;
+    const int tokens = left < 0 ? 0 : left < p.rows ? (int)left : p.rows;
+    u = blockIdx.x / 2;
+    step = gridDim.x / 2;
+    pos = end = 0;
+    limit = p.products == 1 || EPI == kLoss || EPI == kProbs ? 0x7fffffff : kFp32Blocks;
+    part_before = -1;
+    M = EPI == kDW ? p.M : tokens;
+    n_tiles = (p.N + BN - 1) / BN;
+    row_pairs = (M + 2 * BM - 1) / (2 * BM);
+    const int K = EPI == kDW ? tokens : p.K;
+    steps = (long long)p.products * ((K + BK - 1) / BK);
+    if (EPI == kDX) dx = dx_plan(tokens, p.N, p.K, p.products, kPlanPairs);
   }
-  x.n0 = nt * BN;
-  // a multiple of 128: each CTA holds whole 64-column boxes; the logits'
-  // sums are kept by 128 words, so their tiles are never narrower
-  x.nsz = p.rows_first ? BN : min(BN, (p.N - x.n0 + 127) / 128 * 128);
-  x.kb0 = x.split * p.kb_split;
-  x.kb1 = min((p.K + BK - 1) / BK, x.kb0 + p.kb_split);
-  return x;
-}
+  __device__ bool next(Work &w) {
+    if (EPI == kDX) {
+      if (pos == end) {
+        if (u >= (long long)dx.groups * dx.nt) return false;
+        pos = u / dx.nt * dx.run;
+        end = min(pos + dx.run, (long long)dx.row_pairs * dx.steps);
+        part_before = -1;
+        u += step;
+      }
+      const long long unit = u - step;
+      w.rp = (int)(pos / dx.steps);
+      w.n0 = (int)(unit % dx.nt) * BN;
+      w.k0 = pos - w.rp * dx.steps;
+      w.k1 = min(min(dx.steps, w.k0 + (end - pos)), w.k0 + limit);
+      w.part = w.rp + (int)(unit / dx.nt);
+      w.add = w.part == part_before;
+      part_before = w.part;
+      pos += w.k1 - w.k0;
+    } else {
+      if (pos == end) {
+        if (u >= (long long)row_pairs * n_tiles) return false;
+        pos = 0;
+        end = steps;
+        u += step;
+      }
+      const long long tile = u - step;
+      if (EPI == kDW) {
+        w.n0 = (int)(tile % n_tiles) * BN;
+        w.rp = (int)(tile / n_tiles);
+      } else {
+        // rows fastest: the pairs share a tile of W while X stays in L2
+        w.rp = (int)(tile % row_pairs);
+        w.n0 = (int)(tile / row_pairs) * BN;
+      }
+      w.k0 = pos;
+      w.k1 = min(end, pos + limit);
+      w.add = pos > 0 || p.add;
+      pos = w.k1;
+    }
+    // a multiple of 128: each CTA holds whole 64-column boxes; the logits'
+    // sums are kept by 128 words, so their tiles are never narrower
+    w.nsz = EPI == kLoss || EPI == kProbs ? BN : min(BN, (p.N - w.n0 + 127) / 128 * 128);
+    return true;
+  }
+  // k-block s of a product: which term pair, and the depth in it
+  __device__ void locate(long long s, int &product, int &k) const {
+    const unsigned per = (unsigned)(steps / p.products), at = (unsigned)s;
+    product = p.products == 1 ? 0 : (int)(at / per);
+    k = (int)(at - product * per) * BK;
+  }
+};
 
 // Stores one 32-row x 128-byte box from a warp's staging buffer.
 struct Stager {
@@ -141,6 +266,15 @@ struct Stager {
     }
   }
 };
+
+// 32 values as bf16 into columns 8 c0 .. of this lane's row of a box
+__device__ __forceinline__ void put32(Stager &st, int c0, const float (&e)[32]) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    st.put(c0 + q, make_uint4(pack_bf16(e[8 * q], e[8 * q + 1]), pack_bf16(e[8 * q + 2], e[8 * q + 3]),
+                              pack_bf16(e[8 * q + 4], e[8 * q + 5]),
+                              pack_bf16(e[8 * q + 6], e[8 * q + 7])));
+}
 
 template <int EPI>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
@@ -183,17 +317,22 @@ xent_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
   tc_fence_after();
   griddep_wait();
   const uint32_t tmem_base = sm->tmem_base;
-  const int first = blockIdx.x / 2, step = gridDim.x / 2;
+  Walk<EPI> walk(p);
+  Work x;
 
   if (warp == 0) {
     // ------------------------------------------------ TMA producer (both)
     if (elect_one()) {
       int stage = 0;
       uint32_t phase = 0;
-      for (int t = first; t < p.total && !sm->abort_flag; t += step) {
-        const Tile x = tile_of(p, t);
+      while (!sm->abort_flag && walk.next(x)) {
         const int m0 = (x.rp * 2 + rank) * BM, half = x.nsz / 2, hboxes = half / 64;
-        for (int kb = x.kb0; kb < x.kb1; ++kb) {
+        for (long long s = x.k0; s < x.k1; ++s) {
+          int product, k, ta, tb;
+          walk.locate(s, product, k);
+          terms_of(p, product, ta, tb);
+          ta *= p.a_term;
+          tb *= p.b_term;
           if (!mbar_wait(smem_u32(&sm->empty[stage]), phase ^ 1, &sm->abort_flag)) {
             raise_timeout(sm, p.status);
             break;
@@ -206,17 +345,17 @@ xent_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
           const uint32_t b_bytes = B_KM ? 2 * BOX_BYTES : hboxes * BOX_BYTES;
           if (leader) mbar_arrive_expect_tx(full_own, 2 * (A_BYTES + b_bytes));
           if (A_MN) {
-            tma_load_2d_pair(smem_u32(sA), &tmA, full_leader, m0, kb * BK);
-            tma_load_2d_pair(smem_u32(sA + BOX_BYTES), &tmA, full_leader, m0 + 64, kb * BK);
+            tma_load_2d_pair(smem_u32(sA), &tmA, full_leader, ta + m0, k);
+            tma_load_2d_pair(smem_u32(sA + BOX_BYTES), &tmA, full_leader, ta + m0 + 64, k);
           } else {
-            tma_load_2d_pair(smem_u32(sA), &tmA, full_leader, kb * BK, m0);
+            tma_load_2d_pair(smem_u32(sA), &tmA, full_leader, ta + k, m0);
           }
           if (B_KM) {
-            tma_load_2d_pair(smem_u32(sB), &tmB, full_leader, kb * BK, x.n0 + rank * half);
+            tma_load_2d_pair(smem_u32(sB), &tmB, full_leader, tb + k, x.n0 + rank * half);
           } else {
             for (int j = 0; j < hboxes; ++j)
               tma_load_2d_pair(smem_u32(sB + j * BOX_BYTES), &tmB, full_leader,
-                               x.n0 + rank * half + j * 64, kb * BK);
+                               tb + x.n0 + rank * half + j * 64, k);
           }
           if (++stage == STAGES) {
             stage = 0;
@@ -231,8 +370,7 @@ xent_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
       int stage = 0;
       uint32_t phase = 0;
       int local = 0;
-      for (int t = first; t < p.total && !sm->abort_flag; t += step, ++local) {
-        const Tile x = tile_of(p, t);
+      for (; !sm->abort_flag && walk.next(x); ++local) {
         const int acc = local & 1;
         if (!mbar_wait(smem_u32(&sm->acc_empty[acc]), ((local >> 1) & 1) ^ 1, &sm->abort_flag)) {
           raise_timeout(sm, p.status);
@@ -242,7 +380,7 @@ xent_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
         const uint32_t d_tmem = tmem_base + acc * ACC_COLS;
         const uint32_t idesc = idesc_bf16_f32(2 * BM, x.nsz, A_MN ? 1 : 0, B_KM ? 0 : 1);
         bool ok = true;
-        for (int kb = x.kb0; kb < x.kb1; ++kb) {
+        for (long long s = x.k0; s < x.k1; ++s) {
           if (!mbar_wait(smem_u32(&sm->full[stage]), phase, &sm->abort_flag)) {
             raise_timeout(sm, p.status);
             ok = false;
@@ -257,7 +395,7 @@ xent_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
           for (int k = 0; k < BK / 16; ++k)
             mma_f16_ss_pair(d_tmem, desc_advance(da, k * (A_MN ? 2048 : 32)),
                             desc_advance(db, k * (B_KM ? 32 : 2048)), idesc,
-                            kb != x.kb0 || k != 0);
+                            s != x.k0 || k != 0);
           mma_commit_pair_mc(smem_u32(&sm->empty[stage]), kPair);
           if (++stage == STAGES) {
             stage = 0;
@@ -276,24 +414,20 @@ xent_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
     const int half = (warp - 2) >> 2;
     Stager st{tiles + STAGES * STAGE_BYTES + (warp - 2) * STG_BYTES, lane};
     int local = 0;
-    for (int t = first; t < p.total && !sm->abort_flag; t += step, ++local) {
-      const Tile x = tile_of(p, t);
+    for (; !sm->abort_flag && walk.next(x); ++local) {
       const int acc = local & 1;
       const int row0 = (x.rp * 2 + rank) * BM + quarter * 32, row = row0 + lane;
       const int c_begin = half * (x.nsz / 2), c_end = c_begin + x.nsz / 2;
-      const bool live = row < p.M;
+      const bool live = row < walk.M;
       // this row's scalars, before the wait
-      float ref = 0.f, scale = 0.f;
+      float ref = 0.f;
       int label = -1;
       if constexpr (EPI == kLoss || EPI == kProbs) {
         if (live) {
           ref = p.ref[row];
           label = p.labels[row];
-          if (label >= p.N) label = -1;
         }
       }
-      if constexpr (EPI == kDX)
-        if (!p.fp32 && live) scale = p.scale[row];
       if (!mbar_wait(smem_u32(&sm->acc_full[acc]), (local >> 1) & 1, &sm->abort_flag)) {
         raise_timeout(sm, p.status);
         break;
@@ -326,7 +460,7 @@ xent_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
         if (top > ref + kRaise) ref = top;
         float sum[4] = {0.f, 0.f, 0.f, 0.f};
         for (int c0 = c_begin; c0 < c_end; c0 += 64) {
-          if (EPI == kProbs) st.begin();
+          float e[2][32];
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             uint32_t v[32];
@@ -334,52 +468,68 @@ xent_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
             tmem_ld_wait();
             if (c0 + 64 >= c_end && h == 1) drained();
             const int col = x.n0 + c0 + 32 * h;
-            float e[32];
 #pragma unroll
-            for (int j = 0; j < 32; ++j) e[j] = exp2_approx(fmaf(__uint_as_float(v[j]), kLog2e, -ref));
+            for (int j = 0; j < 32; ++j)
+              e[h][j] = exp2_approx(fmaf(__uint_as_float(v[j]), kLog2e, -ref));
             if (!whole) {
 #pragma unroll
               for (int j = 0; j < 32; ++j)
-                if (col + j >= p.N) e[j] = 0.f;
+                if (col + j >= p.N) e[h][j] = 0.f;
             }
             // the label's own term stays out of the sum, exactly
             if ((unsigned)(label - col) < 32u) {
 #pragma unroll
               for (int j = 0; j < 32; ++j)
-                if (label - col == j) e[j] = 0.f;
+                if (label - col == j) e[h][j] = 0.f;
             }
-            if (label < 0) {  // whatever the row holds
+            if (label < 0) {  // no token: whatever the row holds
 #pragma unroll
-              for (int j = 0; j < 32; ++j) e[j] = 0.f;
+              for (int j = 0; j < 32; ++j) e[h][j] = 0.f;
             }
 #pragma unroll
-            for (int j = 0; j < 32; ++j) sum[j & 3] += e[j];
-            if (EPI == kProbs) {
+            for (int j = 0; j < 32; ++j) sum[j & 3] += e[h][j];
+          }
+          // boxes wholly behind an edge are not stored; rows behind the last
+          // one are, as zeros: the products that follow read whole tiles
+          if (EPI == kProbs && x.n0 + c0 < p.N) {
+            for (int term = 0;; ++term) {
+              st.begin();
+              put32(st, 0, e[0]);
+              put32(st, 4, e[1]);
+              st.finish(&tmC, term * p.e_term + x.n0 + c0, row0, false);
+              if (p.products == 1 || term == kTerms - 1) break;
 #pragma unroll
-              for (int q = 0; q < 4; ++q)
-                st.put(4 * h + q, make_uint4(pack_bf16(e[8 * q], e[8 * q + 1]),
-                                             pack_bf16(e[8 * q + 2], e[8 * q + 3]),
-                                             pack_bf16(e[8 * q + 4], e[8 * q + 5]),
-                                             pack_bf16(e[8 * q + 6], e[8 * q + 7])));
+              for (int j = 0; j < 32; ++j) {
+                e[0][j] -= __bfloat162float(__float2bfloat16_rn(e[0][j]));
+                e[1][j] -= __bfloat162float(__float2bfloat16_rn(e[1][j]));
+              }
             }
           }
-          // boxes wholly behind an edge are not stored
-          if (EPI == kProbs && row0 < p.M && x.n0 + c0 < p.N)
-            st.finish(&tmC, x.n0 + c0, row0, false);
         }
         if (live && x.n0 + c_begin < p.N)
-          p.part[(size_t)((x.n0 + c_begin) / 128) * p.M + row] =
+          p.part[(size_t)((x.n0 + c_begin) / 128) * p.rows + row] =
               make_float2(ref, (sum[0] + sum[1]) + (sum[2] + sum[3]));
       } else {
-        const int out_row = row0 + (EPI == kDX ? x.split * p.part_rows : 0);
+        // kDX: parts of 256 rows; nothing but zeros where there are no tokens
+        const int out_row = EPI == kDX ? x.part * 2 * BM + row0 - x.rp * 2 * BM : row0;
+        const bool none = x.k1 == x.k0;
+        if (p.products > 1) {
+          // sums in memory: the work before is there before this one adds
+          if (lane == 0) tma_store_wait<0>();
+          __syncwarp();
+        }
         for (int c0 = c_begin; c0 < c_end; c0 += 64) {
           uint32_t a[32], b[32];
           tmem_ld32(taddr + c0, a);
           tmem_ld32(taddr + c0 + 32, b);
           tmem_ld_wait();
           if (c0 + 64 >= c_end) drained();
-          if (row0 >= p.M || x.n0 + c0 >= p.N) continue;
-          if (p.fp32) {
+          if ((EPI == kDW && row0 >= p.M) || x.n0 + c0 >= p.N) continue;
+          if (none) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) a[j] = b[j] = 0;
+          }
+          if (EPI == kDX || p.fp32) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               const uint32_t *v = h == 0 ? a : b;
@@ -388,24 +538,17 @@ xent_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
 #pragma unroll
               for (int q = 0; q < 8; ++q)
                 st.put(q, make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]));
-              st.finish(&tmC, x.n0 + c0 + 32 * h, out_row, EPI == kDW && p.add);
+              st.finish(&tmC, x.n0 + c0 + 32 * h, out_row, x.add);
             }
           } else {
             st.begin();
 #pragma unroll
             for (int q = 0; q < 8; ++q) {
               const uint32_t *v = q < 4 ? &a[8 * q] : &b[8 * (q - 4)];
-              uint32_t w[4];
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                float lo = __uint_as_float(v[2 * k]), hi = __uint_as_float(v[2 * k + 1]);
-                if (EPI == kDX) {
-                  lo *= scale;
-                  hi *= scale;
-                }
-                w[k] = pack_bf16(lo, hi);
-              }
-              st.put(q, make_uint4(w[0], w[1], w[2], w[3]));
+              st.put(q, make_uint4(pack_bf16(__uint_as_float(v[0]), __uint_as_float(v[1])),
+                                   pack_bf16(__uint_as_float(v[2]), __uint_as_float(v[3])),
+                                   pack_bf16(__uint_as_float(v[4]), __uint_as_float(v[5])),
+                                   pack_bf16(__uint_as_float(v[6]), __uint_as_float(v[7]))));
             }
             st.finish(&tmC, x.n0 + c0, out_row, false);
           }
@@ -426,8 +569,8 @@ xent_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
 
 template <int EPI>
 cudaError_t launch_gemm(const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &c,
-                        const Params &p, int num_sms, cudaStream_t stream) {
-  static int max_pairs[64];
+                        const Params &p, long long works, int num_sms, cudaStream_t stream) {
+  static std::atomic<int> max_pairs[64];
   int dev = 0;
   cudaError_t err = cudaGetDevice(&dev);
   if (err != cudaSuccess) return err;
@@ -446,16 +589,18 @@ cudaError_t launch_gemm(const CUtensorMap &a, const CUtensorMap &b, const CUtens
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  if (max_pairs[dev] == 0) {
+  int pairs = max_pairs[dev].load(std::memory_order_acquire);
+  if (pairs == 0) {
     err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
     if (err != cudaSuccess) return err;
     int n = 0;
     cfg.gridDim = dim3(2 * (num_sms / 2));
     err = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
     if (err != cudaSuccess) return err;
-    max_pairs[dev] = n > 0 ? n : 1;
+    pairs = n > 0 ? n : 1;
+    max_pairs[dev].store(pairs, std::memory_order_release);
   }
-  cfg.gridDim = dim3(2 * (p.total < max_pairs[dev] ? p.total : max_pairs[dev]));
+  cfg.gridDim = dim3(2 * (int)(works < pairs ? works : pairs));
   return cudaLaunchKernelEx(&cfg, kernel, a, b, c, p);
 }
 
@@ -465,357 +610,733 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-__device__ __forceinline__ int label_of(const int *labels, long long i, int V) {
-  const int y = labels[i];
-  return y >= 0 && y < V ? y : -1;
+
+__device__ __forceinline__ bool is_word(int y, int V) { return y >= 0 && y < V; }
+
+// An fp32 value as the sum of three bf16 ones, each the rounding of what the
+// ones before leave.
+__device__ __forceinline__ void split3(float x, float (&t)[kTerms]) {
+#pragma unroll
+  for (int k = 0; k < kTerms; ++k) {
+    t[k] = __bfloat162float(__float2bfloat16_rn(x));
+    x -= t[k];
+  }
+}
+// A row of d fp32 values times `f` as three rows of `term` bf16 ones side by
+// side, zeros behind d; one warp.
+__device__ __forceinline__ void split_row(const float *x, int d, float f, __nv_bfloat16 *out, int term,
+                                          int lane) {
+  for (int k = 2 * lane; k < term; k += 64) {
+    float a[kTerms], b[kTerms];
+    split3(k < d ? x[k] * f : 0.f, a);
+    split3(k + 1 < d ? x[k + 1] * f : 0.f, b);
+#pragma unroll
+    for (int t = 0; t < kTerms; ++t)
+      *reinterpret_cast<uint32_t *>(out + t * term + k) = pack_bf16(a[t], b[t]);
+  }
 }
 
-// One warp a row: ref = log2(e) x . W_y, 0 for rows without a label.  The
-// launch's last block instead counts the labels of all N tokens and writes
-// the factor g of the gradients (count != null).
 __global__ void __launch_bounds__(256)
-xent_target_kernel(const __nv_bfloat16 *__restrict__ X, const __nv_bfloat16 *__restrict__ W,
-                   const int *__restrict__ labels, int rows, int d, int V, float *__restrict__ ref,
-                   const int *__restrict__ all_labels, long long N, int mean, float scale,
-                   float *__restrict__ factor) {
+xent_split_kernel(const float *__restrict__ W, int V, int d, __nv_bfloat16 *__restrict__ out, int term) {
   griddep_wait();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  if (factor && blockIdx.x == gridDim.x - 1) {
-    __shared__ int counts[8];
-    int n = 0;
-    for (long long i = threadIdx.x; i < N; i += blockDim.x) n += label_of(all_labels, i, V) >= 0;
-    n = __reduce_add_sync(0xffffffffu, n);
-    if (lane == 0) counts[warp] = n;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      n = 0;
-      for (int k = 0; k < 8; ++k) n += counts[k];
-      *factor = mean ? scale / (float)(n > 0 ? n : 1) : scale;
-    }
-    return;
-  }
-  const int row = blockIdx.x * 8 + warp;
-  if (row >= rows) return;
-  const int y = label_of(labels, row, V);
-  float s = 0.f;
-  if (y >= 0) {
-    const uint4 *x = reinterpret_cast<const uint4 *>(X + (size_t)row * d);
-    const uint4 *w = reinterpret_cast<const uint4 *>(W + (size_t)y * d);
-    for (int k = lane; k < d / 8; k += 32) {
-      const uint4 a = __ldg(x + k), b = __ldg(w + k);
-      const uint32_t au[4] = {a.x, a.y, a.z, a.w}, bu[4] = {b.x, b.y, b.z, b.w};
+  const int row = blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (row < V)
+    split_row(W + (size_t)row * d, d, 1.f, out + (size_t)row * kTerms * term, term, threadIdx.x & 31);
+}
+
+template <typename T>
+struct GatherArgs {
+  const T *X, *W;
+  const int *labels;
+  long long N;
+  int d, V, mean, block_rows;
+  float scale;
+  XentLayout L;
+  float *loss, *lse;
+  T *dX;
+  int copy;  // there is one piece: its rows are copied here
+};
+
+// A row of X as the products read it; one warp.
+__device__ __forceinline__ void copy_row(const __nv_bfloat16 *x, int d, __nv_bfloat16 *out, int,
+                                         int lane) {
+  for (int k = 8 * lane; k < d; k += 256)
+    *reinterpret_cast<uint4 *>(out + k) = *reinterpret_cast<const uint4 *>(x + k);
+}
+__device__ __forceinline__ void copy_row(const float *x, int d, __nv_bfloat16 *out, int term, int lane) {
+  split_row(x, d, 1.f, out, term, lane);
+}
+// zeros behind the last row, to the end of its k-block: dW's sum over the
+// tokens reads it whole
+__device__ __forceinline__ void zero_tail(__nv_bfloat16 *Xc, long long rows, long long width) {
+  const long long end = (rows + BK - 1) / BK * BK * width;
+  for (long long i = rows * width + threadIdx.x; i < end; i += 256) Xc[i] = __float2bfloat16_rn(0.f);
+}
+
+// The rows of X with a label, one behind another (as three terms for fp32),
+// with their labels, where they came from and their reference, the label's
+// logit; zeros in the outputs of the other rows.  A block finds where its
+// rows go by counting the labels before them, so the order is the tokens'.
+// The last block leaves the number of rows, the gradients' factor, and a
+// tile's worth of rows without a label behind the last one.
+template <typename T>
+__global__ void __launch_bounds__(256) xent_gather_kernel(const GatherArgs<T> a) {
+  __shared__ int counts[8];
+  griddep_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, d = a.d;
+  const long long row0 = (long long)blockIdx.x * a.block_rows;
+  const long long end = min(row0 + a.block_rows, a.N);
+  int n = 0;
+  for (long long i = threadIdx.x; i < row0; i += 256) n += is_word(a.labels[i], a.V);
+  n = __reduce_add_sync(0xffffffffu, n);
+  if (lane == 0) counts[warp] = n;
+  __syncthreads();
+  long long base = 0;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&au[q]));
-        const float2 g = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&bu[q]));
-        s = fmaf(f.x, g.x, fmaf(f.y, g.y, s));
+  for (int k = 0; k < 8; ++k) base += counts[k];
+  const long long width = (long long)(sizeof(T) == 4 ? kTerms : 1) * a.L.term;
+  for (long long r0 = row0; r0 < end; r0 += 8) {
+    const int y8 = lane < 8 && r0 + lane < end ? a.labels[r0 + lane] : -1;
+    const unsigned mask = __ballot_sync(0xffffffffu, is_word(y8, a.V));
+    const int y = __shfl_sync(0xffffffffu, y8, warp);
+    const long long row = r0 + warp, c = base + __popc(mask & ((1u << warp) - 1));
+    base += __popc(mask);
+    if (row >= end) continue;
+    const T *x = a.X + row * d;
+    if (mask >> warp & 1) {
+      const T *w = a.W + (size_t)y * d;
+      float s = 0.f;
+      if constexpr (sizeof(T) == 2) {
+        for (int k = 8 * lane; k < d; k += 256) {
+          const uint4 u = *reinterpret_cast<const uint4 *>(x + k);
+          const uint4 v = __ldg(reinterpret_cast<const uint4 *>(w + k));
+          const uint32_t au[4] = {u.x, u.y, u.z, u.w}, bu[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&au[q]));
+            const float2 g = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&bu[q]));
+            s = fmaf(f.x, g.x, fmaf(f.y, g.y, s));
+          }
+        }
+      } else {
+        for (int k = lane; k < d; k += 32) s = fmaf(x[k], __ldg(w + k), s);
       }
+      if (a.copy) copy_row(x, d, static_cast<__nv_bfloat16 *>(a.L.Xc) + c * width, a.L.term, lane);
+      s = warp_sum(s);
+      if (lane == 0) {
+        a.L.ref[c] = s * kLog2e;
+        a.L.labels[c] = y;
+        a.L.index[c] = (int)row;
+      }
+    } else {
+      if (lane == 0) {
+        a.loss[row] = 0.f;
+        if (a.lse) a.lse[row] = 0.f;
+      }
+      if (a.dX)
+        for (int k = lane; k < d; k += 32) a.dX[row * d + k] = T(0.f);
     }
-    s = warp_sum(s);
   }
-  if (lane == 0) ref[row] = s * kLog2e;
+  if (blockIdx.x != gridDim.x - 1) return;
+  // base is the number of labels now
+  const long long tile = (base + 2 * BM - 1) / (2 * BM) * (2 * BM);
+  for (long long c = base + threadIdx.x; c < tile; c += 256) a.L.labels[c] = -1;
+  if (a.copy) zero_tail(static_cast<__nv_bfloat16 *>(a.L.Xc), base, width);
+  if (threadIdx.x == 0) {
+    *a.L.live = (int)base;
+    *a.L.done = 0;
+    *a.L.factor = a.mean ? a.scale / (float)(base > 0 ? base : 1) : a.scale;
+  }
+}
+
+// The rows of one piece of several; a warp a row.
+template <typename T>
+__global__ void __launch_bounds__(256)
+xent_copy_kernel(const T *__restrict__ X, int d, const XentLayout L, long long first, int rows) {
+  griddep_wait();
+  const long long left = *L.live - first;
+  const int tokens = left < 0 ? 0 : left < rows ? (int)left : rows;
+  const int row = blockIdx.x * 8 + (threadIdx.x >> 5);
+  const long long width = (long long)(sizeof(T) == 4 ? kTerms : 1) * L.term;
+  __nv_bfloat16 *Xc = static_cast<__nv_bfloat16 *>(L.Xc);
+  if (row < tokens)
+    copy_row(X + (long long)L.index[first + row] * d, d, Xc + row * width, L.term, threadIdx.x & 31);
+  if (blockIdx.x == 0) zero_tail(Xc, tokens, width);
 }
 
 struct RowArgs {
-  const float *ref;
-  const int *labels;
-  const float2 *part;
-  int parts, rows, V, d;
-  float *loss, *lse;           // of this piece's rows; lse may be null
-  const float *factor;
-  __nv_bfloat16 *E;            // null: no gradients
-  long long ldE;
-  float *scale;                // g / Z
-  const __nv_bfloat16 *X;
-  __nv_bfloat16 *Xs;           // (g / Z) x, or null
+  XentLayout L;
+  long long first, N;  // this piece's first row; all tokens
+  int rows, V, d;
+  int parts;
+  int grad, scaled;    // E is there; dW wants scaled rows
+  int blocks;          // of every piece's launch
+  const void *X;       // fp32: the tokens' rows
+  float *loss, *lse, *total;
 };
 
-// 32 rows a block: joins the parts of each row's sum (a lane a row, the
-// parts dealt to 8 warps), writes the loss, and with gradients the row's
-// factor, the label's E, the scaled row of X, and where a part took another
-// reference than the row's its E again.
+// (reference, sum) of two parts of a row; whether the references differ
+__device__ __forceinline__ bool join_parts(float &top, float &sum, float ref, float s) {
+  if (ref == top) {
+    sum += s;
+    return false;
+  }
+  const float t = fmaxf(top, ref);
+  // a reference of minus infinity has no terms below it
+  sum = (top == t ? sum : sum * exp2f(top - t)) + (ref == t ? s : s * exp2f(ref - t));
+  top = t;
+  return true;
+}
+
+// log Z - t of a row (times ln 2 where it is in logs of two): sum is of the
+// other words relative to 2^top, t2 the label's logit
+__device__ __forceinline__ float row_loss(float top, float sum, float t2, float *z) {
+  if (top == t2) {
+    // an infinite logit makes both NaN, as inf - inf does
+    *z = 1.0f + sum + 0.f * t2;
+    return log1pf(sum) + 0.f * t2;
+  }
+  *z = exp2f(t2 - top) + sum;
+  return logf(*z) + (top - t2) * kLn2;
+}
+
+// Eight rows a block.  First 32 threads a row join the parts of its sum, then
+// a warp a row writes the loss, and with gradients the row's factor, the
+// label's E, the scaled row of X, and where a part took another reference
+// than the row's its E again.  The last block of all adds the losses up.
+template <typename T>
 __global__ void __launch_bounds__(256) xent_rows_kernel(const RowArgs a) {
-  __shared__ float2 joined[8][32];
-  __shared__ float row_ref[32], row_scale[32];
-  __shared__ int row_mixed[32];
+  __shared__ float2 joined[8][33];
+  __shared__ int differ[8], last;
   griddep_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int row0 = blockIdx.x * 32, row = row0 + lane;
-  const bool live = row < a.rows;
-  const float ref = live ? a.ref[row] : 0.f;
-  float top = ref, sum = 0.f;
-  int mixed = 0;
-  auto join = [&](float2 v) {
-    if (v.x == top) {
-      sum += v.y;
-    } else {
-      mixed = 1;
-      const float t = fmaxf(top, v.x);
-      // a reference of minus infinity has no terms below it
-      sum = (top == t ? sum : sum * exp2f(top - t)) + (v.x == t ? v.y : v.y * exp2f(v.x - t));
-      top = t;
-    }
-  };
-  if (live)
-    for (int k = warp; k < a.parts; k += 8) join(a.part[(size_t)k * a.rows + row]);
-  joined[warp][lane] = make_float2(top, sum);
-  if (warp == 0) row_mixed[lane] = 0;
-  __syncthreads();
-  if (mixed) row_mixed[lane] = 1;
-  if (warp == 0) {
-    for (int k = 1; k < 8; ++k) join(joined[k][lane]);
-    const int label = live ? label_of(a.labels, row, a.V) : -1;
-    float loss = 0.f, scale = 0.f;
-    if (label >= 0) {
-      if (top == ref) {
-        // an infinite logit makes both NaN, as inf - inf does
-        loss = log1pf(sum) + 0.f * ref;
-        scale = *a.factor / (1.0f + sum) + 0.f * ref;
-      } else {
-        const float z = exp2f(ref - top) + sum;
-        loss = logf(z) + (top - ref) * kLn2;
-        scale = *a.factor / z;
-      }
-    }
-    if (live) {
-      a.loss[row] = loss;
-      if (a.lse) a.lse[row] = label >= 0 ? fmaf(ref, kLn2, loss) : 0.f;
-      if (a.E) {
-        if (label >= 0) {
-          const __nv_bfloat16 own = __float2bfloat16_rn(-sum);
-          a.E[(size_t)row * a.ldE + label] = own;
-          // its rounding goes into the row's factor
-          if (sum > 0.f && sum < INFINITY) scale *= sum / -__bfloat162float(own);
+  const long long left = *a.L.live - a.first;
+  const int tokens = left < 0 ? 0 : left < a.rows ? (int)left : a.rows;
+  const int row0 = blockIdx.x * 8;
+  if (row0 < tokens) {
+    if (threadIdx.x < 8) differ[threadIdx.x] = 0;
+    __syncthreads();
+    {
+      const int r = threadIdx.x & 7, row = row0 + r;
+      float top = row < tokens ? a.L.ref[a.first + row] : 0.f, sum = 0.f;
+      bool mixed = false;
+      if (row < tokens) {
+        const float2 *part = a.L.part + row;
+#pragma unroll 4
+        for (int k = threadIdx.x >> 3; k < a.parts; k += 32) {
+          const float2 v = part[(size_t)k * a.rows];
+          mixed |= join_parts(top, sum, v.x, v.y);
         }
-        a.scale[row] = scale;
+      }
+      joined[r][threadIdx.x >> 3] = make_float2(top, sum);
+      if (mixed) differ[r] = 1;
+    }
+    __syncthreads();
+    const int row = row0 + warp;
+    if (row < tokens) {
+      const float ref = a.L.ref[a.first + row];
+      const int label = a.L.labels[a.first + row], token = a.L.index[a.first + row];
+      const float2 own = joined[warp][lane];
+      float top = own.x, sum = own.y;
+      bool mixed = differ[warp];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const float r = __shfl_xor_sync(0xffffffffu, top, o);
+        const float s = __shfl_xor_sync(0xffffffffu, sum, o);
+        mixed |= join_parts(top, sum, r, s);
+      }
+      mixed = __any_sync(0xffffffffu, mixed);
+      float z;
+      const float loss = row_loss(top, sum, ref, &z);
+      float scale = *a.L.factor / z;
+      const int terms = sizeof(T) == 4 ? kTerms : 1;
+      __nv_bfloat16 *E = static_cast<__nv_bfloat16 *>(a.L.E) + (size_t)row * terms * a.L.ldE;
+      if (lane == 0) {
+        a.loss[token] = loss;
+        if (a.lse) a.lse[token] = fmaf(ref, kLn2, loss);
+      }
+      if (a.grad) {
+        if constexpr (sizeof(T) == 2) {
+          const __nv_bfloat16 e = __float2bfloat16_rn(-sum);
+          if (lane == 0) E[label] = e;
+          // its rounding goes into the row's factor
+          if (sum > 0.f && sum < INFINITY) scale *= sum / -__bfloat162float(e);
+        } else {
+          float t[kTerms];
+          split3(-sum, t);
+          if (lane < kTerms)
+            E[lane * a.L.ldE + label] =
+                __float2bfloat16_rn(lane == 0 ? t[0] : lane == 1 ? t[1] : t[2]);
+        }
+        if (lane == 0) a.L.row_scale[row] = scale;
+        if (a.scaled) {
+          __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(a.L.Xc) + (size_t)row * terms * a.L.term;
+          if constexpr (sizeof(T) == 2) {
+            for (int k = 8 * lane; k < a.d; k += 256) {
+              const uint4 w = *reinterpret_cast<const uint4 *>(o + k);
+              uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&u[q]));
+                u[q] = pack_bf16(f.x * scale, f.y * scale);
+              }
+              *reinterpret_cast<uint4 *>(o + k) = make_uint4(u[0], u[1], u[2], u[3]);
+            }
+          } else {
+            split_row(static_cast<const float *>(a.X) + (size_t)token * a.d, a.d, scale, o, a.L.term,
+                      lane);
+          }
+        }
+        if (mixed) {
+          for (int j = 0; j < a.parts; ++j) {
+            const float from = a.L.part[(size_t)j * a.rows + row].x;
+            if (from == top) continue;
+            const float f = exp2f(from - top);
+            for (int c = 128 * j + lane; c < min(128 * j + 128, a.V); c += 32) {
+              if (c == label) continue;
+              float v = 0.f;
+              for (int t = terms - 1; t >= 0; --t) v += __bfloat162float(E[t * a.L.ldE + c]);
+              v *= f;
+              for (int t = 0; t < terms; ++t) {
+                const __nv_bfloat16 e = __float2bfloat16_rn(v);
+                E[t * a.L.ldE + c] = e;
+                v -= __bfloat162float(e);
+              }
+            }
+          }
+        }
       }
     }
-    row_ref[lane] = top;
-    row_scale[lane] = scale;
-    if (mixed) row_mixed[lane] = 1;
   }
-  if (!a.E) return;
+  // total, by whichever block comes last
+  __threadfence();
   __syncthreads();
-  for (int k = warp; k < 32 && row0 + k < a.rows; k += 8) {
-    const int r = row0 + k, label = label_of(a.labels, r, a.V);
-    if (a.Xs) {
-      const uint4 *x = reinterpret_cast<const uint4 *>(a.X + (size_t)r * a.d);
-      uint4 *o = reinterpret_cast<uint4 *>(a.Xs + (size_t)r * a.d);
-      const float s = row_scale[k];
-      for (int j = lane; j < a.d / 8; j += 32) {
-        uint4 w = make_uint4(0, 0, 0, 0);
-        if (label >= 0) {
-          w = __ldg(x + j);
-          uint32_t u[4] = {w.x, w.y, w.z, w.w};
+  if (threadIdx.x == 0) last = atomicAdd(a.L.done, 1) == a.blocks - 1;
+  __syncthreads();
+  if (!last) return;
+  __threadfence();
+  float s[4] = {0.f, 0.f, 0.f, 0.f};
+  for (long long i = threadIdx.x; i < a.N; i += 1024)
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (i + 256 * k < a.N) s[k] += __ldcg(a.loss + i + 256 * k);
+  const float v = warp_sum((s[0] + s[1]) + (s[2] + s[3]));
+  if (lane == 0) joined[0][warp].x = v;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    float t = 0.f;
+    for (int k = 0; k < 8; ++k) t += joined[0][k].x;
+    *a.total = *a.L.factor * t;
+  }
+}
+
+__device__ __forceinline__ void store_as(float *p, float v) { *p = v; }
+__device__ __forceinline__ void store_as(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
+
+// dX from the parts of its sum, in the groups' order, times the row's factor,
+// to where the row came from; a warp a row.
+template <typename T>
+__global__ void __launch_bounds__(256)
+xent_join_kernel(const XentLayout L, long long first, int rows, int d, int V, int products,
+                 T *__restrict__ out) {
+  __shared__ int first_part, parts;
+  griddep_wait();
+  const long long left = *L.live - first;
+  const int tokens = left < 0 ? 0 : left < rows ? (int)left : rows;
+  const int row0 = blockIdx.x * 8, rp = row0 / (2 * BM);  // of one row pair
+  if (row0 >= tokens) return;
+  if (threadIdx.x == 0) {
+    const DxPlan q = dx_plan(tokens, d, V, products, kPlanPairs);
+    const int g0 = (int)(rp * q.steps / q.run), g1 = (int)(((rp + 1) * q.steps - 1) / q.run);
+    first_part = rp + g0;
+    parts = g1 - g0 + 1;
+  }
+  __syncthreads();
+  const int row = row0 + (threadIdx.x >> 5), n = parts;
+  if (row >= tokens) return;
+  const long long step = 2LL * BM * L.ld_part;
+  const float *p = L.dx_part + first_part * step + (long long)(row - rp * 2 * BM) * L.ld_part;
+  const float f = L.row_scale[row];
+  T *o = out + (size_t)L.index[first + row] * d;
+  for (int c = 4 * (threadIdx.x & 31); c < d; c += 128) {
+    float4 s = *reinterpret_cast<const float4 *>(p + c);
+#pragma unroll 4
+    for (int k = 1; k < n; ++k) {
+      const float4 v = *reinterpret_cast<const float4 *>(p + k * step + c);
+      s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+    }
+    if constexpr (sizeof(T) == 2) {  // d is a multiple of 8
+      *reinterpret_cast<uint2 *>(o + c) =
+          make_uint2(pack_bf16(s.x * f, s.y * f), pack_bf16(s.z * f, s.w * f));
+    } else {
+      const float v[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (c + k < d) o[c + k] = v[k] * f;
+    }
+  }
+}
+
+// dW from its fp32 sum, rows of `ld` values
+template <typename T>
+__global__ void __launch_bounds__(256)
+xent_finish_kernel(const float *__restrict__ in, int ld, int V, int d, T *__restrict__ out) {
+  griddep_wait();
+  const int quads = (d + 3) / 4;
+  const long long i = blockIdx.x * 256LL + threadIdx.x;
+  if (i >= (long long)V * quads) return;
+  const long long row = i / quads;
+  const int c = (int)(i % quads) * 4;
+  const float4 s = *reinterpret_cast<const float4 *>(in + row * ld + c);
+  const float v[4] = {s.x, s.y, s.z, s.w};
+  T *o = out + row * d + c;
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    if (c + k < d) store_as(o + k, v[k]);
+}
+
+// ---- a few tokens, no gradients -------------------------------------------
+// W is read once and nothing else counts (50257 x 768 bf16: 77 MB).  A warp
+// takes four words at a time, 16 bytes of each a lane, against the tokens' x
+// in shared memory, and keeps each token's running maximum and sum; blocks
+// leave theirs for the last one to join.
+constexpr int kFewTokens = 8;
+
+struct FewArgs {
+  const void *X, *W;
+  const int *labels;
+  int N, d, V, mean;
+  float scale;
+  float2 *part;    // [blocks][kFewTokens]
+  float *target;   // [kFewTokens] the label's logit in units of ln 2
+  int *done;       // zero before the launch
+  float *loss, *lse, *total;
+};
+
+__device__ __forceinline__ void add_logit(float &top, float &sum, float l) {
+  if (l > top) {
+    sum = fmaf(sum, exp2_approx(top - l), 1.f);  // top minus infinity: sum is zero
+    top = l;
+  } else {
+    // (l - top is NaN where one of them is, or where both are infinite)
+    sum += l == -INFINITY ? 0.f : exp2_approx(l - top);
+  }
+}
+
+template <typename T, int NT>
+__global__ void __launch_bounds__(256) xent_few_kernel(const FewArgs a) {
+  extern __shared__ __align__(16) float xs[];  // [NT][d]
+  __shared__ float2 mine[8][NT];
+  __shared__ float losses[kFewTokens];
+  __shared__ int last;
+  griddep_wait();
+  constexpr int W16 = 16 / sizeof(T);  // values of 16 bytes
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, d = a.d;
+  const T *X = static_cast<const T *>(a.X), *W = static_cast<const T *>(a.W);
+  for (int i = threadIdx.x; i < NT * d; i += 256) xs[i] = i < a.N * d ? (float)X[i] : 0.f;
+  __syncthreads();
+  float top[NT], sum[NT];
+  int label[NT];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    top[n] = -INFINITY;
+    sum[n] = 0.f;
+    label[n] = n < a.N ? a.labels[n] : -1;
+  }
+  for (int w0 = (blockIdx.x * 8 + warp) * 4; w0 < a.V; w0 += gridDim.x * 32) {
+    float acc[4][NT] = {};
+#pragma unroll 2
+    for (int k = W16 * lane; k < d; k += 32 * W16) {
+      uint4 v[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        v[j] = __ldcs(reinterpret_cast<const uint4 *>(W + (size_t)min(w0 + j, a.V - 1) * d + k));
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        float x[W16];
+#pragma unroll
+        for (int q = 0; q < W16; q += 4)
+          *reinterpret_cast<float4 *>(x + q) = *reinterpret_cast<const float4 *>(xs + n * d + k + q);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t u[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&u[q]));
-            u[q] = pack_bf16(f.x * s, f.y * s);
+            if constexpr (sizeof(T) == 2) {
+              acc[j][n] = fmaf(__uint_as_float(u[q] << 16), x[2 * q], acc[j][n]);
+              acc[j][n] = fmaf(__uint_as_float(u[q] & 0xffff0000u), x[2 * q + 1], acc[j][n]);
+            } else {
+              acc[j][n] = fmaf(__uint_as_float(u[q]), x[q], acc[j][n]);
+            }
           }
-          w = make_uint4(u[0], u[1], u[2], u[3]);
         }
-        o[j] = w;
       }
     }
-    if (row_mixed[k] && label >= 0) {
-      for (int j = 0; j < a.parts; ++j) {
-        const float from = a.part[(size_t)j * a.rows + r].x;
-        if (from == row_ref[k]) continue;
-        const float f = exp2f(from - row_ref[k]);
-        for (int c = 128 * j + lane; c < min(128 * j + 128, a.V); c += 32)
-          if (c != label) {
-            __nv_bfloat16 *e = a.E + (size_t)r * a.ldE + c;
-            *e = __float2bfloat16_rn(__bfloat162float(*e) * f);
-          }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (w0 + j >= a.V) break;
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const float l = warp_sum(acc[j][n]) * kLog2e;
+        if (w0 + j == label[n]) {
+          if (lane == 0) a.target[n] = l;
+        } else {
+          add_logit(top[n], sum[n], l);
+        }
       }
     }
   }
-}
-
-// dX from the fp32 parts of its split sum, in the parts' order.
-__global__ void __launch_bounds__(256)
-xent_join_kernel(const float *__restrict__ part, long long stride, int splits,
-                 const float *__restrict__ scale, int rows, int d, __nv_bfloat16 *__restrict__ out) {
-  griddep_wait();
-  const long long i = (blockIdx.x * 256LL + threadIdx.x) * 4;
-  if (i >= (long long)rows * d) return;
-  float4 s = *reinterpret_cast<const float4 *>(part + i);
-  for (int k = 1; k < splits; ++k) {
-    const float4 v = *reinterpret_cast<const float4 *>(part + k * stride + i);
-    s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
-  }
-  const float f = scale[i / d];
-  *reinterpret_cast<uint2 *>(out + i) =
-      make_uint2(pack_bf16(s.x * f, s.y * f), pack_bf16(s.z * f, s.w * f));
-}
-
-__global__ void __launch_bounds__(256)
-xent_round_kernel(const float *__restrict__ in, long long n, __nv_bfloat16 *__restrict__ out) {
-  griddep_wait();
-  const long long i = (blockIdx.x * 256LL + threadIdx.x) * 8;
-  if (i >= n) return;
-  const float4 a = *reinterpret_cast<const float4 *>(in + i);
-  const float4 b = *reinterpret_cast<const float4 *>(in + i + 4);
-  *reinterpret_cast<uint4 *>(out + i) = make_uint4(pack_bf16(a.x, a.y), pack_bf16(a.z, a.w),
-                                                   pack_bf16(b.x, b.y), pack_bf16(b.z, b.w));
-}
-
-// total = factor * sum of the losses, in a fixed order
-__global__ void __launch_bounds__(1024)
-xent_total_kernel(const float *__restrict__ loss, long long N, const float *__restrict__ factor,
-                  float *__restrict__ total) {
-  __shared__ float buf[32];
-  griddep_wait();
-  float s = 0.f;
-  for (long long i = threadIdx.x; i < N; i += 1024) s += loss[i];
-  s = warp_sum(s);
-  if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = s;
+  if (lane == 0)
+#pragma unroll
+    for (int n = 0; n < NT; ++n) mine[warp][n] = make_float2(top[n], sum[n]);
   __syncthreads();
-  if (threadIdx.x < 32) {
-    s = warp_sum(buf[threadIdx.x]);
-    if (threadIdx.x == 0) *total = *factor * s;
+  if (threadIdx.x < NT) {
+    float2 v = mine[0][threadIdx.x];
+    for (int k = 1; k < 8; ++k) join_parts(v.x, v.y, mine[k][threadIdx.x].x, mine[k][threadIdx.x].y);
+    a.part[(size_t)blockIdx.x * kFewTokens + threadIdx.x] = v;
+  }
+  __threadfence();
+  __syncthreads();
+  if (threadIdx.x == 0) last = atomicAdd(a.done, 1) == gridDim.x - 1;
+  __syncthreads();
+  if (!last) return;
+  __threadfence();
+  // a warp a token
+  if (warp < a.N) {
+    const int y = a.labels[warp];
+    float loss = 0.f, lse = 0.f;
+    if (is_word(y, a.V)) {
+      float t = -INFINITY, s = 0.f;
+      for (int k = lane; k < gridDim.x; k += 32) {
+        const float2 v = __ldcg(a.part + (size_t)k * kFewTokens + warp);
+        join_parts(t, s, v.x, v.y);
+      }
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const float r = __shfl_xor_sync(0xffffffffu, t, o);
+        const float u = __shfl_xor_sync(0xffffffffu, s, o);
+        join_parts(t, s, r, u);
+      }
+      const float t2 = __ldcg(a.target + warp);
+      if (t <= t2) {  // relative to the label: log1p keeps a small loss's digits
+        s = t == t2 ? s : s * exp2f(t - t2);
+        t = t2;
+      }
+      float z;
+      loss = row_loss(t, s, t2, &z);
+      lse = fmaf(t2, kLn2, loss);
+    }
+    if (lane == 0) {
+      losses[warp] = loss;
+      a.loss[warp] = loss;
+      if (a.lse) a.lse[warp] = lse;
+    }
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    float s = 0.f;
+    int n = 0;
+    for (int k = 0; k < a.N; ++k) {
+      s += losses[k];
+      n += is_word(a.labels[k], a.V);
+    }
+    *a.total = (a.mean ? a.scale / (float)(n > 0 ? n : 1) : a.scale) * s;
   }
 }
 
-Params gemm_params(int M, int N, int K, int *status) {
+Params gemm_params(int M, int N, int K, const XentLayout &L, long long first, int rows, int products) {
   Params p = {};
   p.M = M;
   p.N = N;
   p.K = K;
-  p.row_pairs = (M + 2 * BM - 1) / (2 * BM);
-  p.n_tiles = (N + BN - 1) / BN;
-  p.splits = 1;
-  p.kb_split = (K + BK - 1) / BK;
-  p.total = p.row_pairs * p.n_tiles;
-  p.status = status;
+  p.live = L.live;
+  p.first = first;
+  p.rows = rows;
+  p.products = products;
+  p.status = L.status;
   return p;
+}
+
+template <typename T>
+cudaError_t run_few(const XentProblem &q) {
+  cudaError_t err = cudaMemsetAsync(q.L.status, 0, 256, q.stream);
+  if (err != cudaSuccess) return err;
+  FewArgs a = {};
+  a.X = q.X;
+  a.W = q.W;
+  a.labels = q.labels;
+  a.N = (int)q.N;
+  a.d = q.d;
+  a.V = q.V;
+  a.mean = q.mean;
+  a.scale = q.scale;
+  a.part = q.L.part;
+  a.target = q.L.ref;
+  a.done = q.L.done;
+  a.loss = q.loss;
+  a.lse = q.lse;
+  a.total = q.total;
+  const int need = (q.V + 31) / 32;
+  const dim3 grid(need < kXentFewBlocks ? need : kXentFewBlocks), block(256);
+  auto go = [&](auto kernel, int nt) {
+    const size_t smem = (size_t)nt * q.d * sizeof(float);
+    if (smem > 48 * 1024) {
+      const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                 kXentFewSmem);
+      if (e != cudaSuccess) return e;
+    }
+    return launch_pdl(kernel, grid, block, smem, q.stream, a);
+  };
+  if (q.N == 1) return go(xent_few_kernel<T, 1>, 1);
+  if (q.N == 2) return go(xent_few_kernel<T, 2>, 2);
+  if (q.N <= 4) return go(xent_few_kernel<T, 4>, 4);
+  return go(xent_few_kernel<T, 8>, 8);
+}
+
+template <typename T>
+cudaError_t run(const XentProblem &q) {
+  constexpr bool bf16 = sizeof(T) == 2;
+  constexpr int products = bf16 ? 1 : kProducts, terms = bf16 ? 1 : kTerms;
+  const XentLayout &L = q.L;
+  const bool grad = q.dX || q.dW;
+  cudaError_t err = cudaMemsetAsync(L.status, 0, sizeof(int), q.stream);
+  if (err != cudaSuccess) return err;
+  GatherArgs<T> g = {};
+  g.X = static_cast<const T *>(q.X);
+  g.W = static_cast<const T *>(q.W);
+  g.labels = q.labels;
+  g.N = q.N;
+  g.d = q.d;
+  g.V = q.V;
+  g.mean = q.mean;
+  g.scale = q.scale;
+  // every block counts the labels before it: at most 2048 of them
+  g.block_rows = (int)(8 * ((q.N + 8 * 2048 - 1) / (8 * 2048)));
+  g.L = L;
+  g.loss = q.loss;
+  g.lse = q.lse;
+  g.dX = static_cast<T *>(q.dX);
+  g.copy = L.piece >= q.N;
+  const unsigned blocks = (unsigned)((q.N + g.block_rows - 1) / g.block_rows);
+  if ((err = launch_pdl(xent_gather_kernel<T>, dim3(blocks), dim3(256), 0, q.stream, g)) != cudaSuccess)
+    return err;
+  const void *W = q.W;
+  if (!bf16) {
+    W = L.Ws;
+    err = launch_pdl(xent_split_kernel, dim3((q.V + 7) / 8), dim3(256), 0, q.stream,
+                     static_cast<const float *>(q.W), q.V, q.d, static_cast<__nv_bfloat16 *>(L.Ws),
+                     L.term);
+    if (err != cudaSuccess) return err;
+  }
+  // an operand's columns: d of the bf16 one (TMA fills what is behind with
+  // zeros), or three padded terms
+  const uint64_t width = bf16 ? (uint64_t)q.d : (uint64_t)terms * L.term;
+  CUtensorMap tW, tWn;
+  if ((err = make_tmap_bf16_2d(&tW, W, q.V, width, width, BN / 2, BK)) != cudaSuccess) return err;
+  if ((err = make_tmap_bf16_2d(&tWn, W, q.V, width, width, BK, 64)) != cudaSuccess) return err;
+  long long row_blocks = 0;
+  for (long long n0 = 0; n0 < q.N; n0 += L.piece)
+    row_blocks += ((q.N - n0 < L.piece ? q.N - n0 : L.piece) + 7) / 8;
+  for (long long n0 = 0; n0 < q.N; n0 += L.piece) {
+    const int rows = (int)(q.N - n0 < L.piece ? q.N - n0 : L.piece);
+    const int whole = (rows + 2 * BM - 1) / (2 * BM) * (2 * BM);  // rows of the buffers
+    const void *x = L.Xc;
+    if (!g.copy) {
+      err = launch_pdl(xent_copy_kernel<T>, dim3((rows + 7) / 8), dim3(256), 0, q.stream, g.X, q.d, L,
+                       n0, rows);
+      if (err != cudaSuccess) return err;
+    }
+    const uint64_t cols = (uint64_t)terms * L.ldE;
+    CUtensorMap tX, tE = tW;
+    if ((err = make_tmap_bf16_2d(&tX, x, whole, width, width, BM, BK)) != cudaSuccess) return err;
+    if (grad && (err = make_tmap_bf16_2d(&tE, L.E, whole, cols, cols, 32, 64)) != cudaSuccess)
+      return err;
+    Params p = gemm_params(rows, q.V, q.d, L, n0, rows, products);
+    p.a_term = p.b_term = L.term;
+    p.ref = L.ref + n0;
+    p.labels = L.labels + n0;
+    p.part = L.part;
+    p.e_term = (int)L.ldE;
+    const long long works = (long long)(whole / (2 * BM)) * ((q.V + BN - 1) / BN);
+    err = grad ? launch_gemm<kProbs>(tX, tW, tE, p, works, q.num_sms, q.stream)
+               : launch_gemm<kLoss>(tX, tW, tE, p, works, q.num_sms, q.stream);
+    if (err != cudaSuccess) return err;
+    RowArgs r = {};
+    r.L = L;
+    r.first = n0;
+    r.N = q.N;
+    r.rows = rows;
+    r.V = q.V;
+    r.d = q.d;
+    r.parts = (q.V + 127) / 128;
+    r.grad = grad;
+    r.scaled = q.dW != nullptr;
+    r.blocks = (int)row_blocks;
+    r.X = q.X;
+    r.loss = q.loss;
+    r.lse = q.lse;
+    r.total = q.total;
+    err = launch_pdl(xent_rows_kernel<T>, dim3((rows + 7) / 8), dim3(256), 0, q.stream, r);
+    if (err != cudaSuccess) return err;
+    if (q.dX) {
+      CUtensorMap tEa, tO;
+      if ((err = make_tmap_bf16_2d(&tEa, L.E, whole, cols, cols, BM, BK)) != cudaSuccess) return err;
+      const uint64_t parts = whole / (2 * BM) + kPlanPairs;
+      if ((err = make_tmap_f32_2d(&tO, L.dx_part, parts * 2 * BM, L.ld_part, L.ld_part, 32, 32)) !=
+          cudaSuccess)
+        return err;
+      Params g2 = gemm_params(rows, q.d, q.V, L, n0, rows, products);
+      g2.a_term = (int)L.ldE;
+      g2.b_term = L.term;
+      if ((err = launch_gemm<kDX>(tEa, tWn, tO, g2, kPlanPairs, q.num_sms, q.stream)) != cudaSuccess)
+        return err;
+      err = launch_pdl(xent_join_kernel<T>, dim3((rows + 7) / 8), dim3(256), 0, q.stream, L, n0, rows, q.d,
+                       q.V, products, static_cast<T *>(q.dX));
+      if (err != cudaSuccess) return err;
+    }
+    if (q.dW) {
+      CUtensorMap tEt, tXs, tO;
+      if ((err = make_tmap_bf16_2d(&tEt, L.E, whole, cols, cols, BK, 64)) != cudaSuccess) return err;
+      if ((err = make_tmap_bf16_2d(&tXs, x, whole, width, width, BK, 64)) != cudaSuccess) return err;
+      if (L.dw_sum) err = make_tmap_f32_2d(&tO, L.dw_sum, q.V, q.d, L.ld_dw, 32, 32);
+      else if (bf16) err = make_tmap_bf16_2d(&tO, q.dW, q.V, q.d, q.d, 32, 64);
+      else err = make_tmap_f32_2d(&tO, q.dW, q.V, q.d, q.d, 32, 32);
+      if (err != cudaSuccess) return err;
+      Params g3 = gemm_params(q.V, q.d, rows, L, n0, rows, products);
+      g3.a_term = (int)L.ldE;
+      g3.b_term = L.term;
+      g3.fp32 = !bf16 || L.dw_sum;
+      g3.add = n0 > 0;
+      const long long tiles = (long long)((q.V + 2 * BM - 1) / (2 * BM)) * ((q.d + BN - 1) / BN);
+      if ((err = launch_gemm<kDW>(tEt, tXs, tO, g3, tiles, q.num_sms, q.stream)) != cudaSuccess)
+        return err;
+    }
+  }
+  if (q.dW && L.dw_sum) {
+    const long long quads = (long long)q.V * ((q.d + 3) / 4);
+    return launch_pdl(xent_finish_kernel<T>, dim3((unsigned)((quads + 255) / 256)), dim3(256), 0,
+                      q.stream, L.dw_sum, L.ld_dw, q.V, q.d, static_cast<T *>(q.dW));
+  }
+  return cudaSuccess;
 }
 
 }  // namespace
 
-// Splits of dX's sum over the words: the count with the least estimated time,
-// the rounds of tiles over the pairs times a split's k-blocks (0.33 us a
-// k-block of a 256 x 256 tile at the measured bf16 rate), plus for more than
-// one the fp32 parts, written and read again at about 5 TB/s.
-int xent_dx_splits(int rows, int d, int V) {
-  const int tiles = ((rows + 2 * BM - 1) / (2 * BM)) * ((d + BN - 1) / BN);
-  const int pairs = kXentPlanSms / 2, kblocks = (V + BK - 1) / BK;
-  int best_n = 1;
-  double best = 0.0;
-  for (int s = 1; s <= 32 && (s == 1 || kblocks / s >= 8); ++s) {
-    const int kb = (kblocks + s - 1) / s, n = (kblocks + kb - 1) / kb;
-    const long long rounds = ((long long)tiles * n + pairs - 1) / pairs;
-    const double cost = 0.33 * (double)rounds * kb +
-                        (n > 1 ? n * (double)rows * d * 8 / 5e6 + 4.0 : 0.0);
-    if (s == 1 || cost < best) {
-      best = cost;
-      best_n = n;
-    }
-  }
-  return best_n;
+size_t xent_dx_part_rows(long long rows) {
+  return (size_t)((rows + 2 * BM - 1) / (2 * BM) + kPlanPairs) * 2 * BM;
 }
 
-cudaError_t xent_bf16(const XentProblem &q) {
-  const XentLayout &L = q.L;
-  cudaError_t err = cudaMemsetAsync(L.status, 0, sizeof(int), q.stream);
-  if (err != cudaSuccess) return err;
-  const bool grad = q.dX || q.dW;
-  const __nv_bfloat16 *X = static_cast<const __nv_bfloat16 *>(q.X);
-  const __nv_bfloat16 *W = static_cast<const __nv_bfloat16 *>(q.W);
-  CUtensorMap tW, tWn;
-  if ((err = make_tmap_bf16_2d(&tW, W, q.V, q.d, q.d, BN / 2, BK)) != cudaSuccess) return err;
-  if ((err = make_tmap_bf16_2d(&tWn, W, q.V, q.d, q.d, BK, 64)) != cudaSuccess) return err;
-  const bool pieces = L.piece < q.N;
-  for (long long n0 = 0; n0 < q.N; n0 += L.piece) {
-    const int rows = (int)(q.N - n0 < L.piece ? q.N - n0 : L.piece);
-    const __nv_bfloat16 *x = X + n0 * q.d;
-    const int *labels = q.labels + n0;
-    float *factor = n0 == 0 ? L.factor : nullptr;
-    err = launch_pdl(xent_target_kernel, dim3((rows + 7) / 8 + (factor ? 1 : 0)), dim3(256), 0,
-                     q.stream, x, W, labels, rows, q.d, q.V, L.ref, q.labels, q.N, q.mean, q.scale,
-                     factor);
-    if (err != cudaSuccess) return err;
-    CUtensorMap tX, tE = tW;
-    if ((err = make_tmap_bf16_2d(&tX, x, rows, q.d, q.d, BM, BK)) != cudaSuccess) return err;
-    if (grad && (err = make_tmap_bf16_2d(&tE, L.E, rows, q.V, L.ldE, 32, 64)) != cudaSuccess)
-      return err;
-    Params p = gemm_params(rows, q.V, q.d, L.status);
-    p.rows_first = 1;
-    p.ref = L.ref;
-    p.labels = labels;
-    p.part = L.part;
-    err = grad ? launch_gemm<kProbs>(tX, tW, tE, p, q.num_sms, q.stream)
-               : launch_gemm<kLoss>(tX, tW, tE, p, q.num_sms, q.stream);
-    if (err != cudaSuccess) return err;
-    RowArgs r = {};
-    r.ref = L.ref;
-    r.labels = labels;
-    r.part = L.part;
-    r.parts = (q.V + 127) / 128;
-    r.rows = rows;
-    r.V = q.V;
-    r.d = q.d;
-    r.loss = q.loss + n0;
-    r.lse = q.lse ? q.lse + n0 : nullptr;
-    r.factor = L.factor;
-    r.E = grad ? static_cast<__nv_bfloat16 *>(L.E) : nullptr;
-    r.ldE = L.ldE;
-    r.scale = L.row_scale;
-    r.X = x;
-    r.Xs = q.dW ? static_cast<__nv_bfloat16 *>(L.Xs) : nullptr;
-    err = launch_pdl(xent_rows_kernel, dim3((rows + 31) / 32), dim3(256), 0, q.stream, r);
-    if (err != cudaSuccess) return err;
-    if (q.dX) {
-      __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(q.dX) + n0 * q.d;
-      CUtensorMap tEa, tO;
-      if ((err = make_tmap_bf16_2d(&tEa, L.E, rows, q.V, L.ldE, BM, BK)) != cudaSuccess) return err;
-      Params g = gemm_params(rows, q.d, q.V, L.status);
-      const int splits = xent_dx_splits(rows, q.d, q.V);
-      g.kb_split = (g.kb_split + splits - 1) / splits;
-      g.splits = splits;
-      g.total *= splits;
-      g.scale = L.row_scale;
-      g.fp32 = splits > 1;
-      g.part_rows = (rows + 31) / 32 * 32;
-      if (splits > 1)
-        err = make_tmap_f32_2d(&tO, L.dx_part, (uint64_t)splits * g.part_rows, q.d, q.d, 32, 32);
-      else
-        err = make_tmap_bf16_2d(&tO, out, rows, q.d, q.d, 32, 64);
-      if (err != cudaSuccess) return err;
-      if ((err = launch_gemm<kDX>(tEa, tWn, tO, g, q.num_sms, q.stream)) != cudaSuccess) return err;
-      if (splits > 1) {
-        const long long quads = (long long)rows * q.d / 4;
-        err = launch_pdl(xent_join_kernel, dim3((unsigned)((quads + 255) / 256)), dim3(256), 0,
-                         q.stream, L.dx_part, (long long)g.part_rows * q.d, splits, L.row_scale,
-                         rows, q.d, out);
-        if (err != cudaSuccess) return err;
-      }
-    }
-    if (q.dW) {
-      CUtensorMap tEt, tXs, tO;
-      if ((err = make_tmap_bf16_2d(&tEt, L.E, rows, q.V, L.ldE, BK, 64)) != cudaSuccess) return err;
-      if ((err = make_tmap_bf16_2d(&tXs, L.Xs, rows, q.d, q.d, BK, 64)) != cudaSuccess) return err;
-      if (pieces) err = make_tmap_f32_2d(&tO, L.dw_sum, q.V, q.d, q.d, 32, 32);
-      else err = make_tmap_bf16_2d(&tO, q.dW, q.V, q.d, q.d, 32, 64);
-      if (err != cudaSuccess) return err;
-      Params g = gemm_params(q.V, q.d, rows, L.status);
-      g.fp32 = pieces;
-      g.add = n0 > 0;
-      if ((err = launch_gemm<kDW>(tEt, tXs, tO, g, q.num_sms, q.stream)) != cudaSuccess) return err;
-    }
-  }
-  if (q.dW && pieces) {
-    const long long n = (long long)q.V * q.d;
-    err = launch_pdl(xent_round_kernel, dim3((unsigned)((n / 8 + 255) / 256)), dim3(256), 0,
-                     q.stream, L.dw_sum, n, static_cast<__nv_bfloat16 *>(q.dW));
-    if (err != cudaSuccess) return err;
-  }
-  return xent_total(q);
+bool xent_few(long long N, int d, int dtype, bool grad) {
+  const int io = dtype == FLASH_GAU_BF16 ? 2 : 4;
+  const long long tokens = N <= 2 ? N : N <= 4 ? 4 : 8;
+  return !grad && N <= kFewTokens && (long long)d * io % 16 == 0 &&
+         tokens * d * (long long)sizeof(float) <= kXentFewSmem;
 }
 
-cudaError_t xent_total(const XentProblem &q) {
-  return launch_pdl(xent_total_kernel, dim3(1), dim3(1024), 0, q.stream, q.loss, q.N, q.L.factor,
-                    q.total);
+cudaError_t xent(const XentProblem &q, int dtype) {
+  const bool few = xent_few(q.N, q.d, dtype, q.dX || q.dW);
+  if (dtype == FLASH_GAU_BF16) return few ? run_few<__nv_bfloat16>(q) : run<__nv_bfloat16>(q);
+  return few ? run_few<float>(q) : run<float>(q);
 }
 
 }  // namespace flashgau

@@ -371,11 +371,12 @@ int flash_gau_rope_toeplitz_bias(const float *a, const float *b, int m, int C,
  * X is [N, d] (the last block's output), W [V, d] (one row a word).  A token
  * whose label y_i is outside [0, V) is left out: its loss, lse and row of dX
  * are zero, it adds nothing to dW, the mean is over the others (of none: 0),
- * and what its row of X holds, NaN included, has no effect.  The tokens are
- * taken in pieces of at most 2 GiB of [tokens, V] in the workspace.  bf16:
- * the products run on the tensor cores with fp32 accumulation and sums; the
- * exponentials enter the gradients' products rounded to bf16.  fp32: all in
- * fp32 on the CUDA cores.                                                   */
+ * and what its row of X holds, NaN included, has no effect (nor does it take
+ * time).  The other tokens are taken in pieces of at most 2 GiB of
+ * [tokens, V] in the workspace.  The products run on the tensor cores with
+ * fp32 accumulation and sums; bf16: the exponentials enter the gradients'
+ * products rounded to bf16; fp32: operands enter as three bf16 terms and a
+ * product as six of theirs, so that what is left out is below 2^-24 of it.  */
 #define FLASH_GAU_MEAN 0
 #define FLASH_GAU_SUM 1
 
@@ -393,7 +394,7 @@ typedef struct flash_gau_xent_out {
  * when the arguments are invalid or unsupported.                            */
 size_t flash_gau_xent_workspace_bytes(long long N, int d, int V, int dtype, int grad);
 
-/* X, W: device, io type, 16-byte aligned for bf16 (as dX and dW); labels:
+/* X, W: device, io type, 16-byte aligned (as dX and dW); labels:
  * device int32 [N]; reduction: FLASH_GAU_MEAN or _SUM; out: host pointer,
  * read during the call.  Outputs must not overlap the inputs, the workspace
  * or one another.  workspace: device, 256-byte aligned; its first word is

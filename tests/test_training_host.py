@@ -317,11 +317,12 @@ def test_xent_workspace(L):
     f = L.flash_gau_xent_workspace_bytes
     assert f(0, 64, 10, bd.BF16, 1) == 0 and f(4, 64, 10, 7, 1) == 0 and f(4, 4, 10, bd.BF16, 1) == 0
     assert f(4, 4, 10, bd.FP32, 1) > 0
-    # a piece's [tokens, V] never passes 2 GiB however many tokens there are
+    # a piece's [tokens, V] never passes 2 GiB however many tokens there are;
+    # a token itself takes three words
     for N in (1, 1000, 16384, 1 << 20, 1 << 30):
-        n = f(N, 768, 50257, bd.BF16, 1)
-        assert 0 < n < (3 << 30)
-        assert 0 < f(N, 768, 50257, bd.BF16, 0) < (300 << 20)
+        assert 0 < f(N, 768, 50257, bd.BF16, 1) < (3 << 30) + 12 * N
+        assert 0 < f(N, 768, 50257, bd.BF16, 0) < (3 << 30) + 12 * N
+        assert 0 < f(N, 768, 50257, bd.FP32, 1) < (3 << 30) + 12 * N
 
 
 def test_xent_binding_refuses_host_tensors(L):
