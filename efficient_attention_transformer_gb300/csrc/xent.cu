@@ -74,7 +74,9 @@ constexpr float kRaise = 40.0f * kLog2e;  // how far above the label's logit E i
 
 // kLoss: the logits' product, sums only; kProbs: sums and E; kDX: E W as
 // fp32 parts; kDW: E^T X', stored in bf16, or in fp32, or added to fp32
-enum Epi { kLoss, kProbs, kDX, kDW };
+// (kProbs3: E as three terms)
+enum Epi { kLoss, kProbs, kProbs3, kDX, kDW };
+constexpr bool is_logits(int epi) { return epi == kLoss || epi == kProbs || epi == kProbs3; }
 
 constexpr int kTerms = 3, kProducts = 6;  // of an fp32 value; of two
 
@@ -107,26 +109,33 @@ __device__ __forceinline__ void terms_of(const Params &p, int product, int &a, i
   b = (int)(kB >> (4 * product) & 15u);
 }
 
-// dX's sum over the words is long and its tiles are few, so it is dealt out
-// by k-blocks: `nt` pairs (one for each 256 columns) form a group, which takes
-// a run of `run` k-blocks of the row pairs' sums laid end to end.  A row pair
-// that two groups share has a part from each, at index row pair + group (each
-// step along the runs raises one or the other, so no two parts meet).
+// dX's sum over the words is long and its tiles are few, so what does not fill
+// a round of them is dealt out by k-blocks.  `nt` pairs (one for each 256
+// columns) form a group.  Each group takes whole row pairs as long as there is
+// one for every group, all at the same words, whose rows of W they share in
+// L2; the sums of the row pairs left are laid end to end and cut into runs of
+// `run` k-blocks, one a group.  A row pair that groups share has a part from
+// each, at index row pair + group (each step along the runs raises one or the
+// other, so no two parts meet); a whole one is the part of its own index.
 struct DxPlan {
-  int row_pairs, nt, groups, run;
-  long long steps;  // k-blocks of a row pair
+  int row_pairs, nt, groups;
+  int rounds;   // of whole row pairs
+  int steps;    // k-blocks of a row pair
+  int run;
+  int runs;     // groups that have one
+  __host__ __device__ int first_left() const { return rounds * groups; }
 };
-__host__ __device__ inline DxPlan dx_plan(long long rows, int d, int V, int products, int pairs) {
+__host__ __device__ inline DxPlan dx_plan(int rows, int d, int V, int products, int pairs) {
   DxPlan q;
-  q.row_pairs = (int)((rows + 2 * BM - 1) / (2 * BM));
+  q.row_pairs = (rows + 2 * BM - 1) / (2 * BM);
   q.nt = (d + BN - 1) / BN;
-  q.steps = (long long)products * ((V + BK - 1) / BK);
+  q.steps = products * ((V + BK - 1) / BK);
   q.groups = pairs / q.nt > 0 ? pairs / q.nt : 1;
-  const long long total = q.row_pairs * q.steps;
-  long long run = (total + q.groups - 1) / q.groups;
-  if (run < 8) run = 8;
-  q.run = (int)(run < 0x7fffffff ? run : 0x7fffffff);
-  q.groups = (int)((total + q.run - 1) / q.run);
+  q.rounds = q.row_pairs / q.groups;
+  const int total = (q.row_pairs - q.first_left()) * q.steps;  // under 2^7 * 2^19
+  q.run = (total + q.groups - 1) / q.groups;
+  if (q.run < 8) q.run = 8;
+  q.runs = (total + q.run - 1) / q.run;
   return q;
 }
 constexpr int kPlanPairs = kXentPlanSms / 2;
@@ -159,26 +168,31 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
 // and nsz columns.
 struct Work {
   int rp, n0, nsz;
-  long long k0, k1;
+  int k0, k1;
   int part;  // kDX: where the result goes
   bool add;  // it adds to what the work before has stored there
 };
 // The tensor cores cut off what an accumulator cannot hold at each step, so
 // a long sum comes out short, by 6e-8 of itself a k-block (fp32 io, 1400
 // k-blocks: 8e-5).  With fp32 io a sum of the gradients' products is
-// therefore taken in works of 32 k-blocks (2e-6), which add up in memory.
-constexpr int kFp32Blocks = 32;
+// therefore taken in works of few k-blocks, which add up in memory (1001
+// tokens, 8003 words, d = 520, error of dX and dW: 32 k-blocks 2.1e-6 and
+// 1.1e-6 in 209 us, 16 1.2e-6 and 0.7e-6 in 233 us, 8 0.7e-6 and 0.5e-6 in
+// 279 us).
+constexpr int kFp32Blocks = 16;
 
 // The works of one pair, in order.  Every role of the kernel walks the same.
 template <int EPI>
 struct Walk {
   const Params &p;
   int M, row_pairs, n_tiles, step;
-  long long steps;    // k-blocks of a whole product
-  long long u;        // next tile (kDX: unit)
-  long long pos, end;  // what is left of the unit's run (kDX) or of the tile
-  int limit;           // k-blocks of a work
-  int part_before;
+  int steps;     // k-blocks of a whole product
+  int limit;     // of a work
+  unsigned u;    // next tile (kDX: unit, a group's columns)
+  int pos, end;  // k-blocks of what is under way
+  int rp, n0, part;
+  // kDX
+  int round, run_pos, run_end;
   DxPlan dx;
   __device__ Walk(const Params &params) : p(params) {
     const long long left = *reinterpret_cast<const volatile int *>(p.live) - p.first;
@@ -186,64 +200,88 @@ struct Walk {
     u = blockIdx.x / 2;
     step = gridDim.x / 2;
     pos = end = 0;
-    limit = p.products == 1 || EPI == kLoss || EPI == kProbs ? 0x7fffffff : kFp32Blocks;
-    part_before = -1;
+    limit = p.products == 1 || is_logits(EPI) ? 0x7fffffff : kFp32Blocks;
     M = EPI == kDW ? p.M : tokens;
     n_tiles = (p.N + BN - 1) / BN;
     row_pairs = (M + 2 * BM - 1) / (2 * BM);
     const int K = EPI == kDW ? tokens : p.K;
-    steps = (long long)p.products * ((K + BK - 1) / BK);
-    if (EPI == kDX) dx = dx_plan(tokens, p.N, p.K, p.products, kPlanPairs);
+    steps = p.products * ((K + BK - 1) / BK);
+    if (EPI == kDX) {
+      dx = dx_plan(tokens, p.N, p.K, p.products, kPlanPairs);
+      round = run_pos = run_end = 0;
+      start_unit();
+    }
+  }
+  __device__ void start_unit() {
+    const int g = (int)(u / dx.nt);
+    n0 = (int)(u % dx.nt) * BN;
+    round = 0;
+    run_pos = g * dx.run;
+    run_end = min(run_pos + dx.run, (dx.row_pairs - dx.first_left()) * dx.steps);
+    part = g;
+  }
+  // the next row pair, or share of one
+  __device__ bool advance_dx() {
+    for (;;) {
+      if (u >= (unsigned)(dx.groups * dx.nt)) return false;
+      const int g = (int)(u / dx.nt);
+      if (round < dx.rounds) {
+        rp = part = round++ * dx.groups + g;
+        pos = 0;
+        end = dx.steps;
+        return true;
+      }
+      if (run_pos < run_end) {
+        const int q = run_pos / dx.steps;
+        rp = dx.first_left() + q;
+        part = rp + g;
+        pos = run_pos - q * dx.steps;
+        end = min(dx.steps, pos + run_end - run_pos);
+        run_pos += end - pos;
+        return true;
+      }
+      u += step;
+      start_unit();
+    }
   }
   __device__ bool next(Work &w) {
-    if (EPI == kDX) {
-      if (pos == end) {
-        if (u >= (long long)dx.groups * dx.nt) return false;
-        pos = u / dx.nt * dx.run;
-        end = min(pos + dx.run, (long long)dx.row_pairs * dx.steps);
-        part_before = -1;
-        u += step;
-      }
-      const long long unit = u - step;
-      w.rp = (int)(pos / dx.steps);
-      w.n0 = (int)(unit % dx.nt) * BN;
-      w.k0 = pos - w.rp * dx.steps;
-      w.k1 = min(min(dx.steps, w.k0 + (end - pos)), w.k0 + limit);
-      w.part = w.rp + (int)(unit / dx.nt);
-      w.add = w.part == part_before;
-      part_before = w.part;
-      pos += w.k1 - w.k0;
-    } else {
-      if (pos == end) {
-        if (u >= (long long)row_pairs * n_tiles) return false;
+    w.add = EPI == kDW && p.add;
+    if (pos == end) {
+      if (EPI == kDX) {
+        if (!advance_dx()) return false;
+      } else {
+        if (u >= (unsigned)row_pairs * n_tiles) return false;
+        if (EPI == kDW) {
+          n0 = (int)(u % n_tiles) * BN;
+          rp = (int)(u / n_tiles);
+        } else {
+          // rows fastest: the pairs share a tile of W while X stays in L2
+          rp = (int)(u % row_pairs);
+          n0 = (int)(u / row_pairs) * BN;
+        }
         pos = 0;
         end = steps;
         u += step;
       }
-      const long long tile = u - step;
-      if (EPI == kDW) {
-        w.n0 = (int)(tile % n_tiles) * BN;
-        w.rp = (int)(tile / n_tiles);
-      } else {
-        // rows fastest: the pairs share a tile of W while X stays in L2
-        w.rp = (int)(tile % row_pairs);
-        w.n0 = (int)(tile / row_pairs) * BN;
-      }
-      w.k0 = pos;
-      w.k1 = min(end, pos + limit);
-      w.add = pos > 0 || p.add;
-      pos = w.k1;
+    } else {
+      w.add = true;
     }
+    w.rp = rp;
+    w.n0 = n0;
+    w.part = part;
+    w.k0 = pos;
+    w.k1 = end - pos < limit ? end : pos + limit;
+    pos = w.k1;
     // a multiple of 128: each CTA holds whole 64-column boxes; the logits'
     // sums are kept by 128 words, so their tiles are never narrower
-    w.nsz = EPI == kLoss || EPI == kProbs ? BN : min(BN, (p.N - w.n0 + 127) / 128 * 128);
+    w.nsz = is_logits(EPI) ? BN : min(BN, (p.N - n0 + 127) / 128 * 128);
     return true;
   }
   // k-block s of a product: which term pair, and the depth in it
-  __device__ void locate(long long s, int &product, int &k) const {
-    const unsigned per = (unsigned)(steps / p.products), at = (unsigned)s;
-    product = p.products == 1 ? 0 : (int)(at / per);
-    k = (int)(at - product * per) * BK;
+  __device__ void locate(int s, int &product, int &k) const {
+    const unsigned per = (unsigned)(EPI == kDX ? dx.steps : steps) / p.products;
+    product = p.products == 1 ? 0 : (int)((unsigned)s / per);
+    k = (int)((unsigned)s - product * per) * BK;
   }
 };
 
@@ -281,7 +319,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 xent_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                  const __grid_constant__ CUtensorMap tmC, const Params p) {
   constexpr bool A_MN = EPI == kDW;                     // E read by columns
-  constexpr bool B_KM = EPI == kLoss || EPI == kProbs;  // W read by rows
+  constexpr bool B_KM = is_logits(EPI);                 // W read by rows
   extern __shared__ uint8_t smem_raw[];
   uint8_t *tiles = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -327,7 +365,7 @@ xent_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
       uint32_t phase = 0;
       while (!sm->abort_flag && walk.next(x)) {
         const int m0 = (x.rp * 2 + rank) * BM, half = x.nsz / 2, hboxes = half / 64;
-        for (long long s = x.k0; s < x.k1; ++s) {
+        for (int s = x.k0; s < x.k1; ++s) {
           int product, k, ta, tb;
           walk.locate(s, product, k);
           terms_of(p, product, ta, tb);
@@ -370,7 +408,9 @@ xent_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
       int stage = 0;
       uint32_t phase = 0;
       int local = 0;
-      for (; !sm->abort_flag && walk.next(x); ++local) {
+      Work following;
+      bool more = walk.next(x);
+      for (; more && !sm->abort_flag; ++local, x = following) {
         const int acc = local & 1;
         if (!mbar_wait(smem_u32(&sm->acc_empty[acc]), ((local >> 1) & 1) ^ 1, &sm->abort_flag)) {
           raise_timeout(sm, p.status);
@@ -380,7 +420,7 @@ xent_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
         const uint32_t d_tmem = tmem_base + acc * ACC_COLS;
         const uint32_t idesc = idesc_bf16_f32(2 * BM, x.nsz, A_MN ? 1 : 0, B_KM ? 0 : 1);
         bool ok = true;
-        for (long long s = x.k0; s < x.k1; ++s) {
+        for (int s = x.k0; s < x.k1; ++s) {
           if (!mbar_wait(smem_u32(&sm->full[stage]), phase, &sm->abort_flag)) {
             raise_timeout(sm, p.status);
             ok = false;
@@ -401,9 +441,12 @@ xent_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
             stage = 0;
             phase ^= 1;
           }
+          // found while the tensor cores work, not between two works
+          if (s == x.k0) more = walk.next(following);
         }
         if (!ok) break;
         mma_commit_pair_mc(smem_u32(&sm->acc_full[acc]), kPair);
+        if (x.k0 == x.k1) more = walk.next(following);
       }
       mma_commit_pair_mc(smem_u32(&sm->drain), kLeader);
       if (!mbar_wait(smem_u32(&sm->drain), 0)) raise_timeout(sm, p.status);
@@ -422,7 +465,7 @@ xent_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
       // this row's scalars, before the wait
       float ref = 0.f;
       int label = -1;
-      if constexpr (EPI == kLoss || EPI == kProbs) {
+      if constexpr (is_logits(EPI)) {
         if (live) {
           ref = p.ref[row];
           label = p.labels[row];
@@ -439,7 +482,7 @@ xent_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&sm->acc_empty[acc]), 0));
       };
-      if constexpr (EPI == kLoss || EPI == kProbs) {
+      if constexpr (is_logits(EPI)) {
         const bool whole = x.n0 + c_end <= p.N;  // every column is a word
         // the largest logit of this row's 128 words
         float top = -INFINITY;
@@ -459,51 +502,61 @@ xent_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
         top *= kLog2e;
         if (top > ref + kRaise) ref = top;
         float sum[4] = {0.f, 0.f, 0.f, 0.f};
-        for (int c0 = c_begin; c0 < c_end; c0 += 64) {
-          float e[2][32];
+        // 32 exponentials of this row from column c on, summed up
+        auto exps = [&](int c, float (&e)[32]) {
+          uint32_t v[32];
+          tmem_ld32(taddr + c, v);
+          tmem_ld_wait();
+          if (c + 32 >= c_end) drained();
+          const int col = x.n0 + c;
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t v[32];
-            tmem_ld32(taddr + c0 + 32 * h, v);
-            tmem_ld_wait();
-            if (c0 + 64 >= c_end && h == 1) drained();
-            const int col = x.n0 + c0 + 32 * h;
+          for (int j = 0; j < 32; ++j) e[j] = exp2_approx(fmaf(__uint_as_float(v[j]), kLog2e, -ref));
+          if (!whole) {
 #pragma unroll
             for (int j = 0; j < 32; ++j)
-              e[h][j] = exp2_approx(fmaf(__uint_as_float(v[j]), kLog2e, -ref));
-            if (!whole) {
-#pragma unroll
-              for (int j = 0; j < 32; ++j)
-                if (col + j >= p.N) e[h][j] = 0.f;
-            }
-            // the label's own term stays out of the sum, exactly
-            if ((unsigned)(label - col) < 32u) {
-#pragma unroll
-              for (int j = 0; j < 32; ++j)
-                if (label - col == j) e[h][j] = 0.f;
-            }
-            if (label < 0) {  // no token: whatever the row holds
-#pragma unroll
-              for (int j = 0; j < 32; ++j) e[h][j] = 0.f;
-            }
-#pragma unroll
-            for (int j = 0; j < 32; ++j) sum[j & 3] += e[h][j];
+              if (col + j >= p.N) e[j] = 0.f;
           }
-          // boxes wholly behind an edge are not stored; rows behind the last
-          // one are, as zeros: the products that follow read whole tiles
-          if (EPI == kProbs && x.n0 + c0 < p.N) {
-            for (int term = 0;; ++term) {
+          // the label's own term stays out of the sum, exactly
+          if ((unsigned)(label - col) < 32u) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (label - col == j) e[j] = 0.f;
+          }
+          if (label < 0) {  // no token: whatever the row holds
+#pragma unroll
+            for (int j = 0; j < 32; ++j) e[j] = 0.f;
+          }
+#pragma unroll
+          for (int j = 0; j < 32; ++j) sum[j & 3] += e[j];
+        };
+        // Boxes wholly behind an edge are not stored; rows behind the last one
+        // are, as zeros: the products that follow read whole tiles.
+        for (int c0 = c_begin; c0 < c_end; c0 += 64) {
+          const bool stored = EPI != kLoss && x.n0 + c0 < p.N;
+          if constexpr (EPI == kProbs3) {
+            float e[2][32];
+            exps(c0, e[0]);
+            exps(c0 + 32, e[1]);
+            for (int term = 0; stored && term < kTerms; ++term) {
               st.begin();
               put32(st, 0, e[0]);
               put32(st, 4, e[1]);
               st.finish(&tmC, term * p.e_term + x.n0 + c0, row0, false);
-              if (p.products == 1 || term == kTerms - 1) break;
 #pragma unroll
               for (int j = 0; j < 32; ++j) {
                 e[0][j] -= __bfloat162float(__float2bfloat16_rn(e[0][j]));
                 e[1][j] -= __bfloat162float(__float2bfloat16_rn(e[1][j]));
               }
             }
+          } else {
+            if (stored) st.begin();
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              float e[32];
+              exps(c0 + 32 * h, e);
+              if (EPI == kProbs && stored) put32(st, 4 * h, e);
+            }
+            if (stored) st.finish(&tmC, x.n0 + c0, row0, false);
           }
         }
         if (live && x.n0 + c_begin < p.N)
@@ -822,7 +875,7 @@ __global__ void __launch_bounds__(256) xent_rows_kernel(const RowArgs a) {
       bool mixed = false;
       if (row < tokens) {
         const float2 *part = a.L.part + row;
-#pragma unroll 4
+#pragma unroll 8
         for (int k = threadIdx.x >> 3; k < a.parts; k += 32) {
           const float2 v = part[(size_t)k * a.rows];
           mixed |= join_parts(top, sum, v.x, v.y);
@@ -934,46 +987,47 @@ __device__ __forceinline__ void store_as(float *p, float v) { *p = v; }
 __device__ __forceinline__ void store_as(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
 
 // dX from the parts of its sum, in the groups' order, times the row's factor,
-// to where the row came from; a warp a row.
+// to where the row came from; four columns a thread.
 template <typename T>
 __global__ void __launch_bounds__(256)
 xent_join_kernel(const XentLayout L, long long first, int rows, int d, int V, int products,
                  T *__restrict__ out) {
-  __shared__ int first_part, parts;
+  __shared__ DxPlan q;
   griddep_wait();
   const long long left = *L.live - first;
   const int tokens = left < 0 ? 0 : left < rows ? (int)left : rows;
-  const int row0 = blockIdx.x * 8, rp = row0 / (2 * BM);  // of one row pair
-  if (row0 >= tokens) return;
-  if (threadIdx.x == 0) {
-    const DxPlan q = dx_plan(tokens, d, V, products, kPlanPairs);
-    const int g0 = (int)(rp * q.steps / q.run), g1 = (int)(((rp + 1) * q.steps - 1) / q.run);
-    first_part = rp + g0;
-    parts = g1 - g0 + 1;
-  }
+  const int quads = (d + 3) / 4;
+  const long long i = blockIdx.x * 256LL + threadIdx.x;
+  if (blockIdx.x * 256LL >= (long long)tokens * quads) return;
+  if (threadIdx.x == 0) q = dx_plan(tokens, d, V, products, kPlanPairs);
   __syncthreads();
-  const int row = row0 + (threadIdx.x >> 5), n = parts;
+  const int row = (int)(i / quads), c = (int)(i % quads) * 4;
   if (row >= tokens) return;
+  const int rp = row / (2 * BM);
+  int g0 = 0, n = 1;
+  if (rp >= q.first_left()) {
+    const int at = (rp - q.first_left()) * q.steps;
+    g0 = at / q.run;
+    n = (at + q.steps - 1) / q.run - g0 + 1;
+  }
   const long long step = 2LL * BM * L.ld_part;
-  const float *p = L.dx_part + first_part * step + (long long)(row - rp * 2 * BM) * L.ld_part;
+  const float *p = L.dx_part + (rp + g0) * step + (long long)(row - rp * 2 * BM) * L.ld_part + c;
   const float f = L.row_scale[row];
-  T *o = out + (size_t)L.index[first + row] * d;
-  for (int c = 4 * (threadIdx.x & 31); c < d; c += 128) {
-    float4 s = *reinterpret_cast<const float4 *>(p + c);
-#pragma unroll 4
-    for (int k = 1; k < n; ++k) {
-      const float4 v = *reinterpret_cast<const float4 *>(p + k * step + c);
-      s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
-    }
-    if constexpr (sizeof(T) == 2) {  // d is a multiple of 8
-      *reinterpret_cast<uint2 *>(o + c) =
-          make_uint2(pack_bf16(s.x * f, s.y * f), pack_bf16(s.z * f, s.w * f));
-    } else {
-      const float v[4] = {s.x, s.y, s.z, s.w};
+  float4 s = __ldcs(reinterpret_cast<const float4 *>(p));
+#pragma unroll 8
+  for (int k = 1; k < n; ++k) {
+    const float4 v = __ldcs(reinterpret_cast<const float4 *>(p + k * step));
+    s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+  }
+  T *o = out + (size_t)L.index[first + row] * d + c;
+  if constexpr (sizeof(T) == 2) {  // d is a multiple of 8
+    *reinterpret_cast<uint2 *>(o) =
+        make_uint2(pack_bf16(s.x * f, s.y * f), pack_bf16(s.z * f, s.w * f));
+  } else {
+    const float v[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (c + k < d) o[c + k] = v[k] * f;
-    }
+    for (int k = 0; k < 4; ++k)
+      if (c + k < d) o[k] = v[k] * f;
   }
 }
 
@@ -1258,7 +1312,7 @@ cudaError_t run(const XentProblem &q) {
     p.part = L.part;
     p.e_term = (int)L.ldE;
     const long long works = (long long)(whole / (2 * BM)) * ((q.V + BN - 1) / BN);
-    err = grad ? launch_gemm<kProbs>(tX, tW, tE, p, works, q.num_sms, q.stream)
+    err = grad ? launch_gemm<bf16 ? kProbs : kProbs3>(tX, tW, tE, p, works, q.num_sms, q.stream)
                : launch_gemm<kLoss>(tX, tW, tE, p, works, q.num_sms, q.stream);
     if (err != cudaSuccess) return err;
     RowArgs r = {};
@@ -1290,8 +1344,9 @@ cudaError_t run(const XentProblem &q) {
       g2.b_term = L.term;
       if ((err = launch_gemm<kDX>(tEa, tWn, tO, g2, kPlanPairs, q.num_sms, q.stream)) != cudaSuccess)
         return err;
-      err = launch_pdl(xent_join_kernel<T>, dim3((rows + 7) / 8), dim3(256), 0, q.stream, L, n0, rows, q.d,
-                       q.V, products, static_cast<T *>(q.dX));
+      const long long quads = (long long)rows * ((q.d + 3) / 4);
+      err = launch_pdl(xent_join_kernel<T>, dim3((unsigned)((quads + 255) / 256)), dim3(256), 0,
+                       q.stream, L, n0, rows, q.d, q.V, products, static_cast<T *>(q.dX));
       if (err != cudaSuccess) return err;
     }
     if (q.dW) {
