@@ -174,12 +174,13 @@ struct Work {
 };
 // The tensor cores cut off what an accumulator cannot hold at each step, so
 // a long sum comes out short, by 6e-8 of itself a k-block (fp32 io, 1400
-// k-blocks: 8e-5).  With fp32 io a sum of the gradients' products is
-// therefore taken in works of few k-blocks, which add up in memory (1001
-// tokens, 8003 words, d = 520, error of dX and dW: 32 k-blocks 2.1e-6 and
-// 1.1e-6 in 209 us, 16 1.2e-6 and 0.7e-6 in 233 us, 8 0.7e-6 and 0.5e-6 in
-// 279 us).
-constexpr int kFp32Blocks = 16;
+// k-blocks: 8e-5).  With fp32 io the large product of a gradient's sum is
+// therefore taken in works of few k-blocks, which add up in memory; the five
+// small products before it lose nothing that counts and go into its first
+// (1001 tokens, 8003 words, d = 520, errors of dX and dW: 16 k-blocks 1.4e-6
+// and 1.1e-6 in 201 us, 8 0.8e-6 and 0.6e-6 in 219 us, 4 0.4e-6 and 0.3e-6 in
+// 280 us).
+constexpr int kFp32Blocks = 8;
 
 // The works of one pair, in order.  Every role of the kernel walks the same.
 template <int EPI>
@@ -187,7 +188,7 @@ struct Walk {
   const Params &p;
   int M, row_pairs, n_tiles, step;
   int steps;     // k-blocks of a whole product
-  int limit;     // of a work
+  int large;     // the first k-block of a work's limit (see kFp32Blocks)
   unsigned u;    // next tile (kDX: unit, a group's columns)
   int pos, end;  // k-blocks of what is under way
   int rp, n0, part;
@@ -200,12 +201,12 @@ struct Walk {
     u = blockIdx.x / 2;
     step = gridDim.x / 2;
     pos = end = 0;
-    limit = p.products == 1 || is_logits(EPI) ? 0x7fffffff : kFp32Blocks;
     M = EPI == kDW ? p.M : tokens;
     n_tiles = (p.N + BN - 1) / BN;
     row_pairs = (M + 2 * BM - 1) / (2 * BM);
     const int K = EPI == kDW ? tokens : p.K;
     steps = p.products * ((K + BK - 1) / BK);
+    large = p.products == 1 || is_logits(EPI) ? 0x7fffffff : steps / p.products * (p.products - 1);
     if (EPI == kDX) {
       dx = dx_plan(tokens, p.N, p.K, p.products, kPlanPairs);
       round = run_pos = run_end = 0;
@@ -270,7 +271,8 @@ struct Walk {
     w.n0 = n0;
     w.part = part;
     w.k0 = pos;
-    w.k1 = end - pos < limit ? end : pos + limit;
+    w.k1 = end;
+    if (end > large) w.k1 = min(end, max(pos, large) + kFp32Blocks);
     pos = w.k1;
     // a multiple of 128: each CTA holds whole 64-column boxes; the logits'
     // sums are kept by 128 words, so their tiles are never narrower
@@ -740,7 +742,8 @@ __global__ void __launch_bounds__(256) xent_gather_kernel(const GatherArgs<T> a)
   const long long row0 = (long long)blockIdx.x * a.block_rows;
   const long long end = min(row0 + a.block_rows, a.N);
   int n = 0;
-  for (long long i = threadIdx.x; i < row0; i += 256) n += is_word(a.labels[i], a.V);
+#pragma unroll 8
+  for (long long i = threadIdx.x; i < row0; i += 256) n += is_word(__ldg(a.labels + i), a.V);
   n = __reduce_add_sync(0xffffffffu, n);
   if (lane == 0) counts[warp] = n;
   __syncthreads();
@@ -961,8 +964,8 @@ __global__ void __launch_bounds__(256) xent_rows_kernel(const RowArgs a) {
       }
     }
   }
-  // total, by whichever block comes last
-  __threadfence();
+  // total, by whichever block comes last (lane 0 wrote the loss)
+  if (lane == 0) __threadfence();
   __syncthreads();
   if (threadIdx.x == 0) last = atomicAdd(a.L.done, 1) == a.blocks - 1;
   __syncthreads();
