@@ -9,6 +9,7 @@ when the library has not been built.
 import ctypes
 import os
 
+import numpy as np
 import torch
 
 from .build import LIB as _LIB_PATH
@@ -675,19 +676,13 @@ def residual_norm_backward(dr, dn, r, y, post_norm=NORM_NONE, post_g=None, post_
         raise FlashGauError(ENOTSUP if M > 0 and d > 0 else EINVAL, "invalid or unsupported problem")
     given, out = out or {}, dict.fromkeys(_GRADS)
     out.update(given)
-    # what is not given: the rows one by one, the parameters' gradients and the
-    # workspace as parts of one array
-    for name, there in (("dh", True), ("dy", y is not None), ("dgate", gate is not None)):
-        if there and out[name] is None:
-            out[name] = torch.empty_like(like)
-    sizes = (d if scale is not None else 0,
-             (0, d, 1)[post_norm] if 0 <= post_norm < 3 else 0, d if post_norm == NORM_LAYER else 0,
-             (0, d, 1)[norm] if 0 <= norm < 3 else 0, d if norm == NORM_LAYER else 0)
-    made = [(name, n) for name, n in zip(_GRADS[3:], sizes) if n and out[name] is None]
-    if made:
-        parts = torch.empty(sum([n for _, n in made]), dtype=f32, device=dev)
-        for (name, _), part in zip(made, parts.split_with_sizes([n for _, n in made])):
-            out[name] = part
+    for name, like_, there in (("dh", like, True), ("dy", like, y is not None), ("dgate", gate, True),
+                               ("dscale", scale, True), ("dpost_g", post_g, post_norm),
+                               ("dpost_b", post_g, post_norm == NORM_LAYER),
+                               ("dnorm_g", norm_g, norm), ("dnorm_b", norm_g, norm == NORM_LAYER)):
+        if there and like_ is not None and out[name] is None:
+            out[name] = torch.empty_like(like_)
+    sizes = (d, 1 if post_norm == NORM_SCALE else d, d, 1 if norm == NORM_SCALE else d, d)
     if workspace is None:
         workspace = torch.empty(nw, dtype=torch.uint8, device=dev)
     else:
@@ -810,6 +805,10 @@ class AdamW:
         spans.sort()
         if any(a[1] > b[0] for a, b in zip(spans, spans[1:])):
             raise ValueError("the tensors' parameters, copies and moments must not overlap")
+        # the array's columns that change from step to step
+        view = np.frombuffer(self._array, dtype=np.dtype(AdamWTensor))
+        self._g, self._g_dtype = view["g"], view["g_dtype"]
+        self._shapes = [p.shape for p in self.params]
         self.hyper = AdamWHyper(0.0, float(betas[0]), float(betas[1]), float(eps), 0, state_bits,
                                 None)
         self.state_bits, self.steps = state_bits, 0
@@ -826,10 +825,14 @@ class AdamW:
             with _scope(self.device, stream):
                 return self.step(grads, lr, step, grad_scale)
         h, dev = self.hyper, self.device
-        for e, p, g in zip(self._array, self.params, grads):
-            if g.shape != p.shape or g.device != dev:
+        at = dev.index
+        for p, g in zip(self._shapes, grads):
+            if g.shape != p or g.get_device() != at:
                 raise ValueError("each gradient must be like its parameter")
-            e.g, e.g_dtype = _dev_ptr(g, "gradient"), dtype_code(g.dtype)
+            if not g.is_contiguous():
+                raise ValueError("gradients must be contiguous")
+        dtypes = [dtype_code(g.dtype) for g in grads]
+        self._g[:], self._g_dtype[:] = [g.data_ptr() for g in grads], dtypes
         h.lr, h.step = lr, self.steps + 1 if step is None else step
         h.grad_scale = _param(grad_scale, "grad_scale", 1, dev.index)
         _check(lib().flash_gau_adamw_step(self._array, len(grads), h, _stream(dev)))
@@ -854,9 +857,9 @@ class AdamW:
         out_m = out_m or [torch.empty_like(p) for p in self.params]
         out_v = out_v or [torch.empty_like(p) for p in self.params]
         for name, out in (("out_m", out_m), ("out_v", out_v)):
-            if len(out) != k or any(o.numel() != p.numel() or o.device != dev
-                                    for o, p in zip(out, self.params)):
+            if len(out) != k:
                 raise ValueError("%s must hold a tensor like each parameter" % name)
-            ptrs.append((ctypes.c_void_p * k)(*(_dev_ptr(o, name, torch.float32) for o in out)))
+            ptrs.append((ctypes.c_void_p * k)(*[_like(o, name, p, torch.float32, dev.index)
+                                                for o, p in zip(out, self._shapes)]))
         _check(lib().flash_gau_adamw_moments(self._array, k, *ptrs, _stream(dev)))
         return out_m, out_v

@@ -354,7 +354,7 @@ struct XentProblem {
 // a device
 constexpr int kXentPlanSms = 152;
 constexpr int kXentFewBlocks = 4 * 152, kXentFewSmem = 64 * 1024;
-size_t xent_dx_part_rows(long long rows);
+size_t xent_dx_part_rows(long long rows, int d);
 // whether a call takes the form for a few tokens, whose workspace is the
 // slot, `ref` and `part` alone
 bool xent_few(long long N, int d, int dtype, bool grad);

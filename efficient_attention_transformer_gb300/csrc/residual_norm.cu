@@ -36,6 +36,7 @@
 #include <type_traits>
 
 #include "flash_gau_internal.h"
+#include "packed_f32.cuh"
 #include "sm103_ptx.cuh"
 
 namespace flashgau {
@@ -306,41 +307,8 @@ __global__ void __launch_bounds__(128) residual_norm_any_kernel(const Args a) {
 }
 
 // --------------------------------------------------------------- backward --
-// Two fp32 values that one instruction works on (fma.rn.f32x2 and the like):
-// the backward is bound by instruction issue more than by memory, and half of
-// what it issues is such arithmetic.
-using f2 = unsigned long long;
-__device__ __forceinline__ f2 pair(float a, float b) {
-  f2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ f2 both(float a) { return pair(a, a); }
-__device__ __forceinline__ float2 split(f2 v) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-  return r;
-}
-__device__ __forceinline__ float sum(f2 v) {
-  const float2 r = split(v);
-  return r.x + r.y;
-}
-__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
-  f2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
-  f2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ f2 add2(f2 a, f2 b) {
-  f2 r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-
+// The backward is bound by instruction issue more than by memory, and half of
+// what it issues is arithmetic on pairs (packed_f32.cuh).
 // Four columns of a row: consecutive ones from c on (VEC; 8 bytes of bf16,
 // 16 of fp32), or c, c + stride, c + 2 stride, c + 3 stride, zeros behind d.
 struct F4 {
@@ -748,8 +716,12 @@ residual_norm_grad_rows_kernel(const Args a) {
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  for (int i = lane; i < kSlots * kSlot; i += 32)
-    ring[i] = T(!a.gate && i % kSlot >= 4 * kWidth ? 1.f : 0.f);
+  // zeros and ones, 16 bytes at a time
+  const uint32_t ones = a.gate ? 0u : sizeof(T) == 2 ? 0x3f803f80u : 0x3f800000u;
+  for (int i = lane * W; i < kSlots * kSlot; i += 32 * W) {
+    const uint32_t v = i % kSlot >= 4 * kWidth ? ones : 0u;
+    *reinterpret_cast<uint4 *>(ring + i) = make_uint4(v, v, v, v);
+  }
   __syncwarp();
   ptx::griddep_wait();
 #pragma unroll

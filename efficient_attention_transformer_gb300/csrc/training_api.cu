@@ -1,6 +1,7 @@
 // C ABI of the operators around the layer in a training step: argument
 // checks, then the launches on the caller's stream (kernels in
 // residual_norm.cu, adamw.cu and xent.cu).
+#include <float.h>
 #include <math.h>
 
 #include "flash_gau_internal.h"
@@ -50,7 +51,8 @@ int check_norm(int kind, const float *g, const float *b) {
 
 int check_residual(const flash_gau_residual *o, long long M, int d, int dtype) {
   if (!o || M <= 0 || d <= 0 || !io_type(dtype)) return FLASH_GAU_EINVAL;
-  if (!(o->eps > 0.f) || !isfinite(o->eps) || !aligned(o->scale, 4)) return FLASH_GAU_EINVAL;
+  // a normal number: its inverse is one too
+  if (!(o->eps >= FLT_MIN) || !isfinite(o->eps) || !aligned(o->scale, 4)) return FLASH_GAU_EINVAL;
   int st = check_norm(o->post, o->post_g, o->post_b);
   if (st == FLASH_GAU_OK) st = check_norm(o->norm, o->norm_g, o->norm_b);
   if (st != FLASH_GAU_OK) return st;
@@ -123,7 +125,7 @@ size_t xent_layout(long long N, int d, int V, int dtype, bool grad, char *base, 
     l.row_scale = reinterpret_cast<float *>(take(n * 4));
     l.E = take(n * terms * l.ldE * 2);
     l.ld_part = (d + 63) / 64 * 64;
-    l.dx_part = reinterpret_cast<float *>(take(xent_dx_part_rows(l.piece) * l.ld_part * 4));
+    l.dx_part = reinterpret_cast<float *>(take(xent_dx_part_rows(l.piece, d) * l.ld_part * 4));
     l.ld_dw = (d + 3) / 4 * 4;
     if (pieces > 1 || (!bf16 && d % 4 != 0))
       l.dw_sum = reinterpret_cast<float *>(take((size_t)V * l.ld_dw * 4));

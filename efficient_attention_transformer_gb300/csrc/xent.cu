@@ -1338,10 +1338,8 @@ cudaError_t run(const XentProblem &q) {
     if (q.dX) {
       CUtensorMap tEa, tO;
       if ((err = make_tmap_bf16_2d(&tEa, L.E, whole, cols, cols, BM, BK)) != cudaSuccess) return err;
-      const uint64_t parts = whole / (2 * BM) + kPlanPairs;
-      if ((err = make_tmap_f32_2d(&tO, L.dx_part, parts * 2 * BM, L.ld_part, L.ld_part, 32, 32)) !=
-          cudaSuccess)
-        return err;
+      err = make_tmap_f32_2d(&tO, L.dx_part, xent_dx_part_rows(rows, q.d), L.ld_part, L.ld_part, 32, 32);
+      if (err != cudaSuccess) return err;
       Params g2 = gemm_params(rows, q.d, q.V, L, n0, rows, products);
       g2.a_term = (int)L.ldE;
       g2.b_term = L.term;
@@ -1380,8 +1378,9 @@ cudaError_t run(const XentProblem &q) {
 
 }  // namespace
 
-size_t xent_dx_part_rows(long long rows) {
-  return (size_t)((rows + 2 * BM - 1) / (2 * BM) + kPlanPairs) * 2 * BM;
+size_t xent_dx_part_rows(long long rows, int d) {
+  const DxPlan q = dx_plan((int)rows, d, 1, 1, kPlanPairs);
+  return (size_t)(q.row_pairs + q.groups) * 2 * BM;
 }
 
 bool xent_few(long long N, int d, int dtype, bool grad) {

@@ -424,7 +424,7 @@ typedef struct flash_gau_residual {
   const float *norm_b;  /* as post_b                                         */
   const float *scale;   /* device fp32 [d]: residual scale, or NULL (ones)   */
   const void *gate;     /* device [M, d], io type, or NULL (ones)            */
-  float eps;            /* of both norms; > 0                                */
+  float eps;            /* of both norms; > 0, a normal number               */
 } flash_gau_residual;
 
 /* h, y: device [M, d], io type; y may be NULL (then r = h; post, gate and

@@ -150,6 +150,7 @@ def _residual(**kw):
     (dict(norm_g=None), dict(), bd.EINVAL),
     (dict(eps=0.0), dict(), bd.EINVAL),
     (dict(eps=float("nan")), dict(), bd.EINVAL),
+    (dict(eps=1e-40), dict(), bd.EINVAL),
     (dict(), dict(n=None), bd.EINVAL),                   # a norm and no place for it
     (dict(norm=bd.NORM_NONE), dict(), bd.EINVAL),        # a place and no norm
     (dict(norm=bd.NORM_NONE), dict(n=None, r=None), bd.EINVAL),
