@@ -572,7 +572,7 @@ class Decoder:
 def _elsewhere(device, stream):
     """Whether a call on `device` needs _scope: a stream of its own, or another
     device than the current one."""
-    return stream is not None or device.index != torch.cuda.current_device()
+    return stream is not None or device.index != torch._C._cuda_getDevice()
 
 
 def _scope(device, stream):
@@ -609,12 +609,14 @@ def _param(t, name, n, index):
 def _residual(shape, dtype, index, post_norm, post_g, post_b, gate, scale, norm, norm_g, norm_b,
               eps):
     d = shape[-1]
-    return Residual(post_norm, norm,
-                    _param(post_g, "post_g", d if post_norm == NORM_LAYER else 1, index),
-                    _param(post_b, "post_b", d, index),
-                    _param(norm_g, "norm_g", d if norm == NORM_LAYER else 1, index),
-                    _param(norm_b, "norm_b", d, index), _param(scale, "scale", d, index),
-                    _like(gate, "gate", shape, dtype, index), eps)
+    return Residual(
+        post_norm, norm,
+        None if post_g is None else _param(post_g, "post_g", d if post_norm == NORM_LAYER else 1, index),
+        None if post_b is None else _param(post_b, "post_b", d, index),
+        None if norm_g is None else _param(norm_g, "norm_g", d if norm == NORM_LAYER else 1, index),
+        None if norm_b is None else _param(norm_b, "norm_b", d, index),
+        None if scale is None else _param(scale, "scale", d, index),
+        None if gate is None else _like(gate, "gate", shape, dtype, index), eps)
 
 
 def residual_norm(h, y=None, post_norm=NORM_NONE, post_g=None, post_b=None, gate=None, scale=None,
@@ -624,24 +626,30 @@ def residual_norm(h, y=None, post_norm=NORM_NONE, post_g=None, post_b=None, gate
     flash_gau_residual_norm.  h, y, gate: [..., d] in one io type; scale and
     the norms' parameters fp32 ([d], a ScaleNorm's g [1]).  Without y only the
     norm is taken and r is h; with norm NORM_NONE n is None."""
-    shape, dtype = h.shape, h.dtype
-    dt, hp, dev = dtype_code(dtype), _dev_ptr(h, "h"), h.device
+    dtype, shape, dev = h.dtype, h.shape, h.device
+    dt, hp, at = dtype_code(dtype), _dev_ptr(h, "h"), dev.index
     if _elsewhere(dev, stream):
         with _scope(dev, stream):
             return residual_norm(h, y, post_norm, post_g, post_b, gate, scale, norm, norm_g,
                                  norm_b, eps, out_r, out_n)
-    at = dev.index
     o = _residual(shape, dtype, at, post_norm, post_g, post_b, gate, scale, norm, norm_g, norm_b,
                   eps)
-    if out_r is None and y is not None:
-        out_r = torch.empty_like(h)
-    if out_n is None and norm != NORM_NONE:
+    yp = rp = np_ = None
+    if y is not None:
+        yp = _like(y, "y", shape, dtype, at)
+        if out_r is None:
+            out_r = torch.empty_like(h)
+            rp = out_r.data_ptr()
+    if out_r is not None and rp is None:
+        rp = _like(out_r, "out_r", shape, dtype, at)
+    if out_n is not None:
+        np_ = _like(out_n, "out_n", shape, dtype, at)
+    elif norm != NORM_NONE:
         out_n = torch.empty_like(h)
+        np_ = out_n.data_ptr()
     d = shape[-1]
-    _check(lib().flash_gau_residual_norm(
-        hp, _like(y, "y", shape, dtype, at), o, h.numel() // max(d, 1), d, dt,
-        _like(out_r, "out_r", shape, dtype, at), _like(out_n, "out_n", shape, dtype, at),
-        _stream(dev)))
+    _check(lib().flash_gau_residual_norm(hp, yp, o, h.numel() // (d or 1), d, dt, rp, np_,
+                                         torch._C._cuda_getCurrentRawStream(at)))
     return (h if out_r is None else out_r), out_n
 
 
@@ -660,39 +668,47 @@ def residual_norm_backward(dr, dn, r, y, post_norm=NORM_NONE, post_g=None, post_
     like = dr if dr is not None else dn
     if like is None:
         raise ValueError("one of dr and dn must be given")
-    shape, dtype, dev = like.shape, like.dtype, like.device
-    dt = dtype_code(dtype)
     _dev_ptr(like, "dr" if dr is not None else "dn")
+    shape, dtype, dev = like.shape, like.dtype, like.device
+    dt, at, d = dtype_code(dtype), dev.index, shape[-1]
     if _elsewhere(dev, stream):
         with _scope(dev, stream):
             return residual_norm_backward(dr, dn, r, y, post_norm, post_g, post_b, gate, scale,
                                           norm, norm_g, norm_b, eps, out, workspace)
-    at, f32, d = dev.index, torch.float32, shape[-1]
     o = _residual(shape, dtype, at, post_norm, post_g, post_b, gate, scale, norm, norm_g, norm_b,
                   eps)
-    M = like.numel() // max(d, 1)
+    M = like.numel() // (d or 1)
+    ins = [None if t is None else _like(t, name, shape, dtype, at)
+           for name, t in (("dr", dr), ("dn", dn), ("r", r), ("y", y))]
     nw = lib().flash_gau_residual_norm_backward_workspace_bytes(M, d)
     if nw == 0:
         raise FlashGauError(ENOTSUP if M > 0 and d > 0 else EINVAL, "invalid or unsupported problem")
-    given, out = out or {}, dict.fromkeys(_GRADS)
-    out.update(given)
-    for name, like_, there in (("dh", like, True), ("dy", like, y is not None), ("dgate", gate, True),
-                               ("dscale", scale, True), ("dpost_g", post_g, post_norm),
-                               ("dpost_b", post_g, post_norm == NORM_LAYER),
-                               ("dnorm_g", norm_g, norm), ("dnorm_b", norm_g, norm == NORM_LAYER)):
-        if there and like_ is not None and out[name] is None:
-            out[name] = torch.empty_like(like_)
-    sizes = (d, 1 if post_norm == NORM_SCALE else d, d, 1 if norm == NORM_SCALE else d, d)
+    given, out, ptrs = out or {}, {}, []
+    if not given.keys() <= set(_GRADS):
+        raise ValueError("out holds %s only" % ", ".join(_GRADS))
+    # each is like a tensor of the forward, which is None where it has no gradient
+    for name, src in zip(_GRADS, (like, y, gate, scale, post_g if post_norm else None,
+                                  post_g if post_norm == NORM_LAYER else None,
+                                  norm_g if norm else None,
+                                  norm_g if norm == NORM_LAYER else None)):
+        t = given.get(name)
+        if t is not None:
+            if src is None:
+                raise ValueError("%s is the gradient of nothing here" % name)
+            ptrs.append(_like(t, name, src.shape, src.dtype, at))
+        elif src is not None:
+            t = torch.empty_like(src)
+            ptrs.append(t.data_ptr())
+        else:
+            ptrs.append(None)
+        out[name] = t
     if workspace is None:
         workspace = torch.empty(nw, dtype=torch.uint8, device=dev)
+        wp = workspace.data_ptr()
     else:
-        nw = workspace.numel() * workspace.element_size()
-    g = ResidualGrads(*[_like(out[k], k, shape, dtype, at) for k in _GRADS[:3]],
-                      *[_param(out[k], k, n, at) for k, n in zip(_GRADS[3:], sizes)])
-    _check(lib().flash_gau_residual_norm_backward(
-        _like(dr, "dr", shape, dtype, at), _like(dn, "dn", shape, dtype, at),
-        _like(r, "r", shape, dtype, at), _like(y, "y", shape, dtype, at), o, M, d, dt, g,
-        _dev_ptr(workspace, "workspace"), nw, _stream(dev)))
+        wp, nw = _dev_ptr(workspace, "workspace"), workspace.numel() * workspace.element_size()
+    _check(lib().flash_gau_residual_norm_backward(*ins, o, M, d, dt, ResidualGrads(*ptrs), wp, nw,
+                                                  torch._C._cuda_getCurrentRawStream(at)))
     return out
 
 
@@ -731,18 +747,22 @@ def xent(X, W, labels, reduction=MEAN, scale=1.0, grad=True, out=None, workspace
         t, shape = out.get(name), () if like is None else like.shape
         if name[0] == "d" and not grad:
             t = out[name] = None
+            ptrs.append(None)
         elif t is None:
             t = out[name] = torch.empty(shape, dtype=dtype, device=dev)
+            ptrs.append(t.data_ptr())
         elif t.shape != shape or t.device != dev:
             raise ValueError("%s must be %s on %s" % (name, tuple(shape), dev))
-        ptrs.append(None if t is None else _dev_ptr(t, name, dtype))
+        else:
+            ptrs.append(_dev_ptr(t, name, dtype))
     if workspace is None:
-        workspace = torch.empty(xent_workspace_bytes(N, d, V, dt, grad), dtype=torch.uint8,
-                                device=dev)
-    _check(lib().flash_gau_xent(
-        xp, wp, lp, N, d, V, dt, reduction, scale, XentOut(*ptrs),
-        _dev_ptr(workspace, "workspace"), workspace.numel() * workspace.element_size(),
-        _stream(dev)))
+        nw = xent_workspace_bytes(N, d, V, dt, grad)
+        workspace = torch.empty(nw, dtype=torch.uint8, device=dev)
+        ws = workspace.data_ptr()
+    else:
+        ws, nw = _dev_ptr(workspace, "workspace"), workspace.numel() * workspace.element_size()
+    _check(lib().flash_gau_xent(xp, wp, lp, N, d, V, dt, reduction, scale, XentOut(*ptrs), ws, nw,
+                                _stream(dev)))
     return out
 
 
@@ -762,7 +782,8 @@ class AdamW:
                  state_bits=32, m=None, v=None, m_scale=None, v_scale=None):
         if state_bits not in (8, 32):
             raise ValueError("state_bits must be 8 or 32")
-        self.params, k = list(params), len(params)
+        self.params = list(params)
+        k = len(self.params)
         self.copies = [None] * k if copies is None else list(copies)
         decay = list(weight_decay) if isinstance(weight_decay, (list, tuple)) else [weight_decay] * k
         f32 = torch.float32
@@ -783,35 +804,41 @@ class AdamW:
         if any(len(x) != k for x in lists):
             raise ValueError("every list must have one entry for each parameter")
         self.device = self.params[0].device if k else None
-        self._array = (AdamWTensor * max(k, 1))()
-        spans = []
-        for i, p in enumerate(self.params):
-            e, n = self._array[i], p.numel()
-            parts = [("p", p, f32, n), ("m", self.m[i], md, n), ("v", self.v[i], vd, n)]
-            if self.copies[i] is not None:
-                parts.append(("copy", self.copies[i], torch.bfloat16, n))
-            if eight:
-                parts += [("m_scale", self.m_scale[i], f32, blocks(n)),
-                          ("v_scale", self.v_scale[i], f32, blocks(n))]
-            for name, t, dtype, size in parts:
-                ptr = _dev_ptr(t, name, dtype)
-                if t.numel() != size or t.device != self.device:
-                    raise ValueError("%s of tensor %d must hold %d values on %s"
-                                     % (name, i, size, self.device))
-                setattr(e, name, ptr)
-                if size:
-                    spans.append((ptr, ptr + size * t.element_size()))
-            e.n, e.weight_decay = n, float(decay[i])
-        spans.sort()
-        if any(a[1] > b[0] for a, b in zip(spans, spans[1:])):
-            raise ValueError("the tensors' parameters, copies and moments must not overlap")
-        # the array's columns that change from step to step
-        view = np.frombuffer(self._array, dtype=np.dtype(AdamWTensor))
-        self._g, self._g_dtype = view["g"], view["g_dtype"]
         self._shapes = [p.shape for p in self.params]
+        self._array = (AdamWTensor * max(k, 1))()
+        columns = np.frombuffer(self._array, dtype=np.dtype(AdamWTensor))
+        n = [p.numel() for p in self.params]
+        columns["n"][:k], columns["weight_decay"][:k] = n, decay
+        kinds = [("p", self.params, f32, n), ("m", self.m, md, n), ("v", self.v, vd, n),
+                 ("copy", self.copies, torch.bfloat16, n)]
+        if eight:
+            scales = [blocks(x) for x in n]
+            kinds += [("m_scale", self.m_scale, f32, scales), ("v_scale", self.v_scale, f32, scales)]
+        begin, end = [], []
+        for name, tensors, dtype, sizes in kinds:
+            ptrs = [self._pointer(t, name, dtype, x) for t, x in zip(tensors, sizes)]
+            columns[name][:k] = ptrs
+            live = [(a, x) for a, x in zip(ptrs, sizes) if a and x]
+            begin += [a for a, _ in live]
+            end += [a + x * dtype.itemsize for a, x in live]
+        order = np.argsort(np.array(begin, dtype=np.uint64))
+        begin, end = np.array(begin, dtype=np.uint64)[order], np.array(end, dtype=np.uint64)[order]
+        if (end[:-1] > begin[1:]).any():
+            raise ValueError("the tensors' parameters, copies and moments must not overlap")
+        # the columns that change from step to step
+        self._g, self._g_dtype = columns["g"], columns["g_dtype"]
         self.hyper = AdamWHyper(0.0, float(betas[0]), float(betas[1]), float(eps), 0, state_bits,
                                 None)
         self.state_bits, self.steps = state_bits, 0
+
+    def _pointer(self, t, name, dtype, size):
+        """0 where there is none (a copy)."""
+        if t is None and name == "copy":
+            return 0
+        ptr = _dev_ptr(t, name, dtype)
+        if t.numel() != size or t.device != self.device:
+            raise ValueError("%s must hold %d values on %s" % (name, size, self.device))
+        return ptr
 
     def step(self, grads, lr, step=None, grad_scale=None, stream=None):
         """One update with `grads`, a list of fp32 or bf16 tensors like the
