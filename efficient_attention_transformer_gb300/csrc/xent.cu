@@ -866,18 +866,24 @@ __global__ void __launch_bounds__(256) xent_rows_kernel(const RowArgs a) {
   __shared__ int differ[8], last;
   griddep_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int row0 = blockIdx.x * 8, row = row0 + warp;  // this warp's row, later
+  // everything that does not wait for the number of rows is asked for first
+  // (the buffers hold a.rows rows; what is behind the last one is not used)
+  const int safe = row < a.rows ? row : a.rows - 1;
+  const float ref = a.L.ref[a.first + safe], factor = *a.L.factor;
+  const int label = a.L.labels[a.first + safe], token = a.L.index[a.first + safe];
+  const int r = threadIdx.x & 7, part_row = row0 + r < a.rows ? row0 + r : a.rows - 1;
+  const float part_ref = a.L.ref[a.first + part_row];
   const long long left = *a.L.live - a.first;
   const int tokens = left < 0 ? 0 : left < a.rows ? (int)left : a.rows;
-  const int row0 = blockIdx.x * 8;
   if (row0 < tokens) {
     if (threadIdx.x < 8) differ[threadIdx.x] = 0;
     __syncthreads();
     {
-      const int r = threadIdx.x & 7, row = row0 + r;
-      float top = row < tokens ? a.L.ref[a.first + row] : 0.f, sum = 0.f;
+      float top = part_ref, sum = 0.f;
       bool mixed = false;
-      if (row < tokens) {
-        const float2 *part = a.L.part + row;
+      if (row0 + r < tokens) {
+        const float2 *part = a.L.part + part_row;
 #pragma unroll 8
         for (int k = threadIdx.x >> 3; k < a.parts; k += 32) {
           const float2 v = part[(size_t)k * a.rows];
@@ -888,10 +894,7 @@ __global__ void __launch_bounds__(256) xent_rows_kernel(const RowArgs a) {
       if (mixed) differ[r] = 1;
     }
     __syncthreads();
-    const int row = row0 + warp;
     if (row < tokens) {
-      const float ref = a.L.ref[a.first + row];
-      const int label = a.L.labels[a.first + row], token = a.L.index[a.first + row];
       const float2 own = joined[warp][lane];
       float top = own.x, sum = own.y;
       bool mixed = differ[warp];
@@ -904,7 +907,7 @@ __global__ void __launch_bounds__(256) xent_rows_kernel(const RowArgs a) {
       mixed = __any_sync(0xffffffffu, mixed);
       float z;
       const float loss = row_loss(top, sum, ref, &z);
-      float scale = *a.L.factor / z;
+      float scale = factor / z;
       const int terms = sizeof(T) == 4 ? kTerms : 1;
       __nv_bfloat16 *E = static_cast<__nv_bfloat16 *>(a.L.E) + (size_t)row * terms * a.L.ldE;
       if (lane == 0) {
@@ -982,7 +985,7 @@ __global__ void __launch_bounds__(256) xent_rows_kernel(const RowArgs a) {
   if (threadIdx.x == 0) {
     float t = 0.f;
     for (int k = 0; k < 8; ++k) t += joined[0][k].x;
-    *a.total = *a.L.factor * t;
+    *a.total = factor * t;
   }
 }
 
@@ -1064,7 +1067,7 @@ struct FewArgs {
   const int *labels;
   int N, d, V, mean;
   float scale;
-  float2 *part;    // [blocks][kFewTokens]
+  float2 *part;    // [kFewTokens][blocks]
   float *target;   // [kFewTokens] the label's logit in units of ln 2
   int *done;       // zero before the launch
   float *loss, *lse, *total;
@@ -1150,7 +1153,7 @@ __global__ void __launch_bounds__(256) xent_few_kernel(const FewArgs a) {
   if (threadIdx.x < NT) {
     float2 v = mine[0][threadIdx.x];
     for (int k = 1; k < 8; ++k) join_parts(v.x, v.y, mine[k][threadIdx.x].x, mine[k][threadIdx.x].y);
-    a.part[(size_t)blockIdx.x * kFewTokens + threadIdx.x] = v;
+    a.part[(size_t)threadIdx.x * gridDim.x + blockIdx.x] = v;
   }
   __threadfence();
   __syncthreads();
@@ -1158,23 +1161,37 @@ __global__ void __launch_bounds__(256) xent_few_kernel(const FewArgs a) {
   __syncthreads();
   if (!last) return;
   __threadfence();
-  // a warp a token
-  if (warp < a.N) {
-    const int y = a.labels[warp];
-    float loss = 0.f, lse = 0.f;
-    if (is_word(y, a.V)) {
-      float t = -INFINITY, s = 0.f;
-      for (int k = lane; k < gridDim.x; k += 32) {
-        const float2 v = __ldcg(a.part + (size_t)k * kFewTokens + warp);
-        join_parts(t, s, v.x, v.y);
+  // 256 / NT threads a token join its blocks' parts
+  constexpr int kShare = 256 / NT, kWarps = kShare / 32;
+  {
+    const int n = threadIdx.x / kShare;
+    float t = -INFINITY, s = 0.f;
+    float2 v[4];
+    for (int k0 = threadIdx.x % kShare; k0 < gridDim.x; k0 += 4 * kShare) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int k = k0 + q * kShare;
+        v[q] = k < gridDim.x ? __ldcg(a.part + (size_t)n * gridDim.x + k) : make_float2(-INFINITY, 0.f);
       }
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const float r = __shfl_xor_sync(0xffffffffu, t, o);
-        const float u = __shfl_xor_sync(0xffffffffu, s, o);
-        join_parts(t, s, r, u);
-      }
-      const float t2 = __ldcg(a.target + warp);
+      for (int q = 0; q < 4; ++q) join_parts(t, s, v[q].x, v[q].y);
+    }
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const float r = __shfl_xor_sync(0xffffffffu, t, o);
+      const float u = __shfl_xor_sync(0xffffffffu, s, o);
+      join_parts(t, s, r, u);
+    }
+    if (lane == 0) mine[warp % kWarps][n] = make_float2(t, s);
+  }
+  __syncthreads();
+  if (threadIdx.x < a.N) {
+    const int n = threadIdx.x, y = a.labels[n];
+    float loss = 0.f, lse = 0.f;
+    if (is_word(y, a.V)) {
+      float t = mine[0][n].x, s = mine[0][n].y;
+      for (int k = 1; k < kWarps; ++k) join_parts(t, s, mine[k][n].x, mine[k][n].y);
+      const float t2 = __ldcg(a.target + n);
       if (t <= t2) {  // relative to the label: log1p keeps a small loss's digits
         s = t == t2 ? s : s * exp2f(t - t2);
         t = t2;
@@ -1183,11 +1200,9 @@ __global__ void __launch_bounds__(256) xent_few_kernel(const FewArgs a) {
       loss = row_loss(t, s, t2, &z);
       lse = fmaf(t2, kLn2, loss);
     }
-    if (lane == 0) {
-      losses[warp] = loss;
-      a.loss[warp] = loss;
-      if (a.lse) a.lse[warp] = lse;
-    }
+    losses[n] = loss;
+    a.loss[n] = loss;
+    if (a.lse) a.lse[n] = lse;
   }
   __syncthreads();
   if (threadIdx.x == 0) {
