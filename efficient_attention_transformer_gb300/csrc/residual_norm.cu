@@ -85,9 +85,17 @@ __device__ __forceinline__ float2 unpack_bf16(uint32_t w) {
 // around zero (ScaleNorm).  The hardware's reciprocal square root (off by at
 // most 2 units in the last place): exact division and root cost a row more
 // instructions than its sums do.
+__device__ __forceinline__ float inv_layer(float m2, float inv_d, float eps) {
+  return rsqrtf(fmaf(m2, inv_d, eps));
+}
+// at most inv_eps = 1 / eps, and not a number where m2 is not (a minimum alone
+// would leave such a row's other values finite)
+__device__ __forceinline__ float inv_scale(float m2, float inv_eps) {
+  const float r = rsqrtf(m2);
+  return r > inv_eps ? inv_eps : r;
+}
 __device__ __forceinline__ float inv_spread(float m2, int kind, float inv_d, float eps) {
-  return kind == FLASH_GAU_NORM_LAYER ? rsqrtf(fmaf(m2, inv_d, eps))
-                                      : fminf(rsqrtf(m2), 1.0f / eps);
+  return kind == FLASH_GAU_NORM_LAYER ? inv_layer(m2, inv_d, eps) : inv_scale(m2, 1.0f / eps);
 }
 // ScaleNorm: whether |x| > eps, where the gradient has its second term
 __device__ __forceinline__ bool longer(float m2, float eps) { return m2 > eps * eps; }
@@ -811,11 +819,11 @@ residual_norm_grad_rows_kernel(const Args a) {
       }
       const float4 q = row_sum(sum(m2), sum(swx), Is<NORM_COL>(), sum(sw));
       if (NORM_COL) {
-        inv_r = rsqrtf(fmaf(q.x, inv_d, a.eps));
+        inv_r = inv_layer(q.x, inv_d, a.eps);
         a_r = -q.z * inv_d;
         b_r = -q.y * inv_r * inv_d;
       } else {
-        inv_r = fminf(rsqrtf(q.x), inv_eps);
+        inv_r = inv_scale(q.x, inv_eps);
         b_r = longer(q.x, a.eps) ? -q.y * inv_r : 0.f;
       }
     }
@@ -847,11 +855,11 @@ residual_norm_grad_rows_kernel(const Args a) {
       if (a.post) {
         const float4 q = row_sum(sum(m2), sum(sgy), Is<PS == 2>(), sum(sg));
         if (PS == 2) {
-          inv_y = rsqrtf(fmaf(q.x, inv_d, a.eps));
+          inv_y = inv_layer(q.x, inv_d, a.eps);
           a_y = -q.z * inv_d;
           b_y = -q.y * inv_y * inv_d;
         } else {
-          inv_y = fminf(rsqrtf(q.x), inv_eps);
+          inv_y = inv_scale(q.x, inv_eps);
           b_y = longer(q.x, a.eps) ? -q.y * inv_y : 0.f;
         }
       }

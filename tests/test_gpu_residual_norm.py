@@ -279,6 +279,25 @@ def test_nan_stays_in_its_row():
     assert n[2].isnan().all() and n[4].isnan().any()
 
 
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("d", [768, 767, 2304])
+def test_nan_takes_its_whole_row_of_a_scale_norm(d, dtype):
+    """A length that is not a number is not one below eps."""
+    p = Problem(6, d, dtype, "scale", "scale", True, True, 11)
+    r0, n0 = bd.residual_norm(p.h, p.y, **p.call)
+    g0 = bd.residual_norm_backward(p.dr, p.dn, p.h, p.y, **p.call)
+    p.y[2, 5] = float("nan")
+    p.h[4, 0] = float("nan")
+    r, n = bd.residual_norm(p.h, p.y, **p.call)
+    g = bd.residual_norm_backward(p.dr, p.dn, p.h, p.y, **p.call)
+    keep = [0, 1, 3, 5]
+    assert r[2].isnan().all() and n[[2, 4]].isnan().all()
+    assert g["dy"][[2, 4]].isnan().all() and g["dh"][4].isnan().all()
+    assert g["dpost_g"].isnan().all() and g["dnorm_g"].isnan().all()
+    for a, b in ((r, r0), (n, n0), (g["dh"], g0["dh"]), (g["dy"], g0["dy"])):
+        assert torch.equal(a[keep], b[keep])
+
+
 def test_other_stream_and_captured():
     p = Problem(300, 768, "bf16", "scale", "layer", True, True, 12)
     r, n = bd.residual_norm(p.h, p.y, **p.call)
