@@ -176,7 +176,9 @@ int flash_gau_residual_norm(const void *h, const void *y, const flash_gau_residu
   const size_t ng = (size_t)(o->norm == FLASH_GAU_NORM_LAYER ? d : 1) * 4;
   const Span in[8] = {{h, bytes},       {y, bytes},       {o->gate, bytes}, {o->scale, (size_t)d * 4},
                       {o->post_g, pg},  {o->post_b, pg},  {o->norm_g, ng},  {o->norm_b, ng}};
-  if (!separate(out, in, true)) return FLASH_GAU_EINVAL;
+  // rows may take their inputs' place; parameters are read for every row
+  const Span params[5] = {in[3], in[4], in[5], in[6], in[7]};
+  if (!separate(out, in, true) || !separate(out, params, false)) return FLASH_GAU_EINVAL;
   ResidualProblem q = residual_problem(o, y, M, d, dtype, stream);
   if ((st = current_sms(&q.num_sms)) != FLASH_GAU_OK) return st;
   return status_of(residual_norm(q, h, r, n));
@@ -215,19 +217,20 @@ int flash_gau_residual_norm_backward(const void *dr, const void *dn, const void 
   const size_t pg = (size_t)(o->post == FLASH_GAU_NORM_LAYER ? d : 1) * 4;
   const size_t ng = (size_t)(o->norm == FLASH_GAU_NORM_LAYER ? d : 1) * 4;
   const size_t col = (size_t)d * 4;
-  const Span rows[3] = {{g->dh, bytes}, {g->dy, bytes}, {g->dgate, bytes}};
-  const Span out[9] = {rows[0], rows[1], rows[2], {g->dscale, col}, {g->dpost_g, pg},
-                       {g->dpost_b, pg}, {g->dnorm_g, ng}, {g->dnorm_b, ng},
+  const Span out[9] = {{g->dh, bytes},   {g->dy, bytes},   {g->dgate, bytes},
+                       {g->dscale, col}, {g->dpost_g, pg}, {g->dpost_b, pg},
+                       {g->dnorm_g, ng}, {g->dnorm_b, ng},
                        {workspace, flash_gau_residual_norm_backward_workspace_bytes(M, d)}};
   const Span in[10] = {{dr, bytes},      {dn, bytes},     {r, bytes},      {y, bytes},
                        {o->gate, bytes}, {o->scale, col}, {o->post_g, pg}, {o->post_b, pg},
                        {o->norm_g, ng},  {o->norm_b, ng}};
-  if (!separate(out, in, true)) return FLASH_GAU_EINVAL;
-  // the parameters' gradients come from a second kernel: none of them may be
-  // an input that the first one still reads, and the first one's outputs
-  // only rows of the same kind
-  const Span sums[5] = {out[3], out[4], out[5], out[6], out[7]};
-  if (!separate(sums, in, false)) return FLASH_GAU_EINVAL;
+  // the rows of the gradients may take their inputs' place; parameters are
+  // read for every row, and their gradients and the workspace written while
+  // other rows are still read
+  const Span sums[6] = {out[3], out[4], out[5], out[6], out[7], out[8]};
+  const Span params[5] = {in[5], in[6], in[7], in[8], in[9]};
+  if (!separate(out, in, true) || !separate(out, params, false) || !separate(sums, in, false))
+    return FLASH_GAU_EINVAL;
   ResidualProblem q = residual_problem(o, y, M, d, dtype, stream);
   if ((st = current_sms(&q.num_sms)) != FLASH_GAU_OK) return st;
   return status_of(residual_norm_grad(q, dr, dn, r, *g, workspace));

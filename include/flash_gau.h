@@ -373,7 +373,7 @@ int flash_gau_rope_toeplitz_bias(const float *a, const float *b, int m, int C,
  * are zero, it adds nothing to dW, the mean is over the others (of none: 0),
  * and what its row of X holds, NaN included, has no effect (nor does it take
  * time).  The other tokens are taken in pieces of at most 2 GiB of
- * [tokens, V] in the workspace.  The products run on the tensor cores with
+ * [tokens, V] in the workspace (or 256 tokens).  The products run on the tensor cores with
  * fp32 accumulation and sums; bf16: the exponentials enter the gradients'
  * products rounded to bf16; fp32: operands enter as three bf16 terms and a
  * product as six of theirs, so that what is left out is below 2^-24 of it.  */
@@ -397,9 +397,9 @@ size_t flash_gau_xent_workspace_bytes(long long N, int d, int V, int dtype, int 
 /* X, W: device, io type, 16-byte aligned (as dX and dW); labels:
  * device int32 [N]; reduction: FLASH_GAU_MEAN or _SUM; out: host pointer,
  * read during the call.  Outputs must not overlap the inputs, the workspace
- * or one another.  workspace: device, 256-byte aligned; its first word is
- * the status word of flash_gau_workspace_status.  Results repeat bit for
- * bit.  Returns FLASH_GAU_OK, FLASH_GAU_EINVAL, FLASH_GAU_ENOTSUP,
+ * or one another.  workspace: device, 256-byte aligned, of this call alone
+ * until it has run; its first word is the status word of
+ * flash_gau_workspace_status.  Results repeat bit for bit.  Returns FLASH_GAU_OK, FLASH_GAU_EINVAL, FLASH_GAU_ENOTSUP,
  * FLASH_GAU_EWORKSPACE, FLASH_GAU_EDEVICE or FLASH_GAU_ECUDA.               */
 int flash_gau_xent(const void *X, const void *W, const int *labels, long long N, int d, int V,
                    int dtype, int reduction, float scale, const flash_gau_xent_out *out,
@@ -412,9 +412,9 @@ int flash_gau_xent(const void *X, const void *W, const int *labels, long long N,
  * h is the stream before the block and y the block's output; post and norm
  * are FLASH_GAU_NORM_* of the flash_block wrapper, with the same formulas.
  * n is taken from r before its rounding to the io type.  Row statistics are
- * fp32.  All rows have d columns; any 1 <= d <= 8192 and
- * 1 <= M <= 2^32 (more: FLASH_GAU_ENOTSUP), rows and arrays need only their element's alignment
- * (16-byte aligned arrays and d a multiple of 16 bytes run fastest).       */
+ * fp32.  Any 1 <= d <= 8192 and 1 <= M <= 2^32 (more:
+ * FLASH_GAU_ENOTSUP); rows and arrays need only their element's alignment
+ * (16-byte aligned arrays and rows of a multiple of 16 bytes run fastest).  */
 typedef struct flash_gau_residual {
   int post;             /* norm of the block's output, FLASH_GAU_NORM_*      */
   int norm;             /* norm of the stream, FLASH_GAU_NORM_*              */
@@ -430,8 +430,8 @@ typedef struct flash_gau_residual {
 /* h, y: device [M, d], io type; y may be NULL (then r = h; post, gate and
  * scale must be unset).  r, n: device [M, d], io type; r may be NULL (the
  * stream is not wanted); n is NULL exactly when o->norm is NONE.  An output
- * may be the same array as an input of its type, otherwise arrays must not
- * overlap.  One kernel, no workspace.  Returns FLASH_GAU_OK,
+ * may be h's, y's or the gate's array, otherwise arrays must not overlap.
+ * One kernel, no workspace.  Returns FLASH_GAU_OK,
  * FLASH_GAU_EINVAL, FLASH_GAU_ENOTSUP, FLASH_GAU_EDEVICE or
  * FLASH_GAU_ECUDA.                                                         */
 int flash_gau_residual_norm(const void *h, const void *y, const flash_gau_residual *o,
@@ -459,8 +459,8 @@ size_t flash_gau_residual_norm_backward_workspace_bytes(long long M, int d);
  * NONE); r: the forward's r (needed with a norm); y: the forward's y (needed
  * with post, gate or scale).  g (a host pointer): a gradient of something
  * that the options leave out must be NULL.  dh, dy and dgate may each be
- * the same array as an input, otherwise arrays must not overlap.
- * workspace: device, 256-byte aligned.                                     */
+ * the array of dr, dn, r, y or the gate, otherwise arrays must not overlap.
+ * workspace: device, 256-byte aligned, of this call alone until it has run. */
 int flash_gau_residual_norm_backward(const void *dr, const void *dn, const void *r,
                                      const void *y, const flash_gau_residual *o,
                                      long long M, int d, int dtype,

@@ -204,6 +204,30 @@ def test_residual_norm_backward_refuses(L, opts, args, code):
         ctypes.byref(g), a["ws"], a["wsb"], None) == code
 
 
+def test_residual_norm_arrays_that_only_look_like_rows(L):
+    """One fp32 row is as long as a parameter, and a row array may be as long
+    as the workspace: neither may stand in for the other."""
+    o = _residual(norm_g=A, scale=B)
+    for r, n in ((A, D), (C, A), (B, D), (C, B)):
+        assert L.flash_gau_residual_norm(E_, F_, ctypes.byref(o), 1, 64, bd.FP32, r, n,
+                                         None) == bd.EINVAL
+    W = 1 << 40
+
+    def back(M, d, ws, **kw):
+        a = dict(dh=E_, dy=7 << 32)
+        a.update(kw)
+        g = bd.ResidualGrads(*(a.get(k) for k, _ in bd.ResidualGrads._fields_))
+        return L.flash_gau_residual_norm_backward(W, C, D, 8 << 32, ctypes.byref(o), M, d, bd.FP32,
+                                                  ctypes.byref(g), ws, 1 << 30, None)
+
+    assert back(1, 64, 1 << 41, dh=A) == bd.EINVAL
+    assert back(1, 64, 1 << 41, dy=B) == bd.EINVAL
+    f = L.flash_gau_residual_norm_backward_workspace_bytes
+    M, d = next((M, d) for M in range(1, 40000) for d in (64, 128, 256, 512, 1024)
+                if f(M, d) == M * d * 4)
+    assert back(M, d, W) == bd.EINVAL                           # the workspace is dr
+
+
 def test_residual_norm_backward_workspace(L):
     f = L.flash_gau_residual_norm_backward_workspace_bytes
     assert f(0, 64) == 0 and f(4, 0) == 0 and f(4, 8193) == 0
