@@ -286,9 +286,10 @@ int flash_gau_xent(const void *X, const void *W, const int *labels, long long N,
 int flash_gau_adamw_step(const flash_gau_adamw_tensor *tensors, int n_tensors,
                          const flash_gau_adamw_hyper *h, void *stream) {
   if (!h || n_tensors < 0 || (n_tensors && !tensors)) return FLASH_GAU_EINVAL;
-  if (!isfinite(h->lr) || h->lr < 0.0 || !(h->beta1 >= 0.0 && h->beta1 < 1.0) ||
-      !(h->beta2 >= 0.0 && h->beta2 < 1.0) || !(h->eps > 0.0) || !isfinite(h->eps) ||
-      h->step < 1 || (h->state_bits != 8 && h->state_bits != 32) || !aligned(h->grad_scale, 4))
+  // the step's size and eps are fp32 on the device, and a subnormal eps zero
+  if (!(h->lr >= 0.0) || !(h->beta1 >= 0.0 && h->beta1 < 1.0) ||
+      !(h->lr / (1.0 - h->beta1) <= FLT_MAX) || !(h->beta2 >= 0.0 && h->beta2 < 1.0) ||
+      !(h->eps >= FLT_MIN && h->eps <= FLT_MAX) || h->step < 1 || (h->state_bits != 8 && h->state_bits != 32) || !aligned(h->grad_scale, 4))
     return FLASH_GAU_EINVAL;
   for (int k = 0; k < n_tensors; ++k)
     if (check_tensor(tensors[k], h->state_bits, true) != FLASH_GAU_OK) return FLASH_GAU_EINVAL;
@@ -314,8 +315,14 @@ int flash_gau_adamw_moments(const flash_gau_adamw_tensor *tensors, int n_tensors
   if (n_tensors < 0 || (n_tensors && (!tensors || !m_out || !v_out))) return FLASH_GAU_EINVAL;
   for (int k = 0; k < n_tensors; ++k) {
     if (check_tensor(tensors[k], 8, false) != FLASH_GAU_OK) return FLASH_GAU_EINVAL;
-    if (tensors[k].n && (!m_out[k] || !v_out[k] || !aligned(m_out[k], 4) || !aligned(v_out[k], 4)))
+    const flash_gau_adamw_tensor &t = tensors[k];
+    if (!t.n) continue;
+    if (!m_out[k] || !v_out[k] || !aligned(m_out[k], 4) || !aligned(v_out[k], 4))
       return FLASH_GAU_EINVAL;
+    const size_t n = (size_t)t.n, ns = (n + 255) / 256 * 4;
+    const Span out[2] = {{m_out[k], n * 4}, {v_out[k], n * 4}};
+    const Span in[4] = {{t.m, n}, {t.v, n}, {t.m_scale, ns}, {t.v_scale, ns}};
+    if (!separate(out, in, false)) return FLASH_GAU_EINVAL;
   }
   AdamwProblem q = {};
   int num_sms = 0;

@@ -494,9 +494,9 @@ typedef struct flash_gau_adamw_tensor {
 } flash_gau_adamw_tensor;
 
 typedef struct flash_gau_adamw_hyper {
-  double lr;            /* >= 0                                              */
+  double lr;            /* >= 0; lr / (1 - beta1) finite in fp32             */
   double beta1, beta2;  /* in [0, 1)                                         */
-  double eps;           /* > 0                                               */
+  double eps;           /* > 0, a normal number in fp32                      */
   long long step;       /* number of this step, from 1                       */
   int state_bits;       /* 32 or 8: how every tensor's moments are held      */
   const float *grad_scale;  /* device fp32 scalar, or NULL (one)             */
@@ -511,8 +511,8 @@ int flash_gau_adamw_step(const flash_gau_adamw_tensor *tensors, int n_tensors,
                          const flash_gau_adamw_hyper *h, void *stream);
 
 /* The values of 8-bit moments (m, v and the scales of each tensor are read)
- * as fp32: m_out[k], v_out[k] device [n] of tensor k; the two lists are host
- * arrays, read during the call.                                            */
+ * as fp32: m_out[k], v_out[k] device [n] of tensor k, apart from everything
+ * else; the two lists are host arrays, read during the call.               */
 int flash_gau_adamw_moments(const flash_gau_adamw_tensor *tensors, int n_tensors,
                             float *const *m_out, float *const *v_out, void *stream);
 

@@ -266,6 +266,22 @@ def test_adamw_refuses(L, tensor, hyper):
     assert L.flash_gau_adamw_step(None, -1, ctypes.byref(_hyper()), None) == bd.EINVAL
 
 
+@pytest.mark.parametrize("hyper", [dict(eps=1e-39), dict(eps=1e39), dict(lr=1e39),
+                                   dict(lr=1e38, beta1=0.999), dict(lr=float("nan"))])
+def test_adamw_refuses_what_fp32_cannot_hold(L, hyper):
+    assert L.flash_gau_adamw_step(ctypes.byref(_tensor()), 1, ctypes.byref(_hyper(**hyper)),
+                                  None) == bd.EINVAL
+
+
+def test_adamw_moments_refuses_overlaps(L):
+    P = ctypes.c_void_p
+    t = _tensor(m_scale=E_, v_scale=F_)
+    far = 7 << 32
+    for m, v in ((far, far + 400), (C, far), (far, D + 500), (far, E_), (F_ + 8, far)):
+        assert L.flash_gau_adamw_moments(ctypes.byref(t), 1, (P * 1)(m), (P * 1)(v),
+                                         None) == bd.EINVAL
+
+
 def test_adamw_moments_refuses(L):
     P = ctypes.c_void_p
     t = _tensor(m_scale=E_, v_scale=F_)
