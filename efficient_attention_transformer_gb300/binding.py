@@ -578,6 +578,8 @@ def _elsewhere(device, stream):
 def _scope(device, stream):
     """Context of one call on `device`: the device is current, and where a
     stream is given it is too, so that what the call allocates belongs to it."""
+    if stream is not None and stream.device != device:
+        raise ValueError("the stream must be one of %s" % device)
     return torch.cuda.stream(stream) if stream is not None else torch.cuda.device(device)
 
 
@@ -776,7 +778,9 @@ class AdamW:
     weight_decay: one value, or one for each tensor.  state_bits: 32 (fp32
     moments) or 8 (codes with a scale for each 256 elements).  m, v, m_scale,
     v_scale: lists of existing moments (a checkpoint's) in place of zeros;
-    they are updated in place."""
+    they are updated in place.  All of them are held by their memory: it is
+    not to be replaced (an assignment to .data; step refuses it for the
+    parameters)."""
 
     def __init__(self, params, copies=None, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.0,
                  state_bits=32, m=None, v=None, m_scale=None, v_scale=None):
@@ -805,6 +809,7 @@ class AdamW:
             raise ValueError("every list must have one entry for each parameter")
         self.device = self.params[0].device if k else None
         self._shapes = [p.shape for p in self.params]
+        self._params_at = [p.data_ptr() for p in self.params]
         self._array = (AdamWTensor * max(k, 1))()
         columns = np.frombuffer(self._array, dtype=np.dtype(AdamWTensor))
         n = [p.numel() for p in self.params]
@@ -843,7 +848,9 @@ class AdamW:
     def step(self, grads, lr, step=None, grad_scale=None, stream=None):
         """One update with `grads`, a list of fp32 or bf16 tensors like the
         parameters.  step: its number from 1 (None: one more than the last
-        one's).  grad_scale: a device fp32 scalar on the gradients, or None."""
+        one's).  grad_scale: a device fp32 scalar on the gradients, or None.
+        A captured step replays with the lr and the number it was captured
+        with, and with grad_scale's value at the time."""
         if len(grads) != len(self.params):
             raise ValueError("one gradient is needed for each parameter")
         if not grads:
@@ -853,6 +860,8 @@ class AdamW:
                 return self.step(grads, lr, step, grad_scale)
         h, dev = self.hyper, self.device
         at = dev.index
+        if [p.data_ptr() for p in self.params] != self._params_at:
+            raise ValueError("the parameters' memory is not that of the optimizer's start")
         for p, g in zip(self._shapes, grads):
             if g.shape != p or g.get_device() != at:
                 raise ValueError("each gradient must be like its parameter")
@@ -870,22 +879,23 @@ class AdamW:
         parameters: the tensors themselves with 32-bit moments (unless out
         lists are given), decoded through flash_gau_adamw_moments with 8-bit
         ones."""
-        if self.state_bits == 32:
-            for src, out in ((self.m, out_m), (self.v, out_v)):
-                for a, b in zip(src, out or []):
-                    b.copy_(a)
-            return out_m or self.m, out_v or self.v
         if not self.params:
             return [], []
         if _elsewhere(self.device, stream):
             with _scope(self.device, stream):
                 return self.moments(out_m, out_v)
         k, dev, ptrs = len(self.params), self.device, []
+        for name, out in (("out_m", out_m), ("out_v", out_v)):
+            if out is not None and len(out) != k:
+                raise ValueError("%s must hold a tensor like each parameter" % name)
+        if self.state_bits == 32:
+            for src, out in ((self.m, out_m), (self.v, out_v)):
+                for a, b in zip(src, out or []):
+                    b.copy_(a)
+            return out_m or self.m, out_v or self.v
         out_m = out_m or [torch.empty_like(p) for p in self.params]
         out_v = out_v or [torch.empty_like(p) for p in self.params]
         for name, out in (("out_m", out_m), ("out_v", out_v)):
-            if len(out) != k:
-                raise ValueError("%s must hold a tensor like each parameter" % name)
             ptrs.append((ctypes.c_void_p * k)(*[_like(o, name, p, torch.float32, dev.index)
                                                 for o, p in zip(out, self._shapes)]))
         _check(lib().flash_gau_adamw_moments(self._array, k, *ptrs, _stream(dev)))

@@ -198,6 +198,34 @@ def test_captured_and_other_stream(bits):
         assert torch.equal(x, y)
 
 
+@pytest.mark.parametrize("bits", [8, 32])
+def test_moments_to_lists_on_a_stream(bits):
+    params, grads = make([300, 5], torch.float32, 33)
+    opt = bd.AdamW(params, state_bits=bits, **HYPER)
+    opt.step(grads[0], lr=LR)
+    want = [[t.clone() for t in x] for x in opt.moments()]
+    m, v = ([torch.full_like(p, 7.0) for p in params] for _ in range(2))
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    got = opt.moments(m, v, stream=s)
+    s.synchronize()
+    assert got[0] is m and got[1] is v
+    for a, b in zip(want[0] + want[1], m + v):
+        assert torch.equal(a, b)
+    for lists in ((m[:1], v), (m, v + v)):
+        with pytest.raises(ValueError):
+            opt.moments(*lists)
+
+
+def test_replaced_memory_is_refused():
+    held = torch.zeros(600, device="cuda")
+    opt = bd.AdamW([held])
+    held.data = torch.ones(600, device="cuda")
+    with pytest.raises(ValueError):
+        opt.step([torch.zeros(600, device="cuda")], lr=LR)
+    assert opt.steps == 0 and bool((held == 1).all())
+
+
 def test_large_stack():
     """The parameters of several layers at the long workload's widths."""
     sizes = [768 * 3200, 1536 * 768, 512, 512, 511] * 3
