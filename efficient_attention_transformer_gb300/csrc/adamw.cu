@@ -22,7 +22,9 @@
 // goes into the kernel's parameters, so that a step is one launch (per 384
 // tensors), needs no workspace and can be captured; a warp takes 256 elements
 // of one tensor at a time as two runs of 128, four consecutive elements a lane
-// (16-byte accesses).
+// (16-byte accesses).  fp32 moments run at the copy rate (43.8 M parameters:
+// 188 us, 6.7 TB/s); 8-bit ones at 5.2 TB/s (82 M: 261 us), issue slots half
+// full of coding; their values at 5.8 TB/s (133 us).
 #include <cuda_bf16.h>
 #include <math.h>
 

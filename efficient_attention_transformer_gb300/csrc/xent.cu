@@ -44,6 +44,11 @@
 //
 // A few tokens without gradients (xent_few_kernel) only read W: dot products
 // on the CUDA cores, one launch.
+//
+// Measured (bf16, V 50257, loss and both gradients): 8192 tokens of d 768
+// 1.23 ms, the products 360, 335 and 335 us (1.76 to 1.89 PFLOP/s) and 47 us
+// around them; 16384 tokens of d 1024, a tenth without label, 2.84 ms, 828,
+// 780 and 822 us (1.83 to 1.95).  The tensor pipe bounds them.
 #include <cuda_bf16.h>
 
 #include <atomic>
@@ -733,7 +738,9 @@ __device__ __forceinline__ void zero_tail(__nv_bfloat16 *Xc, long long rows, lon
 // logit; zeros in the outputs of the other rows.  A block finds where its
 // rows go by counting the labels before them, so the order is the tokens'.
 // The last block leaves the number of rows, the gradients' factor, and a
-// tile's worth of rows without a label behind the last one.
+// tile's worth of rows without a label behind the last one.  Latency bounds
+// it: labels, a row and its word's row one after another (4096 x 768 bf16:
+// 9 us; 16384 x 1024: 21).
 template <typename T>
 __global__ void __launch_bounds__(256) xent_gather_kernel(const GatherArgs<T> a) {
   __shared__ int counts[8];
@@ -860,6 +867,8 @@ __device__ __forceinline__ float row_loss(float top, float sum, float t2, float 
 // a warp a row writes the loss, and with gradients the row's factor, the
 // label's E, the scaled row of X, and where a part took another reference
 // than the row's its E again.  The last block of all adds the losses up.
+// (V 50257: 18 us at 4096 x 768 bf16, 37 at 16384 x 1024; 393 parts a row, read
+// with 32 threads and eight loads in flight each.)
 template <typename T>
 __global__ void __launch_bounds__(256) xent_rows_kernel(const RowArgs a) {
   __shared__ float2 joined[8][33];
@@ -993,7 +1002,7 @@ __device__ __forceinline__ void store_as(float *p, float v) { *p = v; }
 __device__ __forceinline__ void store_as(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
 
 // dX from the parts of its sum, in the groups' order, times the row's factor,
-// to where the row came from; four columns a thread.
+// to where the row came from; four columns a thread (16384 x 1024 bf16: 31 us).
 template <typename T>
 __global__ void __launch_bounds__(256)
 xent_join_kernel(const XentLayout L, long long first, int rows, int d, int V, int products,
@@ -1059,7 +1068,9 @@ xent_finish_kernel(const float *__restrict__ in, int ld, int V, int d, T *__rest
 // W is read once and nothing else counts (50257 x 768 bf16: 77 MB).  A warp
 // takes four words at a time, 16 bytes of each a lane, against the tokens' x
 // in shared memory, and keeps each token's running maximum and sum; blocks
-// leave theirs for the last one to join.
+// leave theirs for the last one to join.  One token of that size takes 24 us
+// (3.3 TB/s; 11 us at the copy rate): four blocks an SM have their loads in
+// flight, and the start, the last loads and the join are not overlapped.
 constexpr int kFewTokens = 8;
 
 struct FewArgs {
