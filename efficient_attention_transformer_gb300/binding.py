@@ -600,25 +600,29 @@ def _like(t, name, shape, dtype, index):
 
 
 def _param(t, name, n, index):
-    """Pointer of n fp32 values on device `index`, or None."""
-    if t is None:
-        return None
-    if t.numel() != n or t.get_device() != index:
-        raise ValueError("%s must hold %d values on device %d" % (name, n, index))
-    return _dev_ptr(t, name, torch.float32)
+    """Pointer of n fp32 values on device `index`."""
+    if t.numel() != n or t.get_device() != index or t.dtype != torch.float32:
+        raise ValueError("%s must hold %d fp32 values on device %d" % (name, n, index))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    return t.data_ptr()
 
 
 def _residual(shape, dtype, index, post_norm, post_g, post_b, gate, scale, norm, norm_g, norm_b,
               eps):
     d = shape[-1]
-    return Residual(
-        post_norm, norm,
-        None if post_g is None else _param(post_g, "post_g", d if post_norm == NORM_LAYER else 1, index),
-        None if post_b is None else _param(post_b, "post_b", d, index),
-        None if norm_g is None else _param(norm_g, "norm_g", d if norm == NORM_LAYER else 1, index),
-        None if norm_b is None else _param(norm_b, "norm_b", d, index),
-        None if scale is None else _param(scale, "scale", d, index),
-        None if gate is None else _like(gate, "gate", shape, dtype, index), eps)
+    if post_g is not None:
+        post_g = _param(post_g, "post_g", d if post_norm == NORM_LAYER else 1, index)
+    if post_b is not None:
+        post_b = _param(post_b, "post_b", d, index)
+    if norm_g is not None:
+        norm_g = _param(norm_g, "norm_g", d if norm == NORM_LAYER else 1, index)
+    if norm_b is not None:
+        norm_b = _param(norm_b, "norm_b", d, index)
+    if scale is not None:
+        scale = _param(scale, "scale", d, index)
+    return Residual(post_norm, norm, post_g, post_b, norm_g, norm_b, scale,
+                    _like(gate, "gate", shape, dtype, index), eps)
 
 
 def residual_norm(h, y=None, post_norm=NORM_NONE, post_g=None, post_b=None, gate=None, scale=None,
@@ -689,20 +693,21 @@ def residual_norm_backward(dr, dn, r, y, post_norm=NORM_NONE, post_g=None, post_
     if not given.keys() <= set(_GRADS):
         raise ValueError("out holds %s only" % ", ".join(_GRADS))
     # each is like a tensor of the forward, which is None where it has no gradient
+    post_layer, norm_layer = post_norm == NORM_LAYER, norm == NORM_LAYER
     for name, src in zip(_GRADS, (like, y, gate, scale, post_g if post_norm else None,
-                                  post_g if post_norm == NORM_LAYER else None,
-                                  norm_g if norm else None,
-                                  norm_g if norm == NORM_LAYER else None)):
-        t = given.get(name)
-        if t is not None:
-            if src is None:
+                                  post_g if post_layer else None, norm_g if norm else None,
+                                  norm_g if norm_layer else None)):
+        t = given.get(name) if given else None
+        if src is None:
+            if t is not None:
                 raise ValueError("%s is the gradient of nothing here" % name)
-            ptrs.append(_like(t, name, src.shape, src.dtype, at))
-        elif src is not None:
+            p = None
+        elif t is None:
             t = torch.empty_like(src)
-            ptrs.append(t.data_ptr())
+            p = t.data_ptr()
         else:
-            ptrs.append(None)
+            p = _like(t, name, src.shape, src.dtype, at)
+        ptrs.append(p)
         out[name] = t
     if workspace is None:
         workspace = torch.empty(nw, dtype=torch.uint8, device=dev)
@@ -730,33 +735,31 @@ def xent(X, W, labels, reduction=MEAN, scale=1.0, grad=True, out=None, workspace
     labels: int32, X's leading shape; a label outside [0, V) leaves its token
     out.  total is scale times the MEAN over the labelled tokens or the SUM.
     `out`: tensors to write to, by the same names."""
-    dt = dtype_code(X.dtype)
-    xp, wp = _dev_ptr(X, "X"), _dev_ptr(W, "W", X.dtype)
-    lp = _dev_ptr(labels, "labels", torch.int32)
-    if W.dim() != 2 or X.shape[-1:] != W.shape[1:] or labels.shape != X.shape[:-1]:
+    io, dev = X.dtype, X.device
+    dt, xp, at = dtype_code(io), _dev_ptr(X, "X"), dev.index
+    lead = labels.shape
+    if W.dim() != 2 or X.shape != lead + W.shape[1:]:
         raise ValueError("X must be [..., d], W [V, d] and labels X's leading shape")
     V, d = W.shape
-    N, dev = labels.numel(), X.device
-    if W.device != dev or labels.device != dev:
-        raise ValueError("X, W and labels must be on one device")
+    wp = _like(W, "W", (V, d), io, at)
+    lp = _like(labels, "labels", lead, torch.int32, at)
     if _elsewhere(dev, stream):
         with _scope(dev, stream):
             return xent(X, W, labels, reduction, scale, grad, out, workspace)
     f32 = torch.float32
-    out, ptrs = dict(out or ()), []
+    out, ptrs = dict(out) if out else {}, []
     for name, like, dtype in (("total", None, f32), ("loss", labels, f32), ("lse", labels, f32),
-                              ("dX", X, X.dtype), ("dW", W, X.dtype)):
-        t, shape = out.get(name), () if like is None else like.shape
-        if name[0] == "d" and not grad:
-            t = out[name] = None
-            ptrs.append(None)
-        elif t is None:
-            t = out[name] = torch.empty(shape, dtype=dtype, device=dev)
-            ptrs.append(t.data_ptr())
-        elif t.shape != shape or t.device != dev:
-            raise ValueError("%s must be %s on %s" % (name, tuple(shape), dev))
-        else:
-            ptrs.append(_dev_ptr(t, name, dtype))
+                              ("dX", X, io), ("dW", W, io))[:5 if grad else 3]:
+        t = out.get(name)
+        if t is not None:
+            ptrs.append(_like(t, name, () if like is None else like.shape, dtype, at))
+            continue
+        t = out[name] = (torch.empty((), dtype=f32, device=dev) if like is None else
+                         torch.empty_like(like, dtype=dtype))
+        ptrs.append(t.data_ptr())
+    if not grad:
+        out["dX"] = out["dW"] = None
+    N = labels.numel()
     if workspace is None:
         nw = xent_workspace_bytes(N, d, V, dt, grad)
         workspace = torch.empty(nw, dtype=torch.uint8, device=dev)
@@ -860,17 +863,16 @@ class AdamW:
                 return self.step(grads, lr, step, grad_scale)
         h, dev = self.hyper, self.device
         at = dev.index
-        if [p.data_ptr() for p in self.params] != self._params_at:
+        if list(map(torch.Tensor.data_ptr, self.params)) != self._params_at:
             raise ValueError("the parameters' memory is not that of the optimizer's start")
-        for p, g in zip(self._shapes, grads):
-            if g.shape != p or g.get_device() != at:
-                raise ValueError("each gradient must be like its parameter")
-            if not g.is_contiguous():
-                raise ValueError("gradients must be contiguous")
+        if [g.shape for g in grads] != self._shapes or any(g.get_device() != at for g in grads):
+            raise ValueError("each gradient must be like its parameter")
+        if not all(map(torch.Tensor.is_contiguous, grads)):
+            raise ValueError("gradients must be contiguous")
         dtypes = [dtype_code(g.dtype) for g in grads]
-        self._g[:], self._g_dtype[:] = [g.data_ptr() for g in grads], dtypes
+        self._g[:], self._g_dtype[:] = list(map(torch.Tensor.data_ptr, grads)), dtypes
         h.lr, h.step = lr, self.steps + 1 if step is None else step
-        h.grad_scale = _param(grad_scale, "grad_scale", 1, dev.index)
+        h.grad_scale = None if grad_scale is None else _param(grad_scale, "grad_scale", 1, at)
         _check(lib().flash_gau_adamw_step(self._array, len(grads), h, _stream(dev)))
         self.steps = h.step
 

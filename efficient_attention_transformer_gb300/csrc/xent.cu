@@ -43,7 +43,7 @@
 // bf16 rate are four times the fp32 units' (1931 / 6 against 80 TFLOP/s).
 //
 // A few tokens without gradients (xent_few_kernel) only read W: dot products
-// on the CUDA cores, one launch.
+// on the CUDA cores.
 //
 // Measured (bf16, V 50257, loss and both gradients): 8192 tokens of d 768
 // 1.23 ms, the products 360, 335 and 335 us (1.76 to 1.89 PFLOP/s) and 47 us
@@ -54,6 +54,7 @@
 #include <atomic>
 
 #include "flash_gau_internal.h"
+#include "packed_f32.cuh"
 #include "sm103_ptx.cuh"
 #include "tma_host.h"
 
@@ -696,14 +697,6 @@ __device__ __forceinline__ void split_row(const float *x, int d, float f, __nv_b
   }
 }
 
-__global__ void __launch_bounds__(256)
-xent_split_kernel(const float *__restrict__ W, int V, int d, __nv_bfloat16 *__restrict__ out, int term) {
-  griddep_wait();
-  const int row = blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (row < V)
-    split_row(W + (size_t)row * d, d, 1.f, out + (size_t)row * kTerms * term, term, threadIdx.x & 31);
-}
-
 template <typename T>
 struct GatherArgs {
   const T *X, *W;
@@ -714,7 +707,8 @@ struct GatherArgs {
   XentLayout L;
   float *loss, *lse;
   T *dX;
-  int copy;  // there is one piece: its rows are copied here
+  int copy;    // there is one piece: its rows are copied here
+  int blocks;  // of the rows; fp32: the others take W's terms
 };
 
 // A row of X as the products read it; one warp.
@@ -737,8 +731,10 @@ __device__ __forceinline__ void zero_tail(__nv_bfloat16 *Xc, long long rows, lon
 // with their labels, where they came from and their reference, the label's
 // logit; zeros in the outputs of the other rows.  A block finds where its
 // rows go by counting the labels before them, so the order is the tokens'.
-// The last block leaves the number of rows, the gradients' factor, and a
-// tile's worth of rows without a label behind the last one.  Latency bounds
+// The last block leaves the number of rows, the gradients' factor, a cleared
+// status word and a tile's worth of rows without a label behind the last one.
+// With fp32 io the blocks behind these write W as three terms, a warp a row
+// (in a launch of its own that took 9 us at 8003 x 520).  Latency bounds
 // it: labels, a row and its word's row one after another (4096 x 768 bf16:
 // 9 us; 16384 x 1024: 21).
 template <typename T>
@@ -746,6 +742,15 @@ __global__ void __launch_bounds__(256) xent_gather_kernel(const GatherArgs<T> a)
   __shared__ int counts[8];
   griddep_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, d = a.d;
+  if constexpr (sizeof(T) == 4) {
+    if (blockIdx.x >= (unsigned)a.blocks) {
+      const int v = (int)(blockIdx.x - a.blocks) * 8 + warp;
+      if (v < a.V)
+        split_row(a.W + (size_t)v * d, d, 1.f,
+                  static_cast<__nv_bfloat16 *>(a.L.Ws) + (size_t)v * kTerms * a.L.term, a.L.term, lane);
+      return;
+    }
+  }
   const long long row0 = (long long)blockIdx.x * a.block_rows;
   const long long end = min(row0 + a.block_rows, a.N);
   int n = 0;
@@ -800,12 +805,13 @@ __global__ void __launch_bounds__(256) xent_gather_kernel(const GatherArgs<T> a)
         for (int k = lane; k < d; k += 32) a.dX[row * d + k] = T(0.f);
     }
   }
-  if (blockIdx.x != gridDim.x - 1) return;
+  if (blockIdx.x != (unsigned)a.blocks - 1) return;
   // base is the number of labels now
   const long long tile = (base + 2 * BM - 1) / (2 * BM) * (2 * BM);
   for (long long c = base + threadIdx.x; c < tile; c += 256) a.L.labels[c] = -1;
   if (a.copy) zero_tail(static_cast<__nv_bfloat16 *>(a.L.Xc), base, width);
   if (threadIdx.x == 0) {
+    *a.L.status = FLASH_GAU_OK;
     *a.L.live = (int)base;
     *a.L.done = 0;
     *a.L.factor = a.mean ? a.scale / (float)(base > 0 ? base : 1) : a.scale;
@@ -1065,13 +1071,16 @@ xent_finish_kernel(const float *__restrict__ in, int ld, int V, int d, T *__rest
 }
 
 // ---- a few tokens, no gradients -------------------------------------------
-// W is read once and nothing else counts (50257 x 768 bf16: 77 MB).  A warp
-// takes four words at a time, 16 bytes of each a lane, against the tokens' x
-// in shared memory, and keeps each token's running maximum and sum; blocks
-// leave theirs for the last one to join.  One token of that size takes 24 us
-// (3.3 TB/s; 11 us at the copy rate): four blocks an SM have their loads in
-// flight, and the start, the last loads and the join are not overlapped.
-constexpr int kFewTokens = 8;
+// W is read once and nothing else counts (50257 x 768 bf16: 77 MB, 11.4 us at
+// the copy rate).  A warp takes four words at a time, 16 bytes of each a lane,
+// against the tokens' x in shared memory; the 4 NT sums over the warp leave
+// each lane one token and word of its own, whose running maximum and sum it
+// keeps, and xent_few_join_kernel joins the blocks'.  Back to back in a graph,
+// W from memory: one token 17 us, two 19, four 23; fp32 29, 30 and 31, eight
+// 40.  By the tensor cores: bf16 29 to 31 whatever the tokens, fp32 160 (W has
+// to be split there), and 12 for 5 at 3000 x 256.  So bf16 takes this way up to four
+// tokens (eight: 36 us), fp32 up to eight.
+constexpr int kFewTokens = 8, kFewTokensBf16 = 4;
 
 struct FewArgs {
   const void *X, *W;
@@ -1080,7 +1089,8 @@ struct FewArgs {
   float scale;
   float2 *part;    // [kFewTokens][blocks]
   float *target;   // [kFewTokens] the label's logit in units of ln 2
-  int *done;       // zero before the launch
+  int blocks;
+  int *status;
   float *loss, *lse, *total;
 };
 
@@ -1094,95 +1104,117 @@ __device__ __forceinline__ void add_logit(float &top, float &sum, float l) {
   }
 }
 
+// R values of every lane summed over the warp, halving what a lane holds with
+// each exchange: lane i is left with the sum of value i / (32 / R).
+template <int R>
+__device__ __forceinline__ float warp_sums(float (&v)[R], int lane) {
+  int o = 16;
+#pragma unroll
+  for (int half = R / 2; half > 0; half /= 2, o /= 2) {
+    const bool upper = lane & o;
+#pragma unroll
+    for (int i = 0; i < half; ++i) {
+      const float keep = upper ? v[i + half] : v[i], give = upper ? v[i] : v[i + half];
+      v[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+    }
+  }
+#pragma unroll
+  for (int k = 16 / R; k > 0; k /= 2) v[0] += __shfl_xor_sync(0xffffffffu, v[0], k);
+  return v[0];
+}
+
+// (blocks an SM and the unrolling by time: 50257 x 768 bf16, two tokens: 19 us
+// for 23 without the bound, four: 23 for 29 with a tighter one; fp32, eight:
+// 40 for 64)
 template <typename T, int NT>
-__global__ void __launch_bounds__(256) xent_few_kernel(const FewArgs a) {
+__global__ void __launch_bounds__(256, NT <= 2 ? 4 : 2) xent_few_kernel(const FewArgs a) {
   extern __shared__ __align__(16) float xs[];  // [NT][d]
   __shared__ float2 mine[8][NT];
-  __shared__ float losses[kFewTokens];
-  __shared__ int last;
   griddep_wait();
   constexpr int W16 = 16 / sizeof(T);  // values of 16 bytes
+  constexpr int kSame = 8 / NT;        // lanes that are left with the same sum
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, d = a.d;
   const T *X = static_cast<const T *>(a.X), *W = static_cast<const T *>(a.W);
   for (int i = threadIdx.x; i < NT * d; i += 256) xs[i] = i < a.N * d ? (float)X[i] : 0.f;
   __syncthreads();
-  float top[NT], sum[NT];
-  int label[NT];
-#pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    top[n] = -INFINITY;
-    sum[n] = 0.f;
-    label[n] = n < a.N ? a.labels[n] : -1;
-  }
+  // this lane's token and which of the four words, of what the sums leave it
+  const int n_own = lane / kSame / 4, j_own = lane / kSame % 4;
+  const int label = n_own < a.N ? a.labels[n_own] : -1;
+  float top = -INFINITY, sum = 0.f;
   for (int w0 = (blockIdx.x * 8 + warp) * 4; w0 < a.V; w0 += gridDim.x * 32) {
-    float acc[4][NT] = {};
-#pragma unroll 2
+    f2 acc[NT][4] = {};
+#pragma unroll (NT <= 4 ? 2 : 1)
     for (int k = W16 * lane; k < d; k += 32 * W16) {
-      uint4 v[4];
+      f2 w[4][W16 / 2];
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        v[j] = __ldcs(reinterpret_cast<const uint4 *>(W + (size_t)min(w0 + j, a.V - 1) * d + k));
+      for (int j = 0; j < 4; ++j) {
+        const uint4 v = __ldcs(reinterpret_cast<const uint4 *>(W + (size_t)min(w0 + j, a.V - 1) * d + k));
+        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        float x[W16];
-#pragma unroll
-        for (int q = 0; q < W16; q += 4)
-          *reinterpret_cast<float4 *>(x + q) = *reinterpret_cast<const float4 *>(xs + n * d + k + q);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t u[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            if constexpr (sizeof(T) == 2) {
-              acc[j][n] = fmaf(__uint_as_float(u[q] << 16), x[2 * q], acc[j][n]);
-              acc[j][n] = fmaf(__uint_as_float(u[q] & 0xffff0000u), x[2 * q + 1], acc[j][n]);
-            } else {
-              acc[j][n] = fmaf(__uint_as_float(u[q]), x[q], acc[j][n]);
-            }
-          }
+        for (int q = 0; q < W16 / 2; ++q) {
+          if constexpr (sizeof(T) == 2)
+            w[j][q] = pair(__uint_as_float(u[q] << 16), __uint_as_float(u[q] & 0xffff0000u));
+          else
+            w[j][q] = pair(__uint_as_float(u[2 * q]), __uint_as_float(u[2 * q + 1]));
         }
       }
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int q = 0; q < W16; q += 4) {
+          const ulonglong2 x = *reinterpret_cast<const ulonglong2 *>(xs + n * d + k + q);
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            acc[n][j] = fma2(w[j][q / 2 + 1], x.y, fma2(w[j][q / 2], x.x, acc[n][j]));
+        }
     }
+    float v[4 * NT];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if (w0 + j >= a.V) break;
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const float l = warp_sum(acc[j][n]) * kLog2e;
-        if (w0 + j == label[n]) {
-          if (lane == 0) a.target[n] = l;
-        } else {
-          add_logit(top[n], sum[n], l);
-        }
-      }
+    for (int r = 0; r < 4 * NT; ++r) {
+      const float2 t = split(acc[r / 4][r % 4]);
+      v[r] = t.x + t.y;
+    }
+    const float l = warp_sums(v, lane) * kLog2e;
+    const int word = w0 + j_own;
+    if (word == label) {
+      if (lane % kSame == 0) a.target[n_own] = l;
+    } else if (word < a.V) {
+      add_logit(top, sum, l);
     }
   }
-  if (lane == 0)
+  // the four words' lanes of a token
 #pragma unroll
-    for (int n = 0; n < NT; ++n) mine[warp][n] = make_float2(top[n], sum[n]);
+  for (int o = kSame; o <= 2 * kSame; o *= 2) {
+    const float t = __shfl_xor_sync(0xffffffffu, top, o), s = __shfl_xor_sync(0xffffffffu, sum, o);
+    join_parts(top, sum, t, s);
+  }
+  if (lane % (4 * kSame) == 0) mine[warp][n_own] = make_float2(top, sum);
   __syncthreads();
   if (threadIdx.x < NT) {
     float2 v = mine[0][threadIdx.x];
     for (int k = 1; k < 8; ++k) join_parts(v.x, v.y, mine[k][threadIdx.x].x, mine[k][threadIdx.x].y);
     a.part[(size_t)threadIdx.x * gridDim.x + blockIdx.x] = v;
   }
-  __threadfence();
-  __syncthreads();
-  if (threadIdx.x == 0) last = atomicAdd(a.done, 1) == gridDim.x - 1;
-  __syncthreads();
-  if (!last) return;
-  __threadfence();
-  // 256 / NT threads a token join its blocks' parts
+}
+
+// The blocks' parts of each token joined by 256 / NT threads, its loss, and
+// the total; one block.
+template <int NT>
+__global__ void __launch_bounds__(256) xent_few_join_kernel(const FewArgs a) {
+  __shared__ float2 mine[8][NT];
+  __shared__ float losses[kFewTokens];
+  griddep_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   constexpr int kShare = 256 / NT, kWarps = kShare / 32;
   {
     const int n = threadIdx.x / kShare;
     float t = -INFINITY, s = 0.f;
     float2 v[4];
-    for (int k0 = threadIdx.x % kShare; k0 < gridDim.x; k0 += 4 * kShare) {
+    for (int k0 = threadIdx.x % kShare; k0 < a.blocks; k0 += 4 * kShare) {
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const int k = k0 + q * kShare;
-        v[q] = k < gridDim.x ? __ldcg(a.part + (size_t)n * gridDim.x + k) : make_float2(-INFINITY, 0.f);
+        v[q] = k < a.blocks ? a.part[(size_t)n * a.blocks + k] : make_float2(-INFINITY, 0.f);
       }
 #pragma unroll
       for (int q = 0; q < 4; ++q) join_parts(t, s, v[q].x, v[q].y);
@@ -1202,7 +1234,7 @@ __global__ void __launch_bounds__(256) xent_few_kernel(const FewArgs a) {
     if (is_word(y, a.V)) {
       float t = mine[0][n].x, s = mine[0][n].y;
       for (int k = 1; k < kWarps; ++k) join_parts(t, s, mine[k][n].x, mine[k][n].y);
-      const float t2 = __ldcg(a.target + n);
+      const float t2 = a.target[n];
       if (t <= t2) {  // relative to the label: log1p keeps a small loss's digits
         s = t == t2 ? s : s * exp2f(t - t2);
         t = t2;
@@ -1224,6 +1256,7 @@ __global__ void __launch_bounds__(256) xent_few_kernel(const FewArgs a) {
       n += is_word(a.labels[k], a.V);
     }
     *a.total = (a.mean ? a.scale / (float)(n > 0 ? n : 1) : a.scale) * s;
+    *a.status = FLASH_GAU_OK;
   }
 }
 
@@ -1242,8 +1275,6 @@ Params gemm_params(int M, int N, int K, const XentLayout &L, long long first, in
 
 template <typename T>
 cudaError_t run_few(const XentProblem &q) {
-  cudaError_t err = cudaMemsetAsync(q.L.status, 0, 256, q.stream);
-  if (err != cudaSuccess) return err;
   FewArgs a = {};
   a.X = q.X;
   a.W = q.W;
@@ -1255,25 +1286,28 @@ cudaError_t run_few(const XentProblem &q) {
   a.scale = q.scale;
   a.part = q.L.part;
   a.target = q.L.ref;
-  a.done = q.L.done;
+  a.status = q.L.status;
   a.loss = q.loss;
   a.lse = q.lse;
   a.total = q.total;
   const int need = (q.V + 31) / 32;
-  const dim3 grid(need < kXentFewBlocks ? need : kXentFewBlocks), block(256);
-  auto go = [&](auto kernel, int nt) {
+  a.blocks = need < kXentFewBlocks ? need : kXentFewBlocks;
+  const dim3 grid(a.blocks), block(256);
+  auto go = [&](auto kernel, auto join, int nt) {
     const size_t smem = (size_t)nt * q.d * sizeof(float);
     if (smem > 48 * 1024) {
       const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                  kXentFewSmem);
       if (e != cudaSuccess) return e;
     }
-    return launch_pdl(kernel, grid, block, smem, q.stream, a);
+    const cudaError_t e = launch_pdl(kernel, grid, block, smem, q.stream, a);
+    return e != cudaSuccess ? e : launch_pdl(join, dim3(1), block, 0, q.stream, a);
   };
-  if (q.N == 1) return go(xent_few_kernel<T, 1>, 1);
-  if (q.N == 2) return go(xent_few_kernel<T, 2>, 2);
-  if (q.N <= 4) return go(xent_few_kernel<T, 4>, 4);
-  return go(xent_few_kernel<T, 8>, 8);
+  if (q.N == 1) return go(xent_few_kernel<T, 1>, xent_few_join_kernel<1>, 1);
+  if (q.N == 2) return go(xent_few_kernel<T, 2>, xent_few_join_kernel<2>, 2);
+  if constexpr (sizeof(T) == 4)
+    if (q.N > 4) return go(xent_few_kernel<T, 8>, xent_few_join_kernel<8>, 8);
+  return go(xent_few_kernel<T, 4>, xent_few_join_kernel<4>, 4);
 }
 
 template <typename T>
@@ -1282,8 +1316,7 @@ cudaError_t run(const XentProblem &q) {
   constexpr int products = bf16 ? 1 : kProducts, terms = bf16 ? 1 : kTerms;
   const XentLayout &L = q.L;
   const bool grad = q.dX || q.dW;
-  cudaError_t err = cudaMemsetAsync(L.status, 0, sizeof(int), q.stream);
-  if (err != cudaSuccess) return err;
+  cudaError_t err;
   GatherArgs<T> g = {};
   g.X = static_cast<const T *>(q.X);
   g.W = static_cast<const T *>(q.W);
@@ -1300,17 +1333,11 @@ cudaError_t run(const XentProblem &q) {
   g.lse = q.lse;
   g.dX = static_cast<T *>(q.dX);
   g.copy = L.piece >= q.N;
-  const unsigned blocks = (unsigned)((q.N + g.block_rows - 1) / g.block_rows);
+  g.blocks = (int)((q.N + g.block_rows - 1) / g.block_rows);
+  const unsigned blocks = (unsigned)(g.blocks + (bf16 ? 0 : (q.V + 7) / 8));
   if ((err = launch_pdl(xent_gather_kernel<T>, dim3(blocks), dim3(256), 0, q.stream, g)) != cudaSuccess)
     return err;
-  const void *W = q.W;
-  if (!bf16) {
-    W = L.Ws;
-    err = launch_pdl(xent_split_kernel, dim3((q.V + 7) / 8), dim3(256), 0, q.stream,
-                     static_cast<const float *>(q.W), q.V, q.d, static_cast<__nv_bfloat16 *>(L.Ws),
-                     L.term);
-    if (err != cudaSuccess) return err;
-  }
+  const void *W = bf16 ? q.W : L.Ws;
   // an operand's columns: d of the bf16 one (TMA fills what is behind with
   // zeros), or three padded terms
   const uint64_t width = bf16 ? (uint64_t)q.d : (uint64_t)terms * L.term;
@@ -1410,9 +1437,10 @@ size_t xent_dx_part_rows(long long rows, int d) {
 }
 
 bool xent_few(long long N, int d, int dtype, bool grad) {
-  const int io = dtype == FLASH_GAU_BF16 ? 2 : 4;
+  const bool bf16 = dtype == FLASH_GAU_BF16;
+  const int io = bf16 ? 2 : 4;
   const long long tokens = N <= 2 ? N : N <= 4 ? 4 : 8;
-  return !grad && N <= kFewTokens && (long long)d * io % 16 == 0 &&
+  return !grad && N <= (bf16 ? kFewTokensBf16 : kFewTokens) && (long long)d * io % 16 == 0 &&
          tokens * d * (long long)sizeof(float) <= kXentFewSmem;
 }
 

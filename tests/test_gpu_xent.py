@@ -152,6 +152,31 @@ def test_few_tokens_sure_far_and_left_out(dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("N", [2, 4])
+def test_few_tokens_keep_to_themselves(N, dtype):
+    """A token that is not a number, a sure one and one without a label beside
+    an ordinary one; the status word of a workspace that held anything."""
+    X, W, y = make(N, 96, 1234, dtype, 15, ignored=0.0)
+    ws = torch.full((bd.xent_workspace_bytes(N, 96, 1234, bd.BF16 if dtype == "bf16" else bd.FP32,
+                                             False),), 255, dtype=torch.uint8, device="cuda")
+    got = bd.xent(X, W, y, grad=False, workspace=ws)
+    check(X, W, y, got=got)
+    assert bd.workspace_status(ws) == 0
+    X[0, 95] = float("nan")
+    if N == 4:
+        y[2] = -7
+        X[2] = float("inf")
+        X[3] = W[int(y[3])] * 64
+    bad = bd.xent(X, W, y, grad=False, workspace=ws)
+    assert bool(bad["loss"][0].isnan()) and torch.equal(bad["loss"][1], got["loss"][1])
+    if N == 4:
+        assert float(bad["loss"][2]) == 0.0 and float(bad["lse"][2]) == 0.0
+        one = bd.xent(X[3:], W, y[3:], grad=False)
+        check(X[3:], W, y[3:], got=one)
+        check(X[1:2], W, y[1:2], got=bd.xent(X[1:2], W, y[1:2], grad=False))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 def test_loss_only_gives_the_same_loss(dtype):
     X, W, y = make(500, 128, 3001, dtype, 1)
     a, b = bd.xent(X, W, y), bd.xent(X, W, y, grad=False)
