@@ -244,6 +244,12 @@ def test_labels_far_below_the_largest_logit(dtype):
     check(X, W, y)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_labels_far_below_in_many_parts(dtype):
+    """Rows of E that are rescaled by the whole block, in more than one step."""
+    check(*make(70, 64, 9001, dtype, 16, size=40.0, pull=0.0))
+
+
 def test_infinite_and_nan_rows():
     X, W, y = make(64, 64, 300, "bf16", 7, ignored=0.0)
     clean = bd.xent(X, W, y)
