@@ -959,6 +959,8 @@ struct Exact {
   }
 };
 
+constexpr int kAtOnce = 10;  // loads under way: half of what 608 blocks leave a thread
+
 // Sums the parts in a fixed order: a thread block takes 32 columns of one
 // kind (blockIdx.y), 32 threads a column.  A ScaleNorm's g gathers terms of
 // either sign from the whole [M, d], which cancel, so the roundings of its
@@ -974,8 +976,16 @@ __global__ void __launch_bounds__(1024) sum_parts_kernel(const SumArgs a) {
     const float *p = a.scalar_part + (s == kPostG ? (long long)a.blocks * kMaxWarps : 0);
     Exact v = {0.f, 0.f};
     if (lane < a.warps)
-#pragma unroll 4
-      for (int b = sub; b < a.blocks; b += 32) v.add(p[(long long)b * kMaxWarps + lane], 0.f);
+      for (int b0 = sub; b0 < a.blocks; b0 += 32 * kAtOnce) {
+        float x[kAtOnce];
+#pragma unroll
+        for (int q = 0; q < kAtOnce; ++q) {
+          const int b = b0 + 32 * q;
+          x[q] = b < a.blocks ? p[(long long)b * kMaxWarps + lane] : 0.f;
+        }
+#pragma unroll
+        for (int q = 0; q < kAtOnce; ++q) v.add(x[q], 0.f);
+      }
     v.join_warp();
     if (lane == 0) sums[sub] = v;
     __syncthreads();
@@ -992,8 +1002,16 @@ __global__ void __launch_bounds__(1024) sum_parts_kernel(const SumArgs a) {
   if (c < a.d) {
     const float *p = a.part + (long long)s * a.d + c;
     const long long step = (long long)kSums * a.d;
-#pragma unroll 4
-    for (int b = sub; b < a.parts; b += 32) v += p[b * step];
+    for (int b0 = sub; b0 < a.parts; b0 += 32 * kAtOnce) {
+      float x[kAtOnce];
+#pragma unroll
+      for (int q = 0; q < kAtOnce; ++q) {
+        const int b = b0 + 32 * q;
+        x[q] = b < a.parts ? p[b * step] : 0.f;
+      }
+#pragma unroll
+      for (int q = 0; q < kAtOnce; ++q) v += x[q];
+    }
   }
   buf[lane][sub] = v;
   __syncthreads();
