@@ -23,10 +23,13 @@
 // tensors), needs no workspace and can be captured; a warp takes 256 elements
 // of one tensor at a time as two runs of 128, four consecutive elements a lane
 // (16-byte accesses).  fp32 moments run at the copy rate (43.8 M parameters:
-// 188 us, 6.7 TB/s); 8-bit ones at 5.2 TB/s (82 M: 261 us), issue slots half
-// full of coding; their values at 5.8 TB/s (133 us).
+// 188 us, 6.7 TB/s), and so do 8-bit ones in long lists, whose values pass
+// through shared memory (82.6 M with fp32 gradients and copies: 221 us); their
+// values are written at 5.8 TB/s (133 us).
 #include <cuda_bf16.h>
 #include <math.h>
+
+#include <atomic>
 
 #include "flash_gau_internal.h"
 #include "packed_f32.cuh"
@@ -37,7 +40,7 @@ namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kBlock = 256;  // elements that share a scale; a warp's at a time
-constexpr int kRuns = 4;     // of them a warp takes from a long list
+constexpr int kRuns = 3;     // of them a warp takes from a long list of 8-bit moments
 
 struct Entry {
   float *p;
@@ -48,7 +51,8 @@ struct Entry {
   long long n;
   float decay;    // 1 - lr * weight_decay
   int first;      // first thread block of the tensor in this launch
-  int g_bf16, vec;  // vec: every pointer aligned for four elements at a time
+  int g_bf16;
+  int vec;  // every pointer aligned for 1: four elements at a time, 2: 16 bytes
 };
 
 // The scalars of a step.
@@ -245,38 +249,47 @@ __device__ __forceinline__ void from_pairs(const f2 *y, float (&x)[4]) {
   x[0] = a.x; x[1] = a.y; x[2] = b.x; x[3] = b.y;
 }
 
+// Where a block's 256 elements are read: the tensor's arrays from there on, or
+// their copies in shared memory.
+struct Source {
+  const float *p;
+  const void *g, *m, *v;
+  float ms, vs;  // 8-bit moments' scales
+};
+
 // One warp's 256 elements of a tensor, block `blk` of it; pairs 2 j and 2 j + 1
 // are the lane's four elements of run j.
 template <int BITS, bool FULL>
-__device__ __forceinline__ void update(const Entry &e, const Step &l, long long blk, int lane,
-                                       float gs) {
+__device__ __forceinline__ void update(const Entry &e, const Source &src, const Step &l,
+                                       long long blk, int lane, float gs) {
   const long long i0 = blk * kBlock + 4 * lane;
   int n[2];
   f2 p[4], g[4], m[4], v[4];
   float x[4];
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
-    const long long i = i0 + 128 * j, left = e.n - i;
+    const long long left = e.n - (i0 + 128 * j);
+    const int i = 4 * lane + 128 * j;
     n[j] = FULL || left >= 4 ? 4 : (left > 0 ? (int)left : 0);
-    load4<FULL>(e.p, i, n[j], x);
+    load4<FULL>(src.p, i, n[j], x);
     to_pairs(x, p + 2 * j);
-    if (e.g_bf16) load4<FULL>(static_cast<const __nv_bfloat16 *>(e.g), i, n[j], x);
-    else load4<FULL>(static_cast<const float *>(e.g), i, n[j], x);
+    if (e.g_bf16) load4<FULL>(static_cast<const __nv_bfloat16 *>(src.g), i, n[j], x);
+    else load4<FULL>(static_cast<const float *>(src.g), i, n[j], x);
     to_pairs(x, g + 2 * j);
     if constexpr (BITS == 32) {
-      load4<FULL>(static_cast<const float *>(e.m), i, n[j], x);
+      load4<FULL>(static_cast<const float *>(src.m), i, n[j], x);
       to_pairs(x, m + 2 * j);
-      load4<FULL>(static_cast<const float *>(e.v), i, n[j], x);
+      load4<FULL>(static_cast<const float *>(src.v), i, n[j], x);
       to_pairs(x, v + 2 * j);
     }
   }
   if constexpr (BITS == 8) {
-    const f2 ms = both(e.m_scale[blk]), vs = both(e.v_scale[blk]);
+    const f2 ms = both(src.ms), vs = both(src.vs);
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       // codes behind the end are read as zeros
-      const uint32_t mc = load_codes<FULL>(e.m, i0 + 128 * j, n[j]) ^ 0x80808080u;
-      const uint32_t vc = load_codes<FULL>(e.v, i0 + 128 * j, n[j]);
+      const uint32_t mc = load_codes<FULL>(src.m, 4 * lane + 128 * j, n[j]) ^ 0x80808080u;
+      const uint32_t vc = load_codes<FULL>(src.v, 4 * lane + 128 * j, n[j]);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         m[2 * j + h] = decode_m(mc, h, ms);
@@ -351,27 +364,112 @@ __device__ __forceinline__ void update(const Entry &e, const Step &l, long long 
   }
 }
 
-// Calls f(entry, block, lane, full) for each of this warp's blocks.
-template <int CAP, typename F>
-__device__ __forceinline__ void each_block(const List<CAP> &l, F f) {
+// The tensor's arrays from block `blk` on.
+template <int BITS>
+__device__ __forceinline__ Source source(const Entry &e, long long blk) {
+  const long long i = blk * kBlock;
+  Source s;
+  s.p = e.p + i;
+  s.g = static_cast<const uint8_t *>(e.g) + i * (e.g_bf16 ? 2 : 4);
+  s.m = static_cast<const uint8_t *>(e.m) + i * (BITS / 8);
+  s.v = static_cast<const uint8_t *>(e.v) + i * (BITS / 8);
+  s.ms = s.vs = 0.f;  // the caller's to read
+  return s;
+}
+
+// A warp's blocks of a tensor: first, and the one behind the last.
+template <int CAP>
+__device__ __forceinline__ const Entry &my_blocks(const List<CAP> &l, long long &blk, long long &end) {
   const Entry &e = l.e[find(l, blockIdx.x)];
+  blk = ((long long)(blockIdx.x - e.first) * kWarps + (threadIdx.x >> 5)) * l.runs;
+  end = min(blk + l.runs, (e.n + kBlock - 1) / kBlock);
+  return e;
+}
+
+// 16 bytes from global into shared memory without passing through registers
+__device__ __forceinline__ void cp_async16(void *dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ptx::smem_u32(dst)), "l"(src)
+               : "memory");
+}
+
+// A block's p, g, codes and scales of 8-bit moments in shared memory.
+struct __align__(16) Staged {
+  float p[kBlock];
+  float g[kBlock];  // bf16 ones in its first half
+  uint8_t m[kBlock], v[kBlock];
+  float scales[4];
+  __device__ void fetch(const Entry &e, long long blk, int lane) {
+    const Source s = source<8>(e, blk);
+    for (int i = lane; i < kBlock / 4; i += 32) cp_async16(p + 4 * i, s.p + 4 * i);
+    const uint8_t *from = static_cast<const uint8_t *>(s.g);
+    for (int i = lane; i < (e.g_bf16 ? kBlock / 8 : kBlock / 4); i += 32)
+      cp_async16(g + 4 * i, from + 16 * i);
+    const int i = 16 * (lane & 15);
+    if (lane < 16) cp_async16(m + i, static_cast<const uint8_t *>(s.m) + i);
+    else cp_async16(v + i, static_cast<const uint8_t *>(s.v) + i);
+    if (lane < 2)
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(ptx::smem_u32(scales + lane)),
+                   "l"(lane ? e.v_scale + blk : e.m_scale + blk)
+                   : "memory");
+  }
+};
+constexpr size_t kStagedBytes = sizeof(Staged) * kRuns * kWarps;
+
+// The blocks from blk on, values read where they are.
+template <int BITS>
+__device__ __forceinline__ void direct(const Entry &e, const Step &step, long long blk, long long end,
+                                       float gs) {
   const int lane = threadIdx.x & 31;
-  long long blk = ((long long)(blockIdx.x - e.first) * kWarps + (threadIdx.x >> 5)) * l.runs;
-  const long long end = min(blk + l.runs, (e.n + kBlock - 1) / kBlock);
-  for (; blk < end; ++blk) f(e, blk, lane, e.vec && blk * kBlock + kBlock <= e.n);
+  for (; blk < end; ++blk) {
+    Source s = source<BITS>(e, blk);
+    if (BITS == 8) {
+      s.ms = e.m_scale[blk];
+      s.vs = e.v_scale[blk];
+    }
+    if (e.vec && blk * kBlock + kBlock <= e.n) update<BITS, true>(e, s, step, blk, lane, gs);
+    else update<BITS, false>(e, s, step, blk, lane, gs);
+  }
 }
 
 // Blocks on an SM: 44 M parameters with fp32 moments take 0.188 ms with five,
-// 0.199 with four (of 64 registers); 82 M with 8-bit ones 0.261 ms with four,
-// 0.264 with five.
+// 0.199 with four (of 64 registers).
 template <int BITS, int CAP>
 __global__ void __launch_bounds__(kThreads, BITS == 8 ? 4 : 5) adamw_kernel(const __grid_constant__ List<CAP> l) {
   ptx::griddep_wait();
+  long long blk, end;
+  const Entry &e = my_blocks(l, blk, end);
+  direct<BITS>(e, l.step, blk, end, l.step.grad_scale ? *l.step.grad_scale : 1.f);
+}
+
+// Long lists with 8-bit moments: a warp asks for the values of all its blocks
+// at once (60 KB of shared memory, three thread blocks an SM) and codes one
+// after the other.
+template <int CAP>
+__global__ void __launch_bounds__(kThreads, 3) adamw_staged_kernel(const __grid_constant__ List<CAP> l) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  ptx::griddep_wait();
+  const int lane = threadIdx.x & 31;
+  long long blk, end;
+  const Entry &e = my_blocks(l, blk, end);
   const float gs = l.step.grad_scale ? *l.step.grad_scale : 1.f;
-  each_block(l, [&](const Entry &e, long long blk, int lane, bool full) {
-    if (full) update<BITS, true>(e, l.step, blk, lane, gs);
-    else update<BITS, false>(e, l.step, blk, lane, gs);
-  });
+  if (e.vec == 2) {
+    Staged *const mine = reinterpret_cast<Staged *>(smem) + (threadIdx.x >> 5) * kRuns;
+    const long long whole = min(end, e.n / kBlock);
+#pragma unroll
+    for (int k = 0; k < kRuns; ++k) {
+      if (blk + k < whole) mine[k].fetch(e, blk + k, lane);
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+    for (int k = 0; blk < whole; ++k, ++blk) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(kRuns - 1) : "memory");
+      __syncwarp();
+      const Staged &in = mine[k];
+      const Source s = {in.p, in.g, in.m, in.v, in.scales[0], in.scales[1]};
+      update<8, true>(e, s, l.step, blk, lane, gs);
+      asm volatile("cp.async.commit_group;" ::: "memory");  // so that the wait counts on
+    }
+  }
+  direct<8>(e, l.step, blk, end, gs);
 }
 
 // m and v of 8-bit moments as fp32: `p` holds m's values, `copy` v's.
@@ -402,16 +500,19 @@ __device__ __forceinline__ void values(const Entry &e, long long blk, int lane) 
 template <int CAP>
 __global__ void __launch_bounds__(kThreads, 8) moments_kernel(const __grid_constant__ List<CAP> l) {
   ptx::griddep_wait();
-  each_block(l, [&](const Entry &e, long long blk, int lane, bool full) {
-    if (full) values<true>(e, blk, lane);
+  const int lane = threadIdx.x & 31;
+  long long blk, end;
+  const Entry &e = my_blocks(l, blk, end);
+  for (; blk < end; ++blk) {
+    if (e.vec && blk * kBlock + kBlock <= e.n) values<true>(e, blk, lane);
     else values<false>(e, blk, lane);
-  });
+  }
 }
 
 bool aligned(const void *p, unsigned bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
 
-template <int BITS, int CAP, typename Kernel, typename Fill>
-cudaError_t run(Kernel kernel, const AdamwProblem &q, Fill fill) {
+template <int CAP, typename Kernel, typename Fill>
+cudaError_t run(Kernel kernel, const AdamwProblem &q, int runs, size_t smem, Fill fill) {
   List<CAP> l;
   l.step.step_size = (float)(q.lr / (1.0 - pow(q.beta1, (double)q.step)));
   l.step.beta1 = (float)q.beta1;
@@ -422,13 +523,7 @@ cudaError_t run(Kernel kernel, const AdamwProblem &q, Fill fill) {
   l.step.eps = (float)q.eps;
   l.step.one = 1.f;
   l.step.grad_scale = q.grad_scale;
-  // 8-bit moments are bound by instructions as much as by memory: of long
-  // lists a warp takes several blocks, so that finding its tensor counts for
-  // little (82 M parameters: 0.36 -> 0.27 ms); with fp32 moments that costs
-  // registers and gains nothing (44 M: 0.183 -> 0.188 ms)
-  long long n = 0;
-  for (int k = 0; k < q.n_tensors; ++k) n += q.tensors[k].n;
-  l.runs = BITS == 8 && n >= (1LL << 22) ? kRuns : 1;
+  l.runs = runs;
   const long long chunk = (long long)kWarps * kBlock * l.runs;
   for (int k = 0; k < q.n_tensors;) {
     l.count = 0;
@@ -447,7 +542,7 @@ cudaError_t run(Kernel kernel, const AdamwProblem &q, Fill fill) {
     }
     if (!l.count) break;
     const cudaError_t err =
-        launch_pdl(kernel, dim3((unsigned)blocks), dim3(kThreads), 0, q.stream, l);
+        launch_pdl(kernel, dim3((unsigned)blocks), dim3(kThreads), smem, q.stream, l);
     if (err != cudaSuccess) return err;
   }
   return cudaSuccess;
@@ -455,6 +550,30 @@ cudaError_t run(Kernel kernel, const AdamwProblem &q, Fill fill) {
 
 // short lists keep the launch's parameters small
 constexpr int kSmall = 16, kLarge = 384;
+
+// With 8-bit moments coding leaves too few loads under way, so long lists take
+// the staged kernel (parameters, gradients and copies of 82 M elements: 0.30 ms
+// direct, 0.22 staged; 9.4 M 35 and 27 us; 4.7 M 14.1 and 14.9 us).  With fp32
+// moments the direct one runs at the copy rate.
+template <int CAP, typename Fill>
+cudaError_t step_by_size(const AdamwProblem &q, Fill fill) {
+  if (q.state_bits != 8) return run<CAP>(adamw_kernel<32, CAP>, q, 1, 0, fill);
+  long long n = 0;
+  for (int k = 0; k < q.n_tensors; ++k) n += q.tensors[k].n;
+  if (n < (1LL << 23)) return run<CAP>(adamw_kernel<8, CAP>, q, 1, 0, fill);
+  auto kernel = adamw_staged_kernel<CAP>;
+  static std::atomic<int> allowed[64];  // per device
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!allowed[dev].load(std::memory_order_acquire)) {
+    err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kStagedBytes);
+    if (err != cudaSuccess) return err;
+    allowed[dev].store(1, std::memory_order_release);
+  }
+  return run<CAP>(kernel, q, kRuns, kStagedBytes, fill);
+}
 
 }  // namespace
 
@@ -473,12 +592,10 @@ cudaError_t adamw_step(const AdamwProblem &q) {
     const unsigned state = q.state_bits == 8 ? 4 : 16;
     e.vec = aligned(t.p, 16) && aligned(t.copy, 8) && aligned(t.g, e.g_bf16 ? 8 : 16) &&
             aligned(t.m, state) && aligned(t.v, state);
+    if (e.vec && aligned(t.g, 16) && aligned(t.m, 16) && aligned(t.v, 16)) e.vec = 2;
   };
-  if (q.n_tensors <= kSmall)
-    return q.state_bits == 8 ? run<8, kSmall>(adamw_kernel<8, kSmall>, q, fill)
-                             : run<32, kSmall>(adamw_kernel<32, kSmall>, q, fill);
-  return q.state_bits == 8 ? run<8, kLarge>(adamw_kernel<8, kLarge>, q, fill)
-                           : run<32, kLarge>(adamw_kernel<32, kLarge>, q, fill);
+  if (q.n_tensors <= kSmall) return step_by_size<kSmall>(q, fill);
+  return step_by_size<kLarge>(q, fill);
 }
 
 cudaError_t adamw_moments(const AdamwProblem &q, float *const *m_out, float *const *v_out) {
@@ -493,8 +610,8 @@ cudaError_t adamw_moments(const AdamwProblem &q, float *const *m_out, float *con
     e.v_scale = t.v_scale;
     e.vec = aligned(e.p, 16) && aligned(e.copy, 16) && aligned(t.m, 4) && aligned(t.v, 4);
   };
-  return q.n_tensors <= kSmall ? run<32, kSmall>(moments_kernel<kSmall>, q, fill)
-                               : run<32, kLarge>(moments_kernel<kLarge>, q, fill);
+  return q.n_tensors <= kSmall ? run<kSmall>(moments_kernel<kSmall>, q, 1, 0, fill)
+                               : run<kLarge>(moments_kernel<kLarge>, q, 1, 0, fill);
 }
 
 }  // namespace flashgau

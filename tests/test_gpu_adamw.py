@@ -146,6 +146,43 @@ def test_8bit_moments_bit_for_bit(sizes, grad_dtype, offset):
         np.testing.assert_array_equal(v[i].cpu().numpy().reshape(-1), wv)
 
 
+@pytest.mark.parametrize("many", [False, True])
+def test_8bit_long_list_as_its_tensors_alone(many):
+    """A list long enough for the staged kernel against a step of each tensor
+    by itself: ragged ends, tensors that end inside a warp's share, either
+    gradient type, arrays that are not on 16 bytes."""
+    sizes = [1000003, 2 ** 20, 1500000, 770, 256, 1, 2300001, 1200 * 1000, 1400000] + [300] * (10 * many)
+    assert sum(sizes) >= 2 ** 23
+    params, copies, m, v = [], [], [], []
+    grads = [[] for _ in range(2)]
+    g = torch.Generator(device="cuda").manual_seed(50)
+    for k, n in enumerate(sizes):
+        off = 1 if k in (2, 4) else 0
+        dev = lambda dt, x=None: torch.empty(n + off, dtype=dt, device="cuda")[off:].copy_(  # noqa: E731
+            x if x is not None else torch.zeros(n, device="cuda"))
+        rand = lambda: torch.randn(n, generator=g, device="cuda")  # noqa: E731
+        params.append(dev(torch.float32, rand() * 0.05))
+        copies.append(dev(torch.bfloat16) if k % 3 else None)
+        m.append(dev(torch.int8))
+        v.append(dev(torch.uint8))
+        for t in range(2):
+            grads[t].append(dev(torch.bfloat16 if k % 2 else torch.float32, rand() * 0.01))
+    clone = lambda x: None if x is None else x.clone()  # noqa: E731
+    alone = [bd.AdamW([params[k].clone()], copies=[clone(copies[k])], state_bits=8, **HYPER)
+             for k in range(len(sizes))]
+    opt = bd.AdamW(params, copies=copies, state_bits=8, m=m, v=v, **HYPER)
+    for t in range(2):
+        opt.step(grads[t], lr=LR)
+        for k, a in enumerate(alone):
+            a.step([grads[t][k]], lr=LR)
+    torch.cuda.synchronize()
+    for k, a in enumerate(alone):
+        for x, y in ((params[k], a.params[0]), (m[k], a.m[0]), (v[k], a.v[0]),
+                     (opt.m_scale[k], a.m_scale[0]), (opt.v_scale[k], a.v_scale[0])):
+            assert torch.equal(x, y), (k, sizes[k])
+        assert copies[k] is None or torch.equal(copies[k], a.copies[0])
+
+
 def test_8bit_stays_near_32bit():
     """Twenty steps with both kinds: a code's first moment is off by at most
     half a step of 2 c + 1 in c^2, so that what differs stays a small part of
