@@ -23,7 +23,7 @@
 // tensors), needs no workspace and can be captured; a warp takes 256 elements
 // of one tensor at a time as two runs of 128, four consecutive elements a lane
 // (16-byte accesses).  fp32 moments run at the copy rate (43.8 M parameters:
-// 188 us, 6.7 TB/s), and so do 8-bit ones in long lists, whose values pass
+// 189 us, 6.7 TB/s), and 8-bit ones nearly do in long lists, whose values pass
 // through shared memory (82.6 M with fp32 gradients and copies: 221 us); their
 // values are written at 5.8 TB/s (133 us).
 #include <cuda_bf16.h>
