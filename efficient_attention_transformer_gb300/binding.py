@@ -145,6 +145,9 @@ class AdamWTensor(ctypes.Structure):
     ]
 
 
+_ADAMW_TENSOR = np.dtype(AdamWTensor)
+
+
 class AdamWHyper(ctypes.Structure):
     _fields_ = [
         ("lr", ctypes.c_double),
@@ -814,7 +817,7 @@ class AdamW:
         self._shapes = [p.shape for p in self.params]
         self._params_at = [p.data_ptr() for p in self.params]
         self._array = (AdamWTensor * max(k, 1))()
-        columns = np.frombuffer(self._array, dtype=np.dtype(AdamWTensor))
+        columns = np.frombuffer(self._array, dtype=_ADAMW_TENSOR)
         n = [p.numel() for p in self.params]
         columns["n"][:k], columns["weight_decay"][:k] = n, decay
         kinds = [("p", self.params, f32, n), ("m", self.m, md, n), ("v", self.v, vd, n),

@@ -369,3 +369,11 @@ def test_xent_workspace(L):
 def test_xent_binding_refuses_host_tensors(L):
     with pytest.raises(ValueError):
         bd.xent(torch.zeros(4, 8), torch.zeros(5, 8), torch.zeros(4, dtype=torch.int32))
+
+
+def test_a_stream_of_another_device_is_refused():
+    class Stream:
+        device = torch.device("cuda", 1)
+
+    with pytest.raises(ValueError):
+        bd._scope(torch.device("cuda", 0), Stream())
