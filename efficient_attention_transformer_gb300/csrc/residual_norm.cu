@@ -22,8 +22,8 @@
 // bytes a lane), no block-wide step at all.  16384 x 768 bf16 with every
 // option takes 26 us, 4.8 TB/s (a persistent form with the next row's loads
 // under way 23 for 23 there and 10 for 8.5 us at 4096 rows, by itself).  Rows
-// wider than 2048 columns, or not on 16-byte boundaries, take a plain form
-// that reads the row again from L1 for each of its sums.
+// wider than 2048 columns, or not on 16-byte boundaries, take a form with
+// eight columns a thread and a block a row.
 //
 // Backward, rows of up to 2048 columns on 16-byte boundaries: one to four
 // warps a row, see residual_norm_grad_rows_kernel (16384 x 768 bf16 with every
@@ -61,7 +61,6 @@ struct Args {
   int d, norm, post;
   float eps;
   int rows, subsets;         // backward: rows of a tile, threads that share a column
-  int flat;                  // backward: tiles start on 16-byte boundaries
 };
 
 // the column sums, in the workspace's order
@@ -270,51 +269,130 @@ __global__ void __launch_bounds__(128) residual_norm_kernel(const Args a) {
   }
 }
 
-// Any width and alignment: one warp a row, element by element, the row read
-// again for each sum.  Outputs are written last, each after the same
-// element's inputs, so they may be the inputs' arrays.
-template <typename T>
-__global__ void __launch_bounds__(128) residual_norm_any_kernel(const Args a) {
+// Any width and alignment: a thread has eight columns of a row in registers,
+// consecutive ones (VEC: rows and arrays on 16-byte boundaries; two runs of
+// four fp32) or one from every `threads`; up to 256 columns are a warp's, and
+// four rows a block, wider ones a block's.  A warp a row that read the row
+// again for each sum took 120 us at 16384 x 767 bf16, and 268 at 3000 x 4096.
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(1024) residual_norm_any_kernel(const Args a) {
+  __shared__ float shared_sums[2][32];
   ptx::griddep_wait();
-  const int lane = threadIdx.x & 31, d = a.d;
-  const long long row = blockIdx.x * (long long)(blockDim.x >> 5) + (threadIdx.x >> 5);
-  if (row >= a.M) return;
-  const T *h = static_cast<const T *>(a.h) + row * d;
-  const T *y = a.y ? static_cast<const T *>(a.y) + row * d : nullptr;
-  const T *gate = a.gate ? static_cast<const T *>(a.gate) + row * d : nullptr;
-  auto stat = [&](auto get, int kind) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, d = a.d;
+  const bool alone = d <= 256;  // a warp a row
+  const int t = alone ? lane : threadIdx.x, threads = alone ? 32 : blockDim.x;
+  const int at_once = alone ? blockDim.x / 32 : 1;
+  auto column = [&](int q) {
+    if (!VEC) return t + threads * q;
+    return sizeof(T) == 2 ? 8 * t + q : 4 * t + (q & 3) + (q < 4 ? 0 : 4 * threads);
+  };
+  auto load = [&](const auto *row, float (&x)[8]) {
+    using E = std::remove_const_t<std::remove_pointer_t<decltype(row)>>;
+    if constexpr (VEC && sizeof(E) == 2) {
+      const uint4 w = t * 8 < d ? *reinterpret_cast<const uint4 *>(row + 8 * t) : make_uint4(0, 0, 0, 0);
+      const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float2 f = unpack_bf16(u[q]);
+        x[2 * q] = f.x;
+        x[2 * q + 1] = f.y;
+      }
+    } else if constexpr (VEC) {
+#pragma unroll
+      for (int q = 0; q < 8; q += 4) {
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (column(q) < d) v = *reinterpret_cast<const float4 *>(row + column(q));
+        x[q] = v.x; x[q + 1] = v.y; x[q + 2] = v.z; x[q + 3] = v.w;
+      }
+    } else {
+#pragma unroll
+      for (int q = 0; q < 8; ++q) x[q] = column(q) < d ? to_f(row[column(q)]) : 0.f;
+    }
+  };
+  auto store = [&](T *row, const float (&x)[8]) {
+    if constexpr (VEC && sizeof(T) == 2) {
+      if (8 * t < d)
+        *reinterpret_cast<uint4 *>(row + 8 * t) = make_uint4(
+            pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+    } else if constexpr (VEC) {
+#pragma unroll
+      for (int q = 0; q < 8; q += 4)
+        if (column(q) < d)
+          *reinterpret_cast<float4 *>(row + column(q)) =
+              make_float4(x[q], x[q + 1], x[q + 2], x[q + 3]);
+    } else {
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        if (column(q) < d) row[column(q)] = (T)x[q];
+    }
+  };
+  int flip = 0;
+  auto row_sum = [&](float v) {
+    v = warp_sum(v);
+    if (alone) return v;
+    if (lane == 0) shared_sums[flip][warp] = v;
+    __syncthreads();
+    v = warp_sum(lane < threads / 32 ? shared_sums[flip][lane] : 0.f);
+    flip ^= 1;  // written again only after the next barrier: everyone has read it
+    return v;
+  };
+  const float inv_d = 1.0f / (float)d;
+  // x becomes its normalised row with parameters, zeros behind it
+  auto normalise = [&](float (&x)[8], int kind, const float *g, const float *b) {
+    const bool layer = kind == FLASH_GAU_NORM_LAYER;
     float mean = 0.f, m2 = 0.f;
-    if (kind == FLASH_GAU_NORM_LAYER) {
+    if (layer) {
       float s = 0.f;
-      for (int c = lane; c < d; c += 32) s += get(c);
-      mean = warp_sum(s) / (float)d;
+#pragma unroll
+      for (int q = 0; q < 8; ++q) s += x[q];
+      mean = row_sum(s) / (float)d;
     }
-    for (int c = lane; c < d; c += 32) {
-      const float v = get(c) - mean;
-      m2 = fmaf(v, v, m2);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      x[q] = column(q) < d ? x[q] - mean : 0.f;
+      m2 = fmaf(x[q], x[q], m2);
     }
-    return make_float2(mean, inv_spread(warp_sum(m2), kind, 1.0f / (float)d, a.eps));
+    const float inv = inv_spread(row_sum(m2), kind, inv_d, a.eps) * (layer ? 1.f : __ldg(g));
+#pragma unroll
+    for (int q = 0; q < 8; ++q) x[q] *= inv;
+    if (!layer) return;
+    float w[8];
+    load(g, w);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) x[q] *= w[q];
+    if (!b) return;
+    load(b, w);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) x[q] += w[q];
   };
-  auto affine = [&](float u, int kind, const float *g, const float *b, int c) {
-    if (kind == FLASH_GAU_NORM_LAYER) return fmaf(u, g[c], b ? b[c] : 0.f);
-    return kind == FLASH_GAU_NORM_SCALE ? u * g[0] : u;
-  };
-  float2 sy = make_float2(0.f, 1.f);
-  if (y && a.post) sy = stat([&](int c) { return to_f(y[c]); }, a.post);
-  auto r = [&](int c) {
-    if (!y) return to_f(h[c]);
-    float v = affine((to_f(y[c]) - sy.x) * sy.y, a.post, a.post_g, a.post_b, c);
-    if (gate) v *= to_f(gate[c]);
-    if (a.scale) v *= a.scale[c];
-    return to_f(h[c]) + v;
-  };
-  float2 sr = make_float2(0.f, 1.f);
-  if (a.norm) sr = stat(r, a.norm);
-  for (int c = lane; c < d; c += 32) {
-    const float v = r(c);
-    const float n = affine((v - sr.x) * sr.y, a.norm, a.norm_g, a.norm_b, c);
-    if (a.r) static_cast<T *>(a.r)[row * d + c] = (T)v;
-    if (a.norm) static_cast<T *>(a.n)[row * d + c] = (T)n;
+  for (long long row = blockIdx.x * (long long)at_once + (alone ? warp : 0); row < a.M;
+       row += gridDim.x * (long long)at_once) {
+    const long long off = row * d;
+    float h[8], r[8], w[8];
+    load(static_cast<const T *>(a.h) + off, h);
+    if (a.y) {
+      load(static_cast<const T *>(a.y) + off, r);
+      if (a.gate) load(static_cast<const T *>(a.gate) + off, w);
+      if (a.post) normalise(r, a.post, a.post_g, a.post_b);
+      if (a.gate) {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) r[q] *= w[q];
+      }
+      if (a.scale) {
+        load(a.scale, w);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) r[q] *= w[q];
+      }
+#pragma unroll
+      for (int q = 0; q < 8; ++q) r[q] = column(q) < d ? r[q] + h[q] : 0.f;
+    } else {
+#pragma unroll
+      for (int q = 0; q < 8; ++q) r[q] = h[q];
+    }
+    if (a.r) store(static_cast<T *>(a.r) + off, r);
+    if (!a.norm) continue;
+    normalise(r, a.norm, a.norm_g, a.norm_b);
+    store(static_cast<T *>(a.n) + off, r);
   }
 }
 
@@ -500,6 +578,12 @@ __device__ __forceinline__ RowSums row_sums(const Args &a, const TileRows<T> &t,
   return s;
 }
 
+// bytes from one array of a tile to the next
+template <typename T, bool VEC>
+__host__ __device__ inline size_t tile_pitch(long long rows, int d) {
+  return ((size_t)rows * d * sizeof(T) + 15) / 16 * 16 + (VEC ? 0 : 16);
+}
+
 template <typename T, bool VEC, int NG, int MAXT, int BLOCKS>
 __global__ void __launch_bounds__(MAXT, BLOCKS) residual_norm_grad_kernel(const Args a) {
   extern __shared__ __align__(16) uint8_t smem[];
@@ -510,7 +594,7 @@ __global__ void __launch_bounds__(MAXT, BLOCKS) residual_norm_grad_kernel(const 
   RowSums *sums = reinterpret_cast<RowSums *>(smem);
   const int dp = (d + 3) / 4 * 4;
   float *ng = reinterpret_cast<float *>(sums + a.rows), *kp = ng + dp;
-  const size_t pitch = ((size_t)a.rows * d * sizeof(T) + 15) / 16 * 16;
+  const size_t pitch = tile_pitch<T, VEC>(a.rows, d);
   const T *src[5] = {static_cast<const T *>(a.norm ? a.h : nullptr), static_cast<const T *>(a.dn),
                      static_cast<const T *>(a.dr), static_cast<const T *>(a.y),
                      static_cast<const T *>(a.gate)};
@@ -521,7 +605,6 @@ __global__ void __launch_bounds__(MAXT, BLOCKS) residual_norm_grad_kernel(const 
     tile[k] = reinterpret_cast<T *>(at);
     if (src[k]) at += pitch;
   }
-  const TileRows<T> rows_in = {tile[0], tile[1], tile[2], tile[3], tile[4], ng, kp};
   ptx::griddep_wait();
   for (int c = t; c < d; c += threads) {
     ng[c] = a.norm ? a.norm_g[norm_layer ? c : 0] : 1.f;
@@ -543,17 +626,25 @@ __global__ void __launch_bounds__(MAXT, BLOCKS) residual_norm_grad_kernel(const 
        row0 += (long long)gridDim.x * a.rows) {
     const int rows = (int)(a.M - row0 < a.rows ? a.M - row0 : a.rows);
     const int n = rows * d;
+    const T *in_tile[5];
 #pragma unroll
     for (int k = 0; k < 5; ++k) {
+      in_tile[k] = tile[k];
       if (!src[k]) continue;
       const T *from = src[k] + row0 * d;
-      // a tile's rows are one run of memory, on a 16-byte boundary (a.flat)
-      // or not; its last elements may not fill 16 bytes
+      // a tile's rows are one run of memory; it stands as far behind a 16-byte
+      // boundary in shared memory as there, so that all but its ends moves 16
+      // bytes at a time
       constexpr int W = 16 / sizeof(T);
-      const int whole = a.flat ? n / W * W : 0;
-      for (int i = t * W; i < whole; i += threads * W) cp_async16(tile[k] + i, from + i);
-      for (int i = whole + t; i < n; i += threads) tile[k][i] = from[i];
+      const int skew = VEC ? 0 : (int)(reinterpret_cast<uintptr_t>(from) % 16 / sizeof(T));
+      T *to = tile[k] + skew;
+      in_tile[k] = to;
+      const int head = min((W - skew) % W, n), whole = head + (n - head) / W * W;
+      for (int i = head + t * W; i < whole; i += threads * W) cp_async16(to + i, from + i);
+      if (t < head) to[t] = from[t];
+      for (int i = whole + t; i < n; i += threads) to[i] = from[i];
     }
+    const TileRows<T> rows_in = {in_tile[0], in_tile[1], in_tile[2], in_tile[3], in_tile[4], ng, kp};
     cp_async_wait();
     __syncthreads();
     // ---- one warp a row: its sums
@@ -1039,8 +1130,14 @@ cudaError_t forward(const Args &a, cudaStream_t stream) {
   const int chunks = (a.d + 255) / 256;
   const bool params = aligned16(a.norm_g) && aligned16(a.norm_b) && aligned16(a.post_g) &&
                       aligned16(a.post_b) && aligned16(a.scale);
-  if (!vectors(a, sizeof(T)) || !params || chunks > 8)
-    return launch_pdl(residual_norm_any_kernel<T>, grid, block, 0, stream, a);
+  const bool vec = vectors(a, sizeof(T)) && params;
+  if (!vec || chunks > 8) {
+    const unsigned threads = a.d <= 256 ? 128 : (unsigned)((a.d + 255) / 256 * 32);
+    const long long rows = a.d <= 256 ? (a.M + 3) / 4 : a.M;
+    const dim3 any((unsigned)(rows < 0x7fffffff ? rows : 0x7fffffff)), of(threads);
+    return vec ? launch_pdl(residual_norm_any_kernel<T, true>, any, of, 0, stream, a)
+               : launch_pdl(residual_norm_any_kernel<T, false>, any, of, 0, stream, a);
+  }
   switch (chunks) {
     case 1: return launch_pdl(residual_norm_kernel<T, 1>, grid, block, 0, stream, a);
     case 2: return launch_pdl(residual_norm_kernel<T, 2>, grid, block, 0, stream, a);
@@ -1103,16 +1200,14 @@ cudaError_t backward(Args &a, int num_sms, int *blocks_out, cudaStream_t stream)
   // few rows in all: spread them over the blocks that fit the SMs
   const long long even = (a.M + 4LL * num_sms - 1) / (4LL * num_sms);
   if (rows > even) rows = even;
-  // rows of odd widths: as many as keep the tiles on 16-byte boundaries
+  // rows of odd widths: up to as many as leave every tile on 16-byte boundaries
+  // (16384 x 767: 128 us for 141 in bf16, 146 for 188 in fp32)
   const long long unit = 16 / (int)sizeof(T);
   if (!VEC && rows >= unit / 2 && (rows + unit - 1) / unit * unit * (long long)row <= 160 * 1024)
     rows = (rows + unit - 1) / unit * unit;
-  a.flat = rows * a.d * (long long)sizeof(T) % 16 == 0;
-  for (const void *p : {a.h, a.y, a.gate, a.dr, a.dn}) a.flat = a.flat && aligned16(p);
   a.rows = (int)rows;
   a.subsets = s.subsets;
-  const size_t pitch = ((size_t)rows * a.d * sizeof(T) + 15) / 16 * 16;
-  const size_t smem = pitch * arrays + (size_t)((a.d + 3) / 4 * 4) * 8 + rows * sizeof(RowSums);
+  const size_t smem = tile_pitch<T, VEC>(rows, a.d) * arrays + (size_t)((a.d + 3) / 4 * 4) * 8 + rows * sizeof(RowSums);
   const long long tiles = (a.M + rows - 1) / rows;
   long long per_sm = (long long)(224 * 1024 / (smem + 1024));
   if (per_sm > 2048 / s.threads) per_sm = 2048 / s.threads;

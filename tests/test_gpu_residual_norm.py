@@ -212,6 +212,21 @@ def test_unaligned_arrays(dtype):
     check_backward(p)
 
 
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("M,d,offset", [(300, 1501, 0), (9, 8191, 0), (6, 8192, 0), (70, 4104, 0),
+                                        (70, 4104, 3), (5, 250, 1), (1300, 255, 0), (40, 2052, 0)])
+def test_wide_and_odd_rows(M, d, offset, dtype):
+    """Forms of eight columns a thread, tiles that start anywhere in memory."""
+    for post, norm in (("layer", "scale"), ("scale", "layer")):
+        p = Problem(M, d, dtype, post, norm, True, True, 17, offset=offset)
+        check_forward(p)
+        check_backward(p)
+    r, n = bd.residual_norm(p.h, p.y, **p.call)
+    h, y = p.h.clone(), p.y.clone()
+    bd.residual_norm(h, y, out_r=h, out_n=y, **p.call)
+    assert torch.equal(h, r) and torch.equal(y, n)
+
+
 def test_rows_far_from_zero():
     """Means 1000 spreads away from zero: the squares around the mean are
     taken after it, so nothing is lost but the inputs' own digits."""
