@@ -1339,7 +1339,8 @@ cudaError_t run_few(const XentProblem &q) {
   const dim3 grid(a.blocks), block(256);
   auto go = [&](auto kernel, auto join, int nt) {
     const size_t smem = (size_t)nt * q.d * sizeof(float);
-    if (smem > 48 * 1024) {
+    // 48 KB are there unasked, for the tokens and the kernel's own array together
+    if (smem + 8 * nt * sizeof(float2) > 48 * 1024) {
       const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                  kXentFewSmem);
       if (e != cudaSuccess) return e;

@@ -385,3 +385,14 @@ def test_refusals():
         bd.xent(X, W, y, workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
     with pytest.raises(bd.FlashGauError):
         bd.xent(X[:0], W, y[:0])
+
+
+@pytest.mark.parametrize("dtype,N,d", [("fp32", 8, 1536), ("fp32", 5, 1524), ("fp32", 8, 1540),
+                                       ("fp32", 8, 2048), ("bf16", 2, 6136), ("bf16", 2, 6144),
+                                       ("fp32", 2, 6144), ("bf16", 1, 12288), ("fp32", 1, 12276),
+                                       ("bf16", 1, 12296), ("bf16", 1, 16384), ("bf16", 4, 4096)])
+def test_few_tokens_at_every_width(dtype, N, d):
+    """The tokens fill shared memory up to and past what a kernel may have
+    without asking for it, beside what it keeps there itself."""
+    X, W, y = make(N, d, 70, dtype, N + d, ignored=0.0)
+    check(X, W, y, got=bd.xent(X, W, y, grad=False))
