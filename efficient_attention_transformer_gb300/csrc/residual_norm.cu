@@ -719,9 +719,12 @@ __global__ void __launch_bounds__(MAXT, BLOCKS) residual_norm_grad_kernel(const 
           acc[kPostG][g].b = fma2(dpb, ub, acc[kPostG][g].b);
           acc[kPostB][g].a = add2(dpa, acc[kPostB][g].a);
           acc[kPostB][g].b = add2(dpb, acc[kPostB][g].b);
-          store4<VEC>(static_cast<T *>(a.dy) + out, c, stride, d,
-                      F4{mul2(i, fma2(ua, by, fma2(dpa, pg.a, ay))),
-                         mul2(i, fma2(ub, by, fma2(dpb, pg.b, ay)))});
+          // without a norm dy is dp: y, which may hold anything, has no part in it
+          F4 dy = {dpa, dpb};
+          if (a.post)
+            dy = {mul2(i, fma2(ua, by, fma2(dpa, pg.a, ay))),
+                  mul2(i, fma2(ub, by, fma2(dpb, pg.b, ay)))};
+          store4<VEC>(static_cast<T *>(a.dy) + out, c, stride, d, dy);
         }
       }
     }
@@ -976,8 +979,10 @@ residual_norm_grad_rows_kernel(const Args a) {
         if (PS) as = {fma2(p.a, gt.a, as.a), fma2(p.b, gt.b, as.b)};
         ag = {fma2(x[j].a, u.a, ag.a), fma2(x[j].b, u.b, ag.b)};
         if (PS == 2) ab = {add2(ab.a, x[j].a), add2(ab.b, x[j].b)};
-        const F4 dy = {mul2(iy, fma2(u.a, by, fma2(x[j].a, g.a, ay))),
-                       mul2(iy, fma2(u.b, by, fma2(x[j].b, g.b, ay)))};
+        F4 dy = {mul2(iy, fma2(u.a, by, fma2(x[j].a, g.a, ay))),
+                 mul2(iy, fma2(u.b, by, fma2(x[j].b, g.b, ay)))};
+        // without a norm dy is dp: y, which may hold anything, has no part in it
+        if (PS != 2 && !a.post) dy = x[j];
         if (c0 + 128 * j < d) {
           store4<true>(static_cast<T *>(a.dy) + out + 128 * j, 0, 0, d, dy);
           if (a.dgate)

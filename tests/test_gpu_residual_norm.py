@@ -357,3 +357,24 @@ def test_refusals():
     with pytest.raises(bd.FlashGauError):
         empty = torch.zeros(0, 16, dtype=torch.bfloat16, device="cuda")
         bd.residual_norm(empty, None, norm=bd.NORM_SCALE, norm_g=torch.ones(1, device="cuda"))
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("M,d", [(9, 200), (9, 768), (5, 2048), (7, 513), (3, 4096), (3, 5000)])
+@pytest.mark.parametrize("norm", ["none", "layer"])
+def test_gradient_of_y_without_a_norm_does_not_read_y(M, d, norm, dtype):
+    """dy = dh scale gate, whatever y holds: infinities and NaN reach the
+    gradients that are formed of y, at their own places."""
+    p = Problem(M, d, dtype, "none", norm, True, True, 21)
+    dn = p.dn if norm != "none" else None
+    clean = bd.residual_norm_backward(p.dr, dn, p.h, p.y, **p.call)
+    p.y[0, 3], p.y[1, d - 1], p.y[2, 0] = float("inf"), float("nan"), -float("inf")
+    got = bd.residual_norm_backward(p.dr, dn, p.h, p.y, **p.call)
+    for k in ("dh", "dy"):
+        assert torch.equal(got[k], clean[k]), k
+    bad = ~torch.isfinite(p.y)
+    assert not torch.isfinite(got["dgate"][bad]).any()
+    assert torch.equal(got["dgate"][~bad], clean["dgate"][~bad])
+    cols = bad.any(0)
+    assert not torch.isfinite(got["dscale"][cols]).any()
+    assert torch.equal(got["dscale"][~cols], clean["dscale"][~cols])
