@@ -868,6 +868,11 @@ __device__ __forceinline__ float row_loss(float top, float sum, float t2, float 
   *z = exp2f(t2 - top) + sum;
   return logf(*z) + (top - t2) * kLn2;
 }
+// and its log sum exp: from the loss only where that is relative to the
+// label's logit, which may be minus infinity elsewhere
+__device__ __forceinline__ float row_lse(float top, float t2, float z, float loss) {
+  return top == t2 ? fmaf(t2, kLn2, loss) : fmaf(top, kLn2, logf(z));
+}
 
 // A row's E from its parts' references to the row's, by the whole block, but
 // for the label's.  Only rows with a logit 40 above the label's need it
@@ -978,7 +983,7 @@ __global__ void __launch_bounds__(256) xent_rows_kernel(const RowArgs a) {
       __nv_bfloat16 *E = static_cast<__nv_bfloat16 *>(a.L.E) + (size_t)row * terms * a.L.ldE;
       if (lane == 0) {
         a.loss[token] = loss;
-        if (a.lse) a.lse[token] = fmaf(ref, kLn2, loss);
+        if (a.lse) a.lse[token] = row_lse(top, ref, z, loss);
       }
       if (a.grad) {
         if constexpr (sizeof(T) == 2) {
@@ -1285,7 +1290,7 @@ __global__ void __launch_bounds__(256) xent_few_join_kernel(const FewArgs a) {
       }
       float z;
       loss = row_loss(t, s, t2, &z);
-      lse = fmaf(t2, kLn2, loss);
+      lse = row_lse(t, t2, z, loss);
     }
     losses[n] = loss;
     a.loss[n] = loss;

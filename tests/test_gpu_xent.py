@@ -396,3 +396,18 @@ def test_few_tokens_at_every_width(dtype, N, d):
     without asking for it, beside what it keeps there itself."""
     X, W, y = make(N, d, 70, dtype, N + d, ignored=0.0)
     check(X, W, y, got=bd.xent(X, W, y, grad=False))
+
+
+@pytest.mark.parametrize("N", [3, 20])
+def test_lse_beside_a_label_at_minus_infinity(N):
+    """The label's own logit at minus infinity: an infinite loss, and the
+    normaliser is the other words'."""
+    X, W, y = make(N, 64, 300, "bf16", 17, ignored=0.0)
+    X[:, 0] = 1.0
+    y.fill_(17)
+    W[17, 0] = -float("inf")
+    want = torch.logsumexp((X.double() @ W.double().t()), 1)
+    got = bd.xent(X, W, y, grad=False)
+    assert bool((got["loss"] == float("inf")).all())
+    # sums of 300 terms and logits below 10 of 64 products each
+    assert float((got["lse"] - want).abs().max()) <= 1e-4
