@@ -80,9 +80,17 @@ constexpr float kRaise = 40.0f * kLog2e;  // how far above the label's logit E i
 
 // kLoss: the logits' product, sums only; kProbs: sums and E; kDX: E W as
 // fp32 parts; kDW: E^T X', stored in bf16, or in fp32, or added to fp32
-// (kProbs3: E as three terms)
-enum Epi { kLoss, kProbs, kProbs3, kDX, kDW };
-constexpr bool is_logits(int epi) { return epi == kLoss || epi == kProbs || epi == kProbs3; }
+// (kLoss3, kProbs3: of fp32 io, E as three terms)
+enum Epi { kLoss, kProbs, kLoss3, kProbs3, kDX, kDW };
+constexpr bool is_logits3(int epi) { return epi == kLoss3 || epi == kProbs3; }
+constexpr bool is_logits(int epi) { return epi == kLoss || epi == kProbs || is_logits3(epi); }
+
+// fp32 io adds up a tile's logits over several works (see kFp32Blocks): an
+// epilogue thread's 128 of them, 64 in registers and 64 in shared memory, in
+// the place of the ring's last two stages.
+constexpr int kSumColumns = 64;
+constexpr int stages_of(int epi) { return is_logits3(epi) ? STAGES - 2 : STAGES; }
+static_assert(EPI_WARPS * kSumColumns * 32 * sizeof(float) == 2 * STAGE_BYTES, "sums of the logits");
 
 constexpr int kTerms = 3, kProducts = 6;  // of an fp32 value; of two
 
@@ -175,17 +183,20 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
 struct Work {
   int rp, n0, nsz;
   int k0, k1;
-  int part;  // kDX: where the result goes
-  bool add;  // it adds to what the work before has stored there
+  int part;   // kDX: where the result goes
+  bool add;   // it adds to what the work before has left there
+  bool last;  // of this product, or share of one
 };
 // The tensor cores cut off what an accumulator cannot hold at each step, so
 // a long sum comes out short, by 6e-8 of itself a k-block (fp32 io, 1400
-// k-blocks: 8e-5).  With fp32 io the large product of a gradient's sum is
-// therefore taken in works of few k-blocks, which add up in memory; the five
-// small products before it lose nothing that counts and go into its first
+// k-blocks: 8e-5).  With fp32 io the large product of a sum is therefore
+// taken in works of few k-blocks, which add up in memory (gradients) or in
+// the epilogue's registers (logits); the five small products before it lose
+// nothing that counts and go into its first
 // (1001 tokens, 8003 words, d = 520, errors of dX and dW: 16 k-blocks 1.4e-6
 // and 1.1e-6 in 201 us, 8 0.8e-6 and 0.6e-6 in 219 us, 4 0.4e-6 and 0.3e-6 in
-// 280 us).
+// 280 us; the logits in works of 8 too, whose error grows with d otherwise,
+// 2% more).
 constexpr int kFp32Blocks = 8;
 
 // The works of one pair, in order.  Every role of the kernel walks the same.
@@ -212,7 +223,7 @@ struct Walk {
     row_pairs = (M + 2 * BM - 1) / (2 * BM);
     const int K = EPI == kDW ? tokens : p.K;
     steps = p.products * ((K + BK - 1) / BK);
-    large = p.products == 1 || is_logits(EPI) ? 0x7fffffff : steps / p.products * (p.products - 1);
+    large = p.products == 1 ? 0x7fffffff : steps / p.products * (p.products - 1);
     if (EPI == kDX) {
       dx = dx_plan(tokens, p.N, p.K, p.products, kPlanPairs);
       round = run_pos = run_end = 0;
@@ -280,6 +291,7 @@ struct Walk {
     w.k1 = end;
     if (end > large) w.k1 = min(end, max(pos, large) + kFp32Blocks);
     pos = w.k1;
+    w.last = pos == end;
     // a multiple of 128: each CTA holds whole 64-column boxes; the logits'
     // sums are kept by 128 words, so their tiles are never narrower
     w.nsz = is_logits(EPI) ? BN : min(BN, (p.N - n0 + 127) / 128 * 128);
@@ -328,6 +340,7 @@ xent_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                  const __grid_constant__ CUtensorMap tmC, const Params p) {
   constexpr bool A_MN = EPI == kDW;                     // E read by columns
   constexpr bool B_KM = is_logits(EPI);                 // W read by rows
+  constexpr int kStages = stages_of(EPI);
   extern __shared__ uint8_t smem_raw[];
   uint8_t *tiles = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -337,7 +350,7 @@ xent_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
   const bool leader = rank == 0;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < STAGES; ++i) {
+    for (int i = 0; i < kStages; ++i) {
       mbar_init(smem_u32(&sm->full[i]), 1);
       mbar_init(smem_u32(&sm->empty[i]), 1);
     }
@@ -403,7 +416,7 @@ xent_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
               tma_load_2d_pair(smem_u32(sB + j * BOX_BYTES), &tmB, full_leader,
                                tb + x.n0 + rank * half + j * 64, k);
           }
-          if (++stage == STAGES) {
+          if (++stage == kStages) {
             stage = 0;
             phase ^= 1;
           }
@@ -445,7 +458,7 @@ xent_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                             desc_advance(db, k * (B_KM ? 32 : 2048)), idesc,
                             s != x.k0 || k != 0);
           mma_commit_pair_mc(smem_u32(&sm->empty[stage]), kPair);
-          if (++stage == STAGES) {
+          if (++stage == kStages) {
             stage = 0;
             phase ^= 1;
           }
@@ -465,6 +478,11 @@ xent_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
     const int half = (warp - 2) >> 2;
     Stager st{tiles + STAGES * STAGE_BYTES + (warp - 2) * STG_BYTES, lane};
     int local = 0;
+    // fp32 io: this row's 128 logits, a work's share added to those before;
+    // column c of the second 64 at far[32 c]
+    float near[is_logits3(EPI) ? 2 : 1][32];
+    float *const far = reinterpret_cast<float *>(tiles + kStages * STAGE_BYTES) +
+                       (warp - 2) * kSumColumns * 32 + lane;
     for (; !sm->abort_flag && walk.next(x); ++local) {
       const int acc = local & 1;
       const int row0 = (x.rp * 2 + rank) * BM + quarter * 32, row = row0 + lane;
@@ -494,31 +512,59 @@ xent_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
         const bool whole = x.n0 + c_end <= p.N;  // every column is a word
         // the largest logit of this row's 128 words
         float top = -INFINITY;
-        for (int c0 = c_begin; c0 < c_end; c0 += 32) {
-          uint32_t v[32];
-          tmem_ld32(taddr + c0, v);
-          tmem_ld_wait();
+        auto largest = [&](int c, const auto &l) {
           if (whole) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) top = fmaxf(top, __uint_as_float(v[j]));
+            for (int j = 0; j < 32; ++j) top = fmaxf(top, l(j));
           } else {
 #pragma unroll
             for (int j = 0; j < 32; ++j)
-              if (x.n0 + c0 + j < p.N) top = fmaxf(top, __uint_as_float(v[j]));
+              if (x.n0 + c + j < p.N) top = fmaxf(top, l(j));
+          }
+        };
+        if constexpr (is_logits3(EPI)) {
+#pragma unroll
+          for (int h = 0; h < 4; ++h) {
+            uint32_t v[32];
+            tmem_ld32(taddr + c_begin + 32 * h, v);
+            tmem_ld_wait();
+            if (h == 3) drained();
+            auto sums = [&](int j) -> float & { return h < 2 ? near[h & 1][j] : far[32 * (32 * (h - 2) + j)]; };
+            float l[32];
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              l[j] = __uint_as_float(v[j]);
+              if (x.add) l[j] += sums(j);
+              sums(j) = l[j];
+            }
+            if (x.last) largest(c_begin + 32 * h, [&](int j) { return l[j]; });
+          }
+          if (!x.last) continue;
+        } else {
+          for (int c0 = c_begin; c0 < c_end; c0 += 32) {
+            uint32_t v[32];
+            tmem_ld32(taddr + c0, v);
+            tmem_ld_wait();
+            largest(c0, [&](int j) { return __uint_as_float(v[j]); });
           }
         }
         top *= kLog2e;
         if (top > ref + kRaise) ref = top;
         float sum[4] = {0.f, 0.f, 0.f, 0.f};
-        // 32 exponentials of this row from column c on, summed up
+        // 32 exponentials of this row from column c on, summed up; fp32 io: in
+        // their logits' place
         auto exps = [&](int c, float (&e)[32]) {
-          uint32_t v[32];
-          tmem_ld32(taddr + c, v);
-          tmem_ld_wait();
-          if (c + 32 >= c_end) drained();
+          if constexpr (!is_logits3(EPI)) {
+            uint32_t v[32];
+            tmem_ld32(taddr + c, v);
+            tmem_ld_wait();
+            if (c + 32 >= c_end) drained();
+#pragma unroll
+            for (int j = 0; j < 32; ++j) e[j] = __uint_as_float(v[j]);
+          }
           const int col = x.n0 + c;
 #pragma unroll
-          for (int j = 0; j < 32; ++j) e[j] = exp2_approx(fmaf(__uint_as_float(v[j]), kLog2e, -ref));
+          for (int j = 0; j < 32; ++j) e[j] = exp2_approx(fmaf(e[j], kLog2e, -ref));
           if (!whole) {
 #pragma unroll
             for (int j = 0; j < 32; ++j)
@@ -539,30 +585,40 @@ xent_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
         };
         // Boxes wholly behind an edge are not stored; rows behind the last one
         // are, as zeros: the products that follow read whole tiles.
-        for (int c0 = c_begin; c0 < c_end; c0 += 64) {
-          const bool stored = EPI != kLoss && x.n0 + c0 < p.N;
-          if constexpr (EPI == kProbs3) {
-            float e[2][32];
-            exps(c0, e[0]);
-            exps(c0 + 32, e[1]);
+        if constexpr (is_logits3(EPI)) {
+#pragma unroll 1
+          for (int c0 = c_begin; c0 < c_end; c0 += 64) {
+            if (c0 > c_begin) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) {
+                near[0][j] = far[32 * j];
+                near[1][j] = far[32 * (32 + j)];
+              }
+            }
+            exps(c0, near[0]);
+            exps(c0 + 32, near[1]);
+            const bool stored = EPI == kProbs3 && x.n0 + c0 < p.N;
             for (int term = 0; stored && term < kTerms; ++term) {
               st.begin();
-              put32(st, 0, e[0]);
-              put32(st, 4, e[1]);
+              put32(st, 0, near[0]);
+              put32(st, 4, near[1]);
               st.finish(&tmC, term * p.e_term + x.n0 + c0, row0, false);
 #pragma unroll
               for (int j = 0; j < 32; ++j) {
-                e[0][j] -= __bfloat162float(__float2bfloat16_rn(e[0][j]));
-                e[1][j] -= __bfloat162float(__float2bfloat16_rn(e[1][j]));
+                near[0][j] -= __bfloat162float(__float2bfloat16_rn(near[0][j]));
+                near[1][j] -= __bfloat162float(__float2bfloat16_rn(near[1][j]));
               }
             }
-          } else {
+          }
+        } else {
+          for (int c0 = c_begin; c0 < c_end; c0 += 64) {
+            const bool stored = EPI == kProbs && x.n0 + c0 < p.N;
             if (stored) st.begin();
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               float e[32];
               exps(c0 + 32 * h, e);
-              if (EPI == kProbs && stored) put32(st, 4 * h, e);
+              if (stored) put32(st, 4 * h, e);
             }
             if (stored) st.finish(&tmC, x.n0 + c0, row0, false);
           }
@@ -1419,7 +1475,7 @@ cudaError_t run(const XentProblem &q) {
     p.e_term = (int)L.ldE;
     const long long works = (long long)(whole / (2 * BM)) * ((q.V + BN - 1) / BN);
     err = grad ? launch_gemm<bf16 ? kProbs : kProbs3>(tX, tW, tE, p, works, q.num_sms, q.stream)
-               : launch_gemm<kLoss>(tX, tW, tE, p, works, q.num_sms, q.stream);
+               : launch_gemm<bf16 ? kLoss : kLoss3>(tX, tW, tE, p, works, q.num_sms, q.stream);
     if (err != cudaSuccess) return err;
     RowArgs r = {};
     r.L = L;

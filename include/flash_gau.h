@@ -376,7 +376,10 @@ int flash_gau_rope_toeplitz_bias(const float *a, const float *b, int m, int C,
  * [tokens, V] in the workspace (or 256 tokens).  The products run on the tensor cores with
  * fp32 accumulation and sums; bf16: the exponentials enter the gradients'
  * products rounded to bf16; fp32: operands enter as three bf16 terms and a
- * product as six of theirs, so that what is left out is below 2^-24 of it.  */
+ * product as six of theirs, so that what is left out is below 2^-24 of it,
+ * and the large one's sums are taken 512 terms at a time, the shares added in
+ * fp32 (values of X and W that are not finite make the logits and gradients
+ * that they enter not finite: with bf16 as the formulas do, with fp32 NaN).  */
 #define FLASH_GAU_MEAN 0
 #define FLASH_GAU_SUM 1
 

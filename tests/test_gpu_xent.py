@@ -411,3 +411,30 @@ def test_lse_beside_a_label_at_minus_infinity(N):
     assert bool((got["loss"] == float("inf")).all())
     # sums of 300 terms and logits below 10 of 64 products each
     assert float((got["lse"] - want).abs().max()) <= 1e-4
+
+
+@pytest.mark.parametrize("grad", [False, True])
+@pytest.mark.parametrize("d", [4096, 8192, 32768])
+def test_fp32_logits_of_wide_rows(d, grad):
+    """Positive terms, whose running sum a tensor core cuts off at each of its
+    d / 16 steps, against a label whose logit is zero exactly: what the others'
+    logits l lose shows in the losses.  In works of n steps that add up in fp32 a
+    step loses under 2^-23 of a sum that grows evenly, (n + 1) / 2 of them for a
+    work's share: 16.5 2^-23 l with the eight k-blocks of four steps each.  The
+    d / 512 works add with roundings of 2^-24 of a sum that grows too, d / 1024
+    2^-24 l in all; the five small products before them are under 2^-8 of l
+    together, and lose 5 d / 32 2^-23 of that.  Then 2^-21 for an exponential,
+    4 u l log2 e for its argument, and (40 + V / 256) u for the sum."""
+    g = torch.Generator().manual_seed(d)
+    N, V = 40, 300
+    X = (torch.rand(N, d, generator=g) / 2 + 0.5).cuda()
+    W = (torch.rand(V, d, generator=g) / 2 + 0.5).mul_(40.0 / d).cuda()
+    W[17] = 0.0
+    y = torch.full((N,), 17, dtype=torch.int32, device="cuda")
+    got = bd.xent(X, W, y, grad=grad)
+    l = X.double() @ W.double().t()
+    err = float((got["loss"] - torch.logsumexp(l, 1)).abs().max())
+    top = float(l.max())
+    lost = (16.5 * 2 + d / 1024 + 5 * d / 16 * 2.0 ** -8) * U
+    limit = lost * top + 2.0 ** -21 + 4 * U * 1.4427 * top + (40 + V / 256) * U + 2 * U * top
+    assert err <= limit, (err, limit)
