@@ -784,9 +784,9 @@ class AdamW:
     weight_decay: one value, or one for each tensor.  state_bits: 32 (fp32
     moments) or 8 (codes with a scale for each 256 elements).  m, v, m_scale,
     v_scale: lists of existing moments (a checkpoint's) in place of zeros;
-    they are updated in place.  All of them are held by their memory: it is
-    not to be replaced (an assignment to .data; step refuses it for the
-    parameters)."""
+    they are updated in place.  All of them are held by the memory they have
+    here, which the handle keeps: what is put into its lists later, or into a
+    tensor's .data, is not taken (step refuses it for the parameters)."""
 
     def __init__(self, params, copies=None, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.0,
                  state_bits=32, m=None, v=None, m_scale=None, v_scale=None):
@@ -836,6 +836,10 @@ class AdamW:
         begin, end = np.array(begin, dtype=np.uint64)[order], np.array(end, dtype=np.uint64)[order]
         if (end[:-1] > begin[1:]).any():
             raise ValueError("the tensors' parameters, copies and moments must not overlap")
+        # the kernels go by address, so the memory stays here whatever becomes of
+        # the lists and tensors
+        self._held = [t.untyped_storage() for _, tensors, _, _ in kinds for t in tensors
+                      if t is not None]
         # the columns that change from step to step
         self._g, self._g_dtype = columns["g"], columns["g_dtype"]
         self.hyper = AdamWHyper(0.0, float(betas[0]), float(betas[1]), float(eps), 0, state_bits,

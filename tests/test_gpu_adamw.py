@@ -300,3 +300,22 @@ def test_refusals():
     with pytest.raises(bd.FlashGauError):
         opt.step([p], lr=LR)                                 # the parameter as its gradient
     assert opt.steps == 0
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+def test_lists_that_are_changed_keep_their_memory(bits):
+    """A handle's lists are read when it is made: what is put into them later
+    is not taken, and the memory of what was there stays the handle's."""
+    p = torch.zeros(3 << 20, device="cuda")
+    opt = bd.AdamW([p], copies=[torch.zeros(3 << 20, dtype=torch.bfloat16, device="cuda")],
+                   state_bits=bits)
+    kinds = ("m", "v", "copies") + (("m_scale", "v_scale") if bits == 8 else ())
+    for k in kinds:
+        old = getattr(opt, k)[0]
+        at, like = old.data_ptr(), torch.zeros_like(old)
+        if k == "v":
+            old.data = like
+        del old
+        getattr(opt, k)[0] = like
+        others = [torch.empty_like(like) for _ in range(8)]
+        assert at not in [t.data_ptr() for t in others], k
