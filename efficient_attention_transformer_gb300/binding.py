@@ -783,10 +783,12 @@ class AdamW:
     values (the weights that a bf16 layer reads), or None; None: no copies.
     weight_decay: one value, or one for each tensor.  state_bits: 32 (fp32
     moments) or 8 (codes with a scale for each 256 elements).  m, v, m_scale,
-    v_scale: lists of existing moments (a checkpoint's) in place of zeros;
-    they are updated in place.  All of them are held by the memory they have
-    here, which the handle keeps: what is put into its lists later, or into a
-    tensor's .data, is not taken (step refuses it for the parameters)."""
+    v_scale: lists of existing moments (a checkpoint's) in place of zeros, m
+    and v together, with 8 bits all four (memory for codes, all of them zero,
+    may come without scales); they are updated in place.  All of them are
+    held by the memory they have here, which the handle keeps: what is put
+    into its lists later, or into a tensor's .data, is not taken (step refuses
+    it for the parameters)."""
 
     def __init__(self, params, copies=None, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.0,
                  state_bits=32, m=None, v=None, m_scale=None, v_scale=None):
@@ -808,6 +810,10 @@ class AdamW:
         blocks = (lambda n: -(-n // 256))
         self.m, self.v = made(m, md), made(v, vd)
         eight = state_bits == 8
+        if (m is None) != (v is None) or (m_scale is None) != (v_scale is None):
+            raise ValueError("existing moments are m and v together, and their scales both")
+        if m_scale is not None and (m is None or not eight):
+            raise ValueError("scales belong to existing 8-bit moments")
         self.m_scale = made(m_scale, f32, blocks) if eight else [None] * k
         self.v_scale = made(v_scale, f32, blocks) if eight else [None] * k
         lists = (self.copies, decay, self.m, self.v, self.m_scale, self.v_scale)
@@ -836,6 +842,8 @@ class AdamW:
         begin, end = np.array(begin, dtype=np.uint64)[order], np.array(end, dtype=np.uint64)[order]
         if (end[:-1] > begin[1:]).any():
             raise ValueError("the tensors' parameters, copies and moments must not overlap")
+        if eight and m is not None and m_scale is None and any(t.any() for t in self.m + self.v):
+            raise ValueError("8-bit moments that are not zero need their scales")
         # the kernels go by address, so the memory stays here whatever becomes of
         # the lists and tensors
         self._held = [t.untyped_storage() for _, tensors, _, _ in kinds for t in tensors

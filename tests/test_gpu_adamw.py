@@ -319,3 +319,34 @@ def test_lists_that_are_changed_keep_their_memory(bits):
         getattr(opt, k)[0] = like
         others = [torch.empty_like(like) for _ in range(8)]
         assert at not in [t.data_ptr() for t in others], k
+
+
+def test_8bit_moments_come_whole():
+    """Codes and scales of a checkpoint belong together: parts of them are
+    refused (codes that are all zero need no scales), and a handle made of
+    copies of all four carries on bit for bit."""
+    params, grads = make([700, 3], torch.float32, 60)
+    a = bd.AdamW(params, state_bits=8, **HYPER)
+    a.step(grads[0], lr=LR)
+    twin = [p.clone() for p in params]
+    kinds = ("m", "v", "m_scale", "v_scale")
+    state = {k: [t.clone() for t in getattr(a, k)] for k in kinds}
+    b = bd.AdamW(twin, state_bits=8, **state, **HYPER)
+    b.steps = a.steps
+    a.step(grads[1], lr=LR)
+    b.step(grads[1], lr=LR)
+    for x, y in zip(params, twin):
+        assert torch.equal(x, y)
+    for k in kinds:
+        for x, y in zip(getattr(a, k), getattr(b, k)):
+            assert torch.equal(x, y), k
+    for left_out in (("m_scale", "v_scale"), ("m", "v"), ("m",), ("v",), ("m_scale",), ("v_scale",),
+                     ("v", "v_scale"), ("m", "m_scale")):
+        part = {k: x for k, x in state.items() if k not in left_out}
+        with pytest.raises(ValueError):
+            bd.AdamW([p.clone() for p in params], state_bits=8, **part)
+    full = [torch.zeros(p.shape, device="cuda") for p in params]
+    for part in (dict(m=full), dict(v=full), dict(m=full, v=[t.clone() for t in full],
+                                                  m_scale=state["m_scale"])):
+        with pytest.raises(ValueError):
+            bd.AdamW([p.clone() for p in params], **part)
