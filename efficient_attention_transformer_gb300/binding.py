@@ -906,9 +906,12 @@ class AdamW:
             if out is not None and len(out) != k:
                 raise ValueError("%s must hold a tensor like each parameter" % name)
         if self.state_bits == 32:
+            for name, out in (("out_m", out_m), ("out_v", out_v)):
+                for o, p in zip(out or [], self._shapes):
+                    _like(o, name, p, torch.float32, dev.index)
             for src, out in ((self.m, out_m), (self.v, out_v)):
                 for a, b in zip(src, out or []):
-                    b.copy_(a)
+                    b.copy_(a.view(b.shape))
             return out_m or self.m, out_v or self.v
         out_m = out_m or [torch.empty_like(p) for p in self.params]
         out_v = out_v or [torch.empty_like(p) for p in self.params]

@@ -350,3 +350,15 @@ def test_8bit_moments_come_whole():
                                                   m_scale=state["m_scale"])):
         with pytest.raises(ValueError):
             bd.AdamW([p.clone() for p in params], **part)
+
+
+def test_moments_of_32_bits_check_their_lists():
+    p = torch.zeros(8, 40, device="cuda")
+    opt = bd.AdamW([p])
+    good = [torch.empty(8, 40, device="cuda")]
+    for bad in (torch.empty(8, 40, device="cuda", dtype=torch.bfloat16), torch.empty(2, 8, 40, device="cuda"),
+                torch.empty(8, 40), torch.empty(40, 8, device="cuda").t()):
+        with pytest.raises(ValueError):
+            opt.moments([bad], good)
+        with pytest.raises(ValueError):
+            opt.moments(good, [bad])
