@@ -730,6 +730,9 @@ def xent_workspace_bytes(N, d, V, dtype, grad=True):
     return n
 
 
+_XENT_OUT = ("total", "loss", "lse", "dX", "dW")
+
+
 def xent(X, W, labels, reduction=MEAN, scale=1.0, grad=True, out=None, workspace=None,
          stream=None):
     """Cross entropy of softmax(X W^T) at the labels, through flash_gau_xent:
@@ -737,7 +740,10 @@ def xent(X, W, labels, reduction=MEAN, scale=1.0, grad=True, out=None, workspace
     dX and dW, the gradients of total in the io type.  X: [..., d], W: [V, d],
     labels: int32, X's leading shape; a label outside [0, V) leaves its token
     out.  total is scale times the MEAN over the labelled tokens or the SUM.
-    `out`: tensors to write to, by the same names."""
+    `out`: tensors to write to, by the same names (dX and dW are not looked
+    at without grad).  workspace: of xent_workspace_bytes; workspace_status
+    reads from it whether a kernel's wait timed out, which nothing shows where
+    the call makes its own."""
     io, dev = X.dtype, X.device
     dt, xp, at = dtype_code(io), _dev_ptr(X, "X"), dev.index
     lead = labels.shape
@@ -751,6 +757,8 @@ def xent(X, W, labels, reduction=MEAN, scale=1.0, grad=True, out=None, workspace
             return xent(X, W, labels, reduction, scale, grad, out, workspace)
     f32 = torch.float32
     out, ptrs = dict(out) if out else {}, []
+    if not out.keys() <= set(_XENT_OUT):
+        raise ValueError("out holds %s only" % ", ".join(_XENT_OUT))
     for name, like, dtype in (("total", None, f32), ("loss", labels, f32), ("lse", labels, f32),
                               ("dX", X, io), ("dW", W, io))[:5 if grad else 3]:
         t = out.get(name)

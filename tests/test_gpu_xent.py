@@ -438,3 +438,11 @@ def test_fp32_logits_of_wide_rows(d, grad):
     lost = (16.5 * 2 + d / 1024 + 5 * d / 16 * 2.0 ** -8) * U
     limit = lost * top + 2.0 ** -21 + 4 * U * 1.4427 * top + (40 + V / 256) * U + 2 * U * top
     assert err <= limit, (err, limit)
+
+
+def test_outputs_of_other_names_are_refused():
+    X, W, y = make(10, 64, 100, "bf16", 19)
+    with pytest.raises(ValueError):
+        bd.xent(X, W, y, out=dict(dx=torch.empty_like(X)))
+    with pytest.raises(ValueError):
+        bd.xent(X, W, y, grad=False, out=dict(losses=torch.empty(10, device="cuda")))
