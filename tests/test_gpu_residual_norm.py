@@ -378,3 +378,33 @@ def test_gradient_of_y_without_a_norm_does_not_read_y(M, d, norm, dtype):
     cols = bad.any(0)
     assert not torch.isfinite(got["dscale"][cols]).any()
     assert torch.equal(got["dscale"][~cols], clean["dscale"][~cols])
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("post,norm", list(itertools.product(KIND, KIND)))
+@pytest.mark.parametrize("gate,scale", [(False, False), (True, False), (False, True), (True, True)])
+@pytest.mark.parametrize("d", [512, 768, 1024, 1536])
+def test_options_of_several_warps_a_row(d, post, norm, gate, scale, dtype):
+    """The row form at the widths that two and four warps share, few rows."""
+    p = Problem(37, d, dtype, post, norm, gate, scale, 12)
+    check_forward(p)
+    check_backward(p)
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("post,norm", list(itertools.product(KIND, KIND)))
+@pytest.mark.parametrize("M,d,on", [(1301, 512, True), (1301, 1024, False), (701, 1536, True),
+                                    (2500, 256, False)])
+def test_options_of_more_rows_than_blocks(M, d, on, post, norm, dtype):
+    p = Problem(M, d, dtype, post, norm, on, on, 13)
+    check_forward(p)
+    check_backward(p)
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("M,d", [(5, 264), (130, 512), (9, 776), (700, 1024), (3, 1280), (6, 256),
+                                 (4, 1288)])
+def test_aligned_widths(M, d, dtype):
+    p = Problem(M, d, dtype, "layer", "layer", True, True, M + d)
+    check_forward(p)
+    check_backward(p)

@@ -446,3 +446,18 @@ def test_outputs_of_other_names_are_refused():
         bd.xent(X, W, y, out=dict(dx=torch.empty_like(X)))
     with pytest.raises(ValueError):
         bd.xent(X, W, y, grad=False, out=dict(losses=torch.empty(10, device="cuda")))
+
+
+@pytest.mark.parametrize("N,d,V,size", [(64, 64, 500, 8.0), (1001, 520, 8003, 1.0)])
+def test_fp32_gradients_take_all_six_products(N, d, V, size):
+    """Relative errors in the 2-norm.  With all six products there is what the
+    sums cut off (under 5e-7 for eight k-blocks) and roundings to fp32 of about
+    2e-7.  Without any one of them it is 2.4e-6 or more in a gradient's product
+    at either size, and without one in the logits' (whose errors the first
+    size's large logits show) 4e-6: each by arithmetic in 64 bits on the split
+    values."""
+    X, W, y = make(N, d, V, "fp32", 18, ignored=0.1, pull=0.0 if size > 1 else 0.2, size=size)
+    got = bd.xent(X, W, y)
+    _, _, dX, dW = reference(X, W, y)
+    near(got["dX"], dX, 1.5e-6)
+    near(got["dW"], dW, 1.5e-6)
