@@ -330,6 +330,7 @@ struct XentLayout {
   void *Ws;          // [V][3][term] bf16: W's terms (fp32)
   long long piece;   // rows of a piece, whole tiles
   float *row_scale;  // [piece] factor / normaliser
+  float *left;       // [piece] what the label's E lost to its rounding (bf16)
   float2 *part;      // [V / 128][piece] (reference, sum) of 128 words
   void *E;           // [piece][terms][ldE] bf16: exp(l - reference)
   long long ldE;

@@ -123,6 +123,7 @@ size_t xent_layout(long long N, int d, int V, int dtype, bool grad, char *base, 
   l.part = reinterpret_cast<float2 *>(take(parts * n * sizeof(float2)));
   if (grad) {
     l.row_scale = reinterpret_cast<float *>(take(n * 4));
+    if (bf16) l.left = reinterpret_cast<float *>(take(n * 4));
     l.E = take(n * terms * l.ldE * 2);
     l.ld_part = (d + 63) / 64 * 64;
     l.dx_part = reinterpret_cast<float *>(take(xent_dx_part_rows(l.piece, d) * l.ld_part * 4));

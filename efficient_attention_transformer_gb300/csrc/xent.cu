@@ -25,8 +25,9 @@
 //   dX_i = (g / Z_i) sum_v E_iv W_v         (scaled when the parts are joined)
 //   dW_v = sum_i E_iv (g / Z_i) x_i         (x scaled and rounded once)
 // Roundings with bf16 io: E, the scaled x, and the results, to bf16.  The
-// label's term outweighs the others, so the row's factor takes its E's
-// rounding out again (and puts that half step on the other words' terms).
+// label's term outweighs the others, so its E's rounding is taken out again:
+// in dX as a multiple of the label's row of W, in dW by the row's factor
+// (which puts that half step on the other words' terms there).
 //
 // All three products run on the 2-SM tcgen05 tiles of the layer's projection
 // (256 x 256 of a CTA pair, 64-deep k-blocks by TMA into a 6-stage ring, two
@@ -1034,7 +1035,7 @@ __global__ void __launch_bounds__(256) xent_rows_kernel(const RowArgs a) {
       mixed = __any_sync(0xffffffffu, mixed);
       float z;
       const float loss = row_loss(top, sum, ref, &z);
-      float scale = factor / z;
+      float scale = factor / z;  // of dX, then of the scaled row
       const int terms = sizeof(T) == 4 ? kTerms : 1;
       __nv_bfloat16 *E = static_cast<__nv_bfloat16 *>(a.L.E) + (size_t)row * terms * a.L.ldE;
       if (lane == 0) {
@@ -1044,17 +1045,21 @@ __global__ void __launch_bounds__(256) xent_rows_kernel(const RowArgs a) {
       if (a.grad) {
         if constexpr (sizeof(T) == 2) {
           const __nv_bfloat16 e = __float2bfloat16_rn(-sum);
-          if (lane == 0) E[label] = e;
-          // its rounding goes into the row's factor
-          if (sum > 0.f && sum < INFINITY) scale *= sum / -__bfloat162float(e);
+          const bool rounded = sum > 0.f && sum < INFINITY;
+          if (lane == 0) {
+            E[label] = e;
+            a.L.row_scale[row] = scale;
+            a.L.left[row] = rounded ? -sum - __bfloat162float(e) : 0.f;
+          }
+          if (rounded) scale *= sum / -__bfloat162float(e);
         } else {
           float t[kTerms];
           split3(-sum, t);
           if (lane < kTerms)
             E[lane * a.L.ldE + label] =
                 __float2bfloat16_rn(lane == 0 ? t[0] : lane == 1 ? t[1] : t[2]);
+          if (lane == 0) a.L.row_scale[row] = scale;
         }
-        if (lane == 0) a.L.row_scale[row] = scale;
         if (a.scaled) {
           __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(a.L.Xc) + (size_t)row * terms * a.L.term;
           if constexpr (sizeof(T) == 2) {
@@ -1112,12 +1117,12 @@ __global__ void __launch_bounds__(256) xent_rows_kernel(const RowArgs a) {
 __device__ __forceinline__ void store_as(float *p, float v) { *p = v; }
 __device__ __forceinline__ void store_as(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
 
-// dX from the parts of its sum, in the groups' order, times the row's factor,
-// to where the row came from; four columns a thread (16384 x 1024 bf16: 31 us).
+// dX from the parts of its sum, in the groups' order, with what the label's
+// term has lost (bf16), times the row's factor, to where the row came from; four columns a thread (16384 x 1024 bf16: 31 us).
 template <typename T>
 __global__ void __launch_bounds__(256)
 xent_join_kernel(const XentLayout L, long long first, int rows, int d, int V, int products,
-                 T *__restrict__ out) {
+                 const T *__restrict__ W, T *__restrict__ out) {
   __shared__ DxPlan q;
   griddep_wait();
   const long long left = *L.live - first;
@@ -1147,6 +1152,12 @@ xent_join_kernel(const XentLayout L, long long first, int rows, int d, int V, in
   }
   T *o = out + (size_t)L.index[first + row] * d + c;
   if constexpr (sizeof(T) == 2) {  // d is a multiple of 8
+    const float left = L.left[row];
+    const uint2 w = __ldg(reinterpret_cast<const uint2 *>(W + (size_t)L.labels[first + row] * d + c));
+    s.x = fmaf(left, __uint_as_float(w.x << 16), s.x);
+    s.y = fmaf(left, __uint_as_float(w.x & 0xffff0000u), s.y);
+    s.z = fmaf(left, __uint_as_float(w.y << 16), s.z);
+    s.w = fmaf(left, __uint_as_float(w.y & 0xffff0000u), s.w);
     *reinterpret_cast<uint2 *>(o) =
         make_uint2(pack_bf16(s.x * f, s.y * f), pack_bf16(s.z * f, s.w * f));
   } else {
@@ -1506,7 +1517,7 @@ cudaError_t run(const XentProblem &q) {
         return err;
       const long long quads = (long long)rows * ((q.d + 3) / 4);
       err = launch_pdl(xent_join_kernel<T>, dim3((unsigned)((quads + 255) / 256)), dim3(256), 0,
-                       q.stream, L, n0, rows, q.d, q.V, products, static_cast<T *>(q.dX));
+                       q.stream, L, n0, rows, q.d, q.V, products, g.W, static_cast<T *>(q.dX));
       if (err != cudaSuccess) return err;
     }
     if (q.dW) {

@@ -461,3 +461,13 @@ def test_fp32_gradients_take_all_six_products(N, d, V, size):
     _, _, dX, dW = reference(X, W, y)
     near(got["dX"], dX, 1.5e-6)
     near(got["dW"], dW, 1.5e-6)
+
+
+@pytest.mark.parametrize("N,d,V", [(2225, 8, 554), (391, 8, 3), (300, 16, 7), (1000, 64, 20)])
+def test_few_other_words_count(N, d, V):
+    """Rows whose gradient is the label's word against one or two others: what
+    the label's term loses to its rounding is not theirs to bear."""
+    X, W, y = make(N, d, V, "bf16", 20, ignored=0.0, size=8.0)
+    W *= (torch.arange(V, device="cuda") % 4 + 1)[:, None].to(W.dtype)
+    check(X, W, y)
+    check(*make(N, d, V, "bf16", 21, ignored=0.1, size=8.0, pull=0.0))
