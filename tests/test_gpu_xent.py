@@ -471,3 +471,25 @@ def test_few_other_words_count(N, d, V):
     W *= (torch.arange(V, device="cuda") % 4 + 1)[:, None].to(W.dtype)
     check(X, W, y)
     check(*make(N, d, V, "bf16", 21, ignored=0.1, size=8.0, pull=0.0))
+
+
+@pytest.mark.parametrize("N,d,V,size", [(6, 8, 5085, 40.0), (92, 24, 3143, 40.0), (29, 32, 812, 8.0)])
+def test_words_that_one_token_reaches(N, d, V, size):
+    """dW where no sum evens roundings out: a word that is not its token's label
+    takes E's rounding, the scaled row's, that of the label's E, which the row's
+    factor carries in dW, and the result's, 2^-8 each."""
+    X, W, y = make(N, d, V, "bf16", 22, ignored=0.0, size=size, pull=0.0)
+    got = bd.xent(X, W, y)
+    x, w, lab = f64(X), f64(W), y.cpu().numpy()
+    want = oracle.xent(x, w, lab)
+    P = np.exp(x @ w.T - want["lse"][:, None])
+    P[np.arange(N), lab] = 0.0
+    P[np.arange(N), lab] = P.sum(1)
+    S = (np.abs(x) @ np.abs(w).T).max(1)
+    el = (d / 16 + 8) * 2.0 ** -22 * S + 8 * U * np.abs(x @ w.T).max(1)
+    h = 2.0 ** -8
+    rel = ((1 + h) ** 3 - 1 + 4 * el + 2.0 ** -20 + V * U / 8)[:, None] + (N / 16 + 8) * 2.0 ** -22
+    bound = (P * rel / N).T @ np.abs(x)
+    lim = bound + h * (np.abs(want["dW"]) + bound) + 1e-33
+    err = np.abs(f64(got["dW"]) - want["dW"])
+    assert np.all(err <= lim), float(np.max(err / lim))
