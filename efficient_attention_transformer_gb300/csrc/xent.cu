@@ -88,10 +88,15 @@ constexpr bool is_logits(int epi) { return epi == kLoss || epi == kProbs || is_l
 
 // fp32 io adds up a tile's logits over several works (see kFp32Blocks): an
 // epilogue thread's 128 of them, 64 in registers and 64 in shared memory, in
-// the place of the ring's last two stages.
+// the place of the ring's last two stages, or without stores of its last one
+// and of the stores' staging.
 constexpr int kSumColumns = 64;
-constexpr int stages_of(int epi) { return is_logits3(epi) ? STAGES - 2 : STAGES; }
-static_assert(EPI_WARPS * kSumColumns * 32 * sizeof(float) == 2 * STAGE_BYTES, "sums of the logits");
+constexpr int stages_of(int epi) {
+  return epi == kProbs3 ? STAGES - 2 : epi == kLoss3 ? STAGES - 1 : STAGES;
+}
+static_assert(EPI_WARPS * kSumColumns * 32 * sizeof(float) == 2 * STAGE_BYTES &&
+                  EPI_WARPS * STG_BYTES == STAGE_BYTES,
+              "sums of the logits");
 
 constexpr int kTerms = 3, kProducts = 6;  // of an fp32 value; of two
 
@@ -1485,8 +1490,13 @@ cudaError_t run(const XentProblem &q) {
     p.part = L.part;
     p.e_term = (int)L.ldE;
     const long long works = (long long)(whole / (2 * BM)) * ((q.V + BN - 1) / BN);
-    err = grad ? launch_gemm<bf16 ? kProbs : kProbs3>(tX, tW, tE, p, works, q.num_sms, q.stream)
-               : launch_gemm<bf16 ? kLoss : kLoss3>(tX, tW, tE, p, works, q.num_sms, q.stream);
+    // fp32 without E: one work a tile needs no sums, and the whole ring is
+    // there (9 x 512 x 50257: 112 us, 119 with four stages of it; gradients,
+    // 1001 x 520 x 8003, alike)
+    if (grad) err = launch_gemm<bf16 ? kProbs : kProbs3>(tX, tW, tE, p, works, q.num_sms, q.stream);
+    else if (bf16 || q.d <= kFp32Blocks * BK)
+      err = launch_gemm<kLoss>(tX, tW, tE, p, works, q.num_sms, q.stream);
+    else err = launch_gemm<kLoss3>(tX, tW, tE, p, works, q.num_sms, q.stream);
     if (err != cudaSuccess) return err;
     RowArgs r = {};
     r.L = L;
