@@ -27,8 +27,9 @@
 //
 // Backward, rows of up to 2048 columns on 16-byte boundaries: one to four
 // warps a row, see residual_norm_grad_rows_kernel (16384 x 768 bf16 with every
-// option 46 us with the join of the column sums, 63 by tiles).  Others, a tile of rows (about 44 KB, four blocks an SM) is brought into
-// shared memory by asynchronous copies.  First one warp a row takes the row's sums;
+// option 44 us with the join of the column sums, 63 by tiles).  Others, a
+// tile of rows (about 44 KB, four blocks an SM) is brought into shared memory by
+// asynchronous copies.  First one warp a row takes the row's sums;
 // means come first and squares around them second (no difference of large
 // squares), and the sums that dx needs ride along, three passes over shared
 // memory in all.  Then the threads turn by 90 degrees: each keeps four
@@ -272,8 +273,9 @@ __global__ void __launch_bounds__(128) residual_norm_kernel(const Args a) {
 // Any width and alignment: a thread has eight columns of a row in registers,
 // consecutive ones (VEC: rows and arrays on 16-byte boundaries; two runs of
 // four fp32) or one from every `threads`; up to 256 columns are a warp's, and
-// four rows a block, wider ones a block's.  A warp a row that read the row
-// again for each sum took 120 us at 16384 x 767 bf16, and 268 at 3000 x 4096.
+// four rows a block, wider ones a block's (16384 x 767 bf16 66 us, 3000 x 4096
+// 54 in either type).  A warp a row that read the row again for each sum took
+// 120 us at 16384 x 767 bf16, and 268 at 3000 x 4096 bf16.
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(1024) residual_norm_any_kernel(const Args a) {
   __shared__ float shared_sums[2][32];
@@ -397,9 +399,10 @@ __global__ void __launch_bounds__(1024) residual_norm_any_kernel(const Args a) {
 }
 
 // --------------------------------------------------------------- backward --
-// The backward is bound by instruction issue (55% of the cycles) as much as by
-// memory (201 MB in 43 us at 16384 x 768), and half of what it issues is
-// arithmetic on pairs (packed_f32.cuh).
+// The backward keeps neither instruction issue (55% of the cycles) nor memory
+// (201 MB in 43 us at 16384 x 768) busy all the time: its registers leave a
+// quarter of the warps.  Half of what it issues is arithmetic on pairs
+// (packed_f32.cuh).
 // Four columns of a row: consecutive ones from c on (VEC; 8 bytes of bf16,
 // 16 of fp32), or c, c + stride, c + 2 stride, c + 3 stride, zeros behind d.
 struct F4 {

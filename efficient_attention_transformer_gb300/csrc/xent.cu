@@ -46,10 +46,11 @@
 // A few tokens without gradients (xent_few_kernel) only read W: dot products
 // on the CUDA cores.
 //
-// Measured (bf16, V 50257, loss and both gradients): 8192 tokens of d 768
-// 1.23 ms, the products 360, 335 and 335 us (1.76 to 1.89 PFLOP/s) and 47 us
-// around them; 16384 tokens of d 1024, a tenth without label, 2.84 ms, 828,
-// 780 and 822 us (1.83 to 1.95).  The tensor pipe bounds them.
+// Measured (bf16, V 50257, loss and both gradients), back to back under the
+// power cap: 8192 tokens of d 768 1.27 ms at 1440 MHz, 429 us of it up to the
+// rows' sums, 424 for dX and 414 for dW; 16384 tokens of d 1024, a tenth
+// without label, 2.92 ms at 1410 MHz, 997, 952 and 974.  The tensor pipe
+// bounds them.
 #include <cuda_bf16.h>
 
 #include <atomic>
@@ -201,8 +202,8 @@ struct Work {
 // nothing that counts and go into its first
 // (1001 tokens, 8003 words, d = 520, errors of dX and dW: 16 k-blocks 1.4e-6
 // and 1.1e-6 in 201 us, 8 0.8e-6 and 0.6e-6 in 219 us, 4 0.4e-6 and 0.3e-6 in
-// 280 us; the logits in works of 8 too, whose error grows with d otherwise,
-// 2% more).
+// 280 us, each 10 less with W's terms written by the gather's launch; the
+// logits in works of 8 too, whose error grows with d otherwise, 2% more).
 constexpr int kFp32Blocks = 8;
 
 // The works of one pair, in order.  Every role of the kernel walks the same.
@@ -1123,7 +1124,8 @@ __device__ __forceinline__ void store_as(float *p, float v) { *p = v; }
 __device__ __forceinline__ void store_as(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
 
 // dX from the parts of its sum, in the groups' order, with what the label's
-// term has lost (bf16), times the row's factor, to where the row came from; four columns a thread (16384 x 1024 bf16: 31 us).
+// term has lost (bf16), times the row's factor, to where the row came from;
+// four columns a thread (4096 x 768 bf16: 15 us).
 template <typename T>
 __global__ void __launch_bounds__(256)
 xent_join_kernel(const XentLayout L, long long first, int rows, int d, int V, int products,
@@ -1157,12 +1159,12 @@ xent_join_kernel(const XentLayout L, long long first, int rows, int d, int V, in
   }
   T *o = out + (size_t)L.index[first + row] * d + c;
   if constexpr (sizeof(T) == 2) {  // d is a multiple of 8
-    const float left = L.left[row];
+    const float lost = L.left[row];
     const uint2 w = __ldg(reinterpret_cast<const uint2 *>(W + (size_t)L.labels[first + row] * d + c));
-    s.x = fmaf(left, __uint_as_float(w.x << 16), s.x);
-    s.y = fmaf(left, __uint_as_float(w.x & 0xffff0000u), s.y);
-    s.z = fmaf(left, __uint_as_float(w.y << 16), s.z);
-    s.w = fmaf(left, __uint_as_float(w.y & 0xffff0000u), s.w);
+    s.x = fmaf(lost, __uint_as_float(w.x << 16), s.x);
+    s.y = fmaf(lost, __uint_as_float(w.x & 0xffff0000u), s.y);
+    s.z = fmaf(lost, __uint_as_float(w.y << 16), s.z);
+    s.w = fmaf(lost, __uint_as_float(w.y & 0xffff0000u), s.w);
     *reinterpret_cast<uint2 *>(o) =
         make_uint2(pack_bf16(s.x * f, s.y * f), pack_bf16(s.z * f, s.w * f));
   } else {
@@ -1197,8 +1199,8 @@ xent_finish_kernel(const float *__restrict__ in, int ld, int V, int d, T *__rest
 // against the tokens' x in shared memory; the 4 NT sums over the warp leave
 // each lane one token and word of its own, whose running maximum and sum it
 // keeps, and xent_few_join_kernel joins the blocks'.  Back to back in a graph,
-// W from memory: one token 17 us, two 19, four 23; fp32 29, 30 and 31, eight
-// 40.  By the tensor cores: bf16 29 to 31 whatever the tokens, fp32 160 (W has
+// W from memory: one token 17 us, two 19, four 23; fp32 29, 31 and 31, eight
+// 40.  By the tensor cores: bf16 30 to 31 whatever the tokens, fp32 169 (W has
 // to be split there), and 12 for 5 at 3000 x 256.  So bf16 takes this way up to four
 // tokens (eight: 36 us), fp32 up to eight.
 constexpr int kFewTokens = 8, kFewTokensBf16 = 4;

@@ -373,13 +373,15 @@ int flash_gau_rope_toeplitz_bias(const float *a, const float *b, int m, int C,
  * are zero, it adds nothing to dW, the mean is over the others (of none: 0),
  * and what its row of X holds, NaN included, has no effect (nor does it take
  * time).  The other tokens are taken in pieces of at most 2 GiB of
- * [tokens, V] in the workspace (or 256 tokens).  The products run on the tensor cores with
- * fp32 accumulation and sums; bf16: the exponentials enter the gradients'
- * products rounded to bf16; fp32: operands enter as three bf16 terms and a
- * product as six of theirs, so that what is left out is below 2^-24 of it,
- * and the large one's sums are taken 512 terms at a time, the shares added in
- * fp32 (values of X and W that are not finite make the logits and gradients
- * that they enter not finite: with bf16 as the formulas do, with fp32 NaN).  */
+ * [tokens, V] in the workspace (or 256 tokens).  The products run on the tensor
+ * cores with fp32 accumulation and sums.  bf16: the exponentials, and in dW the
+ * rows of X times their factors, enter the gradients' products rounded to
+ * bf16.  fp32: operands enter as three bf16 terms and a product as six of
+ * theirs, so that what is left out is below 2^-24 of it, and the large one's
+ * sums are taken 512 terms at a time, the shares added in fp32.  Infinities in
+ * X (of tokens with a label) and W: with bf16 as the formulas have them, but
+ * for a logit of plus infinity, which makes its token's loss infinite or NaN;
+ * with fp32 they may become NaN.                                            */
 #define FLASH_GAU_MEAN 0
 #define FLASH_GAU_SUM 1
 
@@ -415,7 +417,8 @@ int flash_gau_xent(const void *X, const void *W, const int *labels, long long N,
  * h is the stream before the block and y the block's output; post and norm
  * are FLASH_GAU_NORM_* of the flash_block wrapper, with the same formulas.
  * n is taken from r before its rounding to the io type.  Row statistics are
- * fp32.  Any 1 <= d <= 8192 and 1 <= M <= 2^32 (more:
+ * fp32, squares too: to a norm a row below 1e-22 in length is zero, and one
+ * above 1e19 infinite.  Any 1 <= d <= 8192 and 1 <= M <= 2^32 (more:
  * FLASH_GAU_ENOTSUP); rows and arrays need only their element's alignment
  * (16-byte aligned arrays and rows of a multiple of 16 bytes run fastest).  */
 typedef struct flash_gau_residual {
