@@ -10,7 +10,8 @@ from .binding import (  # noqa: F401
     FP32, BF16, GauWeights, FlashGauError, forward, workspace_layout,
     workspace_status, num_stages, stage_names, lib, strerror, EXPORTED,
     xent, xent_workspace_bytes, residual_norm, residual_norm_backward, AdamW,
-    NORM_NONE, NORM_LAYER, NORM_SCALE, MEAN, SUM,
+    bucket_bias, bucket_bias_backward, Checkpoint, checkpoint_pack, checkpoint_restore,
+    checkpoint_backward, sample, NORM_NONE, NORM_LAYER, NORM_SCALE, MEAN, SUM,
 )
 
 __version__ = "0.1.0"

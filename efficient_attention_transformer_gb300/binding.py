@@ -6,6 +6,7 @@ of the computation runs in the library's CUDA kernels.  Loading fails loudly
 when the library has not been built.
 """
 
+import collections
 import ctypes
 import os
 
@@ -61,6 +62,13 @@ EXPORTED = (
     "flash_gau_residual_norm_backward",
     "flash_gau_adamw_step",
     "flash_gau_adamw_moments",
+    "flash_gau_bucket_bias",
+    "flash_gau_bucket_bias_backward",
+    "flash_gau_checkpoint_pack",
+    "flash_gau_checkpoint_restore",
+    "flash_gau_checkpoint_backward_workspace_bytes",
+    "flash_gau_checkpoint_backward",
+    "flash_gau_sample",
 )
 
 # Capacity of the static scratch behind flash_gau_forward_noalloc.
@@ -160,6 +168,10 @@ class AdamWHyper(ctypes.Structure):
     ]
 
 
+class Sampling(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("temperature", "top_k", "top_p", "min_p")]
+
+
 class FlashGauError(RuntimeError):
     def __init__(self, status, msg):
         super().__init__("flash_gau status %d: %s" % (status, msg))
@@ -246,6 +258,23 @@ def lib():
         L.flash_gau_adamw_moments.argtypes = [ctypes.POINTER(AdamWTensor), i, ctypes.POINTER(p),
                                               ctypes.POINTER(p), p]
         L.flash_gau_adamw_moments.restype = i
+        L.flash_gau_bucket_bias.argtypes = [p, i, i, i, i, i, p, p]
+        L.flash_gau_bucket_bias.restype = i
+        L.flash_gau_bucket_bias_backward.argtypes = [p, i, i, i, i, i, i, p, p]
+        L.flash_gau_bucket_bias_backward.restype = i
+        L.flash_gau_checkpoint_pack.argtypes = [p, p, ctypes.POINTER(Residual), ll, i, i, p, p, p,
+                                                p, p]
+        L.flash_gau_checkpoint_pack.restype = i
+        L.flash_gau_checkpoint_restore.argtypes = [p, p, ctypes.POINTER(Residual), ll, i, i, p, p,
+                                                   p]
+        L.flash_gau_checkpoint_restore.restype = i
+        L.flash_gau_checkpoint_backward_workspace_bytes.argtypes = [ll, i]
+        L.flash_gau_checkpoint_backward_workspace_bytes.restype = sz
+        L.flash_gau_checkpoint_backward.argtypes = [p, p, p, p, ctypes.POINTER(Residual), ll, i, i,
+                                                    ctypes.POINTER(ResidualGrads), p, sz, p]
+        L.flash_gau_checkpoint_backward.restype = i
+        L.flash_gau_sample.argtypes = [p, ll, ll, i, i, p, ctypes.POINTER(Sampling), p, p, p, p]
+        L.flash_gau_sample.restype = i
         _lib = L
     return _lib
 
@@ -928,3 +957,222 @@ class AdamW:
                                                 for o, p in zip(out, self._shapes)]))
         _check(lib().flash_gau_adamw_moments(self._array, k, *ptrs, _stream(dev)))
         return out_m, out_v
+
+
+def bucket_bias(table, C, causal, max_distance=128, out=None, stream=None):
+    """The layer's relative position tables [..., 2C-1] from learned values
+    [..., buckets] by buckets of distance (both fp32), through
+    flash_gau_bucket_bias.  Each row is one layer's GauWeights.relpos."""
+    at, dev, f32 = _dev_ptr(table, "table", torch.float32), table.device, torch.float32
+    if table.dim() < 1:
+        raise ValueError("table must be [..., buckets]")
+    if _elsewhere(dev, stream):
+        with _scope(dev, stream):
+            return bucket_bias(table, C, causal, max_distance, out)
+    buckets = table.shape[-1]
+    shape = table.shape[:-1] + (max(2 * C - 1, 0),)
+    if out is None:
+        out = torch.empty(shape, dtype=f32, device=dev)
+    _check(lib().flash_gau_bucket_bias(at, table.numel() // (buckets or 1), buckets, max_distance,
+                                       C, int(bool(causal)),
+                                       _like(out, "out", shape, f32, dev.index), _stream(dev)))
+    return out
+
+
+def bucket_bias_backward(drelpos, buckets, causal, max_distance=128, out=None, stream=None):
+    """Gradient of the values by buckets through
+    flash_gau_bucket_bias_backward: drelpos [2C-1] or [H, 2C-1] as bucket_bias
+    gives tables, or [R, H, 2C-1], R gradients of shared tables, which are
+    added up.  Returns [buckets] or [H, buckets]."""
+    at, dev, f32 = _dev_ptr(drelpos, "drelpos", torch.float32), drelpos.device, torch.float32
+    if not 1 <= drelpos.dim() <= 3 or drelpos.shape[-1] % 2 != 1:
+        raise ValueError("drelpos must be [2C-1], [H, 2C-1] or [R, H, 2C-1]")
+    if _elsewhere(dev, stream):
+        with _scope(dev, stream):
+            return bucket_bias_backward(drelpos, buckets, causal, max_distance, out)
+    C = (drelpos.shape[-1] + 1) // 2
+    R = drelpos.shape[0] if drelpos.dim() == 3 else 1
+    H = 1 if drelpos.dim() == 1 else drelpos.shape[-2]
+    shape = torch.Size((buckets,) if drelpos.dim() == 1 else (H, buckets))
+    if out is None:
+        out = torch.empty(shape, dtype=f32, device=dev)
+    _check(lib().flash_gau_bucket_bias_backward(at, R, H, buckets, max_distance, C,
+                                                int(bool(causal)),
+                                                _like(out, "out", shape, f32, dev.index),
+                                                _stream(dev)))
+    return out
+
+
+class Checkpoint(collections.namedtuple("Checkpoint", ("codes", "scales"))):
+    """A stream kept in 8 bits: codes int8 [..., d], and scales fp32
+    [..., ceil(d / 128)], one for each 128 neighbours of a row."""
+
+    __slots__ = ()
+
+    @staticmethod
+    def empty(shape, device):
+        """Room for a stream of this shape."""
+        shape = tuple(shape)
+        return Checkpoint(torch.empty(shape, dtype=torch.int8, device=device),
+                          torch.empty(shape[:-1] + (-(-shape[-1] // 128),), dtype=torch.float32,
+                                      device=device))
+
+
+def _packed(packed, shape, index):
+    """Pointers of a checkpoint of a stream of this shape on device `index`."""
+    codes, scales = packed
+    if codes is None or scales is None:
+        raise ValueError("a checkpoint is its codes and their scales")
+    groups = torch.Size(tuple(shape[:-1]) + (-(-shape[-1] // 128),))
+    return (_like(codes, "codes", shape, torch.int8, index),
+            _like(scales, "scales", groups, torch.float32, index))
+
+
+def _norm_of(norm, norm_g, norm_b, eps, d, index):
+    if norm_g is not None:
+        norm_g = _param(norm_g, "norm_g", d if norm == NORM_LAYER else 1, index)
+    if norm_b is not None:
+        norm_b = _param(norm_b, "norm_b", d, index)
+    return Residual(NORM_NONE, norm, None, None, norm_g, norm_b, None, None, eps)
+
+
+def checkpoint_pack(h, y=None, norm=NORM_NONE, norm_g=None, norm_b=None, eps=1e-5, out=None,
+                    out_r=None, out_n=None, stream=None):
+    """(Checkpoint of r, r, n) with r = h + y and n = norm(r), through
+    flash_gau_checkpoint_pack: residual_norm with its stream kept in 8 bits
+    for the backward pass.  Without y, r is h itself; with NORM_NONE n is
+    None.  out: a Checkpoint to write to."""
+    dtype, shape, dev = h.dtype, h.shape, h.device
+    dt, hp, at = dtype_code(dtype), _dev_ptr(h, "h"), dev.index
+    if _elsewhere(dev, stream):
+        with _scope(dev, stream):
+            return checkpoint_pack(h, y, norm, norm_g, norm_b, eps, out, out_r, out_n)
+    d = shape[-1]
+    o = _norm_of(norm, norm_g, norm_b, eps, d, at)
+    yp = None
+    if y is not None:
+        yp = _like(y, "y", shape, dtype, at)
+        if out_r is None:
+            out_r = torch.empty_like(h)
+    if out_n is None and norm != NORM_NONE:
+        out_n = torch.empty_like(h)
+    if out is None:
+        out = Checkpoint.empty(shape, dev)
+    cp, sp = _packed(out, shape, at)
+    _check(lib().flash_gau_checkpoint_pack(hp, yp, o, h.numel() // (d or 1), d, dt,
+                                           _like(out_r, "out_r", shape, dtype, at),
+                                           _like(out_n, "out_n", shape, dtype, at), cp, sp,
+                                           _stream(dev)))
+    return out, (h if out_r is None else out_r), out_n
+
+
+def checkpoint_restore(packed, dtype, norm=NORM_NONE, norm_g=None, norm_b=None, eps=1e-5,
+                       want_x=True, out_x=None, out_n=None, stream=None):
+    """(x, n): the stream of a Checkpoint in the io type `dtype`, and n =
+    norm(x) (the input of the layer's backward), through
+    flash_gau_checkpoint_restore.  x is None where it is not wanted, n with
+    NORM_NONE."""
+    codes = packed[0]
+    dt, _, dev = dtype_code(dtype), _dev_ptr(codes, "codes", torch.int8), codes.device
+    if _elsewhere(dev, stream):
+        with _scope(dev, stream):
+            return checkpoint_restore(packed, dtype, norm, norm_g, norm_b, eps, want_x, out_x,
+                                      out_n)
+    shape, at = codes.shape, dev.index
+    d = shape[-1]
+    o = _norm_of(norm, norm_g, norm_b, eps, d, at)
+    cp, sp = _packed(packed, shape, at)
+    if out_x is None and want_x:
+        out_x = torch.empty(shape, dtype=dtype, device=dev)
+    if out_n is None and norm != NORM_NONE:
+        out_n = torch.empty(shape, dtype=dtype, device=dev)
+    _check(lib().flash_gau_checkpoint_restore(cp, sp, o, codes.numel() // (d or 1), d, dt,
+                                              _like(out_x, "out_x", shape, dtype, at),
+                                              _like(out_n, "out_n", shape, dtype, at),
+                                              _stream(dev)))
+    return out_x, out_n
+
+
+_CHECKPOINT_GRADS = ("dh", "dnorm_g", "dnorm_b")
+
+
+def checkpoint_backward(dr, dn, packed, norm=NORM_LAYER, norm_g=None, norm_b=None, eps=1e-5,
+                        out=None, workspace=None, stream=None):
+    """Gradients of sum(dr * x) + sum(dn * norm(x)) at the stream x of a
+    Checkpoint, through flash_gau_checkpoint_backward: a dict with dh (io
+    type; y's gradient too), dnorm_g and dnorm_b (fp32; dnorm_b None for a
+    ScaleNorm).  dr may be None.  out: tensors to write to, by the same names
+    (dh may be dr or dn itself)."""
+    dtype, shape, dev = dn.dtype, dn.shape, dn.device
+    dt, np_, at = dtype_code(dtype), _dev_ptr(dn, "dn"), dev.index
+    if _elsewhere(dev, stream):
+        with _scope(dev, stream):
+            return checkpoint_backward(dr, dn, packed, norm, norm_g, norm_b, eps, out, workspace)
+    d = shape[-1]
+    M = dn.numel() // (d or 1)
+    o = _norm_of(norm, norm_g, norm_b, eps, d, at)
+    cp, sp = _packed(packed, shape, at)
+    nw = lib().flash_gau_checkpoint_backward_workspace_bytes(M, d)
+    if nw == 0:
+        raise FlashGauError(ENOTSUP if M > 0 and d > 0 else EINVAL, "invalid or unsupported problem")
+    out, layer, f32 = dict(out) if out else {}, norm == NORM_LAYER, torch.float32
+    if not out.keys() <= set(_CHECKPOINT_GRADS):
+        raise ValueError("out holds %s only" % ", ".join(_CHECKPOINT_GRADS))
+    if out.get("dnorm_b") is not None and not layer:
+        raise ValueError("dnorm_b is the gradient of nothing here")
+    params = torch.Size((d if layer else 1,))
+    if out.get("dh") is None:
+        out["dh"] = torch.empty_like(dn)
+    if out.get("dnorm_g") is None:
+        out["dnorm_g"] = torch.empty(params, dtype=f32, device=dev)
+    if out.get("dnorm_b") is None:
+        out["dnorm_b"] = torch.empty(params, dtype=f32, device=dev) if layer else None
+    g = ResidualGrads(dh=_like(out["dh"], "dh", shape, dtype, at),
+                      dnorm_g=_like(out["dnorm_g"], "dnorm_g", params, f32, at),
+                      dnorm_b=_like(out["dnorm_b"], "dnorm_b", params, f32, at))
+    if workspace is None:
+        workspace = torch.empty(nw, dtype=torch.uint8, device=dev)
+    wp, nw = _dev_ptr(workspace, "workspace"), workspace.numel() * workspace.element_size()
+    _check(lib().flash_gau_checkpoint_backward(_like(dr, "dr", shape, dtype, at), np_, cp, sp, o, M,
+                                               d, dt, g, wp, nw, _stream(dev)))
+    return out
+
+
+def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, out_token=None,
+           out_logp=None, out_kept=None, stream=None):
+    """(token, logp, kept) of each row of logits [..., V], through
+    flash_gau_sample: the token that the row's random number u (fp32, logits'
+    leading shape, in [0, 1)) draws, the logarithm of the probability with
+    which it was drawn, and how many words the filters kept.  Each filter is
+    a tensor like u (top_k int32, the others fp32), one value for all rows,
+    or None.  Rows of a matrix may stand further apart than V."""
+    dt, dev = dtype_code(logits.dtype), logits.device
+    lead = u.shape
+    if logits.dim() < 1 or logits.shape[:-1] != lead:
+        raise ValueError("logits must be [..., V] and u logits' leading shape")
+    V, N = logits.shape[-1], u.numel()
+    ld = V
+    if logits.dim() == 2 and logits.is_cuda and logits.stride(1) == 1 and logits.stride(0) >= V:
+        lp, ld = logits.data_ptr(), logits.stride(0)
+    else:
+        lp = _dev_ptr(logits, "logits")
+    if _elsewhere(dev, stream):
+        with _scope(dev, stream):
+            return sample(logits, u, temperature, top_k, top_p, min_p, out_token, out_logp,
+                          out_kept)
+    at, f32, i32 = dev.index, torch.float32, torch.int32
+    held, ptrs = [], []  # tensors made of single values live until the launch
+    for name, t, dtype in (("temperature", temperature, f32), ("top_k", top_k, i32),
+                           ("top_p", top_p, f32), ("min_p", min_p, f32)):
+        if t is not None and not isinstance(t, torch.Tensor):
+            t = torch.full(lead, t, dtype=dtype, device=dev)
+            held.append(t)
+        ptrs.append(_like(t, name, lead, dtype, at))
+    outs = []
+    for name, t, dtype in (("out_token", out_token, i32), ("out_logp", out_logp, f32),
+                           ("out_kept", out_kept, i32)):
+        outs.append(torch.empty(lead, dtype=dtype, device=dev) if t is None else t)
+        ptrs.append(_like(outs[-1], name, lead, dtype, at))
+    _check(lib().flash_gau_sample(lp, ld, N, V, dt, _like(u, "u", lead, f32, at),
+                                  Sampling(*ptrs[:4]), *ptrs[4:], _stream(dev)))
+    return tuple(outs)

@@ -361,6 +361,52 @@ size_t xent_dx_part_rows(long long rows, int d);
 bool xent_few(long long N, int d, int dtype, bool grad);
 cudaError_t xent(const XentProblem &q, int dtype);
 
+// Relative position tables by buckets of distance (bucket_bias.cu).
+constexpr int kBucketMax = 256;
+struct BucketProblem {
+  int H, buckets, far, C, causal;
+  cudaStream_t stream;
+};
+cudaError_t bucket_bias(const BucketProblem &q, const float *table, float *relpos);
+cudaError_t bucket_bias_grad(const BucketProblem &q, const float *drelpos, int R, float *dtable);
+
+// Activation checkpoints in 8 bits (checkpoint.cu).
+constexpr int kCheckpointGroup = 128;
+constexpr int kCheckpointMaxD = 8192;
+constexpr int kCheckpointBlocks = 608;  // of the backward kernel
+struct CheckpointArgs {
+  const void *h, *y, *dr, *dn;
+  void *r, *n, *dh;      // restore: r is the restored stream
+  signed char *codes;    // pack writes them, the others only read
+  float *scales;
+  const float *norm_g, *norm_b;
+  float *part;           // backward: [blocks][2][d] column sums
+  long long M;
+  int d, norm, groups;
+  float eps;
+  bool vec, vec_param;   // rows, parameters in whole vectors on their boundaries
+};
+size_t checkpoint_part_bytes(int d);
+cudaError_t checkpoint_pack(const CheckpointArgs &a, int dtype, cudaStream_t stream);
+cudaError_t checkpoint_restore(const CheckpointArgs &a, int dtype, cudaStream_t stream);
+cudaError_t checkpoint_backward(const CheckpointArgs &a, float *dg, float *db, int dtype,
+                                cudaStream_t stream);
+
+// Sampling from rows of logits (sample.cu).
+struct SampleArgs {
+  const void *logits;
+  long long ld;
+  int V;
+  const float *temperature;
+  const int *top_k;
+  const float *top_p, *min_p, *u;
+  int *token;
+  float *logp;
+  int *kept;
+  int drop;  // set by the launch
+};
+cudaError_t sample(SampleArgs a, int N, int dtype, cudaStream_t stream);
+
 using StageFn = cudaError_t (*)(const Problem &);
 
 // Launches `kernel` on the problem's stream with programmatic stream

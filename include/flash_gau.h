@@ -522,6 +522,122 @@ int flash_gau_adamw_step(const flash_gau_adamw_tensor *tensors, int n_tensors,
 int flash_gau_adamw_moments(const flash_gau_adamw_tensor *tensors, int n_tensors,
                             float *const *m_out, float *const *v_out, void *stream);
 
+/* ---- relative position bias by buckets ------------------------------------ */
+/* The layer's relative position table from learned values, one for each bucket
+ * of distances, and the gradient of those values.  o = j - i is a key's offset
+ * from its query:
+ *   relpos[h][o + C - 1] = table[h][bucket(o)]          -(C-1) <= o <= C-1
+ *   dtable[h][b] = sum over r and all o with bucket(o) = b of
+ *                  drelpos[r][h][o + C - 1]
+ * A direction has n buckets: causal n = buckets, of the distance max(-o, 0);
+ * else n = buckets / 2, of |o|, offsets above zero having buckets n .. 2n-1
+ * (then bucket n, of distance 0, is never met).  With near = n / 2 rounded
+ * down, distance t is in bucket t below near, and from there on in
+ *   min(n - 1, near + floor(log(t / near) / log(max_distance / near) * (n - near)))
+ * exactly so: a distance that meets a border is in the upper bucket.
+ *   table      device fp32 [H, buckets]: H layers' (or heads') values
+ *   relpos     device fp32 [H, 2C-1]; row h can be flash_gau_weights.relpos
+ *   drelpos    device fp32 [R, H, 2C-1]: gradients as flash_gau_backward gives
+ *              them; the R ones of a table that layers share are added up
+ *   dtable     device fp32 [H, buckets], written, not added; a call repeats
+ *              bit for bit
+ * Supported: 1 <= C <= 4096, 1 <= H <= 65535, R >= 1, 2 <= buckets <= 256
+ * (not causal: 4 at least, and even), near < max_distance <= 2^20.  One launch
+ * each, no workspace.  Returns FLASH_GAU_OK, FLASH_GAU_EINVAL (null or
+ * overlapping arrays, sizes out of range), FLASH_GAU_EDEVICE or
+ * FLASH_GAU_ECUDA.                                                           */
+int flash_gau_bucket_bias(const float *table, int H, int buckets, int max_distance, int C,
+                          int causal, float *relpos, void *stream);
+int flash_gau_bucket_bias_backward(const float *drelpos, int R, int H, int buckets,
+                                   int max_distance, int C, int causal, float *dtable,
+                                   void *stream);
+
+/* ---- activation checkpoints in 8 bits --------------------------------------- */
+/* The residual stream at a block's boundary, kept in 8 bits between the forward
+ * and the backward pass.  Each 128 neighbouring columns of a row (a group; the
+ * last one may be shorter) share an fp32 scale:
+ *   scale = max |x| * (1 / 127), in fp32, 1 / 127 being fp32's nearest
+ *   code  = x / scale to the nearest whole number, ties to even, of the exact
+ *           quotient;  restored: code * scale
+ * A group whose largest magnitude is below 2^-100 is zero; one that holds an
+ * infinity or NaN is restored as NaN throughout.  codes: device int8 [M, d];
+ * scales: device fp32 [M, ceil(d / 128)].
+ * o gives the norm of flash_gau_residual_norm (norm, norm_g, norm_b, eps); post,
+ * scale and gate must be unset.  Any 1 <= d <= 8192 and 1 <= M <= 2^32 (more:
+ * FLASH_GAU_ENOTSUP); rows and arrays need only their element's alignment
+ * (16-byte aligned arrays and d a multiple of 8 run fastest).               */
+
+/* r = h + y, n = norm(r), and the codes of r as it is stored in the io type:
+ * flash_gau_residual_norm with a checkpoint of its stream.  h, y: device
+ * [M, d], io type; y may be NULL (then r = h).  r, n: device [M, d]; r may be
+ * NULL, n is NULL exactly when o->norm is NONE.  r and n may each be the array
+ * of h or y, otherwise arrays must not overlap.  One kernel, no workspace.   */
+int flash_gau_checkpoint_pack(const void *h, const void *y, const flash_gau_residual *o,
+                              long long M, int d, int dtype, void *r, void *n,
+                              signed char *codes, float *scales, void *stream);
+
+/* x = the restored stream and n = norm(x) (taken before x is rounded to the io
+ * type): what flash_gau_backward and flash_gau_residual_norm_backward read in
+ * the backward pass.  x may be NULL (not wanted); n is NULL exactly when
+ * o->norm is NONE.  One kernel, no workspace.                               */
+int flash_gau_checkpoint_restore(const signed char *codes, const float *scales,
+                                 const flash_gau_residual *o, long long M, int d, int dtype,
+                                 void *x, void *n, void *stream);
+
+/* Workspace bytes of the backward, or 0 when M or d is invalid.            */
+size_t flash_gau_checkpoint_backward_workspace_bytes(long long M, int d);
+
+/* Gradients of sum(dr * x) + sum(dn * norm(x)) at the restored stream x, read
+ * from its codes: dh (what reaches h, and y too), and g's dnorm_g and dnorm_b
+ * (either may be NULL), as flash_gau_residual_norm_backward gives them; g's
+ * other fields must be NULL.  dr: device [M, d], io type, or NULL (zero); dn:
+ * device [M, d]; o->norm must not be NONE.  dh may be the array of dr or dn,
+ * otherwise arrays must not overlap.  workspace: device, 256-byte aligned, of
+ * this call alone until it has run.  Sums are fp32 in a fixed order: a call
+ * repeats bit for bit.                                                      */
+int flash_gau_checkpoint_backward(const void *dr, const void *dn, const signed char *codes,
+                                  const float *scales, const flash_gau_residual *o, long long M,
+                                  int d, int dtype, const flash_gau_residual_grads *g,
+                                  void *workspace, size_t workspace_bytes, void *stream);
+
+/* ---- sampling ----------------------------------------------------------------- */
+/* The next token of each row of logits, from one given random number a row.
+ * w_i = exp((l_i - max l) / T); words in falling order of l, equal ones by
+ * index.  Each filter keeps a beginning of that order:
+ *   top_k  the first k words                          (k <= 0: all)
+ *   top_p  those with less than p of the mass of top_k's words before them
+ *                                                     (p >= 1: all)
+ *   min_p  those with w_i >= min_p, that share of the first one's probability
+ *                                                     (min_p <= 0: all)
+ * the first word always.  The token is the first kept word with more than u of
+ * the kept words' mass up to its own end.  T below 1e-30: the largest logit's
+ * word, the lowest index of equal ones.  A logit of minus infinity is a word
+ * that cannot be drawn.  A row with a NaN or plus infinity, without a finite
+ * logit, or whose settings or u are NaN or T or u below zero, gets token -1,
+ * logp NaN and kept 0.  u >= 1 is taken as 1 - 2^-24.
+ * Masses are whole numbers of units of 2^-44 of the largest (of less for more
+ * than 2^18 words): a result depends neither on the launch nor on what else
+ * the call holds, and a word below half a unit is never drawn.              */
+typedef struct flash_gau_sampling {
+  const float *temperature;  /* device [N], or NULL (1)                      */
+  const int *top_k;          /* device [N], or NULL (all)                    */
+  const float *top_p;        /* device [N], or NULL (all)                    */
+  const float *min_p;        /* device [N], or NULL (all)                    */
+} flash_gau_sampling;
+
+/* logits: device, io type, row n at logits + n * ld elements, V of them (ld >=
+ * V; element alignment, rows on 16-byte boundaries run fastest); u: device
+ * fp32 [N], in [0, 1); s: host pointer, read during the call; token: device
+ * int32 [N]; logp: device fp32 [N], the logarithm of the probability with
+ * which the token was drawn, or NULL; kept: device int32 [N], how many words
+ * the filters kept, or NULL.  Arrays must not overlap.  1 <= V <= 2^22, 1 <= N
+ * <= 2^30 (more: FLASH_GAU_ENOTSUP).  One kernel, no workspace.  Returns
+ * FLASH_GAU_OK, FLASH_GAU_EINVAL, FLASH_GAU_ENOTSUP, FLASH_GAU_EDEVICE or
+ * FLASH_GAU_ECUDA.                                                          */
+int flash_gau_sample(const void *logits, long long ld, long long N, int V, int dtype,
+                     const float *u, const flash_gau_sampling *s, int *token, float *logp,
+                     int *kept, void *stream);
+
 /* ---- allocation-free variant ------------------------------------------- */
 /* No counterpart on the pages: this entry point exists for deployment, not
  * for the method.

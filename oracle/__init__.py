@@ -26,3 +26,7 @@ from .training import (  # noqa: F401,E402
     norm_rows, residual_norm, residual_norm_grad, xent, adamw, adamw_codes, decode_moments,
     encode_moments,
 )
+from .language import (  # noqa: F401,E402
+    buckets_of_offsets, bucket_bias, bucket_bias_grad, checkpoint_codes, checkpoint_values,
+    sample_row,
+)
