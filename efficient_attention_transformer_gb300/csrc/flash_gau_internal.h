@@ -405,7 +405,7 @@ struct SampleArgs {
   int *kept;
   int drop;  // set by the launch
 };
-cudaError_t sample(SampleArgs a, int N, int dtype, cudaStream_t stream);
+cudaError_t sample(SampleArgs a, int N, int dtype, int num_sms, cudaStream_t stream);
 
 using StageFn = cudaError_t (*)(const Problem &);
 

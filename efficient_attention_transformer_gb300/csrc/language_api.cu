@@ -217,7 +217,8 @@ int flash_gau_sample(const void *logits, long long ld, long long N, int V, int d
                       {s->temperature, n * 4}, {s->top_k, n * 4},
                       {s->top_p, n * 4}, {s->min_p, n * 4}};
   if (!separate(out, in, false)) return FLASH_GAU_EINVAL;
-  const int st = supported();
+  int num_sms = 0;
+  const int st = current_sms(&num_sms);
   if (st != FLASH_GAU_OK) return st;
   SampleArgs a = {};
   a.logits = logits;
@@ -231,7 +232,7 @@ int flash_gau_sample(const void *logits, long long ld, long long N, int V, int d
   a.token = token;
   a.logp = logp;
   a.kept = kept;
-  return status_of(sample(a, (int)N, dtype, static_cast<cudaStream_t>(stream)));
+  return status_of(sample(a, (int)N, dtype, num_sms, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

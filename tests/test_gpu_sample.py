@@ -174,6 +174,36 @@ def test_most_words(dtype):
     check(logits, u, dict(top_k=torch.tensor([100, 2000000], dtype=torch.int32)))
 
 
+@pytest.mark.parametrize("mode", MODES)
+def test_bf16_rows_of_every_value(mode):
+    """bf16 rows are counted by value where all words lie between 2^-40 and 2^8
+    in magnitude (or are zero or minus infinity): rows at those borders, rows
+    with words just outside, many equal words, and every value there is."""
+    rng = np.random.default_rng(12)
+    V = 140001
+    l = rng.normal(size=(8, V))
+    l[0, :70000] = 1.5
+    l[1] = np.where(rng.random(V) < 0.5, -0.0, 0.0)
+    l[1, ::1000] = 1.0
+    l[2] = 0.25
+    bits = torch.arange(-32768, 32768, dtype=torch.int32).to(torch.int16).view(torch.bfloat16)
+    bits = bits[torch.isfinite(bits)].double()
+    l[3] = rng.choice(bits[bits.abs() < 1000].numpy(), V)
+    l[4] = rng.choice(bits[(bits.abs() < 256) & ((bits.abs() >= 2.0 ** -40) | (bits == 0))].numpy(), V)
+    l[5, 77] = 255.0
+    l[6, 77] = 256.0
+    l[7] = -np.abs(l[7]) - 0.1
+    l[7, 1000], l[7, 2000] = -2.0 ** -40, -2.0 ** -41
+    kw = settings(mode, 8, rng, V)
+    kw["temperature"][3:5] = 100.0
+    kw["temperature"][5:7] = 60.0
+    check(torch.tensor(l).to(torch.bfloat16), torch.tensor(rng.random(8), dtype=torch.float32), kw)
+    l = torch.tensor(rng.normal(size=(3, 500)) * 20).to(torch.bfloat16)
+    check(l, torch.tensor([0.1, 0.5, 0.9]), dict(min_p=torch.tensor([1e-30, 1e-16, 1e-12])))
+    l = -torch.rand(4, 3000, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16) - 2 ** -9
+    check(l, torch.tensor([0.1, 0.5, 0.9, 0.99]), settings(mode, 4, rng, 3000))
+
+
 def test_draws_follow_the_distribution():
     """4096 even steps of u: each word as often as its probability says, to one
     step at each of its ends."""
