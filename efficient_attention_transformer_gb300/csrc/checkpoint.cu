@@ -20,6 +20,7 @@
 #include <cuda_bf16.h>
 
 #include "flash_gau_internal.h"
+#include "sm103_ptx.cuh"
 
 namespace flashgau {
 namespace {
@@ -101,17 +102,23 @@ __device__ __forceinline__ void store8(float *row, int c, int d, bool vec, const
       if (c + q < d) row[c + q] = x[q];
   }
 }
+// Four codes as fp32: a code and 128 in the last digits of 2^23, less both.
+__device__ __forceinline__ void four_codes(uint32_t w, float *c) {
+  w ^= 0x80808080u;
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    c[q] = __uint_as_float(__byte_perm(w, 0x4b000000u, 0x7440 + q)) - 8388736.f;
+}
 // codes times their group's scale, the values that the checkpoint stands for
 __device__ __forceinline__ void load_codes(const signed char *codes, const float *scales, int c,
                                            int d, bool vec, float (&x)[8]) {
   if (vec) {
     const uint2 w = c < d ? *reinterpret_cast<const uint2 *>(codes + c) : make_uint2(0, 0);
     const float s = c < d ? scales[c / kGroup] : 0.f;
+    four_codes(w.x, x);
+    four_codes(w.y, x + 4);
 #pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      const uint32_t v = q < 4 ? w.x : w.y;
-      x[q] = (float)(signed char)(v >> (8 * (q & 3))) * s;
-    }
+    for (int q = 0; q < 8; ++q) x[q] *= s;
   } else {
     const float s = c < d ? scales[c / kGroup] : 0.f;
 #pragma unroll
@@ -124,18 +131,19 @@ __device__ __forceinline__ float rounded(float x, const __nv_bfloat16 *) {
   return __bfloat162float(__float2bfloat16_rn(x));
 }
 
-// What the threads of a row share: WARPS warps, one row each time.
+// What the threads of a row share: WARPS warps, the block's `group`th so many.
 template <int WARPS>
 struct RowSum {
   float *part;  // [2][WARPS] shared, WARPS > 1
+  int group;
   int turn = 0;
   __device__ float operator()(float v) {
     v = warp_sum(v);
     if (WARPS == 1) return v;
     float *p = part + turn * WARPS;  // two turns: the last sum may still be read
     turn ^= 1;
-    if (threadIdx.x % 32 == 0) p[threadIdx.x / 32] = v;
-    __syncthreads();
+    if (threadIdx.x % 32 == 0) p[threadIdx.x / 32 % WARPS] = v;
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(32 * WARPS) : "memory");
     v = 0.f;
 #pragma unroll
     for (int k = 0; k < WARPS; ++k) v += p[k];
@@ -210,11 +218,12 @@ __device__ __forceinline__ void store_norm(const float (&u)[NC][8], const Checkp
 
 // ------------------------------------------------------------------- pack --
 template <typename T, int NC, int WARPS>
-__global__ void __launch_bounds__(128) pack_kernel(const CheckpointArgs a) {
+__global__ void __launch_bounds__(32 * (WARPS > 4 ? WARPS : 4)) pack_kernel(const CheckpointArgs a) {
   __shared__ float part[2 * WARPS];
-  RowSum<WARPS> sum{part};
+  RowSum<WARPS> sum{part, 0};
   const int t = threadIdx.x % (32 * WARPS);
-  const long long m = (long long)blockIdx.x * (4 / WARPS) + threadIdx.x / (32 * WARPS);
+  const long long m = (long long)blockIdx.x * (WARPS == 1 ? 4 : 1) + threadIdx.x / (32 * WARPS);
+  ptx::griddep_wait();
   if (m >= a.M) return;  // whole warps, and with four warps whole blocks
   const long long at = m * a.d;
   const T *h = static_cast<const T *>(a.h) + at;
@@ -288,11 +297,12 @@ __global__ void __launch_bounds__(128) pack_kernel(const CheckpointArgs a) {
 
 // ---------------------------------------------------------------- restore --
 template <typename T, int NC, int WARPS>
-__global__ void __launch_bounds__(128) restore_kernel(const CheckpointArgs a) {
+__global__ void __launch_bounds__(32 * (WARPS > 4 ? WARPS : 4)) restore_kernel(const CheckpointArgs a) {
   __shared__ float part[2 * WARPS];
-  RowSum<WARPS> sum{part};
+  RowSum<WARPS> sum{part, 0};
   const int t = threadIdx.x % (32 * WARPS);
-  const long long m = (long long)blockIdx.x * (4 / WARPS) + threadIdx.x / (32 * WARPS);
+  const long long m = (long long)blockIdx.x * (WARPS == 1 ? 4 : 1) + threadIdx.x / (32 * WARPS);
+  ptx::griddep_wait();
   if (m >= a.M) return;
   const long long at = m * a.d;
   const bool vec = a.vec;
@@ -318,19 +328,225 @@ __global__ void __launch_bounds__(128) restore_kernel(const CheckpointArgs a) {
 // sum(w u)), the second term only where |x| > eps.  The row's warps walk rows
 // and keep the column sums of dn u and dn in registers; each block leaves its
 // sums in the workspace and a second kernel adds the blocks up in their order.
-template <typename T, int NC, int WARPS>
-__global__ void __launch_bounds__(128) backward_kernel(const CheckpointArgs a) {
-  __shared__ float part[2 * WARPS];
-  extern __shared__ float cols[];  // [2][d], one row of warps after another
-  RowSum<WARPS> sum{part};
-  const int t = threadIdx.x % (32 * WARPS), rows = 4 / WARPS;
-  const bool layer = a.norm == FLASH_GAU_NORM_LAYER, vec = a.vec;
-  const float inv_d = 1.0f / (float)a.d, g1 = layer ? 0.f : a.norm_g[0];
+//
+// A thread's column sums alone are 16 registers for each 8 columns, so few warps
+// fit, and few loads with them (registers alone: 59 us at 16384 x 768 bf16, 1.0
+// TB/s).  In rows on 16-byte boundaries each thread therefore brings its part of
+// the next row into shared memory by asynchronous copies while it works on this
+// one: no registers, no barrier, since it reads what it copied itself.
+
+// dx in place of w = dn's row, from the row's values x, with the column sums.
+template <int NC, int WARPS>
+__device__ __forceinline__ void row_gradient(const CheckpointArgs &a, float (&x)[NC][8],
+                                             float (&w)[NC][8], float (&sg)[NC][8],
+                                             float (&sb)[NC][8], float &s1, int t,
+                                             RowSum<WARPS> &sum) {
+  const bool layer = a.norm == FLASH_GAU_NORM_LAYER;
+  const float inv_d = 1.0f / (float)a.d;
+  float length2 = 0.f;
+  const float inv = normalise<NC, WARPS>(x, a.norm, t, a.d, a.eps, sum, &length2);
+  float sw = 0.f, swu = 0.f;
+  if (layer) {
+#pragma unroll
+    for (int k = 0; k < NC; ++k) {
+      const int c = (k * 32 * WARPS + t) * 8;
+      float g[8];
+      load8(a.norm_g, c, a.d, a.vec_param, g);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        sg[k][q] = fmaf(w[k][q], x[k][q], sg[k][q]);
+        sb[k][q] += w[k][q];
+        w[k][q] *= g[q];
+        sw += w[k][q];
+        swu = fmaf(w[k][q], x[k][q], swu);
+      }
+    }
+    swu = sum(swu) * inv_d;
+    sw = sum(sw) * inv_d;
+  } else {
+    const float g = a.norm_g[0];
+#pragma unroll
+    for (int k = 0; k < NC; ++k)
+#pragma unroll
+      for (int q = 0; q < 8; ++q) swu = fmaf(w[k][q], x[k][q], swu);
+    s1 += swu;
+#pragma unroll
+    for (int k = 0; k < NC; ++k)
+#pragma unroll
+      for (int q = 0; q < 8; ++q) w[k][q] *= g;
+    swu = length2 > a.eps * a.eps ? sum(swu) * g : 0.f;
+  }
+#pragma unroll
+  for (int k = 0; k < NC; ++k)
+#pragma unroll
+    for (int q = 0; q < 8; ++q) w[k][q] = inv * (w[k][q] - sw - x[k][q] * swu);
+}
+
+__device__ __forceinline__ void copy16(void *dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ptx::smem_u32(dst)), "l"(src)
+               : "memory");
+}
+template <int BYTES>
+__device__ __forceinline__ void copy_few(void *dst, const void *src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(ptx::smem_u32(dst)), "l"(src),
+               "n"(BYTES)
+               : "memory");
+}
+
+__device__ __forceinline__ void widen(const uint4 *p, int step, float (&x)[8], const float *) {
+  const uint4 v[2] = {p[0], p[step]};
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    x[4 * q] = __uint_as_float(v[q].x);
+    x[4 * q + 1] = __uint_as_float(v[q].y);
+    x[4 * q + 2] = __uint_as_float(v[q].z);
+    x[4 * q + 3] = __uint_as_float(v[q].w);
+  }
+}
+__device__ __forceinline__ void widen(const uint4 *p, int, float (&x)[8], const __nv_bfloat16 *) {
+  const uint32_t v[4] = {p->x, p->y, p->z, p->w};
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const float2 f = unpack_bf16(v[q]);
+    x[2 * q] = f.x;
+    x[2 * q + 1] = f.y;
+  }
+}
+
+// Shared memory of a step: for each of a thread's NC runs of 8 columns dn, dr,
+// codes and the scale, the threads' side by side.
+template <typename T, int NC, int THREADS>
+struct Ring {
+  static constexpr int kPieces = sizeof(T) * 8 / 16;  // 16-byte pieces of a run
+  static constexpr int kRun = THREADS * (2 * 16 * kPieces + 8 + 4);
+  static constexpr int kStep = NC * kRun;
+  static constexpr int kBytes = 2 * kStep;
+  char *at;
+  __device__ uint4 *dn(int k) const { return reinterpret_cast<uint4 *>(at + k * kRun) + threadIdx.x; }
+  __device__ uint4 *dr(int k) const { return dn(k) + kPieces * THREADS; }
+  __device__ uint2 *codes(int k) const {
+    return reinterpret_cast<uint2 *>(at + k * kRun + 32 * kPieces * THREADS) + threadIdx.x;
+  }
+  __device__ float *scale(int k) const {
+    return reinterpret_cast<float *>(at + k * kRun + (32 * kPieces + 8) * THREADS) + threadIdx.x;
+  }
+};
+
+template <typename T, int NC, int WARPS, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1) ring_backward_kernel(const CheckpointArgs a) {
+  using R = Ring<T, NC, THREADS>;
+  constexpr int kRows = THREADS / 32 / WARPS;
+  extern __shared__ __align__(16) char shared[];
+  __shared__ float part[kRows * 2 * WARPS];
+  const int t = threadIdx.x % (32 * WARPS), group = threadIdx.x / (32 * WARPS);
+  RowSum<WARPS> sum{part + group * 2 * WARPS, group};
   float sg[NC][8], sb[NC][8], s1 = 0.f;
 #pragma unroll
   for (int k = 0; k < NC; ++k)
 #pragma unroll
     for (int q = 0; q < 8; ++q) sg[k][q] = sb[k][q] = 0.f;
+  ptx::griddep_wait();
+  auto fetch = [&](long long m, int turn) {
+    const R r{shared + turn * R::kStep};
+    if (m < a.M) {
+      const long long at = m * a.d;
+#pragma unroll
+      for (int k = 0; k < NC; ++k) {
+        const int c = (k * 32 * WARPS + t) * 8;
+        if (c >= a.d) continue;
+#pragma unroll
+        for (int v = 0; v < R::kPieces; ++v) {
+          constexpr int kElements = 16 / sizeof(T);
+          copy16(r.dn(k) + v * THREADS, static_cast<const T *>(a.dn) + at + c + v * kElements);
+          if (a.dr)
+            copy16(r.dr(k) + v * THREADS, static_cast<const T *>(a.dr) + at + c + v * kElements);
+        }
+        copy_few<8>(r.codes(k), a.codes + at + c);
+        copy_few<4>(r.scale(k), a.scales + m * a.groups + c / kGroup);
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  const long long step = (long long)gridDim.x * kRows;
+  long long m = (long long)blockIdx.x * kRows + group;
+  fetch(m, 0);
+  for (int turn = 0; m < a.M; m += step, turn ^= 1) {
+    fetch(m + step, turn ^ 1);
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+    const R r{shared + turn * R::kStep};
+    float x[NC][8], w[NC][8];
+#pragma unroll
+    for (int k = 0; k < NC; ++k) {
+      const bool in = (k * 32 * WARPS + t) * 8 < a.d;
+      const uint2 v = in ? *r.codes(k) : make_uint2(0, 0);
+      const float s = in ? *r.scale(k) : 0.f;
+      four_codes(v.x, x[k]);
+      four_codes(v.y, x[k] + 4);
+      if (in) widen(r.dn(k), THREADS, w[k], static_cast<const T *>(nullptr));
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        x[k][q] *= s;
+        if (!in) w[k][q] = 0.f;
+      }
+    }
+    row_gradient<NC, WARPS>(a, x, w, sg, sb, s1, t, sum);
+    T *dh = static_cast<T *>(a.dh) + m * a.d;
+#pragma unroll
+    for (int k = 0; k < NC; ++k) {
+      const int c = (k * 32 * WARPS + t) * 8;
+      if (c >= a.d) continue;
+      if (a.dr) {
+        float v[8];
+        widen(r.dr(k), THREADS, v, static_cast<const T *>(nullptr));
+#pragma unroll
+        for (int q = 0; q < 8; ++q) w[k][q] += v[q];
+      }
+      store8(dh, c, a.d, true, w[k]);
+    }
+  }
+  if (!a.part) return;
+  if (a.norm != FLASH_GAU_NORM_LAYER) {
+    s1 = warp_sum(s1);
+    if (threadIdx.x % 32 == 0)
+      a.part[(long long)blockIdx.x * (THREADS / 32) + threadIdx.x / 32] = s1;
+    return;
+  }
+  // the block's sums: every group's in shared memory, then column by column
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  __syncthreads();
+  float *cols = reinterpret_cast<float *>(shared);
+#pragma unroll
+  for (int k = 0; k < NC; ++k) {
+    const int c = (k * 32 * WARPS + t) * 8;
+    if (c >= a.d) continue;
+    store8(cols + (long long)group * 2 * a.d, c, a.d, true, sg[k]);
+    store8(cols + (long long)group * 2 * a.d + a.d, c, a.d, true, sb[k]);
+  }
+  __syncthreads();
+  float *to = a.part + (long long)blockIdx.x * 2 * a.d;
+  for (int c = threadIdx.x; c < 2 * a.d; c += THREADS) {
+    float v = cols[c];
+#pragma unroll
+    for (int g = 1; g < kRows; ++g) v += cols[(long long)g * 2 * a.d + c];
+    to[c] = v;
+  }
+}
+
+// Any rows, element by element where they are not on boundaries.
+template <typename T, int NC, int WARPS>
+__global__ void __launch_bounds__(32 * (WARPS > 4 ? WARPS : 4)) backward_kernel(const CheckpointArgs a) {
+  constexpr int kThreads = 32 * (WARPS > 4 ? WARPS : 4), rows = kThreads / 32 / WARPS;
+  __shared__ float part[2 * WARPS];
+  extern __shared__ float cols[];  // [2][d], one row of warps after another
+  RowSum<WARPS> sum{part, 0};
+  const int t = threadIdx.x % (32 * WARPS);
+  const bool layer = a.norm == FLASH_GAU_NORM_LAYER, vec = a.vec;
+  float sg[NC][8], sb[NC][8], s1 = 0.f;
+#pragma unroll
+  for (int k = 0; k < NC; ++k)
+#pragma unroll
+    for (int q = 0; q < 8; ++q) sg[k][q] = sb[k][q] = 0.f;
+  ptx::griddep_wait();
   for (long long m = (long long)blockIdx.x * rows + threadIdx.x / (32 * WARPS); m < a.M;
        m += (long long)gridDim.x * rows) {
     const long long at = m * a.d;
@@ -341,52 +557,24 @@ __global__ void __launch_bounds__(128) backward_kernel(const CheckpointArgs a) {
 #pragma unroll
     for (int k = 0; k < NC; ++k)
       load8(static_cast<const T *>(a.dn) + at, (k * 32 * WARPS + t) * 8, a.d, vec, w[k]);
-    float length2 = 0.f;
-    const float inv = normalise<NC, WARPS>(x, a.norm, t, a.d, a.eps, sum, &length2);
-    float sw = 0.f, swu = 0.f;
+    row_gradient<NC, WARPS>(a, x, w, sg, sb, s1, t, sum);
 #pragma unroll
     for (int k = 0; k < NC; ++k) {
       const int c = (k * 32 * WARPS + t) * 8;
-      float g[8];
-      if (layer) load8(a.norm_g, c, a.d, a.vec_param, g);
+      if (a.dr) {
+        float v[8];
+        load8(static_cast<const T *>(a.dr) + at, c, a.d, vec, v);
 #pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        if (layer) {
-          sg[k][q] = fmaf(w[k][q], x[k][q], sg[k][q]);
-          sb[k][q] += w[k][q];
-        } else {
-          s1 = fmaf(w[k][q], x[k][q], s1);
-        }
-        w[k][q] *= layer ? g[q] : g1;
-        sw += w[k][q];
-        swu = fmaf(w[k][q], x[k][q], swu);
+        for (int q = 0; q < 8; ++q) w[k][q] += v[q];
       }
-    }
-    swu = sum(swu);
-    float mw = 0.f, mwu;
-    if (layer) {
-      mw = sum(sw) * inv_d;
-      mwu = swu * inv_d;
-    } else {
-      mwu = length2 > a.eps * a.eps ? swu : 0.f;
-    }
-#pragma unroll
-    for (int k = 0; k < NC; ++k) {
-      const int c = (k * 32 * WARPS + t) * 8;
-      float v[8];
-      if (a.dr) load8(static_cast<const T *>(a.dr) + at, c, a.d, vec, v);
-#pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        const float dx = inv * (w[k][q] - mw - x[k][q] * mwu);
-        v[q] = a.dr ? v[q] + dx : dx;
-      }
-      store8(static_cast<T *>(a.dh) + at, c, a.d, vec, v);
+      store8(static_cast<T *>(a.dh) + at, c, a.d, vec, w[k]);
     }
   }
   if (!a.part) return;
   if (!layer) {
     s1 = warp_sum(s1);
-    if (threadIdx.x % 32 == 0) a.part[(long long)blockIdx.x * 4 + threadIdx.x / 32] = s1;
+    if (threadIdx.x % 32 == 0)
+      a.part[(long long)blockIdx.x * (kThreads / 32) + threadIdx.x / 32] = s1;
     return;
   }
   for (int turn = 0; turn < rows; ++turn) {
@@ -405,51 +593,65 @@ __global__ void __launch_bounds__(128) backward_kernel(const CheckpointArgs a) {
     __syncthreads();
   }
   float *to = a.part + (long long)blockIdx.x * 2 * a.d;
-  for (int c = threadIdx.x; c < 2 * a.d; c += 128) to[c] = cols[c];
+  for (int c = threadIdx.x; c < 2 * a.d; c += kThreads) to[c] = cols[c];
 }
 
-// Adds the blocks' sums up: 32 columns a block, 8 warps taking every eighth
-// block's row, then the eight in order.
-__global__ void __launch_bounds__(256)
+// Adds the blocks' sums up: 32 columns a block, its 32 warps taking every 32nd
+// block's row, then the 32 in order.
+__global__ void __launch_bounds__(1024)
 join_columns_kernel(const float *__restrict__ part, int blocks, int d, float *__restrict__ dg,
                     float *__restrict__ db) {
-  __shared__ float s[8][32];
-  const int c = blockIdx.x * 32 + threadIdx.x % 32, w = threadIdx.x / 32;
+  __shared__ float s[32][33];
+  const int lane = threadIdx.x % 32, w = threadIdx.x / 32, c = blockIdx.x * 32 + lane;
+  ptx::griddep_wait();
   float v = 0.f;
   if (c < 2 * d)
-    for (int b = w; b < blocks; b += 8) v += part[(long long)b * 2 * d + c];
-  s[w][threadIdx.x % 32] = v;
+#pragma unroll 5
+    for (int b = w; b < blocks; b += 32) v += part[(long long)b * 2 * d + c];
+  s[lane][w] = v;
   __syncthreads();
-  if (w == 0 && c < 2 * d) {
-#pragma unroll
-    for (int k = 1; k < 8; ++k) v += s[k][threadIdx.x];
-    float *to = c < d ? dg : db;
-    if (to) to[c < d ? c : c - d] = v;
-  }
+  const float all = warp_sum(s[w][lane]);  // warp w's column
+  const int mine = blockIdx.x * 32 + w;
+  float *to = mine < d ? dg : db;
+  if (lane == 0 && mine < 2 * d && to) to[mine < d ? mine : mine - d] = all;
 }
-// ScaleNorm's one g: n sums.  In 64 bits, because terms of both signs nearly cancel.
-__global__ void __launch_bounds__(256)
+// ScaleNorm's one g: n sums of both signs that nearly cancel, so what each
+// addition cuts off is added up beside it.
+__global__ void __launch_bounds__(1024)
 join_scalar_kernel(const float *__restrict__ part, int n, float *__restrict__ dg) {
-  __shared__ double s[256];
-  double v = 0.0;
-  for (int k = threadIdx.x; k < n; k += 256) v += (double)part[k];
-  s[threadIdx.x] = v;
+  __shared__ float2 s[32];
+  ptx::griddep_wait();
+  float2 v = make_float2(0.f, 0.f);
+  auto add = [&](float x, float left) {
+    const float t = v.x + x, b = t - v.x;
+    v.y += (v.x - (t - b)) + (x - b) + left;
+    v.x = t;
+  };
+  auto warp = [&] {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+      add(__shfl_xor_sync(kAll, v.x, o), __shfl_xor_sync(kAll, v.y, o));
+  };
+  for (int k = threadIdx.x; k < n; k += 1024) add(part[k], 0.f);
+  warp();
+  if (threadIdx.x % 32 == 0) s[threadIdx.x / 32] = v;
   __syncthreads();
-  for (int o = 128; o > 0; o >>= 1) {
-    if (threadIdx.x < o) s[threadIdx.x] += s[threadIdx.x + o];
-    __syncthreads();
+  if (threadIdx.x < 32) {
+    v = s[threadIdx.x];
+    warp();
+    if (threadIdx.x == 0) *dg = v.x + v.y;
   }
-  if (threadIdx.x == 0) *dg = (float)s[0];
 }
 
 enum { kPack, kRestore, kBackward };
 
 template <int WHAT, typename T, int NC, int WARPS>
 cudaError_t launch(const CheckpointArgs &a, unsigned grid, cudaStream_t stream) {
+  constexpr int kThreads = 32 * (WARPS > 4 ? WARPS : 4);
   if constexpr (WHAT == kPack) {
-    pack_kernel<T, NC, WARPS><<<grid, 128, 0, stream>>>(a);
+    return launch_pdl(pack_kernel<T, NC, WARPS>, dim3(grid), dim3(kThreads), 0, stream, a);
   } else if constexpr (WHAT == kRestore) {
-    restore_kernel<T, NC, WARPS><<<grid, 128, 0, stream>>>(a);
+    return launch_pdl(restore_kernel<T, NC, WARPS>, dim3(grid), dim3(kThreads), 0, stream, a);
   } else {
     const size_t smem = a.part && a.norm == FLASH_GAU_NORM_LAYER ? 2 * a.d * sizeof(float) : 0;
     if (smem > 48 * 1024) {
@@ -457,15 +659,16 @@ cudaError_t launch(const CheckpointArgs &a, unsigned grid, cudaStream_t stream) 
           backward_kernel<T, NC, WARPS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
       if (err != cudaSuccess) return err;
     }
-    backward_kernel<T, NC, WARPS><<<grid, 128, smem, stream>>>(a);
+    return launch_pdl(backward_kernel<T, NC, WARPS>, dim3(grid), dim3(kThreads), smem, stream, a);
   }
-  return cudaGetLastError();
 }
 
-// One warp a row up to 1024 columns, four beyond.
+// Warps of a row: one up to 1024 columns, four up to 4096, eight beyond.
+int row_warps(int d) { return d <= 1024 ? 1 : d <= 4096 ? 4 : 8; }
+
 template <int WHAT, typename T>
 cudaError_t dispatch(const CheckpointArgs &a, unsigned most_blocks, cudaStream_t stream) {
-  const int rows = a.d <= 1024 ? 4 : 1;
+  const int rows = row_warps(a.d) == 1 ? 4 : 1;
   const long long blocks = (a.M + rows - 1) / rows;
   const unsigned grid = (unsigned)(most_blocks && blocks > most_blocks ? most_blocks : blocks);
   if (a.d <= 256) return launch<WHAT, T, 1, 1>(a, grid, stream);
@@ -474,7 +677,7 @@ cudaError_t dispatch(const CheckpointArgs &a, unsigned most_blocks, cudaStream_t
   if (a.d <= 1024) return launch<WHAT, T, 4, 1>(a, grid, stream);
   if (a.d <= 2048) return launch<WHAT, T, 2, 4>(a, grid, stream);
   if (a.d <= 4096) return launch<WHAT, T, 4, 4>(a, grid, stream);
-  return launch<WHAT, T, 8, 4>(a, grid, stream);
+  return launch<WHAT, T, 4, 8>(a, grid, stream);
 }
 
 template <int WHAT>
@@ -482,6 +685,41 @@ cudaError_t dispatch(const CheckpointArgs &a, int dtype, unsigned most_blocks,
                      cudaStream_t stream) {
   return dtype == FLASH_GAU_BF16 ? dispatch<WHAT, __nv_bfloat16>(a, most_blocks, stream)
                                  : dispatch<WHAT, float>(a, most_blocks, stream);
+}
+
+// The form with copies ahead, one block an SM.  Returns the blocks' number and
+// their warps.
+struct Grid {
+  int blocks, warps;
+};
+template <typename T, int NC, int WARPS>
+cudaError_t launch_ring(const CheckpointArgs &a, int num_sms, cudaStream_t stream, Grid *g) {
+  // as many as the column sums' registers leave, in whole rows, and two steps' memory
+  constexpr int kMost = NC < 4 ? 512 : WARPS <= 4 ? 384 : 256;
+  constexpr int kThreads = Ring<T, NC, kMost>::kBytes <= 200 * 1024 ? kMost : 256;
+  constexpr int kRows = kThreads / 32 / WARPS;
+  auto kernel = ring_backward_kernel<T, NC, WARPS, kThreads>;
+  // two steps, or the groups' column sums
+  const size_t sums = (size_t)kRows * 2 * a.d * sizeof(float);
+  const size_t smem = sums > Ring<T, NC, kThreads>::kBytes ? sums : Ring<T, NC, kThreads>::kBytes;
+  const cudaError_t err =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (err != cudaSuccess) return err;
+  const long long all = (a.M + kRows - 1) / kRows;
+  g->blocks = (int)(all < num_sms ? all : num_sms);
+  if (g->blocks > kCheckpointBlocks) g->blocks = kCheckpointBlocks;
+  g->warps = kThreads / 32;
+  return launch_pdl(kernel, dim3(g->blocks), dim3(kThreads), smem, stream, a);
+}
+template <typename T>
+cudaError_t dispatch_ring(const CheckpointArgs &a, int num_sms, cudaStream_t stream, Grid *g) {
+  if (a.d <= 256) return launch_ring<T, 1, 1>(a, num_sms, stream, g);
+  if (a.d <= 512) return launch_ring<T, 2, 1>(a, num_sms, stream, g);
+  if (a.d <= 768) return launch_ring<T, 3, 1>(a, num_sms, stream, g);
+  if (a.d <= 1024) return launch_ring<T, 4, 1>(a, num_sms, stream, g);
+  if (a.d <= 2048) return launch_ring<T, 2, 4>(a, num_sms, stream, g);
+  if (a.d <= 4096) return launch_ring<T, 4, 4>(a, num_sms, stream, g);
+  return launch_ring<T, 4, 8>(a, num_sms, stream, g);
 }
 
 bool on(const void *p, size_t bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
@@ -507,23 +745,30 @@ cudaError_t checkpoint_restore(const CheckpointArgs &a, int dtype, cudaStream_t 
 }
 
 size_t checkpoint_part_bytes(int d) {
-  return (size_t)kCheckpointBlocks * 2 * (d < 4 ? 4 : d) * sizeof(float);
+  return (size_t)kCheckpointBlocks * 2 * (d < 8 ? 8 : d) * sizeof(float);
 }
 
 cudaError_t checkpoint_backward(const CheckpointArgs &args, float *dg, float *db, int dtype,
-                                cudaStream_t stream) {
+                                int num_sms, cudaStream_t stream) {
   CheckpointArgs a = finish(args);
   if (!dg && !db) a.part = nullptr;
-  cudaError_t err = dispatch<kBackward>(a, dtype, kCheckpointBlocks, stream);
+  Grid g;
+  cudaError_t err;
+  if (a.vec) {
+    err = dtype == FLASH_GAU_BF16 ? dispatch_ring<__nv_bfloat16>(a, num_sms, stream, &g)
+                                  : dispatch_ring<float>(a, num_sms, stream, &g);
+  } else {
+    err = dispatch<kBackward>(a, dtype, kCheckpointBlocks, stream);
+    const int warps = row_warps(a.d), rows = warps == 1 ? 4 : 1;
+    const long long all = (a.M + rows - 1) / rows;
+    g = {(int)(all < kCheckpointBlocks ? all : kCheckpointBlocks), warps > 4 ? warps : 4};
+  }
   if (err != cudaSuccess || !a.part) return err;
-  const int rows = a.d <= 1024 ? 4 : 1;
-  const long long all = (a.M + rows - 1) / rows;
-  const int blocks = (int)(all < kCheckpointBlocks ? all : kCheckpointBlocks);
   if (a.norm == FLASH_GAU_NORM_LAYER)
-    join_columns_kernel<<<(2 * a.d + 31) / 32, 256, 0, stream>>>(a.part, blocks, a.d, dg, db);
-  else
-    join_scalar_kernel<<<1, 256, 0, stream>>>(a.part, blocks * 4, dg);
-  return cudaGetLastError();
+    return launch_pdl(join_columns_kernel, dim3((2 * a.d + 31) / 32), dim3(1024), 0, stream,
+                      a.part, g.blocks, a.d, dg, db);
+  return launch_pdl(join_scalar_kernel, dim3(1), dim3(1024), 0, stream, a.part,
+                    g.blocks * g.warps, dg);
 }
 
 }  // namespace flashgau

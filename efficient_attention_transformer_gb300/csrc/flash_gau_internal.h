@@ -390,7 +390,7 @@ size_t checkpoint_part_bytes(int d);
 cudaError_t checkpoint_pack(const CheckpointArgs &a, int dtype, cudaStream_t stream);
 cudaError_t checkpoint_restore(const CheckpointArgs &a, int dtype, cudaStream_t stream);
 cudaError_t checkpoint_backward(const CheckpointArgs &a, float *dg, float *db, int dtype,
-                                cudaStream_t stream);
+                                int num_sms, cudaStream_t stream);
 
 // Sampling from rows of logits (sample.cu).
 struct SampleArgs {

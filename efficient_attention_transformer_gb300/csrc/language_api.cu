@@ -190,13 +190,14 @@ int flash_gau_checkpoint_backward(const void *dr, const void *dn, const signed c
   if (!separate(rows, grads, true) || !separate(rows, rest, false) || !separate(sums, in, false) ||
       !separate(sums, rows, false))
     return FLASH_GAU_EINVAL;
-  if ((st = supported()) != FLASH_GAU_OK) return st;
+  int num_sms = 0;
+  if ((st = current_sms(&num_sms)) != FLASH_GAU_OK) return st;
   CheckpointArgs a = checkpoint_args(o, codes, scales, M, d);
   a.dr = dr;
   a.dn = dn;
   a.dh = g->dh;
   a.part = static_cast<float *>(workspace);
-  return status_of(checkpoint_backward(a, g->dnorm_g, g->dnorm_b, dtype,
+  return status_of(checkpoint_backward(a, g->dnorm_g, g->dnorm_b, dtype, num_sms,
                                        static_cast<cudaStream_t>(stream)));
 }
 
