@@ -963,19 +963,23 @@ def bucket_bias(table, C, causal, max_distance=128, out=None, stream=None):
     """The layer's relative position tables [..., 2C-1] from learned values
     [..., buckets] by buckets of distance (both fp32), through
     flash_gau_bucket_bias.  Each row is one layer's GauWeights.relpos."""
-    at, dev, f32 = _dev_ptr(table, "table", torch.float32), table.device, torch.float32
-    if table.dim() < 1:
+    dev, f32, lead = table.device, torch.float32, table.shape
+    tp, at = _dev_ptr(table, "table", f32), dev.index
+    if not lead:
         raise ValueError("table must be [..., buckets]")
     if _elsewhere(dev, stream):
         with _scope(dev, stream):
             return bucket_bias(table, C, causal, max_distance, out)
-    buckets = table.shape[-1]
-    shape = table.shape[:-1] + (max(2 * C - 1, 0),)
+    buckets = lead[-1]
+    shape = lead[:-1] + (max(2 * C - 1, 0),)
     if out is None:
-        out = torch.empty(shape, dtype=f32, device=dev)
-    _check(lib().flash_gau_bucket_bias(at, table.numel() // (buckets or 1), buckets, max_distance,
-                                       C, int(bool(causal)),
-                                       _like(out, "out", shape, f32, dev.index), _stream(dev)))
+        out = table.new_empty(shape)
+        op = out.data_ptr()
+    else:
+        op = _like(out, "out", shape, f32, at)
+    _check(lib().flash_gau_bucket_bias(tp, table.numel() // (buckets or 1), buckets, max_distance,
+                                       C, 1 if causal else 0, op,
+                                       torch._C._cuda_getCurrentRawStream(at)))
     return out
 
 
@@ -984,22 +988,24 @@ def bucket_bias_backward(drelpos, buckets, causal, max_distance=128, out=None, s
     flash_gau_bucket_bias_backward: drelpos [2C-1] or [H, 2C-1] as bucket_bias
     gives tables, or [R, H, 2C-1], R gradients of shared tables, which are
     added up.  Returns [buckets] or [H, buckets]."""
-    at, dev, f32 = _dev_ptr(drelpos, "drelpos", torch.float32), drelpos.device, torch.float32
-    if not 1 <= drelpos.dim() <= 3 or drelpos.shape[-1] % 2 != 1:
+    dev, f32, given = drelpos.device, torch.float32, drelpos.shape
+    dp, at, dims = _dev_ptr(drelpos, "drelpos", f32), dev.index, len(given)
+    if not 1 <= dims <= 3 or given[-1] % 2 != 1:
         raise ValueError("drelpos must be [2C-1], [H, 2C-1] or [R, H, 2C-1]")
     if _elsewhere(dev, stream):
         with _scope(dev, stream):
             return bucket_bias_backward(drelpos, buckets, causal, max_distance, out)
-    C = (drelpos.shape[-1] + 1) // 2
-    R = drelpos.shape[0] if drelpos.dim() == 3 else 1
-    H = 1 if drelpos.dim() == 1 else drelpos.shape[-2]
-    shape = torch.Size((buckets,) if drelpos.dim() == 1 else (H, buckets))
+    H = 1 if dims == 1 else given[-2]
+    shape = (buckets,) if dims == 1 else (H, buckets)
     if out is None:
-        out = torch.empty(shape, dtype=f32, device=dev)
-    _check(lib().flash_gau_bucket_bias_backward(at, R, H, buckets, max_distance, C,
-                                                int(bool(causal)),
-                                                _like(out, "out", shape, f32, dev.index),
-                                                _stream(dev)))
+        out = drelpos.new_empty(shape)
+        op = out.data_ptr()
+    else:
+        op = _like(out, "out", torch.Size(shape), f32, at)
+    _check(lib().flash_gau_bucket_bias_backward(dp, given[0] if dims == 3 else 1, H, buckets,
+                                                max_distance, (given[-1] + 1) // 2,
+                                                1 if causal else 0, op,
+                                                torch._C._cuda_getCurrentRawStream(at)))
     return out
 
 
@@ -1023,9 +1029,8 @@ def _packed(packed, shape, index):
     codes, scales = packed
     if codes is None or scales is None:
         raise ValueError("a checkpoint is its codes and their scales")
-    groups = torch.Size(tuple(shape[:-1]) + (-(-shape[-1] // 128),))
     return (_like(codes, "codes", shape, torch.int8, index),
-            _like(scales, "scales", groups, torch.float32, index))
+            _like(scales, "scales", shape[:-1] + (-(-shape[-1] // 128),), torch.float32, index))
 
 
 def _norm_of(norm, norm_g, norm_b, eps, d, index):
@@ -1049,20 +1054,27 @@ def checkpoint_pack(h, y=None, norm=NORM_NONE, norm_g=None, norm_b=None, eps=1e-
             return checkpoint_pack(h, y, norm, norm_g, norm_b, eps, out, out_r, out_n)
     d = shape[-1]
     o = _norm_of(norm, norm_g, norm_b, eps, d, at)
-    yp = None
+    yp = rp = np_ = None
     if y is not None:
         yp = _like(y, "y", shape, dtype, at)
         if out_r is None:
             out_r = torch.empty_like(h)
-    if out_n is None and norm != NORM_NONE:
+            rp = out_r.data_ptr()
+    if out_r is not None and rp is None:
+        rp = _like(out_r, "out_r", shape, dtype, at)
+    if out_n is not None:
+        np_ = _like(out_n, "out_n", shape, dtype, at)
+    elif norm != NORM_NONE:
         out_n = torch.empty_like(h)
+        np_ = out_n.data_ptr()
     if out is None:
-        out = Checkpoint.empty(shape, dev)
-    cp, sp = _packed(out, shape, at)
-    _check(lib().flash_gau_checkpoint_pack(hp, yp, o, h.numel() // (d or 1), d, dt,
-                                           _like(out_r, "out_r", shape, dtype, at),
-                                           _like(out_n, "out_n", shape, dtype, at), cp, sp,
-                                           _stream(dev)))
+        codes = torch.empty_like(h, dtype=torch.int8)
+        scales = h.new_empty(shape[:-1] + (-(-d // 128),), dtype=torch.float32)
+        out, cp, sp = Checkpoint(codes, scales), codes.data_ptr(), scales.data_ptr()
+    else:
+        cp, sp = _packed(out, shape, at)
+    _check(lib().flash_gau_checkpoint_pack(hp, yp, o, h.numel() // (d or 1), d, dt, rp, np_, cp, sp,
+                                           torch._C._cuda_getCurrentRawStream(at)))
     return out, (h if out_r is None else out_r), out_n
 
 
@@ -1073,23 +1085,27 @@ def checkpoint_restore(packed, dtype, norm=NORM_NONE, norm_g=None, norm_b=None, 
     flash_gau_checkpoint_restore.  x is None where it is not wanted, n with
     NORM_NONE."""
     codes = packed[0]
-    dt, _, dev = dtype_code(dtype), _dev_ptr(codes, "codes", torch.int8), codes.device
+    dt, dev, shape = dtype_code(dtype), codes.device, codes.shape
+    _dev_ptr(codes, "codes", torch.int8)
     if _elsewhere(dev, stream):
         with _scope(dev, stream):
             return checkpoint_restore(packed, dtype, norm, norm_g, norm_b, eps, want_x, out_x,
                                       out_n)
-    shape, at = codes.shape, dev.index
-    d = shape[-1]
+    at, d, xp, np_ = dev.index, shape[-1], None, None
     o = _norm_of(norm, norm_g, norm_b, eps, d, at)
     cp, sp = _packed(packed, shape, at)
-    if out_x is None and want_x:
-        out_x = torch.empty(shape, dtype=dtype, device=dev)
-    if out_n is None and norm != NORM_NONE:
-        out_n = torch.empty(shape, dtype=dtype, device=dev)
-    _check(lib().flash_gau_checkpoint_restore(cp, sp, o, codes.numel() // (d or 1), d, dt,
-                                              _like(out_x, "out_x", shape, dtype, at),
-                                              _like(out_n, "out_n", shape, dtype, at),
-                                              _stream(dev)))
+    if out_x is not None:
+        xp = _like(out_x, "out_x", shape, dtype, at)
+    elif want_x:
+        out_x = torch.empty_like(codes, dtype=dtype)
+        xp = out_x.data_ptr()
+    if out_n is not None:
+        np_ = _like(out_n, "out_n", shape, dtype, at)
+    elif norm != NORM_NONE:
+        out_n = torch.empty_like(codes, dtype=dtype)
+        np_ = out_n.data_ptr()
+    _check(lib().flash_gau_checkpoint_restore(cp, sp, o, codes.numel() // (d or 1), d, dt, xp, np_,
+                                              torch._C._cuda_getCurrentRawStream(at)))
     return out_x, out_n
 
 
@@ -1108,33 +1124,40 @@ def checkpoint_backward(dr, dn, packed, norm=NORM_LAYER, norm_g=None, norm_b=Non
     if _elsewhere(dev, stream):
         with _scope(dev, stream):
             return checkpoint_backward(dr, dn, packed, norm, norm_g, norm_b, eps, out, workspace)
-    d = shape[-1]
+    d, layer = shape[-1], norm == NORM_LAYER
     M = dn.numel() // (d or 1)
     o = _norm_of(norm, norm_g, norm_b, eps, d, at)
     cp, sp = _packed(packed, shape, at)
+    rp = None if dr is None else _like(dr, "dr", shape, dtype, at)
     nw = lib().flash_gau_checkpoint_backward_workspace_bytes(M, d)
     if nw == 0:
         raise FlashGauError(ENOTSUP if M > 0 and d > 0 else EINVAL, "invalid or unsupported problem")
-    out, layer, f32 = dict(out) if out else {}, norm == NORM_LAYER, torch.float32
-    if not out.keys() <= set(_CHECKPOINT_GRADS):
-        raise ValueError("out holds %s only" % ", ".join(_CHECKPOINT_GRADS))
-    if out.get("dnorm_b") is not None and not layer:
-        raise ValueError("dnorm_b is the gradient of nothing here")
-    params = torch.Size((d if layer else 1,))
-    if out.get("dh") is None:
-        out["dh"] = torch.empty_like(dn)
-    if out.get("dnorm_g") is None:
-        out["dnorm_g"] = torch.empty(params, dtype=f32, device=dev)
-    if out.get("dnorm_b") is None:
-        out["dnorm_b"] = torch.empty(params, dtype=f32, device=dev) if layer else None
-    g = ResidualGrads(dh=_like(out["dh"], "dh", shape, dtype, at),
-                      dnorm_g=_like(out["dnorm_g"], "dnorm_g", params, f32, at),
-                      dnorm_b=_like(out["dnorm_b"], "dnorm_b", params, f32, at))
+    given, out, ptrs = out or {}, {}, []
+    if given:
+        if not given.keys() <= set(_CHECKPOINT_GRADS):
+            raise ValueError("out holds %s only" % ", ".join(_CHECKPOINT_GRADS))
+        if given.get("dnorm_b") is not None and not layer:
+            raise ValueError("dnorm_b is the gradient of nothing here")
+    for name, src in (("dh", dn), ("dnorm_g", norm_g),
+                      ("dnorm_b", (norm_g if norm_b is None else norm_b) if layer else None)):
+        t = given.get(name)
+        if src is None:
+            p = None
+        elif t is None:
+            t = torch.empty_like(src)
+            p = t.data_ptr()
+        else:
+            p = _like(t, name, src.shape, src.dtype, at)
+        out[name] = t
+        ptrs.append(p)
     if workspace is None:
-        workspace = torch.empty(nw, dtype=torch.uint8, device=dev)
-    wp, nw = _dev_ptr(workspace, "workspace"), workspace.numel() * workspace.element_size()
-    _check(lib().flash_gau_checkpoint_backward(_like(dr, "dr", shape, dtype, at), np_, cp, sp, o, M,
-                                               d, dt, g, wp, nw, _stream(dev)))
+        workspace = dn.new_empty(nw, dtype=torch.uint8)
+        wp = workspace.data_ptr()
+    else:
+        wp, nw = _dev_ptr(workspace, "workspace"), workspace.numel() * workspace.element_size()
+    g = ResidualGrads(ptrs[0], None, None, None, None, None, ptrs[1], ptrs[2])
+    _check(lib().flash_gau_checkpoint_backward(rp, np_, cp, sp, o, M, d, dt, g, wp, nw,
+                                               torch._C._cuda_getCurrentRawStream(at)))
     return out
 
 
@@ -1146,13 +1169,11 @@ def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, out_
     which it was drawn, and how many words the filters kept.  Each filter is
     a tensor like u (top_k int32, the others fp32), one value for all rows,
     or None.  Rows of a matrix may stand further apart than V."""
-    dt, dev = dtype_code(logits.dtype), logits.device
-    lead = u.shape
-    if logits.dim() < 1 or logits.shape[:-1] != lead:
+    dt, dev, lead, shape = dtype_code(logits.dtype), logits.device, u.shape, logits.shape
+    if not shape or shape[:-1] != lead:
         raise ValueError("logits must be [..., V] and u logits' leading shape")
-    V, N = logits.shape[-1], u.numel()
-    ld = V
-    if logits.dim() == 2 and logits.is_cuda and logits.stride(1) == 1 and logits.stride(0) >= V:
+    V = ld = shape[-1]
+    if len(shape) == 2 and logits.is_cuda and logits.stride(1) == 1 and logits.stride(0) >= V:
         lp, ld = logits.data_ptr(), logits.stride(0)
     else:
         lp = _dev_ptr(logits, "logits")
@@ -1161,18 +1182,33 @@ def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, out_
             return sample(logits, u, temperature, top_k, top_p, min_p, out_token, out_logp,
                           out_kept)
     at, f32, i32 = dev.index, torch.float32, torch.int32
+    up = _like(u, "u", lead, f32, at)
     held, ptrs = [], []  # tensors made of single values live until the launch
     for name, t, dtype in (("temperature", temperature, f32), ("top_k", top_k, i32),
                            ("top_p", top_p, f32), ("min_p", min_p, f32)):
-        if t is not None and not isinstance(t, torch.Tensor):
+        if t is None:
+            ptrs.append(None)
+            continue
+        if not isinstance(t, torch.Tensor):
             t = torch.full(lead, t, dtype=dtype, device=dev)
             held.append(t)
         ptrs.append(_like(t, name, lead, dtype, at))
-    outs = []
-    for name, t, dtype in (("out_token", out_token, i32), ("out_logp", out_logp, f32),
-                           ("out_kept", out_kept, i32)):
-        outs.append(torch.empty(lead, dtype=dtype, device=dev) if t is None else t)
-        ptrs.append(_like(outs[-1], name, lead, dtype, at))
-    _check(lib().flash_gau_sample(lp, ld, N, V, dt, _like(u, "u", lead, f32, at),
-                                  Sampling(*ptrs[:4]), *ptrs[4:], _stream(dev)))
-    return tuple(outs)
+    settings = Sampling(*ptrs)
+    if out_token is None:
+        out_token = torch.empty_like(u, dtype=i32)
+        tp = out_token.data_ptr()
+    else:
+        tp = _like(out_token, "out_token", lead, i32, at)
+    if out_logp is None:
+        out_logp = torch.empty_like(u)
+        gp = out_logp.data_ptr()
+    else:
+        gp = _like(out_logp, "out_logp", lead, f32, at)
+    if out_kept is None:
+        out_kept = torch.empty_like(u, dtype=i32)
+        kp = out_kept.data_ptr()
+    else:
+        kp = _like(out_kept, "out_kept", lead, i32, at)
+    _check(lib().flash_gau_sample(lp, ld, u.numel(), V, dt, up, settings, tp, gp, kp,
+                                  torch._C._cuda_getCurrentRawStream(at)))
+    return out_token, out_logp, out_kept

@@ -20,6 +20,7 @@
 #include <cuda_bf16.h>
 
 #include "flash_gau_internal.h"
+#include "packed_f32.cuh"
 #include "sm103_ptx.cuh"
 
 namespace flashgau {
@@ -35,100 +36,183 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+__device__ __forceinline__ uint32_t pack_bf16(f2 v) {
+  const float2 f = split(v);
+  const __nv_bfloat162 h = __floats2bfloat162_rn(f.x, f.y);
   return *reinterpret_cast<const uint32_t *>(&h);
 }
-__device__ __forceinline__ float2 unpack_bf16(uint32_t w) {
-  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+__device__ __forceinline__ f2 unpack_bf16(uint32_t w) {
+  return pair(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
 }
 
-// Eight columns of a row from column c on; `vec`: rows are whole vectors on
-// their boundaries.  Columns behind d are zero and not stored.
-__device__ __forceinline__ void load8(const __nv_bfloat16 *row, int c, int d, bool vec,
-                                      float (&x)[8]) {
+// Eight columns of a row from column c on, in pairs; `vec`: rows are whole
+// vectors on their boundaries.  Columns behind d are zero and not stored.
+struct Eight {
+  f2 v[4];
+  __device__ float get(int q) const {
+    const float2 f = split(v[q / 2]);
+    return q % 2 ? f.y : f.x;
+  }
+  __device__ void of(const float (&x)[8]) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) v[q] = pair(x[2 * q], x[2 * q + 1]);
+  }
+  __device__ void zero_from(int n) {  // columns n .. 7
+    float x[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) x[q] = q < n ? get(q) : 0.f;
+    of(x);
+  }
+};
+
+__device__ __forceinline__ Eight load8(const __nv_bfloat16 *row, int c, int d, bool vec) {
+  Eight e;
   if (vec) {
     const uint4 w = c < d ? *reinterpret_cast<const uint4 *>(row + c) : make_uint4(0, 0, 0, 0);
-    const uint32_t v[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const float2 f = unpack_bf16(v[q]);
-      x[2 * q] = f.x;
-      x[2 * q + 1] = f.y;
-    }
+    e.v[0] = unpack_bf16(w.x);
+    e.v[1] = unpack_bf16(w.y);
+    e.v[2] = unpack_bf16(w.z);
+    e.v[3] = unpack_bf16(w.w);
   } else {
+    float x[8];
 #pragma unroll
     for (int q = 0; q < 8; ++q) x[q] = c + q < d ? __bfloat162float(row[c + q]) : 0.f;
+    e.of(x);
   }
+  return e;
 }
-__device__ __forceinline__ void load8(const float *row, int c, int d, bool vec, float (&x)[8]) {
+__device__ __forceinline__ Eight load8(const float *row, int c, int d, bool vec) {
+  Eight e;
   if (vec) {
-#pragma unroll
-    for (int q = 0; q < 8; q += 4) {
-      const float4 w = c < d ? *reinterpret_cast<const float4 *>(row + c + q)
-                             : make_float4(0.f, 0.f, 0.f, 0.f);
-      x[q] = w.x;
-      x[q + 1] = w.y;
-      x[q + 2] = w.z;
-      x[q + 3] = w.w;
+    ulonglong2 w[2] = {make_ulonglong2(0, 0), make_ulonglong2(0, 0)};
+    if (c < d) {
+      w[0] = *reinterpret_cast<const ulonglong2 *>(row + c);
+      w[1] = *reinterpret_cast<const ulonglong2 *>(row + c + 4);
     }
+    e.v[0] = w[0].x;
+    e.v[1] = w[0].y;
+    e.v[2] = w[1].x;
+    e.v[3] = w[1].y;
   } else {
+    float x[8];
 #pragma unroll
     for (int q = 0; q < 8; ++q) x[q] = c + q < d ? row[c + q] : 0.f;
+    e.of(x);
   }
+  return e;
 }
-__device__ __forceinline__ void store8(__nv_bfloat16 *row, int c, int d, bool vec,
-                                       const float (&x)[8]) {
+__device__ __forceinline__ void store8(__nv_bfloat16 *row, int c, int d, bool vec, const Eight &e) {
   if (vec) {
     if (c < d)
-      *reinterpret_cast<uint4 *>(row + c) =
-          make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]),
-                     pack_bf16(x[6], x[7]));
+      *reinterpret_cast<uint4 *>(row + c) = make_uint4(pack_bf16(e.v[0]), pack_bf16(e.v[1]),
+                                                       pack_bf16(e.v[2]), pack_bf16(e.v[3]));
   } else {
 #pragma unroll
     for (int q = 0; q < 8; ++q)
-      if (c + q < d) row[c + q] = __float2bfloat16_rn(x[q]);
+      if (c + q < d) row[c + q] = __float2bfloat16_rn(e.get(q));
   }
 }
-__device__ __forceinline__ void store8(float *row, int c, int d, bool vec, const float (&x)[8]) {
+__device__ __forceinline__ void store8(float *row, int c, int d, bool vec, const Eight &e) {
   if (vec) {
     if (c < d) {
-      *reinterpret_cast<float4 *>(row + c) = make_float4(x[0], x[1], x[2], x[3]);
-      *reinterpret_cast<float4 *>(row + c + 4) = make_float4(x[4], x[5], x[6], x[7]);
+      *reinterpret_cast<ulonglong2 *>(row + c) = make_ulonglong2(e.v[0], e.v[1]);
+      *reinterpret_cast<ulonglong2 *>(row + c + 4) = make_ulonglong2(e.v[2], e.v[3]);
     }
   } else {
 #pragma unroll
     for (int q = 0; q < 8; ++q)
-      if (c + q < d) row[c + q] = x[q];
-  }
-}
-// Four codes as fp32: a code and 128 in the last digits of 2^23, less both.
-__device__ __forceinline__ void four_codes(uint32_t w, float *c) {
-  w ^= 0x80808080u;
-#pragma unroll
-  for (int q = 0; q < 4; ++q)
-    c[q] = __uint_as_float(__byte_perm(w, 0x4b000000u, 0x7440 + q)) - 8388736.f;
-}
-// codes times their group's scale, the values that the checkpoint stands for
-__device__ __forceinline__ void load_codes(const signed char *codes, const float *scales, int c,
-                                           int d, bool vec, float (&x)[8]) {
-  if (vec) {
-    const uint2 w = c < d ? *reinterpret_cast<const uint2 *>(codes + c) : make_uint2(0, 0);
-    const float s = c < d ? scales[c / kGroup] : 0.f;
-    four_codes(w.x, x);
-    four_codes(w.y, x + 4);
-#pragma unroll
-    for (int q = 0; q < 8; ++q) x[q] *= s;
-  } else {
-    const float s = c < d ? scales[c / kGroup] : 0.f;
-#pragma unroll
-    for (int q = 0; q < 8; ++q) x[q] = c + q < d ? (float)codes[c + q] * s : 0.f;
+      if (c + q < d) row[c + q] = e.get(q);
   }
 }
 
-__device__ __forceinline__ float rounded(float x, const float *) { return x; }
-__device__ __forceinline__ float rounded(float x, const __nv_bfloat16 *) {
-  return __bfloat162float(__float2bfloat16_rn(x));
+// Eight codes times their group's scale, the values that the checkpoint stands
+// for.  A code as fp32: it and 128 in the last digits of 2^23, less both.
+__device__ __forceinline__ Eight times_scale(uint2 codes, float s) {
+  const uint32_t w[2] = {codes.x ^ 0x80808080u, codes.y ^ 0x80808080u};
+  Eight e;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const f2 c = pair(__uint_as_float(__byte_perm(w[q / 2], 0x4b000000u, 0x7440 + 2 * (q % 2))),
+                      __uint_as_float(__byte_perm(w[q / 2], 0x4b000000u, 0x7441 + 2 * (q % 2))));
+    e.v[q] = mul2(add2(c, both(-8388736.f)), both(s));
+  }
+  return e;
+}
+__device__ __forceinline__ Eight load_codes(const signed char *codes, const float *scales, int c,
+                                            int d, bool vec) {
+  uint2 w = make_uint2(0, 0);
+  const float s = c < d ? scales[c / kGroup] : 0.f;
+  if (vec) {
+    if (c < d) w = *reinterpret_cast<const uint2 *>(codes + c);
+  } else {
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      const uint32_t b = c + q < d ? (uint32_t)(uint8_t)codes[c + q] : 0u;
+      (q < 4 ? w.x : w.y) |= b << (8 * (q & 3));
+    }
+  }
+  Eight e = times_scale(w, s);
+  if (!vec && c + 8 > d) e.zero_from(d - c);  // 0 times a scale that is not finite
+  return e;
+}
+
+// The values as they are stored, and the bits of the largest magnitude: as whole
+// numbers magnitudes keep their order, NaN above infinity.
+__device__ __forceinline__ Eight stored(const Eight &e, const float *, uint32_t *top) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int q = 0; q < 8; ++q) m = max(m, __float_as_uint(e.get(q)) & 0x7fffffffu);
+  *top = m;
+  return e;
+}
+__device__ __forceinline__ Eight stored(const Eight &e, const __nv_bfloat16 *, uint32_t *top) {
+  Eight r;
+  uint32_t m = 0;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const uint32_t w = pack_bf16(e.v[q]);
+    m = __vmaxu2(m, w & 0x7fff7fffu);
+    r.v[q] = unpack_bf16(w);
+  }
+  *top = max(m << 16, m & 0xffff0000u);
+  return r;
+}
+
+// Codes of eight values.  t = v / s to the nearest whole number in the digits of
+// 1.5 * 2^23 is at most one off; the remainder v - t s is exact, and where one of
+// eight is half a scale or more, each is looked at: it moves above a half, and
+// from an odd number at a half.
+__device__ __forceinline__ uint2 codes_of(const Eight &e, float s) {
+  const float magic = 12582912.f;
+  if (!(s > 0.f && s < __int_as_float(0x7f800000))) return make_uint2(0, 0);  // restores 0 or NaN
+  const float inv = __fdiv_rn(1.f, s), half = 0.5f * s;
+  f2 t[4], rest[4];
+  float most = 0.f;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    t[q] = fma2(e.v[q], both(inv), both(magic));
+    rest[q] = fma2(add2(both(magic), mul2(t[q], both(-1.f))), both(s), e.v[q]);
+    const float2 f = split(rest[q]);
+    most = fmaxf(most, fmaxf(fabsf(f.x), fabsf(f.y)));
+  }
+  uint32_t c[8];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const float2 f = split(t[q]);
+    c[2 * q] = __float_as_uint(f.x);
+    c[2 * q + 1] = __float_as_uint(f.y);
+  }
+  if (most >= half) {
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      const float2 f = split(rest[q / 2]);
+      const float x = q % 2 ? f.y : f.x;
+      if (fabsf(x) > half || (fabsf(x) == half && (c[q] & 1))) c[q] += x > 0.f ? 1 : -1;
+    }
+  }
+  // the last byte of each
+  return make_uint2(__byte_perm(__byte_perm(c[0], c[1], 0x40), __byte_perm(c[2], c[3], 0x40), 0x5410),
+                    __byte_perm(__byte_perm(c[4], c[5], 0x40), __byte_perm(c[6], c[7], 0x40), 0x5410));
 }
 
 // What the threads of a row share: WARPS warps, the block's `group`th so many.
@@ -155,64 +239,67 @@ struct RowSum {
 // spread; the hardware's reciprocal square root as in the residual stream's
 // operator.  `length2`: ScaleNorm's sum of squares.
 template <int NC, int WARPS>
-__device__ __forceinline__ float normalise(float (&x)[NC][8], int kind, int t, int d, float eps,
-                                           RowSum<WARPS> &sum, float *length2) {
-  const float inv_d = 1.0f / (float)d;
-  float s = 0.f;
+__device__ __forceinline__ float normalise(Eight (&x)[NC], int kind, int t, int d, float eps,
+                                           RowSum<WARPS> &row_sum, float *length2) {
+  f2 s = 0;
+  float scale;
   if (kind == FLASH_GAU_NORM_LAYER) {
+    const float inv_d = 1.0f / (float)d;
 #pragma unroll
     for (int k = 0; k < NC; ++k)
 #pragma unroll
-      for (int q = 0; q < 8; ++q) s += x[k][q];
-    const float mean = sum(s) * inv_d;
-    s = 0.f;
+      for (int q = 0; q < 4; ++q) s = add2(s, x[k].v[q]);
+    const float mean = row_sum(sum(s)) * inv_d;
+    s = 0;
 #pragma unroll
     for (int k = 0; k < NC; ++k) {
       const int c = (k * 32 * WARPS + t) * 8;
+      const f2 less = both(c < d ? -mean : 0.f);
 #pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        x[k][q] = c + q < d ? x[k][q] - mean : 0.f;
-        s = fmaf(x[k][q], x[k][q], s);
-      }
+      for (int q = 0; q < 4; ++q) x[k].v[q] = add2(x[k].v[q], less);
+      if (c < d && c + 8 > d) x[k].zero_from(d - c);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) s = fma2(x[k].v[q], x[k].v[q], s);
     }
-    s = sum(s);
-    s = rsqrtf(fmaf(s, inv_d, eps));
+    scale = rsqrtf(fmaf(row_sum(sum(s)), inv_d, eps));
   } else {
 #pragma unroll
     for (int k = 0; k < NC; ++k)
 #pragma unroll
-      for (int q = 0; q < 8; ++q) s = fmaf(x[k][q], x[k][q], s);
-    s = sum(s);
-    *length2 = s;
-    const float r = rsqrtf(s), most = 1.0f / eps;
-    s = r > most ? most : r;  // not a number where the row is not
+      for (int q = 0; q < 4; ++q) s = fma2(x[k].v[q], x[k].v[q], s);
+    *length2 = row_sum(sum(s));
+    const float r = rsqrtf(*length2), most = 1.0f / eps;
+    scale = r > most ? most : r;  // not a number where the row is not
   }
 #pragma unroll
   for (int k = 0; k < NC; ++k)
 #pragma unroll
-    for (int q = 0; q < 8; ++q) x[k][q] *= s;
-  return s;
+    for (int q = 0; q < 4; ++q) x[k].v[q] = mul2(x[k].v[q], both(scale));
+  return scale;
 }
 
 // n = u * g + b in the io type
 template <int NC, int WARPS, typename T>
-__device__ __forceinline__ void store_norm(const float (&u)[NC][8], const CheckpointArgs &a, int t,
-                                           T *n, bool vec) {
+__device__ __forceinline__ void store_norm(const Eight (&u)[NC], const CheckpointArgs &a, int t,
+                                           T *n) {
   const bool layer = a.norm == FLASH_GAU_NORM_LAYER;
-  const float g1 = layer ? 0.f : a.norm_g[0];
+  const f2 g1 = both(layer ? 0.f : a.norm_g[0]);
 #pragma unroll
   for (int k = 0; k < NC; ++k) {
     const int c = (k * 32 * WARPS + t) * 8;
     if (c >= a.d) continue;
-    float v[8], g[8], b[8];
+    Eight v;
     if (layer) {
-      load8(a.norm_g, c, a.d, a.vec_param, g);
-      if (a.norm_b) load8(a.norm_b, c, a.d, a.vec_param, b);
-    }
+      const Eight g = load8(a.norm_g, c, a.d, a.vec_param);
+      Eight b = {{0, 0, 0, 0}};
+      if (a.norm_b) b = load8(a.norm_b, c, a.d, a.vec_param);
 #pragma unroll
-    for (int q = 0; q < 8; ++q)
-      v[q] = layer ? fmaf(u[k][q], g[q], a.norm_b ? b[q] : 0.f) : u[k][q] * g1;
-    store8(n, c, a.d, vec, v);
+      for (int q = 0; q < 4; ++q) v.v[q] = fma2(u[k].v[q], g.v[q], b.v[q]);
+    } else {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) v.v[q] = mul2(u[k].v[q], g1);
+    }
+    store8(n, c, a.d, a.vec, v);
   }
 }
 
@@ -220,78 +307,53 @@ __device__ __forceinline__ void store_norm(const float (&u)[NC][8], const Checkp
 template <typename T, int NC, int WARPS>
 __global__ void __launch_bounds__(32 * (WARPS > 4 ? WARPS : 4)) pack_kernel(const CheckpointArgs a) {
   __shared__ float part[2 * WARPS];
-  RowSum<WARPS> sum{part, 0};
+  RowSum<WARPS> row_sum{part, 0};
   const int t = threadIdx.x % (32 * WARPS);
   const long long m = (long long)blockIdx.x * (WARPS == 1 ? 4 : 1) + threadIdx.x / (32 * WARPS);
   ptx::griddep_wait();
-  if (m >= a.M) return;  // whole warps, and with four warps whole blocks
+  if (m >= a.M) return;  // whole warps, and with more than one whole blocks
   const long long at = m * a.d;
   const T *h = static_cast<const T *>(a.h) + at;
   const T *y = a.y ? static_cast<const T *>(a.y) + at : nullptr;
   const bool vec = a.vec;
-  float x[NC][8];
+  Eight x[NC];
 #pragma unroll
-  for (int k = 0; k < NC; ++k) load8(h, (k * 32 * WARPS + t) * 8, a.d, vec, x[k]);
+  for (int k = 0; k < NC; ++k) x[k] = load8(h, (k * 32 * WARPS + t) * 8, a.d, vec);
   if (y) {
 #pragma unroll
     for (int k = 0; k < NC; ++k) {
-      float v[8];
-      load8(y, (k * 32 * WARPS + t) * 8, a.d, vec, v);
+      const Eight v = load8(y, (k * 32 * WARPS + t) * 8, a.d, vec);
 #pragma unroll
-      for (int q = 0; q < 8; ++q) x[k][q] += v[q];
+      for (int q = 0; q < 4; ++q) x[k].v[q] = add2(x[k].v[q], v.v[q]);
     }
   }
-  if (a.r) {
-    T *r = static_cast<T *>(a.r) + at;
-#pragma unroll
-    for (int k = 0; k < NC; ++k) store8(r, (k * 32 * WARPS + t) * 8, a.d, vec, x[k]);
-  }
+  T *r = a.r ? static_cast<T *>(a.r) + at : nullptr;
   signed char *codes = a.codes + at;
   float *scales = a.scales + m * a.groups;
 #pragma unroll
   for (int k = 0; k < NC; ++k) {
     const int c = (k * 32 * WARPS + t) * 8;
-    float v[8], top = 0.f;
-    bool odd = false;  // not a number: a maximum would pass over it
+    if (r) store8(r, c, a.d, vec, x[k]);
+    uint32_t top;
+    const Eight v = stored(x[k], h, &top);
 #pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      v[q] = rounded(x[k][q], h);
-      top = fmaxf(top, fabsf(v[q]));
-      odd |= v[q] != v[q];
-    }
-    if (odd) top = __int_as_float(0x7fffffff);
-    // as integers, magnitudes keep their order and NaN lies above infinity
-    int big = __float_as_int(top);
-#pragma unroll
-    for (int o = 8; o > 0; o >>= 1) big = max(big, __shfl_xor_sync(kAll, big, o));
-    top = __int_as_float(big);
+    for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(kAll, top, o));
     if (c >= a.d) continue;
-    const float s = top < kLeast ? 0.f : top * (1.f / 127.f);
-    const float inv = s > 0.f && s < __int_as_float(0x7f800000) ? __fdiv_rn(1.f, s) : 0.f;
+    const float big = __uint_as_float(top), s = big < kLeast ? 0.f : big * (1.f / 127.f);
     if (t % 16 == 0) scales[c / kGroup] = s;
-    uint32_t w[2] = {0, 0};
-#pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      // in a group with an infinity or NaN every code is zero: it restores to NaN
-      float e = inv > 0.f ? rintf(v[q] * inv) : 0.f;
-      const float rest = inv > 0.f ? fmaf(-e, s, v[q]) : 0.f;
-      const float twice = 2.f * fabsf(rest);
-      const int i = (int)e;
-      const int move = twice > s || (twice == s && (i & 1)) ? (rest > 0.f ? 1 : -1) : 0;
-      w[q / 4] |= ((uint32_t)(i + move) & 0xffu) << (8 * (q & 3));
-    }
+    const uint2 w = codes_of(v, s);
     if (vec) {
-      *reinterpret_cast<uint2 *>(codes + c) = make_uint2(w[0], w[1]);
+      *reinterpret_cast<uint2 *>(codes + c) = w;
     } else {
 #pragma unroll
       for (int q = 0; q < 8; ++q)
-        if (c + q < a.d) codes[c + q] = (signed char)(w[q / 4] >> (8 * (q & 3)));
+        if (c + q < a.d) codes[c + q] = (signed char)((q < 4 ? w.x : w.y) >> (8 * (q & 3)));
     }
   }
   if (a.n) {
     float length2;
-    normalise<NC, WARPS>(x, a.norm, t, a.d, a.eps, sum, &length2);
-    store_norm<NC, WARPS>(x, a, t, static_cast<T *>(a.n) + at, vec);
+    normalise<NC, WARPS>(x, a.norm, t, a.d, a.eps, row_sum, &length2);
+    store_norm<NC, WARPS>(x, a, t, static_cast<T *>(a.n) + at);
   }
 }
 
@@ -299,26 +361,25 @@ __global__ void __launch_bounds__(32 * (WARPS > 4 ? WARPS : 4)) pack_kernel(cons
 template <typename T, int NC, int WARPS>
 __global__ void __launch_bounds__(32 * (WARPS > 4 ? WARPS : 4)) restore_kernel(const CheckpointArgs a) {
   __shared__ float part[2 * WARPS];
-  RowSum<WARPS> sum{part, 0};
+  RowSum<WARPS> row_sum{part, 0};
   const int t = threadIdx.x % (32 * WARPS);
   const long long m = (long long)blockIdx.x * (WARPS == 1 ? 4 : 1) + threadIdx.x / (32 * WARPS);
   ptx::griddep_wait();
   if (m >= a.M) return;
   const long long at = m * a.d;
-  const bool vec = a.vec;
-  float x[NC][8];
+  Eight x[NC];
 #pragma unroll
   for (int k = 0; k < NC; ++k)
-    load_codes(a.codes + at, a.scales + m * a.groups, (k * 32 * WARPS + t) * 8, a.d, vec, x[k]);
+    x[k] = load_codes(a.codes + at, a.scales + m * a.groups, (k * 32 * WARPS + t) * 8, a.d, a.vec);
   if (a.r) {
     T *r = static_cast<T *>(a.r) + at;
 #pragma unroll
-    for (int k = 0; k < NC; ++k) store8(r, (k * 32 * WARPS + t) * 8, a.d, vec, x[k]);
+    for (int k = 0; k < NC; ++k) store8(r, (k * 32 * WARPS + t) * 8, a.d, a.vec, x[k]);
   }
   if (a.n) {
     float length2;
-    normalise<NC, WARPS>(x, a.norm, t, a.d, a.eps, sum, &length2);
-    store_norm<NC, WARPS>(x, a, t, static_cast<T *>(a.n) + at, vec);
+    normalise<NC, WARPS>(x, a.norm, t, a.d, a.eps, row_sum, &length2);
+    store_norm<NC, WARPS>(x, a, t, static_cast<T *>(a.n) + at);
   }
 }
 
@@ -336,50 +397,52 @@ __global__ void __launch_bounds__(32 * (WARPS > 4 ? WARPS : 4)) restore_kernel(c
 // one: no registers, no barrier, since it reads what it copied itself.
 
 // dx in place of w = dn's row, from the row's values x, with the column sums.
-template <int NC, int WARPS>
-__device__ __forceinline__ void row_gradient(const CheckpointArgs &a, float (&x)[NC][8],
-                                             float (&w)[NC][8], float (&sg)[NC][8],
-                                             float (&sb)[NC][8], float &s1, int t,
-                                             RowSum<WARPS> &sum) {
+// gain(k): a LayerNorm's g of the thread's k-th run.
+template <int NC, int WARPS, typename G>
+__device__ __forceinline__ void row_gradient(const CheckpointArgs &a, Eight (&x)[NC],
+                                             Eight (&w)[NC], Eight (&sg)[NC], Eight (&sb)[NC],
+                                             float &s1, int t, RowSum<WARPS> &row_sum,
+                                             const G &gain) {
   const bool layer = a.norm == FLASH_GAU_NORM_LAYER;
-  const float inv_d = 1.0f / (float)a.d;
   float length2 = 0.f;
-  const float inv = normalise<NC, WARPS>(x, a.norm, t, a.d, a.eps, sum, &length2);
-  float sw = 0.f, swu = 0.f;
+  const float inv = normalise<NC, WARPS>(x, a.norm, t, a.d, a.eps, row_sum, &length2);
+  f2 sw2 = 0, swu2 = 0;
+  float sw = 0.f, swu;
   if (layer) {
 #pragma unroll
     for (int k = 0; k < NC; ++k) {
-      const int c = (k * 32 * WARPS + t) * 8;
-      float g[8];
-      load8(a.norm_g, c, a.d, a.vec_param, g);
+      const Eight g = gain(k);
 #pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        sg[k][q] = fmaf(w[k][q], x[k][q], sg[k][q]);
-        sb[k][q] += w[k][q];
-        w[k][q] *= g[q];
-        sw += w[k][q];
-        swu = fmaf(w[k][q], x[k][q], swu);
+      for (int q = 0; q < 4; ++q) {
+        sg[k].v[q] = fma2(w[k].v[q], x[k].v[q], sg[k].v[q]);
+        sb[k].v[q] = add2(sb[k].v[q], w[k].v[q]);
+        w[k].v[q] = mul2(w[k].v[q], g.v[q]);
+        sw2 = add2(sw2, w[k].v[q]);
+        swu2 = fma2(w[k].v[q], x[k].v[q], swu2);
       }
     }
-    swu = sum(swu) * inv_d;
-    sw = sum(sw) * inv_d;
+    const float inv_d = 1.0f / (float)a.d;
+    swu = row_sum(sum(swu2)) * inv_d;
+    sw = row_sum(sum(sw2)) * inv_d;
   } else {
+#pragma unroll
+    for (int k = 0; k < NC; ++k)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) swu2 = fma2(w[k].v[q], x[k].v[q], swu2);
+    swu = sum(swu2);
+    s1 += swu;
     const float g = a.norm_g[0];
 #pragma unroll
     for (int k = 0; k < NC; ++k)
 #pragma unroll
-      for (int q = 0; q < 8; ++q) swu = fmaf(w[k][q], x[k][q], swu);
-    s1 += swu;
-#pragma unroll
-    for (int k = 0; k < NC; ++k)
-#pragma unroll
-      for (int q = 0; q < 8; ++q) w[k][q] *= g;
-    swu = length2 > a.eps * a.eps ? sum(swu) * g : 0.f;
+      for (int q = 0; q < 4; ++q) w[k].v[q] = mul2(w[k].v[q], both(g));
+    swu = length2 > a.eps * a.eps ? row_sum(swu) * g : 0.f;
   }
 #pragma unroll
   for (int k = 0; k < NC; ++k)
 #pragma unroll
-    for (int q = 0; q < 8; ++q) w[k][q] = inv * (w[k][q] - sw - x[k][q] * swu);
+    for (int q = 0; q < 4; ++q)
+      w[k].v[q] = mul2(fma2(x[k].v[q], both(-swu), add2(w[k].v[q], both(-sw))), both(inv));
 }
 
 __device__ __forceinline__ void copy16(void *dst, const void *src) {
@@ -393,34 +456,31 @@ __device__ __forceinline__ void copy_few(void *dst, const void *src) {
                : "memory");
 }
 
-__device__ __forceinline__ void widen(const uint4 *p, int step, float (&x)[8], const float *) {
-  const uint4 v[2] = {p[0], p[step]};
-#pragma unroll
-  for (int q = 0; q < 2; ++q) {
-    x[4 * q] = __uint_as_float(v[q].x);
-    x[4 * q + 1] = __uint_as_float(v[q].y);
-    x[4 * q + 2] = __uint_as_float(v[q].z);
-    x[4 * q + 3] = __uint_as_float(v[q].w);
-  }
+__device__ __forceinline__ Eight widen(const uint4 *p, int step, const float *) {
+  const ulonglong2 *q = reinterpret_cast<const ulonglong2 *>(p);
+  const ulonglong2 v[2] = {q[0], q[step]};
+  return {{v[0].x, v[0].y, v[1].x, v[1].y}};
 }
-__device__ __forceinline__ void widen(const uint4 *p, int, float (&x)[8], const __nv_bfloat16 *) {
-  const uint32_t v[4] = {p->x, p->y, p->z, p->w};
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const float2 f = unpack_bf16(v[q]);
-    x[2 * q] = f.x;
-    x[2 * q + 1] = f.y;
-  }
+__device__ __forceinline__ Eight widen(const uint4 *p, int, const __nv_bfloat16 *) {
+  const uint4 w = *p;
+  return {{unpack_bf16(w.x), unpack_bf16(w.y), unpack_bf16(w.z), unpack_bf16(w.w)}};
 }
 
 // Shared memory of a step: for each of a thread's NC runs of 8 columns dn, dr,
 // codes and the scale, the threads' side by side.
+constexpr int ring_run(int io, int threads) { return threads * (2 * 8 * io + 8 + 4); }
+// steps under way: as many as fit, up to four
+constexpr int ring_steps(int io, int runs, int threads) {
+  const int n = 200 * 1024 / (runs * ring_run(io, threads));
+  return n < 4 ? n : 4;
+}
 template <typename T, int NC, int THREADS>
 struct Ring {
   static constexpr int kPieces = sizeof(T) * 8 / 16;  // 16-byte pieces of a run
-  static constexpr int kRun = THREADS * (2 * 16 * kPieces + 8 + 4);
+  static constexpr int kRun = ring_run(sizeof(T), THREADS);
   static constexpr int kStep = NC * kRun;
-  static constexpr int kBytes = 2 * kStep;
+  static constexpr int kSteps = ring_steps(sizeof(T), NC, THREADS);
+  static constexpr int kBytes = kSteps * kStep;
   char *at;
   __device__ uint4 *dn(int k) const { return reinterpret_cast<uint4 *>(at + k * kRun) + threadIdx.x; }
   __device__ uint4 *dr(int k) const { return dn(k) + kPieces * THREADS; }
@@ -439,12 +499,10 @@ __global__ void __launch_bounds__(THREADS, 1) ring_backward_kernel(const Checkpo
   extern __shared__ __align__(16) char shared[];
   __shared__ float part[kRows * 2 * WARPS];
   const int t = threadIdx.x % (32 * WARPS), group = threadIdx.x / (32 * WARPS);
-  RowSum<WARPS> sum{part + group * 2 * WARPS, group};
-  float sg[NC][8], sb[NC][8], s1 = 0.f;
-#pragma unroll
-  for (int k = 0; k < NC; ++k)
-#pragma unroll
-    for (int q = 0; q < 8; ++q) sg[k][q] = sb[k][q] = 0.f;
+  RowSum<WARPS> row_sum{part + group * 2 * WARPS, group};
+  const bool layer = a.norm == FLASH_GAU_NORM_LAYER;
+  float s1 = 0.f;
+  Eight sg[NC] = {}, sb[NC] = {};
   ptx::griddep_wait();
   auto fetch = [&](long long m, int turn) {
     const R r{shared + turn * R::kStep};
@@ -469,43 +527,46 @@ __global__ void __launch_bounds__(THREADS, 1) ring_backward_kernel(const Checkpo
   };
   const long long step = (long long)gridDim.x * kRows;
   long long m = (long long)blockIdx.x * kRows + group;
-  fetch(m, 0);
-  for (int turn = 0; m < a.M; m += step, turn ^= 1) {
-    fetch(m + step, turn ^ 1);
-    asm volatile("cp.async.wait_group 1;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < R::kSteps - 1; ++i) fetch(m + i * step, i);
+  // a LayerNorm's g, behind the steps
+  float *gains = reinterpret_cast<float *>(shared + R::kBytes);
+  if (layer)
+    for (int c = threadIdx.x; c < a.d; c += THREADS) gains[c] = a.norm_g[c];
+  __syncthreads();
+  const Eight none = {{0, 0, 0, 0}};
+  for (int turn = 0; m < a.M; m += step, turn = turn + 1 == R::kSteps ? 0 : turn + 1) {
+    fetch(m + (R::kSteps - 1) * step, turn ? turn - 1 : R::kSteps - 1);
+    asm volatile("cp.async.wait_group %0;" ::"n"(R::kSteps - 1) : "memory");
     const R r{shared + turn * R::kStep};
-    float x[NC][8], w[NC][8];
+    Eight x[NC], w[NC];
 #pragma unroll
     for (int k = 0; k < NC; ++k) {
-      const bool in = (k * 32 * WARPS + t) * 8 < a.d;
-      const uint2 v = in ? *r.codes(k) : make_uint2(0, 0);
-      const float s = in ? *r.scale(k) : 0.f;
-      four_codes(v.x, x[k]);
-      four_codes(v.y, x[k] + 4);
-      if (in) widen(r.dn(k), THREADS, w[k], static_cast<const T *>(nullptr));
-#pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        x[k][q] *= s;
-        if (!in) w[k][q] = 0.f;
+      x[k] = w[k] = none;
+      if ((k * 32 * WARPS + t) * 8 < a.d) {
+        x[k] = times_scale(*r.codes(k), *r.scale(k));
+        w[k] = widen(r.dn(k), THREADS, static_cast<const T *>(nullptr));
       }
     }
-    row_gradient<NC, WARPS>(a, x, w, sg, sb, s1, t, sum);
+    row_gradient<NC, WARPS>(a, x, w, sg, sb, s1, t, row_sum, [&](int k) {
+      const int c = (k * 32 * WARPS + t) * 8;
+      return c < a.d ? load8(gains, c, a.d, true) : none;
+    });
     T *dh = static_cast<T *>(a.dh) + m * a.d;
 #pragma unroll
     for (int k = 0; k < NC; ++k) {
       const int c = (k * 32 * WARPS + t) * 8;
       if (c >= a.d) continue;
       if (a.dr) {
-        float v[8];
-        widen(r.dr(k), THREADS, v, static_cast<const T *>(nullptr));
+        const Eight v = widen(r.dr(k), THREADS, static_cast<const T *>(nullptr));
 #pragma unroll
-        for (int q = 0; q < 8; ++q) w[k][q] += v[q];
+        for (int q = 0; q < 4; ++q) w[k].v[q] = add2(w[k].v[q], v.v[q]);
       }
       store8(dh, c, a.d, true, w[k]);
     }
   }
   if (!a.part) return;
-  if (a.norm != FLASH_GAU_NORM_LAYER) {
+  if (!layer) {
     s1 = warp_sum(s1);
     if (threadIdx.x % 32 == 0)
       a.part[(long long)blockIdx.x * (THREADS / 32) + threadIdx.x / 32] = s1;
@@ -538,34 +599,32 @@ __global__ void __launch_bounds__(32 * (WARPS > 4 ? WARPS : 4)) backward_kernel(
   constexpr int kThreads = 32 * (WARPS > 4 ? WARPS : 4), rows = kThreads / 32 / WARPS;
   __shared__ float part[2 * WARPS];
   extern __shared__ float cols[];  // [2][d], one row of warps after another
-  RowSum<WARPS> sum{part, 0};
+  RowSum<WARPS> row_sum{part, 0};
   const int t = threadIdx.x % (32 * WARPS);
   const bool layer = a.norm == FLASH_GAU_NORM_LAYER, vec = a.vec;
-  float sg[NC][8], sb[NC][8], s1 = 0.f;
-#pragma unroll
-  for (int k = 0; k < NC; ++k)
-#pragma unroll
-    for (int q = 0; q < 8; ++q) sg[k][q] = sb[k][q] = 0.f;
+  float s1 = 0.f;
+  Eight sg[NC] = {}, sb[NC] = {};
   ptx::griddep_wait();
   for (long long m = (long long)blockIdx.x * rows + threadIdx.x / (32 * WARPS); m < a.M;
        m += (long long)gridDim.x * rows) {
     const long long at = m * a.d;
-    float x[NC][8], w[NC][8];
+    Eight x[NC], w[NC];
 #pragma unroll
     for (int k = 0; k < NC; ++k)
-      load_codes(a.codes + at, a.scales + m * a.groups, (k * 32 * WARPS + t) * 8, a.d, vec, x[k]);
+      x[k] = load_codes(a.codes + at, a.scales + m * a.groups, (k * 32 * WARPS + t) * 8, a.d, vec);
 #pragma unroll
     for (int k = 0; k < NC; ++k)
-      load8(static_cast<const T *>(a.dn) + at, (k * 32 * WARPS + t) * 8, a.d, vec, w[k]);
-    row_gradient<NC, WARPS>(a, x, w, sg, sb, s1, t, sum);
+      w[k] = load8(static_cast<const T *>(a.dn) + at, (k * 32 * WARPS + t) * 8, a.d, vec);
+    row_gradient<NC, WARPS>(a, x, w, sg, sb, s1, t, row_sum, [&](int k) {
+      return load8(a.norm_g, (k * 32 * WARPS + t) * 8, a.d, a.vec_param);
+    });
 #pragma unroll
     for (int k = 0; k < NC; ++k) {
       const int c = (k * 32 * WARPS + t) * 8;
       if (a.dr) {
-        float v[8];
-        load8(static_cast<const T *>(a.dr) + at, c, a.d, vec, v);
+        const Eight v = load8(static_cast<const T *>(a.dr) + at, c, a.d, vec);
 #pragma unroll
-        for (int q = 0; q < 8; ++q) w[k][q] += v[q];
+        for (int q = 0; q < 4; ++q) w[k].v[q] = add2(w[k].v[q], v.v[q]);
       }
       store8(static_cast<T *>(a.dh) + at, c, a.d, vec, w[k]);
     }
@@ -585,8 +644,8 @@ __global__ void __launch_bounds__(32 * (WARPS > 4 ? WARPS : 4)) backward_kernel(
         for (int q = 0; q < 8; ++q) {
           const int c = (k * 32 * WARPS + t) * 8 + q;
           if (c < a.d) {
-            cols[c] = turn ? cols[c] + sg[k][q] : sg[k][q];
-            cols[a.d + c] = turn ? cols[a.d + c] + sb[k][q] : sb[k][q];
+            cols[c] = turn ? cols[c] + sg[k].get(q) : sg[k].get(q);
+            cols[a.d + c] = turn ? cols[a.d + c] + sb[k].get(q) : sb[k].get(q);
           }
         }
     }
@@ -655,8 +714,8 @@ cudaError_t launch(const CheckpointArgs &a, unsigned grid, cudaStream_t stream) 
   } else {
     const size_t smem = a.part && a.norm == FLASH_GAU_NORM_LAYER ? 2 * a.d * sizeof(float) : 0;
     if (smem > 48 * 1024) {
-      const cudaError_t err = cudaFuncSetAttribute(
-          backward_kernel<T, NC, WARPS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+      const cudaError_t err =
+          allow_shared<backward_kernel<T, NC, WARPS>>(2 * kCheckpointMaxD * sizeof(float));
       if (err != cudaSuccess) return err;
     }
     return launch_pdl(backward_kernel<T, NC, WARPS>, dim3(grid), dim3(kThreads), smem, stream, a);
@@ -694,17 +753,24 @@ struct Grid {
 };
 template <typename T, int NC, int WARPS>
 cudaError_t launch_ring(const CheckpointArgs &a, int num_sms, cudaStream_t stream, Grid *g) {
-  // as many as the column sums' registers leave, in whole rows, and two steps' memory
-  constexpr int kMost = NC < 4 ? 512 : WARPS <= 4 ? 384 : 256;
-  constexpr int kThreads = Ring<T, NC, kMost>::kBytes <= 200 * 1024 ? kMost : 256;
+  // as many as the column sums' registers leave, and three steps' memory where a
+  // row's warps allow
+  constexpr int kMost = NC < 3 ? 512 : NC == 3 ? 384 : 256, kIo = sizeof(T);
+  constexpr int kThreads = ring_steps(kIo, NC, kMost) >= 3               ? kMost
+                           : kMost > 384 && ring_steps(kIo, NC, 384) >= 3 ? 384
+                           : ring_steps(kIo, NC, 256) >= 3 || WARPS == 8 ? 256
+                           : WARPS == 4                                  ? 128
+                                                                         : 192;
   constexpr int kRows = kThreads / 32 / WARPS;
-  auto kernel = ring_backward_kernel<T, NC, WARPS, kThreads>;
-  // two steps, or the groups' column sums
-  const size_t sums = (size_t)kRows * 2 * a.d * sizeof(float);
-  const size_t smem = sums > Ring<T, NC, kThreads>::kBytes ? sums : Ring<T, NC, kThreads>::kBytes;
-  const cudaError_t err =
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  constexpr auto kernel = ring_backward_kernel<T, NC, WARPS, kThreads>;
+  // the steps and a LayerNorm's g, then the groups' column sums; d is at most kD
+  constexpr size_t kD = NC * WARPS * 256, kSteps = Ring<T, NC, kThreads>::kBytes;
+  constexpr size_t kSums = kRows * 2 * kD * sizeof(float), kAll = kSteps + kD * sizeof(float);
+  constexpr size_t kMostShared = kSums > kAll ? kSums : kAll;
+  const cudaError_t err = allow_shared<kernel>(kMostShared);
   if (err != cudaSuccess) return err;
+  const size_t sums = (size_t)kRows * 2 * a.d * sizeof(float);
+  const size_t steps = kSteps + a.d * sizeof(float), smem = sums > steps ? sums : steps;
   const long long all = (a.M + kRows - 1) / kRows;
   g->blocks = (int)(all < num_sms ? all : num_sms);
   if (g->blocks > kCheckpointBlocks) g->blocks = kCheckpointBlocks;

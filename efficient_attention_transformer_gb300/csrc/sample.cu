@@ -1159,15 +1159,12 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_bf16_kernel(co
   any_bf16_row<THREADS>(*reinterpret_cast<Shared *>(raw), a, set, blockIdx.x);
 }
 
-cudaError_t launch(void (*kernel)(const SampleArgs), size_t smem, bool most, int threads,
-                   const SampleArgs &a, int N, cudaStream_t stream) {
-  cudaError_t err =
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (err == cudaSuccess && most)
-    err = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
-                               cudaSharedmemCarveoutMaxShared);
+template <auto KERNEL>
+cudaError_t launch(size_t smem, bool most, int threads, const SampleArgs &a, int N,
+                   cudaStream_t stream) {
+  const cudaError_t err = allow_shared<KERNEL>(smem, most);
   if (err != cudaSuccess) return err;
-  kernel<<<N, threads, smem, stream>>>(a);
+  KERNEL<<<N, threads, smem, stream>>>(a);
   return cudaGetLastError();
 }
 
@@ -1183,10 +1180,10 @@ cudaError_t sample(SampleArgs a, int N, int dtype, int num_sms, cudaStream_t str
   // which keep the row in the rest of that memory.
   constexpr size_t kSmem = sizeof(Counted) > sizeof(Shared) ? sizeof(Counted) : sizeof(Shared);
   if (dtype == FLASH_GAU_BF16)
-    return launch(sample_bf16_kernel<512>, kSmem, true, 512, a, N, stream);
+    return launch<sample_bf16_kernel<512>>(kSmem, true, 512, a, N, stream);
   if (N > num_sms)
-    return launch(sample_f32_kernel<512>, sizeof(Shared), false, 512, a, N, stream);
-  return launch(sample_f32_kernel<1024>, sizeof(Shared), false, 1024, a, N, stream);
+    return launch<sample_f32_kernel<512>>(sizeof(Shared), false, 512, a, N, stream);
+  return launch<sample_f32_kernel<1024>>(sizeof(Shared), false, 1024, a, N, stream);
 }
 
 }  // namespace flashgau
