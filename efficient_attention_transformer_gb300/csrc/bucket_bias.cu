@@ -27,9 +27,10 @@ namespace {
 namespace cg = cooperative_groups;
 
 constexpr int kThreads = 256;
+constexpr int kGradThreads = 512;
 constexpr int kMaxCluster = 8;
-// rows of drelpos added up in one fp32 sum before it joins the next one
-constexpr int kRun = 16;
+constexpr int kEach = 2;  // offsets a thread: a cluster of eight takes 8192
+constexpr int kRun = 8;   // rows of drelpos under way at once, and in one fp32 sum
 
 struct Starts {
   int n;       // buckets of a direction
@@ -130,30 +131,38 @@ bucket_bias_kernel(const Starts s, const float *__restrict__ table, int buckets,
 // A cluster takes one table; its blocks take runs of offsets, add up the R
 // rows of each into shared memory, then each warp the runs of some buckets, and
 // the first block joins the blocks' sums in their order.
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kGradThreads)
 bucket_bias_grad_kernel(const Starts s, const float *__restrict__ drelpos, int R, int H,
                         int buckets, int C, int slice, float *__restrict__ dtable) {
-  extern __shared__ float column[];  // [slice]
+  __shared__ float column[kEach * kGradThreads];
   __shared__ float sum[kBucketMax];
   const cg::cluster_group cluster = cg::this_cluster();
   const int h = blockIdx.y, rows = 2 * C - 1, tid = threadIdx.x;
   const int k0 = (int)cluster.block_rank() * slice, k1 = min(rows, k0 + slice);
-  const float *src = drelpos + (long long)h * rows;
+  const float *src = drelpos + (long long)h * rows + k0 + tid;
   const long long step = (long long)H * rows;
-  for (int k = k0 + tid; k < k1; k += kThreads) {
-    float total = 0.f;
-    for (int r0 = 0; r0 < R; r0 += kRun) {
-      float part = 0.f;
-      const float *p = src + k + r0 * step;
-      const int m = min(kRun, R - r0);
-#pragma unroll 8
-      for (int r = 0; r < m; ++r) part += p[r * step];
-      total += part;
+  float total[kEach] = {};
+  for (int r0 = 0; r0 < R; r0 += kRun) {
+    float x[kEach][kRun];
+#pragma unroll
+    for (int j = 0; j < kEach; ++j)
+#pragma unroll
+      for (int r = 0; r < kRun; ++r)
+        x[j][r] = k0 + tid + j * kGradThreads < k1 && r0 + r < R
+                      ? src[j * kGradThreads + (r0 + r) * step]
+                      : 0.f;
+#pragma unroll
+    for (int j = 0; j < kEach; ++j) {
+      float part = x[j][0];
+#pragma unroll
+      for (int r = 1; r < kRun; ++r) part += x[j][r];
+      total[j] += part;
     }
-    column[k - k0] = total;
   }
+#pragma unroll
+  for (int j = 0; j < kEach; ++j) column[tid + j * kGradThreads] = total[j];
   __syncthreads();
-  for (int b = tid / 32; b < buckets; b += kThreads / 32) {
+  for (int b = tid / 32; b < buckets; b += kGradThreads / 32) {
     const bool past = b < s.n;
     const int i = past ? b : b - s.n;
     // distances [t0, t1) of this bucket, then its offsets' places [lo, hi)
@@ -171,9 +180,14 @@ bucket_bias_grad_kernel(const Starts s, const float *__restrict__ drelpos, int R
   cluster.sync();
   if (cluster.block_rank() == 0) {
     const int blocks = (int)cluster.num_blocks();
-    for (int b = tid; b < buckets; b += kThreads) {
-      float v = sum[b];
-      for (int j = 1; j < blocks; ++j) v += cluster.map_shared_rank(sum, j)[b];
+    for (int b = tid; b < buckets; b += kGradThreads) {
+      float x[kMaxCluster];
+#pragma unroll
+      for (int j = 0; j < kMaxCluster; ++j)
+        x[j] = j < blocks ? cluster.map_shared_rank(sum, j)[b] : 0.f;
+      float v = x[0];
+#pragma unroll
+      for (int j = 1; j < kMaxCluster; ++j) v += x[j];
       dtable[(long long)h * buckets + b] = v;
     }
   }
@@ -184,7 +198,9 @@ bucket_bias_grad_kernel(const Starts s, const float *__restrict__ drelpos, int R
 
 cudaError_t bucket_bias(const BucketProblem &q, const float *table, float *relpos) {
   const int rows = 2 * q.C - 1;
-  bucket_bias_kernel<<<dim3((rows + kThreads - 1) / kThreads, q.H), kThreads, 0, q.stream>>>(
+  // an offset a thread where there are few, four blocks an SM where there are many
+  const int most = q.H < 608 ? 608 / q.H : 1, blocks = (rows + kThreads - 1) / kThreads;
+  bucket_bias_kernel<<<dim3(blocks < most ? blocks : most, q.H), kThreads, 0, q.stream>>>(
       make_starts(q), table, q.buckets, q.C, relpos);
   return cudaGetLastError();
 }
@@ -192,12 +208,11 @@ cudaError_t bucket_bias(const BucketProblem &q, const float *table, float *relpo
 cudaError_t bucket_bias_grad(const BucketProblem &q, const float *drelpos, int R, float *dtable) {
   const int rows = 2 * q.C - 1;
   int blocks = 1;
-  while (blocks < kMaxCluster && rows > blocks * kThreads) blocks *= 2;
+  while (blocks < kMaxCluster && rows > blocks * kThreads) blocks *= 2;  // 256 offsets a block
   const int slice = (rows + blocks - 1) / blocks;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(blocks, q.H);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = slice * sizeof(float);
+  cfg.blockDim = dim3(kGradThreads);
   cfg.stream = q.stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;

@@ -138,23 +138,28 @@ __device__ __forceinline__ Eight times_scale(uint2 codes, float s) {
   }
   return e;
 }
-__device__ __forceinline__ Eight load_codes(const signed char *codes, const float *scales, int c,
-                                            int d, bool vec) {
-  uint2 w = make_uint2(0, 0);
-  const float s = c < d ? scales[c / kGroup] : 0.f;
-  if (vec) {
-    if (c < d) w = *reinterpret_cast<const uint2 *>(codes + c);
-  } else {
+struct Packed {
+  uint2 codes;
+  float scale;
+  __device__ void load(const signed char *row, const float *scales, int c, int d, bool vec) {
+    codes = make_uint2(0, 0);
+    scale = c < d ? scales[c / kGroup] : 0.f;
+    if (vec) {
+      if (c < d) codes = *reinterpret_cast<const uint2 *>(row + c);
+    } else {
 #pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      const uint32_t b = c + q < d ? (uint32_t)(uint8_t)codes[c + q] : 0u;
-      (q < 4 ? w.x : w.y) |= b << (8 * (q & 3));
+      for (int q = 0; q < 8; ++q) {
+        const uint32_t b = c + q < d ? (uint32_t)(uint8_t)row[c + q] : 0u;
+        (q < 4 ? codes.x : codes.y) |= b << (8 * (q & 3));
+      }
     }
   }
-  Eight e = times_scale(w, s);
-  if (!vec && c + 8 > d) e.zero_from(d - c);  // 0 times a scale that is not finite
-  return e;
-}
+  __device__ Eight values(int c, int d, bool vec) const {
+    Eight e = times_scale(codes, scale);
+    if (!vec && c + 8 > d) e.zero_from(d - c);  // 0 times a scale that is not finite
+    return e;
+  }
+};
 
 // The values as they are stored, and the bits of the largest magnitude: as whole
 // numbers magnitudes keep their order, NaN above infinity.
@@ -358,6 +363,8 @@ __global__ void __launch_bounds__(32 * (WARPS > 4 ? WARPS : 4)) pack_kernel(cons
 }
 
 // ---------------------------------------------------------------- restore --
+// (two or four rows a warp with all their codes asked for at first: 13.0 and 17.3
+// us for 12.3 at 16384 x 768 bf16)
 template <typename T, int NC, int WARPS>
 __global__ void __launch_bounds__(32 * (WARPS > 4 ? WARPS : 4)) restore_kernel(const CheckpointArgs a) {
   __shared__ float part[2 * WARPS];
@@ -365,12 +372,15 @@ __global__ void __launch_bounds__(32 * (WARPS > 4 ? WARPS : 4)) restore_kernel(c
   const int t = threadIdx.x % (32 * WARPS);
   const long long m = (long long)blockIdx.x * (WARPS == 1 ? 4 : 1) + threadIdx.x / (32 * WARPS);
   ptx::griddep_wait();
-  if (m >= a.M) return;
+  if (m >= a.M) return;  // whole warps, and with more than one whole blocks
   const long long at = m * a.d;
-  Eight x[NC];
+  Packed p[NC];
 #pragma unroll
   for (int k = 0; k < NC; ++k)
-    x[k] = load_codes(a.codes + at, a.scales + m * a.groups, (k * 32 * WARPS + t) * 8, a.d, a.vec);
+    p[k].load(a.codes + at, a.scales + m * a.groups, (k * 32 * WARPS + t) * 8, a.d, a.vec);
+  Eight x[NC];
+#pragma unroll
+  for (int k = 0; k < NC; ++k) x[k] = p[k].values((k * 32 * WARPS + t) * 8, a.d, a.vec);
   if (a.r) {
     T *r = static_cast<T *>(a.r) + at;
 #pragma unroll
@@ -610,8 +620,12 @@ __global__ void __launch_bounds__(32 * (WARPS > 4 ? WARPS : 4)) backward_kernel(
     const long long at = m * a.d;
     Eight x[NC], w[NC];
 #pragma unroll
-    for (int k = 0; k < NC; ++k)
-      x[k] = load_codes(a.codes + at, a.scales + m * a.groups, (k * 32 * WARPS + t) * 8, a.d, vec);
+    for (int k = 0; k < NC; ++k) {
+      const int c = (k * 32 * WARPS + t) * 8;
+      Packed p;
+      p.load(a.codes + at, a.scales + m * a.groups, c, a.d, vec);
+      x[k] = p.values(c, a.d, vec);
+    }
 #pragma unroll
     for (int k = 0; k < NC; ++k)
       w[k] = load8(static_cast<const T *>(a.dn) + at, (k * 32 * WARPS + t) * 8, a.d, vec);
