@@ -973,7 +973,7 @@ def bucket_bias(table, C, causal, max_distance=128, out=None, stream=None):
     buckets = lead[-1]
     shape = lead[:-1] + (max(2 * C - 1, 0),)
     if out is None:
-        out = table.new_empty(shape)
+        out = torch.empty(shape, dtype=f32, device=dev)
         op = out.data_ptr()
     else:
         op = _like(out, "out", shape, f32, at)
@@ -998,7 +998,7 @@ def bucket_bias_backward(drelpos, buckets, causal, max_distance=128, out=None, s
     H = 1 if dims == 1 else given[-2]
     shape = (buckets,) if dims == 1 else (H, buckets)
     if out is None:
-        out = drelpos.new_empty(shape)
+        out = torch.empty(shape, dtype=f32, device=dev)
         op = out.data_ptr()
     else:
         op = _like(out, "out", torch.Size(shape), f32, at)
@@ -1069,7 +1069,7 @@ def checkpoint_pack(h, y=None, norm=NORM_NONE, norm_g=None, norm_b=None, eps=1e-
         np_ = out_n.data_ptr()
     if out is None:
         codes = torch.empty_like(h, dtype=torch.int8)
-        scales = h.new_empty(shape[:-1] + (-(-d // 128),), dtype=torch.float32)
+        scales = torch.empty(shape[:-1] + (-(-d // 128),), dtype=torch.float32, device=dev)
         out, cp, sp = Checkpoint(codes, scales), codes.data_ptr(), scales.data_ptr()
     else:
         cp, sp = _packed(out, shape, at)
@@ -1151,7 +1151,7 @@ def checkpoint_backward(dr, dn, packed, norm=NORM_LAYER, norm_g=None, norm_b=Non
         out[name] = t
         ptrs.append(p)
     if workspace is None:
-        workspace = dn.new_empty(nw, dtype=torch.uint8)
+        workspace = torch.empty(nw, dtype=torch.uint8, device=dev)
         wp = workspace.data_ptr()
     else:
         wp, nw = _dev_ptr(workspace, "workspace"), workspace.numel() * workspace.element_size()

@@ -229,9 +229,12 @@ __device__ __forceinline__ void each(const T *row, int V, const F &f) {
   const int body = (V - head) / kVec, tail = head + body * kVec;
   if ((int)threadIdx.x < head) f(as_float(row[threadIdx.x]), (int)threadIdx.x);
   const uint4 *v = reinterpret_cast<const uint4 *>(row + head);
+  uint4 next = make_uint4(0, 0, 0, 0);  // on its way while another is worked on
+  if ((int)threadIdx.x < body) next = v[threadIdx.x];
 #pragma unroll 1
   for (int k = threadIdx.x; k < body; k += THREADS) {
-    const uint4 w = v[k];
+    const uint4 w = next;
+    if (k + THREADS < body) next = v[k + THREADS];
     const int i = head + k * kVec;
     const uint32_t part[4] = {w.x, w.y, w.z, w.w};
     if constexpr (sizeof(T) == 4) {
@@ -516,7 +519,7 @@ struct Row {
     {
       uint32_t lo = 0xffffffffu, hi = 0;
       each<THREADS>(row, V, [&](float l, int i) {
-        if (l > __int_as_float(0xff800000) && bin(l) == b) {
+        if (l > -kInf && bin(l) == b) {
           const uint32_t key = key_of(l);
           lo = min(lo, key);
           hi = max(hi, key);
@@ -1027,8 +1030,8 @@ __device__ void any_row(Shared &s, const SampleArgs &a, const Settings &set, lon
     uint32_t top = 0;
     int bad = 0, finite = 0;
     each<THREADS>(r.row, a.V, [&](float l, int) {
-      bad |= !(l < __int_as_float(0x7f800000));
-      finite += l > __int_as_float(0xff800000);
+      bad |= !(l < kInf);
+      finite += l > -kInf;
       top = max(top, key_of(l));
     });
     bad = __any_sync(kAll, bad);
@@ -1071,7 +1074,7 @@ __device__ void any_row(Shared &s, const SampleArgs &a, const Settings &set, lon
   if (set.top_k > 0 && set.top_k < finite) {
     k_count = (u64)set.top_k;
     each<THREADS>(r.row, a.V, [&](float l, int) {
-      if (l > __int_as_float(0xff800000)) atomicAdd(&s.first.count[r.bin(l)], 1u);
+      if (l > -kInf) atomicAdd(&s.first.count[r.bin(l)], 1u);
     });
     __syncthreads();
     find_bin<THREADS>(s, s.first, false, k_count, 0, 0);
@@ -1085,9 +1088,8 @@ __device__ void any_row(Shared &s, const SampleArgs &a, const Settings &set, lon
     u64 mass = 0, q_mass = 0;
     uint32_t q_count = 0;
     each<THREADS>(r.row, a.V, [&](float l, int) {
-      if (!(l > __int_as_float(0xff800000))) return;
       const int b = r.bin(l);
-      if (b > last_bin) return;
+      if (b > last_bin || !(l > -kInf)) return;
       const u64 w = r.w(l);
       s.first.add(b, w);
       mass += w;
