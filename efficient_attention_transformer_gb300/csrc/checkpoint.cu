@@ -402,23 +402,26 @@ __global__ void __launch_bounds__(32 * (WARPS > 4 ? WARPS : 4)) restore_kernel(c
 //
 // A thread's column sums alone are 16 registers for each 8 columns, so few warps
 // fit, and few loads with them (registers alone: 59 us at 16384 x 768 bf16, 1.0
-// TB/s).  In rows on 16-byte boundaries each thread therefore brings its part of
-// the next row into shared memory by asynchronous copies while it works on this
-// one: no registers, no barrier, since it reads what it copied itself.
+// TB/s).  For a LayerNorm of rows on 16-byte boundaries each thread therefore
+// brings its part of the next rows into shared memory by asynchronous copies while
+// it works on this one: no registers, no barrier, since it reads what it copied
+// itself.  A ScaleNorm has no column sums; its rows go through registers alone,
+// with as many warps as those leave.
 
-// dx in place of w = dn's row, from the row's values x, with the column sums.
+// dx in place of w = dn's row, from the row's values x, with the column sums (a
+// ScaleNorm has none, its one g's sum is s1).
 // gain(k): a LayerNorm's g of the thread's k-th run.
-template <int NC, int WARPS, typename G>
+template <bool LAYER, int NC, int WARPS, typename G>
 __device__ __forceinline__ void row_gradient(const CheckpointArgs &a, Eight (&x)[NC],
-                                             Eight (&w)[NC], Eight (&sg)[NC], Eight (&sb)[NC],
+                                             Eight (&w)[NC], Eight *sg, Eight *sb,
                                              float &s1, int t, RowSum<WARPS> &row_sum,
                                              const G &gain) {
-  const bool layer = a.norm == FLASH_GAU_NORM_LAYER;
   float length2 = 0.f;
-  const float inv = normalise<NC, WARPS>(x, a.norm, t, a.d, a.eps, row_sum, &length2);
+  const float inv = normalise<NC, WARPS>(
+      x, LAYER ? FLASH_GAU_NORM_LAYER : FLASH_GAU_NORM_SCALE, t, a.d, a.eps, row_sum, &length2);
   f2 sw2 = 0, swu2 = 0;
   float sw = 0.f, swu;
-  if (layer) {
+  if constexpr (LAYER) {
 #pragma unroll
     for (int k = 0; k < NC; ++k) {
       const Eight g = gain(k);
@@ -510,8 +513,7 @@ __global__ void __launch_bounds__(THREADS, 1) ring_backward_kernel(const Checkpo
   __shared__ float part[kRows * 2 * WARPS];
   const int t = threadIdx.x % (32 * WARPS), group = threadIdx.x / (32 * WARPS);
   RowSum<WARPS> row_sum{part + group * 2 * WARPS, group};
-  const bool layer = a.norm == FLASH_GAU_NORM_LAYER;
-  float s1 = 0.f;
+  float s1;
   Eight sg[NC] = {}, sb[NC] = {};
   ptx::griddep_wait();
   auto fetch = [&](long long m, int turn) {
@@ -541,8 +543,7 @@ __global__ void __launch_bounds__(THREADS, 1) ring_backward_kernel(const Checkpo
   for (int i = 0; i < R::kSteps - 1; ++i) fetch(m + i * step, i);
   // a LayerNorm's g, behind the steps
   float *gains = reinterpret_cast<float *>(shared + R::kBytes);
-  if (layer)
-    for (int c = threadIdx.x; c < a.d; c += THREADS) gains[c] = a.norm_g[c];
+  for (int c = threadIdx.x; c < a.d; c += THREADS) gains[c] = a.norm_g[c];
   __syncthreads();
   const Eight none = {{0, 0, 0, 0}};
   for (int turn = 0; m < a.M; m += step, turn = turn + 1 == R::kSteps ? 0 : turn + 1) {
@@ -558,7 +559,7 @@ __global__ void __launch_bounds__(THREADS, 1) ring_backward_kernel(const Checkpo
         w[k] = widen(r.dn(k), THREADS, static_cast<const T *>(nullptr));
       }
     }
-    row_gradient<NC, WARPS>(a, x, w, sg, sb, s1, t, row_sum, [&](int k) {
+    row_gradient<true, NC, WARPS>(a, x, w, sg, sb, s1, t, row_sum, [&](int k) {
       const int c = (k * 32 * WARPS + t) * 8;
       return c < a.d ? load8(gains, c, a.d, true) : none;
     });
@@ -576,12 +577,6 @@ __global__ void __launch_bounds__(THREADS, 1) ring_backward_kernel(const Checkpo
     }
   }
   if (!a.part) return;
-  if (!layer) {
-    s1 = warp_sum(s1);
-    if (threadIdx.x % 32 == 0)
-      a.part[(long long)blockIdx.x * (THREADS / 32) + threadIdx.x / 32] = s1;
-    return;
-  }
   // the block's sums: every group's in shared memory, then column by column
   asm volatile("cp.async.wait_group 0;" ::: "memory");
   __syncthreads();
@@ -604,16 +599,17 @@ __global__ void __launch_bounds__(THREADS, 1) ring_backward_kernel(const Checkpo
 }
 
 // Any rows, element by element where they are not on boundaries.
-template <typename T, int NC, int WARPS>
-__global__ void __launch_bounds__(32 * (WARPS > 4 ? WARPS : 4)) backward_kernel(const CheckpointArgs a) {
+template <typename T, int NC, int WARPS, bool LAYER>
+__global__ void __launch_bounds__(32 * (WARPS > 4 ? WARPS : 4), LAYER ? 1 : WARPS > 4 ? 3 : 6)
+backward_kernel(const CheckpointArgs a) {
   constexpr int kThreads = 32 * (WARPS > 4 ? WARPS : 4), rows = kThreads / 32 / WARPS;
   __shared__ float part[2 * WARPS];
   extern __shared__ float cols[];  // [2][d], one row of warps after another
   RowSum<WARPS> row_sum{part, 0};
   const int t = threadIdx.x % (32 * WARPS);
-  const bool layer = a.norm == FLASH_GAU_NORM_LAYER, vec = a.vec;
+  const bool vec = a.vec;
   float s1 = 0.f;
-  Eight sg[NC] = {}, sb[NC] = {};
+  Eight sg[LAYER ? NC : 1] = {}, sb[LAYER ? NC : 1] = {};
   ptx::griddep_wait();
   for (long long m = (long long)blockIdx.x * rows + threadIdx.x / (32 * WARPS); m < a.M;
        m += (long long)gridDim.x * rows) {
@@ -629,7 +625,7 @@ __global__ void __launch_bounds__(32 * (WARPS > 4 ? WARPS : 4)) backward_kernel(
 #pragma unroll
     for (int k = 0; k < NC; ++k)
       w[k] = load8(static_cast<const T *>(a.dn) + at, (k * 32 * WARPS + t) * 8, a.d, vec);
-    row_gradient<NC, WARPS>(a, x, w, sg, sb, s1, t, row_sum, [&](int k) {
+    row_gradient<LAYER, NC, WARPS>(a, x, w, sg, sb, s1, t, row_sum, [&](int k) {
       return load8(a.norm_g, (k * 32 * WARPS + t) * 8, a.d, a.vec_param);
     });
 #pragma unroll
@@ -644,29 +640,29 @@ __global__ void __launch_bounds__(32 * (WARPS > 4 ? WARPS : 4)) backward_kernel(
     }
   }
   if (!a.part) return;
-  if (!layer) {
+  if constexpr (!LAYER) {
     s1 = warp_sum(s1);
     if (threadIdx.x % 32 == 0)
       a.part[(long long)blockIdx.x * (kThreads / 32) + threadIdx.x / 32] = s1;
-    return;
-  }
-  for (int turn = 0; turn < rows; ++turn) {
-    if (threadIdx.x / (32 * WARPS) == turn) {
+  } else {
+    for (int turn = 0; turn < rows; ++turn) {
+      if (threadIdx.x / (32 * WARPS) == turn) {
 #pragma unroll
-      for (int k = 0; k < NC; ++k)
+        for (int k = 0; k < NC; ++k)
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          const int c = (k * 32 * WARPS + t) * 8 + q;
-          if (c < a.d) {
-            cols[c] = turn ? cols[c] + sg[k].get(q) : sg[k].get(q);
-            cols[a.d + c] = turn ? cols[a.d + c] + sb[k].get(q) : sb[k].get(q);
+          for (int q = 0; q < 8; ++q) {
+            const int c = (k * 32 * WARPS + t) * 8 + q;
+            if (c < a.d) {
+              cols[c] = turn ? cols[c] + sg[k].get(q) : sg[k].get(q);
+              cols[a.d + c] = turn ? cols[a.d + c] + sb[k].get(q) : sb[k].get(q);
+            }
           }
-        }
+      }
+      __syncthreads();
     }
-    __syncthreads();
+    float *to = a.part + (long long)blockIdx.x * 2 * a.d;
+    for (int c = threadIdx.x; c < 2 * a.d; c += kThreads) to[c] = cols[c];
   }
-  float *to = a.part + (long long)blockIdx.x * 2 * a.d;
-  for (int c = threadIdx.x; c < 2 * a.d; c += kThreads) to[c] = cols[c];
 }
 
 // Adds the blocks' sums up: 32 columns a block, its 32 warps taking every 32nd
@@ -726,13 +722,17 @@ cudaError_t launch(const CheckpointArgs &a, unsigned grid, cudaStream_t stream) 
   } else if constexpr (WHAT == kRestore) {
     return launch_pdl(restore_kernel<T, NC, WARPS>, dim3(grid), dim3(kThreads), 0, stream, a);
   } else {
-    const size_t smem = a.part && a.norm == FLASH_GAU_NORM_LAYER ? 2 * a.d * sizeof(float) : 0;
+    if (a.norm != FLASH_GAU_NORM_LAYER)
+      return launch_pdl(backward_kernel<T, NC, WARPS, false>, dim3(grid), dim3(kThreads), 0, stream,
+                        a);
+    const size_t smem = a.part ? 2 * a.d * sizeof(float) : 0;
     if (smem > 48 * 1024) {
       const cudaError_t err =
-          allow_shared<backward_kernel<T, NC, WARPS>>(2 * kCheckpointMaxD * sizeof(float));
+          allow_shared<backward_kernel<T, NC, WARPS, true>>(2 * kCheckpointMaxD * sizeof(float));
       if (err != cudaSuccess) return err;
     }
-    return launch_pdl(backward_kernel<T, NC, WARPS>, dim3(grid), dim3(kThreads), smem, stream, a);
+    return launch_pdl(backward_kernel<T, NC, WARPS, true>, dim3(grid), dim3(kThreads), smem, stream,
+                      a);
   }
 }
 
@@ -825,7 +825,8 @@ cudaError_t checkpoint_restore(const CheckpointArgs &a, int dtype, cudaStream_t 
 }
 
 size_t checkpoint_part_bytes(int d) {
-  return (size_t)kCheckpointBlocks * 2 * (d < 8 ? 8 : d) * sizeof(float);
+  const size_t columns = (size_t)kCheckpointBlocks * 2 * d, warps = kCheckpointScaleBlocks * 8;
+  return (columns > warps ? columns : warps) * sizeof(float);
 }
 
 cudaError_t checkpoint_backward(const CheckpointArgs &args, float *dg, float *db, int dtype,
@@ -834,17 +835,19 @@ cudaError_t checkpoint_backward(const CheckpointArgs &args, float *dg, float *db
   if (!dg && !db) a.part = nullptr;
   Grid g;
   cudaError_t err;
-  if (a.vec) {
+  const bool layer = a.norm == FLASH_GAU_NORM_LAYER;
+  if (a.vec && layer) {
     err = dtype == FLASH_GAU_BF16 ? dispatch_ring<__nv_bfloat16>(a, num_sms, stream, &g)
                                   : dispatch_ring<float>(a, num_sms, stream, &g);
   } else {
-    err = dispatch<kBackward>(a, dtype, kCheckpointBlocks, stream);
+    const unsigned most = layer ? kCheckpointBlocks : kCheckpointScaleBlocks;
+    err = dispatch<kBackward>(a, dtype, most, stream);
     const int warps = row_warps(a.d), rows = warps == 1 ? 4 : 1;
     const long long all = (a.M + rows - 1) / rows;
-    g = {(int)(all < kCheckpointBlocks ? all : kCheckpointBlocks), warps > 4 ? warps : 4};
+    g = {(int)(all < most ? all : most), warps > 4 ? warps : 4};
   }
   if (err != cudaSuccess || !a.part) return err;
-  if (a.norm == FLASH_GAU_NORM_LAYER)
+  if (layer)
     return launch_pdl(join_columns_kernel, dim3((2 * a.d + 31) / 32), dim3(1024), 0, stream,
                       a.part, g.blocks, a.d, dg, db);
   return launch_pdl(join_scalar_kernel, dim3(1), dim3(1024), 0, stream, a.part,

@@ -375,7 +375,8 @@ cudaError_t bucket_bias_grad(const BucketProblem &q, const float *drelpos, int R
 // Activation checkpoints in 8 bits (checkpoint.cu).
 constexpr int kCheckpointGroup = 128;
 constexpr int kCheckpointMaxD = 8192;
-constexpr int kCheckpointBlocks = 608;  // of the backward kernel
+constexpr int kCheckpointBlocks = 608;       // of the backward kernel, LayerNorm
+constexpr int kCheckpointScaleBlocks = 16384;  // and ScaleNorm, which keeps no columns
 struct CheckpointArgs {
   const void *h, *y, *dr, *dn;
   void *r, *n, *dh;      // restore: r is the restored stream

@@ -15,7 +15,7 @@
 //
 // Masses are whole numbers, w in units of 2^-44 (a power that leaves room for
 // V of them): sums do not depend on their order, so a token does not depend on
-// the launch, and a word's place is decided to 2^-41 of the mass where fp32
+// the launch, and a word's place is decided to 2^-40 of the mass where fp32
 // sums would err once in some hundred tokens of a large vocabulary.  Nothing
 // here is in fp64, whose units are so few that one thread's logarithm took
 // longer than a whole row's search: pairs of fp32 numbers and products of whole

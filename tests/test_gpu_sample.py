@@ -1,10 +1,9 @@
 """GPU checks of sampling against the float64 oracle.
 
 Tokens and counts are equal to the oracle's.  Both turn on sums of w, which
-the kernel knows to 2^-41 of w and half a unit of 2^-44, so of the rows here
-(some thousand with up to 50000 words) fewer than one in a million could
-differ.  logp is one rounding of its value, and 2 * 2^-41 and V / 2 units of
-2^-44 of the mass."""
+the kernel knows to 2^-40 of w and half a unit of 2^-44: of the rows here (some
+thousand with up to 140000 words) one in a hundred thousand could differ.  logp
+is one rounding of its value, and 2^-40 and V / 2 units of 2^-44 of the mass."""
 
 import ctypes
 
