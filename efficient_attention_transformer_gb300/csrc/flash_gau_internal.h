@@ -387,8 +387,14 @@ struct CheckpointArgs {
   long long M;
   int d, norm, groups;
   float eps;
-  bool vec, vec_param;   // rows, parameters in whole vectors on their boundaries
+  bool vec;              // rows and parameters in whole vectors on their boundaries
 };
+// Warps of a row: one up to 1024 columns, four up to 4096, eight beyond.
+constexpr int checkpoint_row_warps(int d) { return d <= 1024 ? 1 : d <= 4096 ? 4 : 8; }
+enum { kCheckpointPack, kCheckpointRestore, kCheckpointBackward };
+// the kernels over rows that are not on vectors' boundaries (checkpoint_odd.cu)
+cudaError_t checkpoint_rows_odd(int what, const CheckpointArgs &a, int dtype,
+                                unsigned most_blocks, cudaStream_t stream);
 size_t checkpoint_part_bytes(int d);
 cudaError_t checkpoint_pack(const CheckpointArgs &a, int dtype, cudaStream_t stream);
 cudaError_t checkpoint_restore(const CheckpointArgs &a, int dtype, cudaStream_t stream);
