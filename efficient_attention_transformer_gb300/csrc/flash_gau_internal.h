@@ -387,14 +387,16 @@ struct CheckpointArgs {
   long long M;
   int d, norm, groups;
   float eps;
-  bool vec;              // rows and parameters in whole vectors on their boundaries
+  int form, width;       // how rows lie in memory, columns that a row's threads span
 };
-// Warps of a row: one up to 1024 columns, four up to 4096, eight beyond.
-constexpr int checkpoint_row_warps(int d) { return d <= 1024 ? 1 : d <= 4096 ? 4 : 8; }
 enum { kCheckpointPack, kCheckpointRestore, kCheckpointBackward };
-// the kernels over rows that are not on vectors' boundaries (checkpoint_odd.cu)
-cudaError_t checkpoint_rows_odd(int what, const CheckpointArgs &a, int dtype,
-                                unsigned most_blocks, cudaStream_t stream);
+struct CheckpointGrid {  // of the backward pass: its blocks, and a block's warps
+  int blocks, warps;
+};
+// the kernels over rows that are not whole vectors on their boundaries
+// (checkpoint_odd.cu)
+cudaError_t checkpoint_rows_odd(int what, const CheckpointArgs &a, int dtype, int num_sms,
+                                cudaStream_t stream, CheckpointGrid *g);
 size_t checkpoint_part_bytes(int d);
 cudaError_t checkpoint_pack(const CheckpointArgs &a, int dtype, cudaStream_t stream);
 cudaError_t checkpoint_restore(const CheckpointArgs &a, int dtype, cudaStream_t stream);

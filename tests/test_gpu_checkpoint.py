@@ -132,6 +132,39 @@ def test_sizes(M, d, dtype):
     check(Problem(M, d, dtype, "layer", M + d))
 
 
+# Widths on both sides of what a row's threads span with up to seven columns in
+# front, and enough rows that each of a LayerNorm's warps has several.
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("norm", ["layer", "scale"])
+@pytest.mark.parametrize("M,d", [(2600, 249), (2500, 250), (2500, 511), (3001, 761), (1999, 762),
+                                 (1500, 767), (1300, 1017), (1301, 1018), (700, 1501), (333, 2041),
+                                 (334, 2042), (320, 4089), (317, 4090), (200, 6001), (170, 8185),
+                                 (170, 8186), (4001, 12), (5000, 7)])
+def test_rows_that_are_not_whole_vectors(M, d, norm, dtype):
+    check(Problem(M, d, dtype, norm, 5))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("M,d", [(1, 5), (3, 129), (5, 767), (9, 1500), (3, 4099), (4, 256)])
+def test_nothing_beside_the_arrays_is_written(M, d, dtype):
+    """codes, scales and r in the middle of larger buffers; the others' neighbours
+    are the rows before and behind, whose values every test compares."""
+    groups, g = -(-d // 128), torch.Generator().manual_seed(3)
+    codes = torch.full((16 + M * d + 16,), 77, dtype=torch.int8, device="cuda")
+    scales = torch.full((16 + M * groups + 16,), 7.0, device="cuda")
+    h = torch.full((16 + M * d + 16,), 3.0, dtype=dtype, device="cuda")
+    inner = lambda x, n: x[16:16 + n]  # noqa: E731
+    rows = inner(h, M * d).view(M, d)
+    rows.copy_(torch.randn(M, d, generator=g))
+    packed = bd.Checkpoint(inner(codes, M * d).view(M, d),
+                           inner(scales, M * groups).view(M, groups))
+    want = oracle.checkpoint_codes(f64(rows) * 2)
+    bd.checkpoint_pack(rows, rows.clone(), out=packed, out_r=rows)
+    for x, v in ((codes, 77), (scales, 7.0), (h, 3.0)):
+        assert (x[:16] == v).all() and (x[-16:] == v).all()
+    assert (packed.codes.cpu().numpy() == want[0]).all()
+
+
 @pytest.mark.parametrize("dtype", ["fp32", "bf16"])
 @pytest.mark.parametrize("norm", ["none", "layer", "scale"])
 @pytest.mark.parametrize("with_y", [True, False])
