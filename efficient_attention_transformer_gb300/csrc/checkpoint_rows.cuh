@@ -9,9 +9,11 @@
 //
 // All three move rows once: in bf16 9, 5 and 7 bytes an element with the
 // scales' 4 / 128, so memory bounds them.  A row belongs to one warp (up to
-// 1024 columns) or to the four warps of a block, 8 consecutive columns a
+// 1024 columns), to four or to the eight of a block, 8 consecutive columns a
 // thread and step: 16 or 32 bytes of a row, 8 codes, and a group is 16
-// neighbouring threads, whose maximum is four shuffles.
+// neighbouring threads, whose maximum is four shuffles.  32768 x 1024 fp32 with
+// ScaleNorm: pack 84 us, 6.8 TB/s, restore 55, 5.5, gradients 71, 6.1; 16384 x
+// 768 bf16 with LayerNorm, half of it in L2: 20, 12 and 22 us.
 //
 // A code is exact by its definition, not by the luck of a reciprocal: the
 // rounded product x * (1 / scale) is at most one off, the remainder x - code *
@@ -587,7 +589,7 @@ restore_kernel(const CheckpointArgs a) {
 //
 // A thread's column sums alone are 16 registers for each 8 columns, so few warps
 // fit, and few loads with them (registers alone: 59 us at 16384 x 768 bf16, 1.0
-// TB/s).  For a LayerNorm of rows on 16-byte boundaries each thread therefore
+// TB/s; with the copies 22).  For a LayerNorm of rows on 16-byte boundaries each thread therefore
 // brings its part of the next rows into shared memory by asynchronous copies while
 // it works on this one: no registers, no barrier, since it reads what it copied
 // itself.  A ScaleNorm has no column sums; its rows go through registers alone,
