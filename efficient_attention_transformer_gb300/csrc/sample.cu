@@ -20,12 +20,15 @@
 // here is in fp64, whose units are so few that one thread's logarithm took
 // longer than a whole row's search: pairs of fp32 numbers and products of whole
 // numbers give the digits.
+#include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
 #include "flash_gau_internal.h"
 
 namespace flashgau {
 namespace {
+
+namespace cg = cooperative_groups;
 
 constexpr unsigned kAll = 0xffffffffu;
 constexpr int kBins = 2048;
@@ -221,20 +224,47 @@ __device__ __forceinline__ float value_of(uint32_t key) {
 __device__ __forceinline__ float as_float(float x) { return x; }
 __device__ __forceinline__ float as_float(__nv_bfloat16 x) { return __bfloat162float(x); }
 
-// f(l, i) for every word of a row: 16 bytes a load between its boundaries.
-template <int THREADS, typename T, typename F>
-__device__ __forceinline__ void each(const T *row, int V, const F &f) {
+constexpr int kMostBlocks = 8;
+
+// The blocks of a row: one, or a cluster's (two, four or eight), each of which
+// reads a part of the row and then holds what all have found.  They decide on the
+// same numbers, so that all come to the same barriers.
+template <bool MANY>
+struct Blocks {
+  int rank = 0, size = 1;
+  __device__ Blocks() {
+    if constexpr (MANY) {
+      rank = (int)cg::this_cluster().block_rank();
+      size = (int)cg::this_cluster().num_blocks();
+    }
+  }
+  __device__ void meet() const {
+    if constexpr (MANY) cg::this_cluster().sync();
+    else __syncthreads();
+  }
+  template <typename P>
+  __device__ P *of(P *p, int other) const {
+    if constexpr (MANY) return cg::this_cluster().map_shared_rank(p, other);
+    else return p;
+  }
+};
+
+// f(l, i) for every word of a row, or the block's part of it: 16 bytes a load
+// between the row's boundaries.
+template <int THREADS, typename T, typename B, typename F>
+__device__ __forceinline__ void each(const T *row, int V, const B &blocks, const F &f) {
   constexpr int kVec = 16 / sizeof(T);
   const int head = min(V, (int)((16 - reinterpret_cast<uintptr_t>(row) % 16) % 16 / sizeof(T)));
   const int body = (V - head) / kVec, tail = head + body * kVec;
-  if ((int)threadIdx.x < head) f(as_float(row[threadIdx.x]), (int)threadIdx.x);
+  const int first = blocks.rank * THREADS + (int)threadIdx.x, step = blocks.size * THREADS;
+  if (first < head) f(as_float(row[first]), first);
   const uint4 *v = reinterpret_cast<const uint4 *>(row + head);
   uint4 next = make_uint4(0, 0, 0, 0);  // on its way while another is worked on
-  if ((int)threadIdx.x < body) next = v[threadIdx.x];
+  if (first < body) next = v[first];
 #pragma unroll 1
-  for (int k = threadIdx.x; k < body; k += THREADS) {
+  for (int k = first; k < body; k += step) {
     const uint4 w = next;
-    if (k + THREADS < body) next = v[k + THREADS];
+    if (k + step < body) next = v[k + step];
     const int i = head + k * kVec;
     const uint32_t part[4] = {w.x, w.y, w.z, w.w};
     if constexpr (sizeof(T) == 4) {
@@ -248,7 +278,7 @@ __device__ __forceinline__ void each(const T *row, int V, const F &f) {
       }
     }
   }
-  if (tail + (int)threadIdx.x < V) f(as_float(row[tail + threadIdx.x]), tail + (int)threadIdx.x);
+  if (tail + first < V) f(as_float(row[tail + first]), tail + first);
 }
 
 struct Bins {
@@ -412,7 +442,43 @@ struct Shared : Tally {
   u64 weight[kFew];
   int listed;
   uint32_t lo, hi;
+  // of all the row's blocks
+  uint32_t all_top, all_q_count;
+  int all_bad, all_finite;
+  u64 all_mass, all_q_mass;
 };
+
+// What each block has added to its bins becomes what all have, and `also` is done
+// by the first warp while the blocks' other sums stand.
+template <bool MANY, typename F>
+__device__ void share(const Blocks<MANY> &blocks, Bins &bins, const F &also) {
+  blocks.meet();
+  if constexpr (MANY) {  // a block adds up some of the bins for all
+    const int some = kBins / blocks.size;
+    for (int t = threadIdx.x; t < some; t += blockDim.x) {
+      const int b = blocks.rank * some + t;
+      uint32_t count = 0;
+      u64 mass = 0;
+#pragma unroll
+      for (int k = 0; k < kMostBlocks; ++k) {  // their loads under way at once
+        if (k >= blocks.size) continue;
+        const Bins *other = blocks.of(&bins, (blocks.rank + k) & (blocks.size - 1));
+        count += other->count[b];
+        mass += other->mass(b);
+      }
+#pragma unroll
+      for (int k = 0; k < kMostBlocks; ++k) {
+        if (k >= blocks.size) continue;
+        Bins *other = blocks.of(&bins, (blocks.rank + k) & (blocks.size - 1));
+        other->count[b] = count;
+        other->low[b] = (uint32_t)mass;
+        other->high[b] = (uint32_t)(mass >> 32);
+      }
+    }
+    if (threadIdx.x < 32) also();
+    blocks.meet();
+  }
+}
 
 // A place in the order of words: all words above `key`, and `ties` of those
 // with that key.
@@ -490,13 +556,14 @@ __device__ void find_bin(Shared &s, const Bins &b, bool by_mass, u64 target, u64
   first_threads(THREADS);
 }
 
-template <typename T, int THREADS>
+template <typename T, int THREADS, bool MANY>
 struct Row {
   static constexpr int kThreads = THREADS, kWarps = THREADS / 32;
   const T *row;
   int V;
   Weigh w;
   float per;  // bins of l a unit of l
+  Blocks<MANY> blocks;
 
   __device__ int bin(float l) const {
     return min(kBins - 1, __float2int_rz((w.top - l) * per));
@@ -515,29 +582,40 @@ struct Row {
       s.hi = 0;
     }
     first_threads(THREADS);
+    if (MANY) blocks.meet();  // before the others write to these
     const bool list = n <= kList;
     {
       uint32_t lo = 0xffffffffu, hi = 0;
-      each<THREADS>(row, V, [&](float l, int i) {
+      each<THREADS>(row, V, blocks, [&](float l, int i) {
         if (l > -kInf && bin(l) == b) {
           const uint32_t key = key_of(l);
           lo = min(lo, key);
           hi = max(hi, key);
           if (list) {
-            const int at = atomicAdd(&s.listed, 1);
+            const int at = atomicAdd(blocks.of(&s.listed, 0), 1);
             if (at < kList) {
-              s.key[at] = key;
-              s.index[at] = i;
+              for (int k = 0; k < blocks.size; ++k) {
+                blocks.of(s.key, k)[at] = key;
+                blocks.of(s.index, k)[at] = i;
+              }
             }
           }
         }
       });
-      if (lo <= hi) {
+      if (MANY) {
+        lo = __reduce_min_sync(kAll, lo);
+        hi = __reduce_max_sync(kAll, hi);
+        if ((int)(threadIdx.x % 32) < blocks.size && lo <= hi) {
+          atomicMin(blocks.of(&s.lo, threadIdx.x % 32), lo);
+          atomicMax(blocks.of(&s.hi, threadIdx.x % 32), hi);
+        }
+      } else if (lo <= hi) {
         atomicMin(&s.lo, lo);
         atomicMax(&s.hi, hi);
       }
     }
-    first_threads(THREADS);
+    if (MANY) blocks.meet();
+    else first_threads(THREADS);
     uint32_t lo = s.lo, hi = s.hi;
     if (lo < hi && n <= kFew) return place_few(s, by_mass, target, count0, mass0, (int)n);
     // down to one key: bins of (hi - key) >> shift, 11 bits of 32 each time
@@ -551,10 +629,11 @@ struct Row {
           if (key >= lo && key <= hi) s.fine.add((hi - key) >> shift, w(value_of(key)));
         }
       } else {
-        each<THREADS>(row, V, [&](float l, int) {
+        each<THREADS>(row, V, blocks, [&](float l, int) {
           const uint32_t key = key_of(l);
           if (key >= lo && key <= hi && bin(l) == b) s.fine.add((hi - key) >> shift, w(l));
         });
+        if (MANY) share(blocks, s.fine, [] {});
       }
       first_threads(THREADS);
       find_bin<THREADS>(s, s.fine, by_mass, target, count0, mass0);
@@ -1005,14 +1084,16 @@ __device__ bool counted_row(Counted &s, const SampleArgs &a, const Settings &set
 }
 
 // ---- the general form ---------------------------------------------------------
+// (Of few long rows each block of a cluster reads a part: what a pass finds is
+// joined at its end, and the steps between the passes are taken by all alike.)
 // One pass finds the largest logit, one adds words and masses into 2048 bins of l
 // over the range in which w is not zero, a scan over the bins finds the bin of a
 // place, and the few words of that bin are looked at one by one, or, where they
 // are many, by bins of their keys, as often as it takes to come down to one value.
-template <typename T, int THREADS>
+template <typename T, int THREADS, bool MANY>
 __device__ void any_row(Shared &s, const SampleArgs &a, const Settings &set, long long n) {
   const int tid = threadIdx.x, lane = tid % 32;
-  Row<T, THREADS> r;
+  Row<T, THREADS, MANY> r;
   r.row = static_cast<const T *>(a.logits) + n * a.ld;
   r.V = a.V;
 
@@ -1029,7 +1110,7 @@ __device__ void any_row(Shared &s, const SampleArgs &a, const Settings &set, lon
   {
     uint32_t top = 0;
     int bad = 0, finite = 0;
-    each<THREADS>(r.row, a.V, [&](float l, int) {
+    each<THREADS>(r.row, a.V, r.blocks, [&](float l, int) {
       bad |= !(l < kInf);
       finite += l > -kInf;
       top = max(top, key_of(l));
@@ -1043,17 +1124,31 @@ __device__ void any_row(Shared &s, const SampleArgs &a, const Settings &set, lon
       atomicAdd(&s.finite, finite);
     }
   }
-  __syncthreads();
-  const uint32_t top_key = s.lo;
-  const int finite = s.finite;
-  // settings that are no numbers, or a row without a distribution
-  if (s.bad || !finite || !set.usable()) {
-    if (tid == 0) no_token(a, n);
-    return;
+  r.blocks.meet();
+  if (MANY) {
+    if (tid < 32) {
+      const Shared *other = r.blocks.of(&s, tid < r.blocks.size ? tid : r.blocks.rank);
+      const uint32_t most = __reduce_max_sync(kAll, other->lo);
+      const int any_bad = __any_sync(kAll, other->bad);
+      const int some = __reduce_add_sync(kAll, tid < r.blocks.size ? other->finite : 0);
+      if (tid == 0) {
+        s.all_top = most;
+        s.all_bad = any_bad;
+        s.all_finite = some;
+      }
+    }
+    __syncthreads();
   }
+  const uint32_t top_key = MANY ? s.all_top : s.lo;
+  const int finite = MANY ? s.all_finite : s.finite;
   r.w.top = value_of(top_key);
-  if (set.temperature < kNoTemperature) {
-    greedy<THREADS>(s, a, n, r.row, r.w.top);
+  // settings that are no numbers, or a row without a distribution
+  const bool none = (MANY ? s.all_bad : s.bad) || !finite || !set.usable();
+  if (none || set.temperature < kNoTemperature) {
+    if (MANY) r.blocks.meet();  // the others may still read
+    if (r.blocks.rank) return;
+    if (!none) greedy<THREADS>(s, a, n, r.row, r.w.top);
+    else if (tid == 0) no_token(a, n);
     return;
   }
   r.w.temperature(set.temperature);
@@ -1073,10 +1168,10 @@ __device__ void any_row(Shared &s, const SampleArgs &a, const Settings &set, lon
   u64 k_count = 0;
   if (set.top_k > 0 && set.top_k < finite) {
     k_count = (u64)set.top_k;
-    each<THREADS>(r.row, a.V, [&](float l, int) {
+    each<THREADS>(r.row, a.V, r.blocks, [&](float l, int) {
       if (l > -kInf) atomicAdd(&s.first.count[r.bin(l)], 1u);
     });
-    __syncthreads();
+    share(r.blocks, s.first, [] {});
     find_bin<THREADS>(s, s.first, false, k_count, 0, 0);
     last_bin = s.bin;
     __syncthreads();
@@ -1087,7 +1182,7 @@ __device__ void any_row(Shared &s, const SampleArgs &a, const Settings &set, lon
   {
     u64 mass = 0, q_mass = 0;
     uint32_t q_count = 0;
-    each<THREADS>(r.row, a.V, [&](float l, int) {
+    each<THREADS>(r.row, a.V, r.blocks, [&](float l, int) {
       const int b = r.bin(l);
       if (b > last_bin || !(l > -kInf)) return;
       const u64 w = r.w(l);
@@ -1110,10 +1205,25 @@ __device__ void any_row(Shared &s, const SampleArgs &a, const Settings &set, lon
       atomicAdd(&s.q_count, q_count);
     }
   }
-  __syncthreads();
-  u64 kept = (u64)finite, mass = s.sum_mass;
-  const u64 q_mass = s.q_mass;
-  const uint32_t q_count = s.q_count;
+  share(r.blocks, s.first, [&] {
+    const bool is = tid < r.blocks.size;
+    const Shared *other = r.blocks.of(&s, is ? tid : r.blocks.rank);
+    u64 all = is ? other->sum_mass : 0, q = is ? other->q_mass : 0;
+    const uint32_t count = __reduce_add_sync(kAll, is ? other->q_count : 0);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      all += __shfl_xor_sync(kAll, all, o);
+      q += __shfl_xor_sync(kAll, q, o);
+    }
+    if (tid == 0) {
+      s.all_mass = all;
+      s.all_q_mass = q;
+      s.all_q_count = count;
+    }
+  });
+  u64 kept = (u64)finite, mass = MANY ? s.all_mass : s.sum_mass;
+  const u64 q_mass = MANY ? s.all_q_mass : s.q_mass;
+  const uint32_t q_count = MANY ? s.all_q_count : s.q_count;
   if (k_count) {
     find_bin<THREADS>(s, s.first, false, k_count, 0, 0);
     const Place p = r.place(s, false, k_count);
@@ -1136,20 +1246,22 @@ __device__ void any_row(Shared &s, const SampleArgs &a, const Settings &set, lon
   const u64 target = set.draw(mass);
   find_bin<THREADS>(s, s.first, true, target, 0, 0);
   const Place p = r.place(s, true, target);
+  if (r.blocks.rank) return;
   finish<THREADS>(s, a, n, r.row, r.w, value_of(p.key), p.ties, p.equal, p.index, kept, mass);
 }
 
-template <int THREADS>
+template <int THREADS, bool MANY>
 __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_f32_kernel(const SampleArgs a) {
   extern __shared__ __align__(16) unsigned char raw[];
-  const Settings set(a, blockIdx.x);
-  any_row<float, THREADS>(*reinterpret_cast<Shared *>(raw), a, set, blockIdx.x);
+  const long long n = MANY ? blockIdx.y : blockIdx.x;
+  const Settings set(a, n);
+  any_row<float, THREADS, MANY>(*reinterpret_cast<Shared *>(raw), a, set, n);
 }
 
 template <int THREADS>
 __device__ __noinline__ void any_bf16_row(Shared &s, const SampleArgs &a, const Settings &set,
                                           long long n) {
-  any_row<__nv_bfloat16, THREADS>(s, a, set, n);
+  any_row<__nv_bfloat16, THREADS, false>(s, a, set, n);
 }
 
 template <int THREADS>
@@ -1178,14 +1290,40 @@ cudaError_t sample(SampleArgs a, int N, int dtype, int num_sms, cudaStream_t str
   // bf16: two blocks an SM, the memory that can be shared being theirs, so that one
   // counts while the other searches (256 x 131072: 42 us; one of 1024 threads 46;
   // a single row takes the same either way).  fp32: the same for more rows than
-  // SMs (333 x 8003: 25 us for 32), else one of 1024 (64 x 32000: 29 us for 39),
-  // which keep the row in the rest of that memory.
+  // SMs (333 x 8003: 25 us for 32), else blocks of 1024 (64 x 32000 in one a row: 29
+  // us for 39), which keep the row in the rest of that memory.
   constexpr size_t kSmem = sizeof(Counted) > sizeof(Shared) ? sizeof(Counted) : sizeof(Shared);
   if (dtype == FLASH_GAU_BF16)
     return launch<sample_bf16_kernel<512>>(kSmem, true, 512, a, N, stream);
   if (N > num_sms)
-    return launch<sample_f32_kernel<512>>(sizeof(Shared), false, 512, a, N, stream);
-  return launch<sample_f32_kernel<1024>>(sizeof(Shared), false, 1024, a, N, stream);
+    return launch<sample_f32_kernel<512, false>>(sizeof(Shared), false, 512, a, N, stream);
+  // Few long rows: a cluster of blocks a row, where its clusters find room at once
+  // (fewer as they grow: a cluster is one GPC's) and a row's passes are long
+  // enough for the two barriers and the exchange at each pass's end.  Of fp32, no
+  // filter, one block, two, four and eight: 1 x 131072 79, 49, 31, 23 us; 14 x 131072
+  // 87, 59, 41, 32; 33 x 50257 39, 31, 24, 50; 76 x 50257 47, 39, 61, 97; 4 x 24000
+  // 21, 19, 17, 15.  The mean over all filters breaks even near 28000 words for
+  // two, 20000 for four, 16000 for eight.
+  int blocks = 1;
+  if (a.V >= 16384 && N * kMostBlocks <= num_sms * 3 / 4) blocks = 8;
+  else if (a.V >= 20480 && N * 4 <= num_sms * 7 / 8) blocks = 4;
+  else if (a.V >= 28672 && N * 2 <= num_sms) blocks = 2;
+  if (blocks == 1)
+    return launch<sample_f32_kernel<1024, false>>(sizeof(Shared), false, 1024, a, N, stream);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(blocks, N);
+  cfg.blockDim = dim3(1024);
+  cfg.dynamicSmemBytes = sizeof(Shared);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = blocks;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t err = allow_shared<sample_f32_kernel<1024, true>>(sizeof(Shared), false);
+  if (err != cudaSuccess) return err;
+  return cudaLaunchKernelEx(&cfg, sample_f32_kernel<1024, true>, a);
 }
 
 }  // namespace flashgau

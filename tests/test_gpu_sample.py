@@ -147,6 +147,90 @@ def test_masked_and_unusable_rows(mode, dtype):
     check(torch.tensor(l).to(dtype), torch.tensor(rng.random(N), dtype=torch.float32), kw)
 
 
+# Long rows of fp32, few enough that several blocks take each.
+@pytest.mark.parametrize("mode", MODES)
+@pytest.mark.parametrize("N,V", [(1, 16384), (14, 16385), (1, 131072), (15, 20480), (33, 20483),
+                                 (34, 28672), (76, 28675), (77, 28672), (2, 300001)])
+def test_long_rows(N, V, mode):
+    rng = np.random.default_rng(V + N)
+    logits = torch.tensor(rng.normal(size=(N, V)) * 3, dtype=torch.float32)
+    logits[torch.tensor(rng.random((N, V)) < 0.1)] = -float("inf")
+    check(logits, torch.tensor(rng.random(N), dtype=torch.float32), settings(mode, N, rng, V),
+          rows=sorted({0, N // 2, N - 1}))
+
+
+@pytest.mark.parametrize("mode", MODES)
+@pytest.mark.parametrize("N", [3, 20, 40])
+@pytest.mark.parametrize("kind", ["few values", "close together", "one word", "last words"])
+def test_long_rows_of_a_kind(kind, N, mode):
+    V = 30011
+    rng = np.random.default_rng(N)
+    if kind == "few values":
+        x = rng.integers(0, 3, (N, V)) * 0.37 - 1
+    elif kind == "close together":
+        x = 20 + rng.normal(size=(N, V)) * 1e-3
+    else:
+        x = np.full((N, V), -np.inf)
+        if kind == "one word":
+            x[np.arange(N), rng.integers(0, V, N)] = rng.normal(size=N)
+        else:
+            x[:, V - 5:] = rng.normal(size=(N, 5))
+    kw = settings(mode, N, rng, V)
+    if "top_k" in kw:
+        kw["top_k"] = torch.tensor(rng.integers(1, V, N), dtype=torch.int32)
+    check(torch.tensor(x, dtype=torch.float32), torch.tensor(rng.random(N), dtype=torch.float32),
+          kw, rows=sorted({0, 1, N - 1}))
+
+
+@pytest.mark.parametrize("N", [8, 24, 60])
+def test_long_rows_of_every_outcome_at_once(N):
+    """Greedy rows, rows without a distribution and unusable settings beside
+    ordinary ones: each leaves by a way of its own."""
+    V, rng = 30000, np.random.default_rng(N)
+    logits = torch.tensor(rng.normal(size=(N, V)), dtype=torch.float32)
+    kw = settings("all", N, rng, V)
+    logits[0] = -float("inf")
+    logits[1, 29999] = float("nan")
+    logits[2, 7] = float("inf")
+    kw["temperature"][3] = 0.0
+    kw["temperature"][4] = -1.0
+    kw["top_p"][5] = float("nan")
+    kw["top_k"][6] = 1
+    token, _, _ = check(logits, torch.tensor(rng.random(N), dtype=torch.float32), kw)
+    assert (token[[0, 1, 2, 4, 5]] == -1).all()
+
+
+def test_long_rows_do_not_depend_on_their_number():
+    """One block a row, or a cluster of two, four or eight: the same bits, on
+    replays of a captured call too."""
+    V, rng = 33001, np.random.default_rng(8)
+    rows = torch.tensor(rng.normal(size=(100, V)) * 2, dtype=torch.float32).cuda()
+    u = torch.tensor(rng.random(100), dtype=torch.float32).cuda()
+    kw = dict(top_k=1000, top_p=0.9, min_p=0.001, temperature=0.8)
+    want = [x.clone() for x in bd.sample(rows, u, **kw)]
+    for n in (1, 14, 33, 76):
+        got = bd.sample(rows[:n], u[:n], **kw)
+        assert all(torch.equal(g, w[:n]) for g, w in zip(got, want)), n
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            again = bd.sample(rows[:n], u[:n], **kw)
+        for _ in range(3):
+            for x in again:
+                x.fill_(-7)
+            graph.replay()
+            torch.cuda.synchronize()
+            assert all(torch.equal(g, w[:n]) for g, w in zip(again, want)), n
+
+
+@pytest.mark.parametrize("N,offset,ld", [(5, 1, 20001), (16, 3, 24007), (40, 2, 30002)])
+def test_long_rows_further_apart_and_odd_addresses(N, offset, ld):
+    V, rng = ld - 9, np.random.default_rng(ld)
+    flat = torch.tensor(rng.normal(size=N * ld + offset), dtype=torch.float32).cuda()
+    logits = flat[offset:].view(N, ld)[:, :V]
+    u = torch.tensor(rng.random(N), dtype=torch.float32)
+    check(logits, u, settings("all", N, rng, V), rows=[0, N - 1])
+
+
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("offset,ld", [(1, 1001), (3, 1016), (0, 1004), (5, 2001)])
 def test_rows_further_apart_and_odd_addresses(dtype, offset, ld):
