@@ -160,7 +160,8 @@ __device__ __forceinline__ uint32_t words_to(u64 mass, u64 one) {
   return n;
 }
 
-// A row's settings, as they are given.
+// A row's settings.  No word reaches a min_p above 1: the first one alone is left,
+// as of top_k 1.
 struct Settings {
   float temperature, top_p, min_p, u;
   int top_k;
@@ -169,7 +170,12 @@ struct Settings {
         top_p(a.top_p ? a.top_p[n] : 1.f),
         min_p(a.min_p ? a.min_p[n] : 0.f),
         u(a.u[n]),
-        top_k(a.top_k ? a.top_k[n] : 0) {}
+        top_k(a.top_k ? a.top_k[n] : 0) {
+    if (min_p > 1.f) {
+      min_p = 0.f;
+      top_k = 1;
+    }
+  }
   __device__ bool usable() const {
     return temperature >= 0.f && top_p == top_p && min_p == min_p && u >= 0.f;
   }
@@ -187,7 +193,7 @@ struct Settings {
   }
   // the smallest logit that min_p lets through: top + T ln(min_p), rounded up
   __device__ float least(float top, const u64 *pow) const {
-    if (min_p >= 1.f) return top;
+    if (min_p == 1.f) return top;
     const uint32_t b = __float_as_uint(min_p), e = b >> 23;
     const uint32_t digits = e ? (b & 0x7fffffu) | 0x800000u : b;
     const int lead = __clz(digits);  // min_p = digits 2^(max(e, 1) - 150)

@@ -109,7 +109,7 @@ def sample_row(l, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0):
             before += w[kept]
             kept += 1
     if min_p > 0:
-        kept = min(kept, max(1, int((w >= min(np.float64(min_p), 1.0)).sum())))
+        kept = min(kept, max(1, int((w >= np.float64(min_p)).sum())))
     end = np.cumsum(w[:kept])
     j = int((end <= min(np.float64(u), 1 - 2.0 ** -24) * end[-1]).sum())
     j = min(j, kept - 1)

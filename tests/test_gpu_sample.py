@@ -365,3 +365,19 @@ def test_binding_refuses():
         bd.sample(l[:0], u[:0])
     with pytest.raises(bd.FlashGauError):
         bd.sample(l[:, :0], u)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("N,V", [(6, 3), (6, 5000), (6, 40000), (40, 30000)])
+def test_min_p_above_one_keeps_the_first_word(N, V, dtype):
+    """Rows whose largest word has equals, with the other filters on and off: at
+    min_p 1 all of them are kept, above it the first one alone."""
+    rng = np.random.default_rng(V)
+    logits = torch.tensor(rng.normal(size=(N, V))).clamp(max=1.0)
+    logits[:, 1:3] = 1.0
+    m = torch.tensor(np.resize([1.0, 1.0 + 2.0 ** -23, 2.0, INF], N), dtype=torch.float32)
+    u = torch.full((N,), 0.9)
+    for kw in (dict(), dict(top_p=torch.full((N,), 0.95)),
+               dict(top_k=torch.full((N,), 3, dtype=torch.int32))):
+        _, _, kept = check(logits.to(dtype), u, dict(min_p=m, **kw), rows=range(min(N, 8)))
+        assert (kept[m.cuda() > 1] == 1).all()

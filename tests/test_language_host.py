@@ -147,6 +147,13 @@ def test_oracle_sampling_special_rows():
     assert oracle.sample_row([1.0, 1.0, 1.0, 1.0], 0.0, top_p=0.5)[2] == 2
 
 
+def test_oracle_min_p_above_one_keeps_the_first_word():
+    """No word's share reaches it, those that tie with the largest neither."""
+    for m in (1.0000001, 2.0, np.inf):
+        assert oracle.sample_row([1.0, 1.0, 0.0], 0.9, min_p=m) == (0, 0.0, 1)
+    assert oracle.sample_row([1.0, 1.0, 0.0], 0.9, min_p=1.0)[::2] == (1, 2)
+
+
 # ---- refusals of the C ABI -----------------------------------------------------
 A, B, C, D, E_, F_ = (1 << 32, 2 << 32, 3 << 32, 4 << 32, 5 << 32, 6 << 32)  # fake arrays
 
