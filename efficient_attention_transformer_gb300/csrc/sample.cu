@@ -93,20 +93,27 @@ __device__ __forceinline__ Pair times(float a, float bh, float bl) {
 constexpr float kLog2eH = 1.44269502f, kLog2eL = 1.92596303e-8f;
 constexpr float kLn2H = 0.693145751953125f, kLn2L = 1.42860677e-6f;
 
-// What a row's words are weighed with.
+// What a row's words are weighed with.  From a T of 2^64 on logits and T are
+// taken 2^64 times smaller, so that finite logits have a finite difference and
+// log2(e) / T its digits; below, a difference that overflows has no weight.
 struct Weigh {
-  float top;     // largest logit
-  float ch, cl;  // log2(e) / T as a pair
+  float unit;    // 1, or 2^-64
+  float top;     // the largest logit times unit
+  float ch, cl;  // log2(e) / (T unit) as a pair
   int drop;      // bits of the unit given up for many words
   const u64 *pow;
 
   __device__ void temperature(float T) {
+    unit = T >= 0x1p64f ? 0x1p-64f : 1.f;
+    T *= unit;
     ch = kLog2eH / T;
     cl = T < 1e38f ? (fmaf(-ch, T, kLog2eH) + kLog2eL) / T : 0.f;
   }
   // (l - top) log2(e) / T
   __device__ Pair exponent(float l) const {
-    const Pair d = add(l, -top);
+    // the sum of l unit and -top with its error, the product being exact
+    const float s = fmaf(l, unit, -top), bv = fmaf(-l, unit, s), av = s - bv;
+    const Pair d = {s, fmaf(l, unit, -av) - (top + bv)};
     const float yh = d.h * ch;
     return {yh, fmaf(d.h, cl, fmaf(d.l, ch, fmaf(d.h, ch, -yh)))};
   }
@@ -568,11 +575,11 @@ struct Row {
   const T *row;
   int V;
   Weigh w;
-  float per;  // bins of l a unit of l
+  float per;  // bins of l a (scaled) unit of l
   Blocks<MANY> blocks;
 
   __device__ int bin(float l) const {
-    return min(kBins - 1, __float2int_rz((w.top - l) * per));
+    return min(kBins - 1, __float2int_rz(fmaf(-l, w.unit, w.top) * per));
   }
 
   // The place at which words (or masses) reach `target`, which lies in bin
@@ -999,13 +1006,14 @@ __device__ bool counted_row(Counted &s, const SampleArgs &a, const Settings &set
   const int top = s.most                 ? (int)(kLeast16 + kValues - 1 - s.most)
                   : s.count[kValues] ? (int)kValues
                                      : (int)(kValues + 128 + s.least_bits - kLeast16);
-  w.top = value16(top);
+  const float largest = value16(top);
   if (set.temperature < kNoTemperature) {
-    greedy<THREADS>(s, a, n, row, w.top);
+    greedy<THREADS>(s, a, n, row, largest);
     return true;
   }
+  w.top = largest * w.unit;
   // Values with a weight: 2^-45 lies 31.2 T below the largest.
-  const uint32_t low = __float_as_uint(fmaf(-32.f, set.temperature, w.top)) >> 16;
+  const uint32_t low = __float_as_uint(fmaf(-32.f, set.temperature, largest)) >> 16;
   const int size = (int)(low & 0x7fffu) - (int)kLeast16;
   const int last = size < 0           ? (int)kValues
                    : low & 0x8000u ? (int)kValues + 128 + min(size, (int)kValues - 1)
@@ -1065,7 +1073,7 @@ __device__ bool counted_row(Counted &s, const SampleArgs &a, const Settings &set
       } else if (step == 2) {
         if (!(set.min_p > 0.f)) continue;
         how = kByLeast;
-        least = set.least(w.top, s.pow);
+        least = set.least(largest, s.pow);
       } else {
         target = set.draw(kept_mass);
       }
@@ -1147,22 +1155,23 @@ __device__ void any_row(Shared &s, const SampleArgs &a, const Settings &set, lon
   }
   const uint32_t top_key = MANY ? s.all_top : s.lo;
   const int finite = MANY ? s.all_finite : s.finite;
-  r.w.top = value_of(top_key);
+  const float largest = value_of(top_key);
   // settings that are no numbers, or a row without a distribution
   const bool none = (MANY ? s.all_bad : s.bad) || !finite || !set.usable();
   if (none || set.temperature < kNoTemperature) {
     if (MANY) r.blocks.meet();  // the others may still read
     if (r.blocks.rank) return;
-    if (!none) greedy<THREADS>(s, a, n, r.row, r.w.top);
+    if (!none) greedy<THREADS>(s, a, n, r.row, largest);
     else if (tid == 0) no_token(a, n);
     return;
   }
   r.w.temperature(set.temperature);
+  r.w.top = largest * r.w.unit;
   r.w.drop = a.drop;
   r.w.pow = s.pow;
   const bool by_min = set.min_p > 0.f;
   if (by_min) {
-    if (tid == 0) s.least = set.least(r.w.top, s.pow);
+    if (tid == 0) s.least = set.least(largest, s.pow);
     __syncthreads();
   }
   const float least = s.least;

@@ -381,3 +381,27 @@ def test_min_p_above_one_keeps_the_first_word(N, V, dtype):
                dict(top_k=torch.full((N,), 3, dtype=torch.int32))):
         _, _, kept = check(logits.to(dtype), u, dict(min_p=m, **kw), rows=range(min(N, 8)))
         assert (kept[m.cuda() > 1] == 1).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("mode", MODES)
+@pytest.mark.parametrize("N,V", [(9, 7), (9, 3000), (9, 30000)])
+def test_logits_and_temperatures_of_every_size(N, V, mode, dtype):
+    """Differences of finite logits that fp32 does not hold, temperatures at
+    which those have a weight, and the same in other sizes."""
+    rng = np.random.default_rng(V)
+    most = 3.3e38
+    l, kw = rng.uniform(-1, 1, (N, V)), settings(mode, N, rng, V)
+    T = kw["temperature"]
+    for i, (size, t) in enumerate([(most, 1e38), (most, 3e37), (most, INF), (most, 1.0),
+                                   (1e36, 2.5e35), (2.0 ** 63, 2.0 ** 64), (1e20, 1.8e19),
+                                   (1e-30, 1e-30), (1e-38, 3.4e38)]):
+        l[i] *= size
+        T[i] = t
+    l[:3, 0], l[:3, 1] = most, -most
+    u = torch.tensor(rng.random(N), dtype=torch.float32)
+    u[0] = 1 - 2.0 ** -24  # the last word, which weighs e^-6.6 here
+    check(torch.tensor(l).to(dtype), u, kw)
+    if mode == "none":
+        x = torch.tensor([[3e38, -3e38]], dtype=dtype)
+        assert check(x, u[:1], dict(temperature=torch.tensor([1e38])))[0].tolist() == [1]
