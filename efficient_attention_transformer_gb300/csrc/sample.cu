@@ -208,6 +208,7 @@ struct Settings {
     const Pair d = times(temperature, ln.h, ln.l);
     if (!(d.h > -kInf)) return -kInf;
     const Pair s = add(top, d.h);
+    if (!(s.h > -kInf)) return -kInf;  // below every finite logit
     return __fadd_ru(s.h, s.l + d.l);
   }
 };

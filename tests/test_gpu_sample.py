@@ -405,3 +405,16 @@ def test_logits_and_temperatures_of_every_size(N, V, mode, dtype):
     if mode == "none":
         x = torch.tensor([[3e38, -3e38]], dtype=dtype)
         assert check(x, u[:1], dict(temperature=torch.tensor([1e38])))[0].tolist() == [1]
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("V", [2, 3000, 30000])
+def test_min_p_that_lets_every_finite_logit_through(V, dtype):
+    """top + T ln(min_p) below the lowest finite number, and where it is not."""
+    rng = np.random.default_rng(V)
+    l = rng.uniform(-3.3e38, -3e38, (6, V))
+    T = torch.tensor([1e38, 1e38, 1e37, INF, 3.4e38, 1e30])
+    m = torch.tensor([0.1, 2.0 ** -140, 0.01, 0.999, 0.5, 0.9])
+    u = torch.tensor(rng.random(6), dtype=torch.float32)
+    _, _, kept = check(torch.tensor(l).to(dtype), u, dict(temperature=T, min_p=m))
+    assert (kept[:5] == V).all()
