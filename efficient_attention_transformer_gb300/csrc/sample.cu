@@ -138,9 +138,10 @@ __device__ __noinline__ Pair logarithm(int k, u64 x, const u64 *pow) {
   return {s.h, s.l + fmaf((float)k, kLn2L, miss)};
 }
 
-// The whole part of x * m, 0 <= x < 1, and whether anything is cut off.
+// The whole part of x * m, 0 <= x < 1 (a zero of either sign), and whether
+// anything is cut off.
 __device__ __forceinline__ u64 part_of(float x, u64 m, bool *cut) {
-  const uint32_t b = __float_as_uint(x), e = b >> 23;
+  const uint32_t b = __float_as_uint(x) & 0x7fffffffu, e = b >> 23;
   const u64 digits = e ? (b & 0x7fffffu) | 0x800000u : b & 0x7fffffu;
   const int shift = 150 - (int)(e ? e : 1);  // 24 or more
   const u64 hi = __umul64hi(digits, m), lo = digits * m;

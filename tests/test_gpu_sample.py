@@ -418,3 +418,21 @@ def test_min_p_that_lets_every_finite_logit_through(V, dtype):
     u = torch.tensor(rng.random(6), dtype=torch.float32)
     _, _, kept = check(torch.tensor(l).to(dtype), u, dict(temperature=T, min_p=m))
     assert (kept[:5] == V).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("V", [5, 3000, 30000])
+def test_zeros_of_either_sign(V, dtype):
+    """u, T, top_p and min_p at minus zero are at zero."""
+    rng = np.random.default_rng(V)
+    logits = torch.tensor(rng.normal(size=(6, V))).to(dtype)
+    zero = torch.zeros(6)
+    zero[1::2] = -0.0
+    logits[1::2] = logits[::2]
+    settings = [dict(), dict(top_p=torch.full((6,), 0.9)), dict(min_p=zero),
+                dict(top_k=torch.full((6,), 3, dtype=torch.int32)), dict(top_p=zero),
+                dict(temperature=zero)]
+    for kw in settings:
+        got = check(logits, zero, kw)
+        assert all(torch.equal(x[::2], x[1::2]) for x in got)
+        assert torch.equal(got[0], check(logits, torch.zeros(6), dict(temperature=torch.zeros(6)))[0])
