@@ -365,6 +365,7 @@ cudaError_t xent(const XentProblem &q, int dtype);
 
 // Relative position tables by buckets of distance (bucket_bias.cu).
 constexpr int kBucketMax = 256;
+constexpr int kBucketMostShared = 1 << 20;  // gradients of a table, added up by one thread each
 struct BucketProblem {
   int H, buckets, far, C, causal;
   cudaStream_t stream;

@@ -97,8 +97,8 @@ int flash_gau_bucket_bias(const float *table, int H, int buckets, int max_distan
 int flash_gau_bucket_bias_backward(const float *drelpos, int R, int H, int buckets,
                                    int max_distance, int C, int causal, float *dtable,
                                    void *stream) {
-  if (!drelpos || !dtable || !aligned(drelpos, 4) || !aligned(dtable, 4) || R < 1)
-    return FLASH_GAU_EINVAL;
+  if (!drelpos || !dtable || !aligned(drelpos, 4) || !aligned(dtable, 4)) return FLASH_GAU_EINVAL;
+  if (R < 1 || R > kBucketMostShared) return FLASH_GAU_EINVAL;
   int st = check_buckets(H, buckets, max_distance, C, causal);
   if (st != FLASH_GAU_OK) return st;
   const Span out[1] = {{dtable, (size_t)H * buckets * 4}};

@@ -541,8 +541,8 @@ int flash_gau_adamw_moments(const flash_gau_adamw_tensor *tensors, int n_tensors
  *              them; the R ones of a table that layers share are added up
  *   dtable     device fp32 [H, buckets], written, not added; a call repeats
  *              bit for bit
- * Supported: 1 <= C <= 4096, 1 <= H <= 65535, R >= 1, 2 <= buckets <= 256
- * (not causal: 4 at least, and even), near < max_distance <= 2^20.  One launch
+ * Supported: 1 <= C <= 4096, 1 <= H <= 65535, 1 <= R <= 2^20, 2 <= buckets
+ * <= 256 (not causal: 4 at least, and even), near < max_distance <= 2^20.  One launch
  * each, no workspace.  Returns FLASH_GAU_OK, FLASH_GAU_EINVAL (null or
  * overlapping arrays, sizes out of range), FLASH_GAU_EDEVICE or
  * FLASH_GAU_ECUDA.                                                           */

@@ -120,3 +120,18 @@ def test_repeats_writes_only_its_rows_and_replays():
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(a, 2 * rel) and torch.equal(b, 2 * dt)
+
+
+@pytest.mark.parametrize("R,H,C", [(5000, 2, 130), (1 << 20, 1, 1), (100003, 1, 3)])
+def test_many_gradients_of_a_table(R, H, C):
+    """Eight gradients behind one another, then R / 8 of those sums, then a run's
+    offsets and the blocks as ever."""
+    g = torch.Generator().manual_seed(R)
+    d = torch.randn(R, H, 2 * C - 1, generator=g).cuda()
+    for causal in (True, False):
+        dt = bd.bucket_bias_backward(d, 16, causal, max_distance=64)
+        d64 = d.double().cpu().numpy()
+        want = oracle.bucket_bias_grad(d64, 16, 64, causal)
+        most = oracle.bucket_bias_grad(np.abs(d64), 16, 64, causal)
+        adds = 8 + -(-R // 8) + 32 + 5 + 8
+        assert np.all(np.abs(dt.double().cpu().numpy() - want) <= adds * U * most)

@@ -188,6 +188,11 @@ def test_bucket_bias_refuses(L, args, code):
                                             a["C"], a["causal"], a["table"], None) == code
 
 
+@pytest.mark.parametrize("R", [(1 << 20) + 1, (1 << 31) - 8, (1 << 31) - 1])
+def test_bucket_bias_backward_refuses_more_tables_than_it_sums(L, R):
+    assert L.flash_gau_bucket_bias_backward(B, R, 1, 32, 128, 1, 1, A, None) == bd.EINVAL
+
+
 def _norm(**kw):
     o = dict(post=bd.NORM_NONE, norm=bd.NORM_LAYER, post_g=None, post_b=None, norm_g=64,
              norm_b=None, scale=None, gate=None, eps=EPS)
