@@ -959,6 +959,14 @@ class AdamW:
         return out_m, out_v
 
 
+def _ints(*values):
+    """Refuses whole numbers that the C ABI's int does not hold, which ctypes
+    would pass on without their upper bits."""
+    for v in values:
+        if not -0x80000000 <= v <= 0x7fffffff:
+            _check(EINVAL)
+
+
 def bucket_bias(table, C, causal, max_distance=128, out=None, stream=None):
     """The layer's relative position tables [..., 2C-1] from learned values
     [..., buckets] by buckets of distance (both fp32), through
@@ -971,14 +979,15 @@ def bucket_bias(table, C, causal, max_distance=128, out=None, stream=None):
         with _scope(dev, stream):
             return bucket_bias(table, C, causal, max_distance, out)
     buckets = lead[-1]
+    H = table.numel() // (buckets or 1)
+    _ints(H, buckets, max_distance, C)
     shape = lead[:-1] + (max(2 * C - 1, 0),)
     if out is None:
         out = torch.empty(shape, dtype=f32, device=dev)
         op = out.data_ptr()
     else:
         op = _like(out, "out", shape, f32, at)
-    _check(lib().flash_gau_bucket_bias(tp, table.numel() // (buckets or 1), buckets, max_distance,
-                                       C, 1 if causal else 0, op,
+    _check(lib().flash_gau_bucket_bias(tp, H, buckets, max_distance, C, 1 if causal else 0, op,
                                        torch._C._cuda_getCurrentRawStream(at)))
     return out
 
@@ -995,15 +1004,15 @@ def bucket_bias_backward(drelpos, buckets, causal, max_distance=128, out=None, s
     if _elsewhere(dev, stream):
         with _scope(dev, stream):
             return bucket_bias_backward(drelpos, buckets, causal, max_distance, out)
-    H = 1 if dims == 1 else given[-2]
+    R, H, C = given[0] if dims == 3 else 1, 1 if dims == 1 else given[-2], (given[-1] + 1) // 2
+    _ints(R, H, buckets, max_distance, C)
     shape = (buckets,) if dims == 1 else (H, buckets)
     if out is None:
         out = torch.empty(shape, dtype=f32, device=dev)
         op = out.data_ptr()
     else:
         op = _like(out, "out", torch.Size(shape), f32, at)
-    _check(lib().flash_gau_bucket_bias_backward(dp, given[0] if dims == 3 else 1, H, buckets,
-                                                max_distance, (given[-1] + 1) // 2,
+    _check(lib().flash_gau_bucket_bias_backward(dp, R, H, buckets, max_distance, C,
                                                 1 if causal else 0, op,
                                                 torch._C._cuda_getCurrentRawStream(at)))
     return out
@@ -1034,6 +1043,7 @@ def _packed(packed, shape, index):
 
 
 def _norm_of(norm, norm_g, norm_b, eps, d, index):
+    _ints(norm, d)
     if norm_g is not None:
         norm_g = _param(norm_g, "norm_g", d if norm == NORM_LAYER else 1, index)
     if norm_b is not None:
@@ -1181,6 +1191,7 @@ def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, out_
         with _scope(dev, stream):
             return sample(logits, u, temperature, top_k, top_p, min_p, out_token, out_logp,
                           out_kept)
+    _ints(V)
     at, f32, i32 = dev.index, torch.float32, torch.int32
     up = _like(u, "u", lead, f32, at)
     held, ptrs = [], []  # tensors made of single values live until the launch

@@ -238,3 +238,33 @@ def test_streams_and_threads_at_once(dtype):
     for t in threads:
         t.join()
     assert not wrong
+
+
+def test_whole_numbers_that_the_library_does_not_take():
+    """Refused, not taken without their upper 32 bits: sizes as arguments, and
+    those of tensors of that many elements."""
+    more = 1 << 32
+    t, d = torch.randn(3, 32, device="cuda"), torch.randn(1, 3, 39, device="cuda")
+    h = torch.zeros(4, 64, device="cuda")
+    g = torch.ones(1, device="cuda")
+    packed = bd.checkpoint_pack(h)[0]
+    long = torch.empty(1, more + 128, dtype=torch.bfloat16, device="cuda")
+    bytes_ = long.view(torch.int8)[:, :more + 128]
+    many = torch.empty(more + 1, 1, 1, device="cuda")
+    u = torch.rand(1, device="cuda")
+    calls = [lambda: bd.bucket_bias(t, 20, True, max_distance=more + 128),
+             lambda: bd.bucket_bias(t, more + 20, True),
+             lambda: bd.bucket_bias(t, 20 - more, True),
+             lambda: bd.bucket_bias(many.view(1, -1), 20, True),
+             lambda: bd.bucket_bias_backward(d, more + 32, True),
+             lambda: bd.bucket_bias_backward(d, 32, True, max_distance=more + 128),
+             lambda: bd.bucket_bias_backward(many, 32, True),
+             lambda: bd.checkpoint_pack(long),
+             lambda: bd.checkpoint_pack(h, norm=more + bd.NORM_SCALE, norm_g=g),
+             lambda: bd.checkpoint_restore((bytes_, u), torch.float32),
+             lambda: bd.checkpoint_backward(None, long, (bytes_, u)),
+             lambda: bd.checkpoint_backward(None, h, packed, norm=more + bd.NORM_SCALE, norm_g=g),
+             lambda: bd.sample(long, u)]
+    for call in calls:
+        with pytest.raises(bd.FlashGauError):
+            call()
