@@ -27,7 +27,8 @@ join_columns_kernel(const float *__restrict__ part, int blocks, int d, float *__
   if (lane == 0 && mine < 2 * d && to) to[mine < d ? mine : mine - d] = all;
 }
 // ScaleNorm's one g: n sums of both signs that nearly cancel, so what each
-// addition cuts off is added up beside it.
+// addition cuts off is added up beside it (of an infinite sum nothing is: infinity
+// less itself is no number).
 __global__ void __launch_bounds__(1024)
 join_scalar_kernel(const float *__restrict__ part, int n, float *__restrict__ dg) {
   __shared__ float2 s[32];
@@ -50,7 +51,7 @@ join_scalar_kernel(const float *__restrict__ part, int n, float *__restrict__ dg
   if (threadIdx.x < 32) {
     v = s[threadIdx.x];
     warp();
-    if (threadIdx.x == 0) *dg = v.x + v.y;
+    if (threadIdx.x == 0) *dg = isfinite(v.x) ? v.x + v.y : v.x;
   }
 }
 

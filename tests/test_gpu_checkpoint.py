@@ -359,3 +359,36 @@ def test_binding_refuses():
               lambda: bd.checkpoint_pack(p.h[:0])):
         with pytest.raises(bd.FlashGauError):
             f()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("norm", ["layer", "scale"])
+@pytest.mark.parametrize("M,d", [(1, 64), (50, 256), (50, 255), (700, 1501)])
+def test_infinite_sums(M, d, norm, dtype):
+    """An infinity of dn makes the parameters' sums it enters infinite, two of
+    unlike signs make them no number, and nothing else does."""
+    gen = torch.Generator().manual_seed(d)
+    h = (torch.rand(M, d, generator=gen) + torch.linspace(-3, 3, d)).to(dtype).cuda()
+    dn = torch.randn(M, d, generator=gen).to(dtype).cuda()
+    g = torch.ones(d if norm == "layer" else 1, device="cuda")
+    packed = bd.checkpoint_pack(h)[0]
+    x = oracle.checkpoint_values(*(t.cpu().numpy() for t in packed))
+    inf = float("inf")
+    m, c = M // 2, d - 1
+    for values in ({c: inf}, {c: -inf}, {0: inf}, {0: inf, c: inf}, {0: float("nan")}):
+        dirty = dn.clone()
+        for k, v in values.items():
+            dirty[m, k] = v
+        got = bd.checkpoint_backward(None, dirty, packed, norm=KIND[norm], norm_g=g)
+        with np.errstate(invalid="ignore"):
+            u = oracle.norm_rows(x, norm, f64(g), None, 1e-5)[0]
+            terms = f64(dirty) * u
+            want = dict(dnorm_g=terms.sum(0) if norm == "layer" else terms.sum().reshape(1),
+                        dnorm_b=f64(dirty).sum(0) if norm == "layer" else None)
+        for name, w in want.items():
+            if w is None:
+                assert got[name] is None
+                continue
+            a = f64(got[name])
+            assert np.array_equal(np.isnan(a), np.isnan(w)), (values, name)
+            assert np.array_equal(np.where(np.isinf(a), a, 0), np.where(np.isinf(w), w, 0))
