@@ -1041,9 +1041,11 @@ struct SumArgs {
   int parts, blocks, warps, d;
 };
 
-// A sum with what its roundings have left out (Knuth's two-sum).
+// A sum with what its roundings have left out (Knuth's two-sum; nothing of a sum
+// that is not finite, infinity less itself being no number).
 struct Exact {
   float sum, left;
+  __device__ float all() const { return isfinite(sum) ? sum + left : sum; }
   __device__ void add(float x, float x_left) {
     const float t = sum + x, b = t - sum;
     left += x_left + ((sum - (t - b)) + (x - b));
@@ -1091,7 +1093,7 @@ __global__ void __launch_bounds__(1024) sum_parts_kernel(const SumArgs a) {
     if (sub == 0) {
       v = sums[lane];
       v.join_warp();
-      if (lane == 0) a.out[s][0] = v.sum + v.left;
+      if (lane == 0) a.out[s][0] = v.all();
     }
     return;
   }

@@ -408,3 +408,24 @@ def test_aligned_widths(M, d, dtype):
     p = Problem(M, d, dtype, "layer", "layer", True, True, M + d)
     check_forward(p)
     check_backward(p)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("M,d", [(1, 64), (50, 255), (700, 1024)])
+def test_infinite_sums_of_a_scale_norms_g(M, d, dtype):
+    """An infinity of dn makes norm_g's gradient infinite and one of dr post_g's,
+    two of unlike signs make it no number."""
+    gen = torch.Generator().manual_seed(d)
+    rows = lambda: (torch.rand(M, d, generator=gen) + torch.linspace(-3, 3, d)).to(dtype).cuda()  # noqa: E731
+    r, y, g = rows(), rows(), torch.ones(1, device="cuda")
+    inf, m = float("inf"), M // 2
+    for values, want in (({d - 1: inf}, inf), ({d - 1: -inf}, -inf), ({0: inf}, -inf),
+                         ({0: inf, d - 1: inf}, None), ({0: float("nan")}, None)):
+        grad = torch.randn(M, d, generator=gen).to(dtype).cuda()
+        for k, v in values.items():
+            grad[m, k] = v
+        a = bd.residual_norm_backward(None, grad, r, None, norm=bd.NORM_SCALE, norm_g=g)["dnorm_g"]
+        b = bd.residual_norm_backward(grad, None, None, y, post_norm=bd.NORM_SCALE, post_g=g,
+                                      norm=bd.NORM_NONE)["dpost_g"]
+        for x in (a, b):
+            assert bool(torch.isnan(x)) if want is None else float(x) == want
