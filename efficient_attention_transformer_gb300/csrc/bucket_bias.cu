@@ -35,7 +35,7 @@ constexpr int kRun = 8;   // rows of drelpos under way at once, and in one fp32 
 struct Starts {
   int n;       // buckets of a direction
   int ahead;   // offsets above zero have buckets n .. 2n-1 of their own
-  int start[kBucketMax];  // first distance of each bucket, rising
+  int start[kBucketMax];  // first distance of each bucket, rising; C or more: of none
 };
 
 // Whether (t / near)^m >= (far / near)^i, in whole numbers: t^m near^i against
@@ -88,9 +88,17 @@ Starts make_starts(const BucketProblem &q) {
       continue;
     }
     // the smallest t with t >= near ratio^((b - near) / rest); where that is
-    // next to a whole number, the whole number itself decides
+    // next to a whole number, the whole number itself decides.  x is off by less
+    // than 4e-15 of itself: the exponent's rounding times log(ratio) <= 14, a
+    // rounding of ratio and of the product, and pow's.  Distances end at C - 1,
+    // so the starts behind are anything above (to look at all of 128 of them up
+    // to 2^20 took the host half a millisecond).
     const double x = near * pow(ratio, (double)(b - near) / rest), r = nearbyint(x);
-    if (fabs(x - r) > 1e-6 * x)
+    if (x > q.C + 1.0) {
+      for (; b < s.n; ++b) s.start[b] = q.C + 1 > near ? q.C + 1 : near;
+      break;
+    }
+    if (fabs(x - r) > 1e-12 * x)
       s.start[b] = (int)ceil(x);
     else
       s.start[b] = (int)r + !reaches((uint32_t)r, near, q.far, b - near, rest);

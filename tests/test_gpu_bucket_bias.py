@@ -5,6 +5,9 @@ gradient is a sum of fp32 values, of at most 16 behind one another, R / 16 of
 those, then 1024 / 32 in a lane of a warp, 5 shuffles and 8 blocks: its error
 is below that many roundings of 2^-24 of the sum of magnitudes."""
 
+import random
+import time
+
 import numpy as np
 import pytest
 import torch
@@ -135,3 +138,34 @@ def test_many_gradients_of_a_table(R, H, C):
         most = oracle.bucket_bias_grad(np.abs(d64), 16, 64, causal)
         adds = 8 + -(-R // 8) + 32 + 5 + 8
         assert np.all(np.abs(dt.double().cpu().numpy() - want) <= adds * U * most)
+
+
+@pytest.mark.parametrize("seed", range(6))
+def test_distances_of_every_size(seed):
+    """max_distance from next to the exact buckets up to the largest, far behind
+    the chunk among them, and borders that are whole numbers."""
+    rng = random.Random(seed)
+    for _ in range(12):
+        causal = rng.random() < 0.5
+        buckets = rng.randint(2, 256) if causal else 2 * rng.randint(2, 128)
+        near = (buckets if causal else buckets // 2) // 2
+        far = rng.choice([near + 1, rng.randint(near + 1, 4096), rng.randint(near + 1, 1 << 20),
+                          near << rng.randint(1, 10), near * rng.randint(2, 40), 1 << 20])
+        check(2, rng.choice([1, 2, rng.randint(3, 300), 4096]), buckets, far, causal, seed=seed)
+
+
+def test_large_distances_cost_the_host_no_more():
+    """A call's time on the host, the least of many: with max_distance at its
+    largest within four times that of a small one."""
+    table = torch.randn(1, 256, device="cuda")
+
+    def least(far):
+        best = 1.0
+        for _ in range(50):
+            torch.cuda.synchronize()
+            start = time.perf_counter()
+            bd.bucket_bias(table, 256, True, max_distance=far)
+            best = min(best, time.perf_counter() - start)
+        return best
+
+    assert least(1 << 20) <= 4 * least(200)
