@@ -392,3 +392,77 @@ def test_infinite_sums(M, d, norm, dtype):
             a = f64(got[name])
             assert np.array_equal(np.isnan(a), np.isnan(w)), (values, name)
             assert np.array_equal(np.where(np.isinf(a), a, 0), np.where(np.isinf(w), w, 0))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("norm", ["none", "layer", "scale"])
+@pytest.mark.parametrize("M,d", [(1, 5), (3, 129), (5, 767), (9, 1500), (3, 4099), (4, 256),
+                                 (1, 8191), (350, 767), (333, 2041), (2, 1)])
+@pytest.mark.parametrize("offset", [16, 17])
+def test_nothing_beside_any_output_is_written(M, d, norm, dtype, offset):
+    """Every output of the three calls in the middle of a larger buffer, on a
+    vector's boundary and one element behind it: what stands before and behind
+    is left, and the outputs are those of arrays of their own."""
+    gen = torch.Generator().manual_seed(M + d)
+    rows = lambda: torch.randn(M, d, generator=gen).to(dtype).cuda()  # noqa: E731
+    groups, held = -(-d // 128), []
+
+    def inner(shape, dt=dtype):
+        n = int(np.prod(shape))
+        flat = torch.full((offset + n + 16,), 7, dtype=dt, device="cuda")
+        held.append((flat, n))
+        return flat[offset:offset + n].view(shape)
+
+    h, y, dr, dn = rows(), rows(), rows(), rows()
+    kw = dict(norm=KIND[norm], norm_g=None, norm_b=None)
+    if norm == "layer":
+        kw.update(norm_g=torch.randn(d, generator=gen).cuda(),
+                  norm_b=torch.randn(d, generator=gen).cuda())
+    elif norm == "scale":
+        kw.update(norm_g=torch.ones(1, device="cuda"))
+    packed, r, n = bd.checkpoint_pack(h, y, **kw)
+    x, xn = bd.checkpoint_restore(packed, dtype, **kw)
+    want = [packed.codes, packed.scales, r, n, x, xn]
+    out = bd.Checkpoint(inner((M, d), torch.int8), inner((M, groups), torch.float32))
+    a, b = inner((M, d)), None if norm == "none" else inner((M, d))
+    bd.checkpoint_pack(h, y, out=out, out_r=a, out_n=b, **kw)
+    e, f = inner((M, d)), None if norm == "none" else inner((M, d))
+    bd.checkpoint_restore(packed, dtype, out_x=e, out_n=f, **kw)
+    got = [out.codes, out.scales, a, b, e, f]
+    if norm != "none":
+        grads = bd.checkpoint_backward(dr, dn, packed, **kw)
+        to = dict(dh=inner((M, d)), dnorm_g=inner(kw["norm_g"].shape, torch.float32))
+        if norm == "layer":
+            to["dnorm_b"] = inner((d,), torch.float32)
+        bd.checkpoint_backward(dr, dn, packed, out=to, **kw)
+        # element by element the sums are added up in another order
+        exact = [("dh", dtype)] if offset == 16 else []
+        want += [grads[k] for k, _ in exact]
+        got += [to[k] for k, _ in exact]
+        for k, t in to.items():
+            torch.testing.assert_close(t, grads[k], rtol=1e-2, atol=1e-2)
+    torch.cuda.synchronize()
+    for flat, size in held:
+        assert bool((flat[:offset] == 7).all()) and bool((flat[offset + size:] == 7).all())
+    for k, (p, q) in enumerate(zip(got, want)):
+        if p is not None and (offset == 16 or k in (0, 1, 2, 4)):
+            assert torch.equal(p, q), k
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_rows_whose_statistics_fp32_does_not_hold(dtype):
+    """A hundred values of 3e38 add up to infinity in fp32, which is the norm's
+    word for a row above 1e19 in length: no number of a LayerNorm, as of the
+    residual stream's, zero of a ScaleNorm, and the rows beside it as ever."""
+    h = torch.zeros(3, 300)
+    h[1, ::3] = 3e38
+    h[::2] = torch.randn(2, 300, generator=torch.Generator().manual_seed(6))
+    h = h.to(dtype).cuda()
+    packed = bd.checkpoint_pack(h)[0]
+    for kind, g in (("layer", torch.ones(300)), ("scale", torch.ones(1))):
+        kw = dict(norm=KIND[kind], norm_g=g.cuda())
+        x, n = bd.checkpoint_restore(packed, dtype, **kw)
+        other = bd.residual_norm(x, **kw)[1]
+        for t in (n, other):
+            assert bool((torch.isnan(t[1]) if kind == "layer" else t[1] == 0).all())
+            assert bool(torch.isfinite(t[::2]).all())
