@@ -268,3 +268,50 @@ def test_whole_numbers_that_the_library_does_not_take():
     for call in calls:
         with pytest.raises(bd.FlashGauError):
             call()
+
+
+@pytest.mark.parametrize("d", [2048, 2047])
+def test_checkpoints_of_more_than_31_bits_of_elements(d):
+    """The last rows come out as those of a call of their own."""
+    M, last, io = 1_100_000, 16, torch.bfloat16
+    gen = torch.Generator(device="cuda").manual_seed(d)
+    h = torch.empty(M, d, dtype=io, device="cuda").normal_(generator=gen)
+    for kind, g in ((bd.NORM_LAYER, torch.rand(d, generator=gen, device="cuda")),
+                    (bd.NORM_SCALE, torch.ones(1, device="cuda"))):
+        kw = dict(norm=kind, norm_g=g)
+        packed, _, n = bd.checkpoint_pack(h, **kw)
+        x, xn = bd.checkpoint_restore(packed, io, **kw)
+        dh = bd.checkpoint_backward(x, h, packed, **kw)["dh"]
+        few = h[-last:].clone()
+        p, _, fn = bd.checkpoint_pack(few, **kw)
+        fx, fxn = bd.checkpoint_restore(p, io, **kw)
+        want = [p.codes, p.scales, fn, fx, fxn, bd.checkpoint_backward(fx, few, p, **kw)["dh"]]
+        got = [packed.codes, packed.scales, n, x, xn, dh]
+        assert all(torch.equal(a[-last:], b) for a, b in zip(got, want))
+        del packed, n, x, xn, dh, got
+
+
+def test_logits_of_more_than_31_bits_of_elements():
+    N, V = 40_000, 60_001
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    logits = torch.empty(N, V, dtype=torch.bfloat16, device="cuda").normal_(generator=gen)
+    u = torch.rand(N, generator=gen, device="cuda")
+    kw = dict(temperature=0.8, top_k=500, top_p=0.9)
+    got = bd.sample(logits, u, **kw)
+    want = bd.sample(logits[-9:].clone(), u[-9:].clone(), **kw)
+    assert all(torch.equal(a[-9:], b) for a, b in zip(got, want))
+
+
+def test_bias_gradients_of_more_than_31_bits_of_elements():
+    """Whole numbers: an offset's sum, 700000 at most and so below 2^24, is
+    exact, and a bucket's where it is below 2^24 too; above, a lane adds up to
+    32 offsets, then there are 5 shuffles and 8 blocks, and each addition is off
+    by 2^-24 of the bucket's sum at most."""
+    R, H, C = 70_000, 10, 1700
+    d = torch.empty(R, H, 2 * C - 1, device="cuda")
+    d.copy_(torch.arange(1.0, H + 1, device="cuda")[:, None])
+    got = bd.bucket_bias_backward(d, 32, False)
+    size = np.bincount(oracle.buckets_of_offsets(C, 32, 128, False), minlength=32)
+    want = size * R * np.arange(1, H + 1)[:, None]
+    err = np.abs(f64(got) - want)
+    assert np.all(err <= (32 + 5 + 8) * 2.0 ** -24 * want) and not err[want < 2 ** 24].any()
