@@ -77,7 +77,8 @@ __device__ __forceinline__ u64 power(float yh, float yl, int drop, const u64 *po
   return (w + ((1ull << down) >> 1)) >> down;
 }
 
-// Sums and products of fp32 numbers with what their rounding cuts off.
+// Sums (Knuth) and products (Dekker, by a fused addition) of fp32 numbers with
+// what their rounding cuts off.
 struct Pair {
   float h, l;
 };
@@ -334,7 +335,7 @@ __device__ __forceinline__ void first_threads(int threads) {
 struct Tally {
   u64 warp_mass[32];
   uint32_t warp_count[32], turn_count[2][32];
-  u64 mass, sum_mass, q_mass, target;
+  u64 mass, sum_mass, q_mass;
   uint32_t count, q_count;
   int bin, at, bad, finite;
   float least;
@@ -763,7 +764,9 @@ __device__ void finish(Tally &s, const SampleArgs &a, long long n, const T *row,
 // neighbouring values are a bin, as far down as a weight reaches; warps weigh the
 // bins by turns, four values a lane.  One warp then holds what lies before each
 // bin and finds one place after the other without a barrier of the block.  Rows
-// with other words (but minus infinity) take the general form.
+// with other words (but minus infinity) take the general form, such as those masked
+// with a finite number: of 256 x 131072 with top_p, a tenth of the words at -1e4,
+// 446 us for 38.  Vectors that hold minus infinity go word by word (240).
 //
 // The counting bounds it: 32 lanes add to random banks, and the fullest of the
 // 32 sets the pace at 9 words a cycle and SM, whatever is done there (plain

@@ -542,8 +542,8 @@ int flash_gau_adamw_moments(const flash_gau_adamw_tensor *tensors, int n_tensors
  *   dtable     device fp32 [H, buckets], written, not added; a call repeats
  *              bit for bit
  * Supported: 1 <= C <= 4096, 1 <= H <= 65535, 1 <= R <= 2^20, 2 <= buckets
- * <= 256 (not causal: 4 at least, and even), near < max_distance <= 2^20.  One launch
- * each, no workspace.  Returns FLASH_GAU_OK, FLASH_GAU_EINVAL (null or
+ * <= 256 (not causal: 4 at least, and even), near < max_distance <= 2^20.  One
+ * launch each, no workspace.  Returns FLASH_GAU_OK, FLASH_GAU_EINVAL (null or
  * overlapping arrays, sizes out of range), FLASH_GAU_EDEVICE or
  * FLASH_GAU_ECUDA.                                                           */
 int flash_gau_bucket_bias(const float *table, int H, int buckets, int max_distance, int C,
@@ -563,9 +563,10 @@ int flash_gau_bucket_bias_backward(const float *drelpos, int R, int H, int bucke
  * infinity or NaN is restored as NaN throughout.  codes: device int8 [M, d];
  * scales: device fp32 [M, ceil(d / 128)].
  * o gives the norm of flash_gau_residual_norm (norm, norm_g, norm_b, eps); post,
- * scale and gate must be unset.  Any 1 <= d <= 8192 and 1 <= M <= 2^32 (more:
- * FLASH_GAU_ENOTSUP); rows and arrays need only their element's alignment
- * (16-byte aligned arrays and d a multiple of 8 run fastest).               */
+ * scale and gate must be unset; row statistics are fp32, squares too, as there.
+ * Any 1 <= d <= 8192 and 1 <= M <= 2^32 (more: FLASH_GAU_ENOTSUP); rows and
+ * arrays need only their element's alignment (16-byte aligned arrays, norm_g and
+ * norm_b among them, and d a multiple of 8 run fastest).                    */
 
 /* r = h + y, n = norm(r), and the codes of r as it is stored in the io type:
  * flash_gau_residual_norm with a checkpoint of its stream.  h, y: device
@@ -609,12 +610,13 @@ int flash_gau_checkpoint_backward(const void *dr, const void *dn, const signed c
  *                                                     (p >= 1: all)
  *   min_p  those with w_i >= min_p, that share of the first one's probability
  *                                                     (min_p <= 0: all)
- * the first word always.  The token is the first kept word with more than u of
- * the kept words' mass up to its own end.  T below 1e-30: the largest logit's
- * word, the lowest index of equal ones.  A logit of minus infinity is a word
- * that cannot be drawn.  A row with a NaN or plus infinity, without a finite
- * logit, or whose settings or u are NaN or T or u below zero, gets token -1,
- * logp NaN and kept 0.  u >= 1 is taken as 1 - 2^-24.
+ * the first word always (no other one reaches a min_p above 1).  The token is
+ * the first kept word with more than u of the kept words' mass up to its own
+ * end.  T below 1e-30: the largest logit's word, the lowest index of equal
+ * ones.  A logit of minus infinity is a word that cannot be drawn.  A row with
+ * a NaN or plus infinity, without a finite logit, or whose settings or u are
+ * NaN or T or u below zero, gets token -1, logp NaN and kept 0.  u >= 1 is
+ * taken as 1 - 2^-24.
  * Masses are whole numbers of units of 2^-44 of the largest (of less for more
  * than 2^18 words): a result depends neither on the launch nor on what else
  * the call holds, and a word below half a unit is never drawn.              */
@@ -626,14 +628,14 @@ typedef struct flash_gau_sampling {
 } flash_gau_sampling;
 
 /* logits: device, io type, row n at logits + n * ld elements, V of them (ld >=
- * V; element alignment, rows on 16-byte boundaries run fastest); u: device
- * fp32 [N], in [0, 1); s: host pointer, read during the call; token: device
- * int32 [N]; logp: device fp32 [N], the logarithm of the probability with
- * which the token was drawn, or NULL; kept: device int32 [N], how many words
- * the filters kept, or NULL.  Arrays must not overlap.  1 <= V <= 2^22, 1 <= N
- * <= 2^30 (more: FLASH_GAU_ENOTSUP).  One kernel, no workspace.  Returns
- * FLASH_GAU_OK, FLASH_GAU_EINVAL, FLASH_GAU_ENOTSUP, FLASH_GAU_EDEVICE or
- * FLASH_GAU_ECUDA.                                                          */
+ * V; element alignment; rows on 16-byte boundaries run fastest, and bf16 ones
+ * without masked words or words of 256 and more in magnitude); u: device fp32
+ * [N], in [0, 1); s: host pointer, read during the call; token: device int32
+ * [N]; logp: device fp32 [N], the logarithm of the probability with which the
+ * token was drawn, or NULL; kept: device int32 [N], how many words the filters
+ * kept, or NULL.  Arrays must not overlap.  1 <= V <= 2^22, 1 <= N <= 2^30
+ * (more: FLASH_GAU_ENOTSUP).  One kernel, no workspace.  Returns FLASH_GAU_OK,
+ * FLASH_GAU_EINVAL, FLASH_GAU_ENOTSUP, FLASH_GAU_EDEVICE or FLASH_GAU_ECUDA. */
 int flash_gau_sample(const void *logits, long long ld, long long N, int V, int dtype,
                      const float *u, const flash_gau_sampling *s, int *token, float *logp,
                      int *kept, void *stream);
